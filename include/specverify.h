@@ -39,8 +39,7 @@
  *     owns every buffer.  The library never allocates or frees device memory and
  *     keeps no state between calls except per-device caches of launch facts (SM
  *     count, resident CTAs per SM, resident CTA clusters per cluster size) and, for
- *     spec_verify_noalloc only, its one
- *     static scratch array and that array's cached device address (see there).
+ *     spec_verify_noalloc only, its one static scratch array and that array's cached device address (see there).
  *   - Work is queued on `cuda_stream` (a cudaStream_t; NULL = legacy default stream)
  *     and the call returns at once.  The return value reports only errors the host
  *     can see: bad arguments, misalignment, a too-small workspace, a launch failure.
@@ -66,7 +65,7 @@ extern "C" {
 typedef enum {
   SV_OK = 0,
   SV_ERR_ARG = -1,         /* null required pointer, size out of range, temperature <= 0 */
-  SV_ERR_DTYPE = -2,       /* dtype not SV_F32 / SV_BF16                                  */
+  SV_ERR_DTYPE = -2,       /* dtype not one the entry point takes (logits: F32 / BF16)    */
   SV_ERR_ALIGN = -3,       /* pointer misaligned (see conventions)                       */
   SV_ERR_WORKSPACE = -4,   /* workspace null or smaller than sv_workspace_bytes()        */
   SV_ERR_CUDA = -5,        /* a CUDA runtime call or kernel launch failed                */
@@ -74,7 +73,7 @@ typedef enum {
                               support (stated at that entry point)                     */
 } sv_status;
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1 } sv_dtype;
+typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2, SV_E4M3 = 3 } sv_dtype;
 
 /* Per-batch-row flags written to out_flags[b] (bitwise OR). */
 enum {
@@ -88,7 +87,12 @@ enum {
   SV_FLAG_TIMEOUT = 8,           /* a bounded device-side wait of the fused LM head gave up
                                     (a tile that never arrived); the row's outputs are then
                                     unspecified                                          */
-  SV_FLAG_BAD_TOKEN = 16         /* a draft token outside [0, V): treated as p = q = 0    */
+  SV_FLAG_BAD_TOKEN = 16,        /* a draft token outside [0, V): treated as p = q = 0    */
+  SV_FLAG_BAD_PAGE = 32,         /* a page index that the call needed lies outside the pool:
+                                    nothing is written there, and it reads as zeros       */
+  SV_FLAG_BAD_LENGTH = 64        /* q_start falls or leaves [0, total] (the sequence is then
+                                    skipped), or kv_len lies outside what its pages hold
+                                    (it is then clamped)                                  */
 };
 
 enum { SV_MODE_SAMPLE = 0, SV_MODE_GREEDY = 1, SV_MODE_LMHEAD = 2, SV_MODE_DRAFT = 3 };
@@ -310,6 +314,146 @@ int spec_lmhead_verify_drafted(const void* h_target, const void* W_target, int H
                                int32_t* out_tokens, int32_t* out_counts, float* out_p_at_draft,
                                float* out_q_at_draft, uint8_t* out_flags, float* debug_logits,
                                void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* ---------------------------------------------------------------------------
+ * The target's cache and its attention.
+ *
+ * The target scores the gamma drafts of a round in one pass over a chunk of new
+ * tokens per sequence ("Fast Inference ...", section "The loop", step 2), and
+ * keeps the keys and values of the prefix in a cache.  The cache is cut into
+ * pages of page_size tokens; sequence b finds token j in page
+ * block_table[b][j / page_size], slot j % page_size.  A round writes the chunk's
+ * keys and values (spec_kv_append), attends (spec_chunk_attention), verifies, and
+ * forgets the rejected drafts by shortening kv_len: nothing moves.
+ *
+ * A cache of type SV_E4M3 holds each head's vector of a token as 8-bit floats
+ * (4 exponent bits, 3 of mantissa, largest value 448) times a power of two of
+ * its own, held as one byte s that stands for 2^(s - 127), 1 <= s <= 254.  A
+ * power of two loses nothing against an arbitrary factor, because the codes are
+ * floating point themselves, and makes every dequantised value exact in bf16.
+ * ------------------------------------------------------------------------- */
+
+/* The pool: element (page, head, token, i) of k is at
+ * k[page * page_stride + head * head_stride + token * token_stride + i], and the
+ * same in v; strides are in elements, so pages may be head-major or token-major.
+ * k and v are 16-byte aligned and the strides whole multiples of 16 bytes. */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_scale;     /* SV_E4M3: [num_pages][kv_heads][page_size]; else NULL */
+  uint8_t* v_scale;
+  int64_t num_pages;    /* < 2^31                                              */
+  int64_t page_stride, head_stride, token_stride;
+  int32_t kv_heads;
+  int32_t page_size;
+  int32_t head_dim;     /* a multiple of 16, at most 256                       */
+  int32_t dtype;        /* SV_BF16, SV_F16 or SV_E4M3                          */
+} sv_kv_cache;
+
+/* B sequences and their chunks, packed one after another: sequence b's new tokens
+ * are rows q_start[b] .. q_start[b+1]-1 of the packed arrays, and kv_len[b] is
+ * its length with them, so that new token i sits at position
+ * kv_len[b] - (q_start[b+1] - q_start[b]) + i.  All three arrays are on the
+ * device; table entries behind a sequence's last token are not read. */
+typedef struct {
+  const int32_t* block_table;  /* [B][max_pages] */
+  const int32_t* q_start;      /* [B+1]          */
+  const int32_t* kv_len;       /* [B]            */
+  int64_t total;               /* rows of the packed arrays (>= q_start[B])    */
+  int32_t B;
+  int32_t max_pages;
+} sv_kv_batch;
+
+/*
+ * spec_kv_append -- write the chunk's keys and values into the pages.
+ *   new_k, new_v  [total][kv_heads][head_dim] of `dtype` (SV_BF16 or SV_F16);
+ *                 token_stride and head_stride in elements, multiples of 8,
+ *                 bases 16-byte aligned
+ * A 16-bit cache has the same dtype and gets copies.  An SV_E4M3 cache gets, per
+ * token and head, s = 2^k with the smallest k >= -120 that keeps the largest
+ * finite |x| / s within 448, and codes rounded to nearest, ties to even; NaN and
+ * infinities become the NaN code.  No two of the new tokens may share a slot.
+ *   out_flags     [B] uint8 or NULL: SV_FLAG_BAD_PAGE, SV_FLAG_BAD_LENGTH (here
+ *                 also where a new token's position is negative: it is dropped)
+ */
+int spec_kv_append(const sv_kv_cache* cache, const sv_kv_batch* batch, const void* new_k,
+                   const void* new_v, int dtype, int64_t token_stride, int64_t head_stride,
+                   uint8_t* out_flags, void* cuda_stream);
+
+/*
+ * spec_kv_read -- tokens out of the pages into packed arrays.
+ *   first         [B] int32 on the device: sequence b's tokens first[b] ..
+ *                 first[b] + out_start[b+1] - out_start[b] - 1 are read
+ *   out_start     [B+1] int32 on the device, as q_start of sv_kv_batch
+ *   out_k, out_v  [total][kv_heads][head_dim] of `dtype` (SV_BF16 or SV_F16: the
+ *                 cache's own, or either for an SV_E4M3 cache: exact in SV_BF16,
+ *                 rounded to nearest in SV_F16), 16-byte aligned
+ *   out_flags     [B] uint8 or NULL, as spec_kv_append; what a flagged token would
+ *                 have held is written as zeros
+ */
+int spec_kv_read(const sv_kv_cache* cache, const int32_t* block_table, const int32_t* first,
+                 const int32_t* out_start, int B, int max_pages, int64_t total, void* out_k,
+                 void* out_v, int dtype, uint8_t* out_flags, void* cuda_stream);
+
+/* Bytes of workspace a spec_chunk_attention call on this cache with `heads` query
+ * heads needs (0 for bad sizes); it does not grow with the batch. */
+size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
+
+/*
+ * spec_chunk_attention -- causal attention of each sequence's chunk over its pages.
+ *   q         [total][heads][head_dim] of `dtype` (SV_BF16 or SV_F16; the cache's
+ *             own type, or either for an SV_E4M3 cache); strides as new_k's above
+ *   heads     a multiple of kv_heads; query head h reads key head
+ *             h / (heads / kv_heads); at most 128 query heads to a key head
+ *   scale     factor of the scores, finite; head_dim^-1/2 is usual
+ *   window    0: a query at position t sees keys 0..t.  w > 0: keys t-w+1..t
+ * The chunk's own keys and values are read from the cache: append them first.
+ * out = sum_j p_j v_j with p = softmax(scale q.k_j over the keys seen), the
+ * scores, the softmax's maximum and sum and the products' sums in fp32; p may be
+ * rounded to `dtype` for the product with v, and an SV_E4M3 cache is dequantised
+ * to `dtype` (exact in SV_BF16).
+ *   out       [total][heads][head_dim] of `dtype`, contiguous, 16-byte aligned
+ *   out_lse   [total][heads] float or NULL: log sum_j exp(scale q.k_j)
+ *   out_flags [B] uint8 or NULL: SV_FLAG_BAD_PAGE, SV_FLAG_BAD_LENGTH, and
+ *             SV_FLAG_TIMEOUT on every sequence if a bounded device-side wait
+ *             gave up (outputs are then unspecified)
+ * A query that sees no key (kv_len shorter than the chunk) gets out = 0 and
+ * lse = -inf.  Slots behind kv_len may hold anything.  A key or value inside
+ * kv_len that is not finite may reach queries of the same chunk that do not see
+ * it (their weight for it is 0).
+ *   workspace >= sv_attention_workspace_bytes(cache, heads), 256-byte aligned
+ */
+int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, const void* q,
+                         int dtype, int heads, int64_t token_stride, int64_t head_stride,
+                         float scale, int window, void* out, float* out_lse,
+                         uint8_t* out_flags, void* workspace, size_t workspace_bytes,
+                         void* cuda_stream);
+
+/*
+ * spec_verify_probs -- the round of spec_verify from given probabilities and given
+ * random numbers (a caller with its own adjusted distributions and generator, or
+ * one that replays another implementation's round).
+ *   target_probs  [B][gamma+1][V] dtype (SV_F32 or SV_BF16), rows summing to about 1
+ *   draft_probs   [B][gamma][V]   dtype
+ *   draft_tokens  [B][gamma] int32
+ *   uniforms      [B][gamma+1] float in [0, 1): u_0..u_{gamma-1} of the accept
+ *                 tests, then the draw's
+ * Draft i is accepted iff u_i <= p_i(x_i) / q_i(x_i) (IEEE fp32 quotient; 0/0
+ * rejects).  The token at the first rejection n is drawn from w = max(0, p_n -
+ * q_n) (fp32 differences), from p_n if that has no positive entry, and from
+ * p_gamma after a clean sweep, by the inverse transform: the smallest v with
+ * w_0 + ... + w_v > u_gamma (w_0 + ... + w_{V-1}).  The sums are integers in
+ * units of 2^-61 (each weight truncated to one), so they do not depend on the
+ * order of summation.
+ *   out_tokens, out_counts, out_flags as spec_verify.  A probability that is
+ *   negative, not finite or above 2 counts as 0 and sets SV_FLAG_NONFINITE, as
+ *   does a uniform outside [0, 1) (clamped into it; NaN as 0); a row whose sum
+ *   is 4 or more gives an unspecified token in range.  No workspace.
+ */
+int spec_verify_probs(const void* target_probs, const void* draft_probs,
+                      const int32_t* draft_tokens, const float* uniforms, int B, int gamma,
+                      int64_t V, int dtype, int32_t* out_tokens, int32_t* out_counts,
+                      uint8_t* out_flags, void* cuda_stream);
 
 /* Profiling aid (not thread-safe): when `events` is non-NULL, following calls
  * record events on their stream: for spec_verify events[0] before the first

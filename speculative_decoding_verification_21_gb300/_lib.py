@@ -14,13 +14,15 @@ import threading
 from . import build as _build
 
 SV_OK = 0
-SV_F32, SV_BF16 = 0, 1
+SV_F32, SV_BF16, SV_F16, SV_E4M3 = 0, 1, 2, 3
 SV_MODE_SAMPLE, SV_MODE_GREEDY, SV_MODE_LMHEAD, SV_MODE_DRAFT = 0, 1, 2, 3
 FLAG_ZERO_MASS, FLAG_NONFINITE, FLAG_RESIDUAL_FALLBACK, FLAG_TIMEOUT, FLAG_BAD_TOKEN = 1, 2, 4, 8, 16
+FLAG_BAD_PAGE, FLAG_BAD_LENGTH = 32, 64
 
 EXPORTS = ("sv_workspace_bytes", "sv_workspace_init", "spec_verify", "spec_verify_opts",
            "spec_verify_greedy", "spec_lmhead_verify", "spec_lmhead_draft",
-           "spec_lmhead_verify_drafted",
+           "spec_lmhead_verify_drafted", "spec_kv_append", "spec_kv_read", "spec_chunk_attention",
+           "spec_verify_probs", "sv_attention_workspace_bytes",
            "sv_set_timing_events", "sv_test_lmhead_stall", "sv_status_string", "sv_version")
 
 
@@ -28,6 +30,23 @@ class Options(ctypes.Structure):
     """sv_options of include/specverify.h."""
     _fields_ = [("lenience", ctypes.c_float), ("top_k", ctypes.c_int32),
                 ("top_p", ctypes.c_float), ("sampler", ctypes.c_int32)]
+
+
+class _CacheStruct(ctypes.Structure):
+    """sv_kv_cache of include/specverify.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class _BatchStruct(ctypes.Structure):
+    """sv_kv_batch of include/specverify.h."""
+    _fields_ = [("block_table", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("total", ctypes.c_int64), ("B", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
 
 
 SV_SAMPLER_GUMBEL, SV_SAMPLER_INVERSE = 0, 1
@@ -81,6 +100,16 @@ def load(build_if_missing: bool = True):
                                                  U64, P, P, P, P, P, P, P, SZ, P]
         L.spec_lmhead_verify_drafted.restype = I
         L.spec_lmhead_draft.restype = I
+        L.spec_kv_append.argtypes = [P, P, P, P, I, I64, I64, P, P]
+        L.spec_kv_append.restype = I
+        L.spec_kv_read.argtypes = [P, P, P, P, I, I, I64, P, P, I, P, P]
+        L.spec_kv_read.restype = I
+        L.sv_attention_workspace_bytes.argtypes = [P, I]
+        L.sv_attention_workspace_bytes.restype = SZ
+        L.spec_chunk_attention.argtypes = [P, P, P, I, I, I64, I64, F, I, P, P, P, P, SZ, P]
+        L.spec_chunk_attention.restype = I
+        L.spec_verify_probs.argtypes = [P, P, P, P, I, I, I64, I, P, P, P, P]
+        L.spec_verify_probs.restype = I
         L.sv_set_timing_events.argtypes = [P, I]
         L.sv_set_timing_events.restype = I
         L.sv_test_lmhead_stall.argtypes = [I, ctypes.c_uint32]
@@ -347,4 +376,224 @@ def spec_lmhead_draft(h_draft, W_draft, *, pos: int, temperature: float = 1.0, s
                              _ptr(debug_logits), _ptr(ws), ws.numel(), sh)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_lmhead_draft")
+    return o
+
+
+class KVCache:
+    """A paged cache: two pools of one shape and one set of strides,
+    k, v [num_pages, kv_heads, page_size, head_dim] in bfloat16, float16 or
+    float8_e4m3fn, the last dimension contiguous (a token-major pool is passed as
+    its transpose), and for float8_e4m3fn k_scale, v_scale [num_pages, kv_heads,
+    page_size] uint8, a byte s standing for 2^(s - 127).  Sequences find their
+    pages through a block_table [B, max_pages] int32.  The tensors are the
+    caller's; this object only names them."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        torch = _torch()
+        codes = {torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3}
+        if k.dtype not in codes:
+            raise TypeError(f"a cache is bfloat16, float16 or float8_e4m3fn, got {k.dtype}")
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
+            raise ValueError("k and v: [num_pages, kv_heads, page_size, head_dim], alike in "
+                             "shape, type and strides")
+        if k.stride(3) != 1:
+            raise ValueError("the head dimension must be contiguous")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to float8_e4m3fn caches, and only there")
+        if e4m3:
+            for s in (k_scale, v_scale):
+                if s.dtype != torch.uint8 or tuple(s.shape) != tuple(k.shape[:3]):
+                    raise ValueError("scales: uint8 [num_pages, kv_heads, page_size]")
+        _check_cuda(k_scale, v_scale)
+        if not (k.is_cuda and v.device == k.device):
+            raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.dtype = k.dtype
+        self._struct = _CacheStruct(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+            v_scale.data_ptr() if e4m3 else None, k.shape[0], k.stride(0), k.stride(1),
+            k.stride(2), k.shape[1], k.shape[2], k.shape[3], codes[k.dtype])
+        self._ref = ctypes.addressof(self._struct)
+        self._attention_ws = {}  # workspace bytes by query heads
+
+
+def alloc_kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, *, dtype,
+                   device="cuda") -> KVCache:
+    """A head-major cache of zeros."""
+    torch = _torch()
+    shape = (num_pages, kv_heads, page_size, head_dim)
+    k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return KVCache(k, v)
+    ks, vs = (torch.full(shape[:3], 127, dtype=torch.uint8, device=device) for _ in range(2))
+    return KVCache(k, v, ks, vs)
+
+
+def _row_code(t) -> int:
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return SV_BF16
+    if t.dtype == torch.float16:
+        return SV_F16
+    raise TypeError(f"rows must be bfloat16 or float16, got {t.dtype}")
+
+
+def _check_rows(t, heads, cache, what):
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads and t.shape[1] != heads):
+        raise ValueError(f"{what}: [total, heads, head_dim]")
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
+    if t.stride(2) != 1:
+        raise ValueError(f"{what}: the head dimension must be contiguous")
+
+
+def _check_index(block_table, start, length):
+    torch = _torch()
+    _check_cuda(block_table, start, length)
+    if block_table.dtype != torch.int32 or start.dtype != torch.int32 or length.dtype != torch.int32:
+        raise TypeError("block_table, q_start and lengths must be int32")
+    B = length.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(start.shape) != (B + 1,):
+        raise ValueError("shape mismatch: block_table [B, max_pages], q_start [B+1], lengths [B]")
+    return B
+
+
+def spec_kv_append(cache: KVCache, new_k, new_v, block_table, q_start, kv_len, *,
+                   want_flags: bool = False, out=None, stream=None):
+    """Write the chunk's keys and values new_k, new_v [total, kv_heads, head_dim]
+    (bfloat16 or float16; any token and head strides, alike in both) into the
+    cache's pages: sequence b's rows q_start[b] .. q_start[b+1]-1 become its last
+    tokens before kv_len[b].  Returns a dict with flags [B] uint8 (if want_flags)."""
+    torch = _torch()
+    L = load()
+    _check_rows(new_k, cache.kv_heads, cache, "new_k")
+    if new_v.shape != new_k.shape or new_v.dtype != new_k.dtype or new_v.stride() != new_k.stride():
+        raise ValueError("new_v must match new_k in shape, type and strides")
+    B = _check_index(block_table, q_start, kv_len)
+    o = dict(out or {})
+    if want_flags:
+        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=new_k.device))
+    batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                         new_k.shape[0], B, block_table.shape[1])
+    rc = L.spec_kv_append(cache._ref, ctypes.addressof(batch), _ptr(new_k), _ptr(new_v),
+                          _row_code(new_k), new_k.stride(0), new_k.stride(1),
+                          _ptr(o.get("flags")), _stream_handle(stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_kv_append")
+    return o
+
+
+def spec_kv_read(cache: KVCache, block_table, first, out_start, total: int, *, dtype=None,
+                 want_flags: bool = False, out=None, stream=None):
+    """Tokens first[b] .. of every sequence out of the pages, out_start[b+1] -
+    out_start[b] of them, packed.  dtype: the cache's own (the default), or either
+    16-bit type (default bfloat16) for a float8_e4m3fn cache.  Returns a dict:
+    k, v [total, kv_heads, head_dim], flags [B] uint8 (if want_flags)."""
+    torch = _torch()
+    L = load()
+    B = _check_index(block_table, out_start, first)
+    if dtype is None:
+        dtype = torch.bfloat16 if cache.dtype == torch.float8_e4m3fn else cache.dtype
+    dev = block_table.device
+    o = dict(out or {})
+    for name in ("k", "v"):
+        if name not in o:
+            o[name] = torch.empty((total, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev)
+    if want_flags:
+        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+    _check_cuda(o["k"], o["v"])
+    for name in ("k", "v"):
+        if tuple(o[name].shape) != (total, cache.kv_heads, cache.head_dim) or \
+                o[name].dtype != dtype:
+            raise ValueError("out k, v: [total, kv_heads, head_dim] of the asked type")
+    rc = L.spec_kv_read(cache._ref, _ptr(block_table), _ptr(first), _ptr(out_start), B,
+                        block_table.shape[1], int(total), _ptr(o["k"]), _ptr(o["v"]),
+                        _row_code(o["k"]), _ptr(o.get("flags")), _stream_handle(stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_kv_read")
+    return o
+
+
+def attention_workspace_bytes(cache: KVCache, heads: int) -> int:
+    n = cache._attention_ws.get(heads)
+    if n is None:
+        n = int(load().sv_attention_workspace_bytes(cache._ref, int(heads)))
+        cache._attention_ws[heads] = n
+    return n
+
+
+def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, scale=None,
+                         window: int = 0, want_lse: bool = True, want_flags: bool = False,
+                         out=None, workspace=None, stream=None):
+    """Causal attention of each sequence's chunk q [total, heads, head_dim]
+    (bfloat16 or float16, any token and head strides) over its pages; the chunk's
+    own keys and values must be in the cache (spec_kv_append).  scale defaults to
+    head_dim^-1/2; window w > 0 shows a query only its last w keys.  Returns a dict:
+    out [total, heads, head_dim], lse [total, heads] float32 (if want_lse),
+    flags [B] uint8 (if want_flags)."""
+    torch = _torch()
+    L = load()
+    _check_rows(q, 0, cache, "q")
+    B = _check_index(block_table, q_start, kv_len)
+    total, heads, dim = q.shape
+    dev = q.device
+    o = dict(out or {})
+    if "out" not in o:
+        o["out"] = torch.empty((total, heads, dim), dtype=q.dtype, device=dev)
+    elif tuple(o["out"].shape) != (total, heads, dim) or o["out"].dtype != q.dtype:
+        raise ValueError("out: [total, heads, head_dim] of q's type")
+    if want_lse and "lse" not in o:
+        o["lse"] = torch.empty((total, heads), dtype=torch.float32, device=dev)
+    if want_flags:
+        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+    _check_cuda(o["out"], o.get("lse"))
+    sh = _stream_handle(stream)
+    need = attention_workspace_bytes(cache, heads)
+    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value)
+    batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), total, B,
+                         block_table.shape[1])
+    rc = L.spec_chunk_attention(cache._ref, ctypes.addressof(batch), _ptr(q), _row_code(q), heads,
+                                q.stride(0), q.stride(1),
+                                dim ** -0.5 if scale is None else float(scale), int(window),
+                                _ptr(o["out"]), _ptr(o.get("lse")), _ptr(o.get("flags")),
+                                _ptr(ws), ws.numel(), sh)
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_chunk_attention")
+    return o
+
+
+def spec_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, *,
+                      want_flags: bool = False, out=None, stream=None):
+    """The round from given probabilities (float32 or bfloat16) and given uniforms
+    [B, gamma+1] float32 (the accept tests', then the draw's).  Returns a dict:
+    tokens [B, g+1] int32, counts [B] int32, flags [B] uint8 (if want_flags)."""
+    torch = _torch()
+    L = load()
+    B, g1, V = target_probs.shape
+    g = g1 - 1
+    if tuple(draft_probs.shape) != (B, g, V) or tuple(draft_tokens.shape) != (B, g) or \
+            tuple(uniforms.shape) != (B, g1):
+        raise ValueError("shape mismatch: target [B,g+1,V], draft [B,g,V], tokens [B,g], "
+                         "uniforms [B,g+1]")
+    if draft_probs.dtype != target_probs.dtype or draft_tokens.dtype != torch.int32 or \
+            uniforms.dtype != torch.float32:
+        raise TypeError("draft probs must match target dtype; draft tokens must be int32, "
+                        "uniforms float32")
+    _check_cuda(target_probs, draft_probs, draft_tokens, uniforms)
+    dev = target_probs.device
+    o = dict(out or {})
+    if "tokens" not in o:
+        o["tokens"] = torch.empty((B, g1), dtype=torch.int32, device=dev)
+    if "counts" not in o:
+        o["counts"] = torch.empty((B,), dtype=torch.int32, device=dev)
+    if want_flags:
+        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+    rc = L.spec_verify_probs(_ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens),
+                             _ptr(uniforms), B, g, V, _dtype_code(target_probs),
+                             _ptr(o["tokens"]), _ptr(o["counts"]), _ptr(o.get("flags")),
+                             _stream_handle(stream))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_probs")
     return o

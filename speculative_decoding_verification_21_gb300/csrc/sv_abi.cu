@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "specverify.h"
+#include "sv_attention.h"
 #include "sv_plan.h"
 #include "sv_launch.h"
 
@@ -34,6 +35,16 @@ int lmhead_draft(const void* h_draft, const void* W_draft, int Hd, int B, int64_
                  float* out_q, float* out_lse, float* out_logit, float* debug_logits,
                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
 size_t lmhead_draft_workspace_bytes(int B, int64_t V);
+cudaError_t launch_kv_append(const sv_kv_cache& c, const sv_kv_batch& b, const void* new_k,
+                             const void* new_v, int dtype, int64_t token_stride,
+                             int64_t head_stride, uint8_t* out_flags, cudaStream_t stream);
+cudaError_t launch_kv_read(const sv_kv_cache& c, const int32_t* block_table, const int32_t* first,
+                           const int32_t* out_start, int B, int max_pages, int64_t total,
+                           void* out_k, void* out_v, int dtype, uint8_t* out_flags,
+                           cudaStream_t stream);
+cudaError_t launch_verify_probs(const void* p, const void* q, const int32_t* x, const float* u,
+                                int B, int gamma, int64_t V, int dtype, int32_t* out_tokens,
+                                int32_t* out_counts, uint8_t* out_flags, cudaStream_t stream);
 }  // namespace sv
 
 namespace sv {
@@ -66,6 +77,50 @@ int check_workspace(const void* ws, size_t have, size_t need) {
   if (!ws || have < need) return SV_ERR_WORKSPACE;
   if (!aligned(ws, sv::kAlign)) return SV_ERR_ALIGN;
   return SV_OK;
+}
+
+constexpr int kMaxHeadDim = 256;
+constexpr int kMaxGroup = 128;                    // query heads per key head
+constexpr int64_t kMaxRows = (int64_t)1 << 31;    // rows of a packed array
+
+// A cache whose shape, type and strides the kernels can walk.
+int check_cache(const sv_kv_cache* c) {
+  if (!c) return SV_ERR_ARG;
+  if (c->dtype != SV_BF16 && c->dtype != SV_F16 && c->dtype != SV_E4M3) return SV_ERR_DTYPE;
+  if (c->num_pages < 0 || c->num_pages >= kMaxRows || c->kv_heads < 1 || c->page_size < 1 ||
+      c->head_dim < 1 || c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0)
+    return SV_ERR_ARG;
+  if (c->head_dim % 16 || c->head_dim > kMaxHeadDim) return SV_ERR_UNSUPPORTED;
+  if (c->num_pages == 0) return SV_OK;  // every page index is then out of range
+  if (!c->k || !c->v || (c->dtype == SV_E4M3 && (!c->k_scale || !c->v_scale))) return SV_ERR_ARG;
+  const int64_t vec = c->dtype == SV_E4M3 ? 16 : 8;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % vec || c->head_stride % vec ||
+      c->token_stride % vec)
+    return SV_ERR_ALIGN;
+  return SV_OK;
+}
+
+// The table and lengths of B sequences over `total` packed rows.
+int check_batch(const int32_t* table, const int32_t* start, const int32_t* len, int B,
+                int max_pages, int64_t total, int page_size) {
+  if (B < 0 || max_pages < 0 || total < 0 || total >= kMaxRows) return SV_ERR_ARG;
+  if ((int64_t)max_pages * page_size >= kMaxRows) return SV_ERR_ARG;
+  if (B == 0) return SV_OK;
+  if (!start || !len || (!table && max_pages > 0)) return SV_ERR_ARG;
+  if (!aligned(table, 4) || !aligned(start, 4) || !aligned(len, 4)) return SV_ERR_ALIGN;
+  return SV_OK;
+}
+
+// The packed rows' type beside the cache's.
+int check_row_type(const sv_kv_cache* c, int dtype) {
+  if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
+  if (c->dtype != SV_E4M3 && c->dtype != dtype) return SV_ERR_DTYPE;
+  return SV_OK;
+}
+
+int check_strides(int64_t token_stride, int64_t head_stride) {
+  if (token_stride < 0 || head_stride < 0) return SV_ERR_ARG;
+  return token_stride % 8 || head_stride % 8 ? SV_ERR_ALIGN : SV_OK;
 }
 
 }  // namespace
@@ -213,6 +268,112 @@ int spec_lmhead_draft(const void* h_draft, const void* W_draft, int Hd, int B, i
   return sv::lmhead_draft(h_draft, W_draft, Hd, B, V, temperature, seed, round, pos, out_tokens,
                           out_q, out_lse, out_logit, debug_logits, workspace, workspace_bytes,
                           (cudaStream_t)cuda_stream);
+}
+
+int spec_kv_append(const sv_kv_cache* cache, const sv_kv_batch* batch, const void* new_k,
+                   const void* new_v, int dtype, int64_t token_stride, int64_t head_stride,
+                   uint8_t* out_flags, void* cuda_stream) {
+  int st = check_cache(cache);
+  if (st == SV_OK && !batch) st = SV_ERR_ARG;
+  if (st == SV_OK) st = check_row_type(cache, dtype);
+  if (st == SV_OK) st = check_strides(token_stride, head_stride);
+  if (st == SV_OK)
+    st = check_batch(batch->block_table, batch->q_start, batch->kv_len, batch->B, batch->max_pages,
+                     batch->total, cache->page_size);
+  if (st != SV_OK) return st;
+  if (batch->B == 0) return SV_OK;
+  if (batch->total > 0 && (!new_k || !new_v)) return SV_ERR_ARG;
+  if (!aligned(new_k, 16) || !aligned(new_v, 16)) return SV_ERR_ALIGN;
+  return sv::launch_kv_append(*cache, *batch, new_k, new_v, dtype, token_stride, head_stride,
+                              out_flags, (cudaStream_t)cuda_stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+int spec_kv_read(const sv_kv_cache* cache, const int32_t* block_table, const int32_t* first,
+                 const int32_t* out_start, int B, int max_pages, int64_t total, void* out_k,
+                 void* out_v, int dtype, uint8_t* out_flags, void* cuda_stream) {
+  int st = check_cache(cache);
+  if (st == SV_OK) st = check_row_type(cache, dtype);
+  if (st == SV_OK)
+    st = check_batch(block_table, out_start, first, B, max_pages, total, cache->page_size);
+  if (st != SV_OK) return st;
+  if (B == 0) return SV_OK;
+  if (total > 0 && (!out_k || !out_v)) return SV_ERR_ARG;
+  if (!aligned(out_k, 16) || !aligned(out_v, 16)) return SV_ERR_ALIGN;
+  return sv::launch_kv_read(*cache, block_table, first, out_start, B, max_pages, total, out_k,
+                            out_v, dtype, out_flags, (cudaStream_t)cuda_stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads) {
+  if (check_cache(cache) != SV_OK || heads < 1 || heads % cache->kv_heads ||
+      heads / cache->kv_heads > kMaxGroup)
+    return 0;
+  return sv::attention_workspace_bytes(cache->head_dim);
+}
+
+int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, const void* q,
+                         int dtype, int heads, int64_t token_stride, int64_t head_stride,
+                         float scale, int window, void* out, float* out_lse,
+                         uint8_t* out_flags, void* workspace, size_t workspace_bytes,
+                         void* cuda_stream) {
+  int st = check_cache(cache);
+  if (st == SV_OK && !batch) st = SV_ERR_ARG;
+  if (st == SV_OK) st = check_row_type(cache, dtype);
+  if (st == SV_OK) st = check_strides(token_stride, head_stride);
+  if (st == SV_OK)
+    st = check_batch(batch->block_table, batch->q_start, batch->kv_len, batch->B, batch->max_pages,
+                     batch->total, cache->page_size);
+  if (st != SV_OK) return st;
+  if (heads < 1 || heads % cache->kv_heads || window < 0 || !std::isfinite(scale))
+    return SV_ERR_ARG;
+  if (heads / cache->kv_heads > kMaxGroup || batch->total * heads >= kMaxRows)
+    return SV_ERR_UNSUPPORTED;
+  if (batch->B == 0) return SV_OK;
+  if (batch->total > 0 && (!q || !out)) return SV_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(out_lse, 4)) return SV_ERR_ALIGN;
+  st = check_workspace(workspace, workspace_bytes, sv_attention_workspace_bytes(cache, heads));
+  if (st != SV_OK) return st;
+  sv::AttendArgs a{};
+  a.c = sv::cache_view(*cache);
+  a.b = sv::BatchView{batch->block_table, batch->q_start, batch->kv_len, (int)batch->total,
+                      batch->B, batch->max_pages};
+  a.q = (const char*)q;
+  a.q_token = token_stride * 2;
+  a.q_head = head_stride * 2;
+  a.heads = heads;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.window = window;
+  a.out = (char*)out;
+  a.lse = out_lse;
+  a.flags = out_flags;
+  a.ws = (char*)workspace;
+  return sv::launch_attention(a, dtype, cache->dtype == SV_E4M3, (cudaStream_t)cuda_stream) ==
+                 cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+int spec_verify_probs(const void* target_probs, const void* draft_probs,
+                      const int32_t* draft_tokens, const float* uniforms, int B, int gamma,
+                      int64_t V, int dtype, int32_t* out_tokens, int32_t* out_counts,
+                      uint8_t* out_flags, void* cuda_stream) {
+  const int st = check_shape(B, gamma, V);
+  if (st != SV_OK) return st;
+  if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_DTYPE;
+  if (B == 0) return SV_OK;
+  if (!target_probs || !draft_probs || !draft_tokens || !uniforms || !out_tokens || !out_counts)
+    return SV_ERR_ARG;
+  if (!aligned(target_probs, 16) || !aligned(draft_probs, 16) || !aligned(draft_tokens, 4) ||
+      !aligned(uniforms, 4) || !aligned(out_tokens, 4) || !aligned(out_counts, 4))
+    return SV_ERR_ALIGN;
+  return sv::launch_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, B, gamma, V,
+                                 dtype, out_tokens, out_counts, out_flags,
+                                 (cudaStream_t)cuda_stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
 }
 
 int sv_set_timing_events(void* const* events, int n) {

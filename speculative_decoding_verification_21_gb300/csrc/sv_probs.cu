@@ -1,0 +1,341 @@
+// sv_probs.cu -- spec_verify_probs: the round from given probabilities and given
+// uniforms.
+//
+//   n = first i with not (u_i <= p_i(x_i) / q_i(x_i)), else gamma
+//   w = max(0, p_n - q_n) (p_n where that is empty, p_gamma for n = gamma)
+//   t = smallest v with W_v > u W_{V-1},  W_v = w_0 + ... + w_v
+//
+// Bound by HBM: the rows p_n and q_n are read once, 2 V values per batch row.  A
+// row is cut over a cluster of CTAs and their warps; each warp sums its run of
+// the row, the totals are exchanged through shared memory (distributed between
+// the CTAs), and the one warp whose run holds the target reads that run again
+// (from L2) and stops inside it.  W is an integer in units of 2^-61, so the split
+// changes nothing, and the target floor(u W) is exact: u = m 2^-e with a 24-bit m,
+// so u W is a 128-bit product shifted right.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "specverify.h"
+#include "sv_device.cuh"
+#include "sv_launch.h"
+#include "sv_plan.h"
+#include "sv_tma.cuh"
+
+namespace sv {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kProbWarps = 16;
+constexpr int kProbThreads = kProbWarps * 32;
+constexpr int kProbMaxCluster = 8;
+
+struct ProbArgs {
+  const void* p;
+  const void* q;
+  const int32_t* x;
+  const float* u;
+  int B, gamma;
+  int64_t V;
+  int32_t* out_tokens;
+  int32_t* out_counts;
+  uint8_t* out_flags;
+};
+
+// A probability as given: 0 where it is none (and `odd` is set).
+__device__ __forceinline__ float sane(float p, bool& odd) {
+  const bool ok = p >= 0.0f && p <= 2.0f;
+  odd |= !ok;
+  return ok ? p : 0.0f;
+}
+
+// w in units of 2^-61, 0 <= w <= 2 (the product is exact, the conversion truncates).
+__device__ __forceinline__ unsigned long long units(float w) {
+  return __float2ull_rz(w * 0x1p61f);
+}
+
+// floor(u w) for 0 <= u < 1.
+__device__ __forceinline__ unsigned long long times(float u, unsigned long long w) {
+  const uint32_t bits = __float_as_uint(u);
+  const int e = (int)(bits >> 23);  // u = m 2^(e - 150) (e = 0: m 2^-149, no hidden bit)
+  const unsigned long long m = e ? ((bits & 0x7fffffu) | 0x800000u) : (bits & 0x7fffffu);
+  const int sh = 150 - (e ? e : 1);  // >= 24
+  const unsigned long long hi = __umul64hi(w, m), lo = w * m;
+  if (sh >= 128) return 0;
+  if (sh >= 64) return hi >> (sh - 64);
+  return (hi << (64 - sh)) | (lo >> sh);
+}
+
+struct Weights {
+  const void* p;
+  const void* q;  // null: w = p
+};
+
+// Weights of elements i .. i+N-1 of the row (N consecutive ones, aligned if VEC).
+template <int DT, bool VEC>
+struct Piece {
+  static constexpr int N = VEC ? VecInfo<DT>::kElems : 1;
+};
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_weights(const Weights& r, int64_t i, float* w, bool& odd) {
+  constexpr int N = Piece<DT, VEC>::N;
+  if (VEC) {
+    constexpr int es = DT == SV_F32 ? 4 : 2;
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>((const char*)r.p + i * es));
+    float fp[N];
+    unpack<DT>(a, fp);
+    float fq[N];
+    if (r.q) {
+      const uint4 b = __ldg(reinterpret_cast<const uint4*>((const char*)r.q + i * es));
+      unpack<DT>(b, fq);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      w[j] = sane(fp[j], odd);
+      if (r.q) w[j] = fmaxf(0.0f, w[j] - sane(fq[j], odd));
+    }
+  } else {
+    w[0] = sane(load_logit<DT>(r.p, i), odd);
+    if (r.q) w[0] = fmaxf(0.0f, w[0] - sane(load_logit<DT>(r.q, i), odd));
+  }
+}
+
+__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct ProbShared {
+  unsigned long long warp_total[kProbWarps];
+  unsigned long long total;
+  int any;   // some weight of this CTA is positive
+  int odd;   // some value was no probability
+  int n, flags;
+};
+
+// The accept tests of batch row b (one warp): n, and the flags they raise.
+template <int DT>
+__device__ void accept_tests(const ProbArgs& a, int b, ProbShared& sh) {
+  const int lane = threadIdx.x & 31, g = a.gamma;
+  bool ok = false, bad_token = false, odd = false;
+  if (lane < g) {
+    const int x = __ldg(a.x + (int64_t)b * g + lane);
+    const float u = __ldg(a.u + (int64_t)b * (g + 1) + lane);
+    float p = 0.0f, q = 0.0f;
+    bad_token = x < 0 || (int64_t)x >= a.V;
+    if (!bad_token) {
+      p = sane(load_logit<DT>(a.p, ((int64_t)b * (g + 1) + lane) * a.V + x), odd);
+      q = sane(load_logit<DT>(a.q, ((int64_t)b * g + lane) * a.V + x), odd);
+    }
+    ok = u <= p / q;
+    odd |= !(u >= 0.0f && u < 1.0f) || (!bad_token && q == 0.0f);
+  }
+  const unsigned fail = __ballot_sync(0xffffffffu, lane < g && !ok);
+  const int n = fail ? __ffs(fail) - 1 : g;
+  // only what was tested says something about the round
+  const unsigned seen = n >= 31 ? 0xffffffffu : (2u << n) - 1u;
+  const unsigned bt = __ballot_sync(0xffffffffu, bad_token) & seen;
+  const unsigned od = __ballot_sync(0xffffffffu, odd) & seen;
+  if (lane == 0) {
+    sh.n = n;
+    sh.flags = (bt ? SV_FLAG_BAD_TOKEN : 0) | (od ? SV_FLAG_NONFINITE : 0);
+  }
+}
+
+// This warp's run of the row: its share of the CTA's slice.
+struct Run {
+  int64_t lo, hi;
+};
+template <int DT, bool VEC>
+__device__ __forceinline__ Run run_of(int64_t V, int parts, int part) {
+  constexpr int N = Piece<DT, VEC>::N;
+  const int64_t pieces = V / N;  // VEC: V is a multiple of N
+  return Run{pieces * part / parts * N, pieces * (part + 1) / parts * N};
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ unsigned long long sum_run(const Weights& r, Run run, bool& any,
+                                                      bool& odd) {
+  constexpr int N = Piece<DT, VEC>::N, U = 4;
+  const int lane = threadIdx.x & 31;
+  unsigned long long s = 0;
+  int64_t i = run.lo + (int64_t)lane * N;
+  for (; i + (U - 1) * 32 * N < run.hi; i += U * 32 * N) {
+    float w[U][N];
+#pragma unroll
+    for (int k = 0; k < U; ++k) load_weights<DT, VEC>(r, i + k * 32 * N, w[k], odd);
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        s += units(w[k][j]);
+        any |= w[k][j] > 0.0f;
+      }
+  }
+  for (; i < run.hi; i += 32 * N) {
+    float w[N];
+    load_weights<DT, VEC>(r, i, w, odd);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      s += units(w[j]);
+      any |= w[j] > 0.0f;
+    }
+  }
+  return s;
+}
+
+// The first element of the run at which the running sum, `before` in front of
+// the run, passes `target`; -1 if none does.
+template <int DT, bool VEC>
+__device__ int64_t find_in_run(const Weights& r, Run run, unsigned long long before,
+                               unsigned long long target) {
+  constexpr int N = Piece<DT, VEC>::N;
+  const int lane = threadIdx.x & 31;
+  bool odd = false;
+  for (int64_t base = run.lo; base < run.hi; base += 32 * N) {
+    const int64_t i = base + (int64_t)lane * N;
+    float w[N];
+    unsigned long long mine = 0;
+    const bool in = i < run.hi;
+    if (in) {
+      load_weights<DT, VEC>(r, i, w, odd);
+#pragma unroll
+      for (int j = 0; j < N; ++j) mine += units(w[j]);
+    }
+    unsigned long long scan = mine;  // inclusive over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long v = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + scan > target);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      int at = 0;
+      if (lane == l) {
+        unsigned long long c = before + scan - mine;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          c += units(w[j]);
+          if (c > target) {
+            at = j;
+            break;
+          }
+        }
+      }
+      at = __shfl_sync(0xffffffffu, at, l);
+      return base + (int64_t)l * N + at;
+    }
+    before += __shfl_sync(0xffffffffu, scan, 31);
+  }
+  return -1;
+}
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kProbThreads, 2) k_verify_probs(ProbArgs a) {
+  __shared__ ProbShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int b = (int)(blockIdx.x / C), g = a.gamma;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (threadIdx.x == 0) {
+    sh.any = 0;
+    sh.odd = 0;
+  }
+  if (warp == 0) accept_tests<DT>(a, b, sh);
+  __syncthreads();
+  const int n = sh.n;
+  constexpr int es = DT == SV_F32 ? 4 : 2;
+  Weights r;
+  r.p = (const char*)a.p + ((int64_t)b * (g + 1) + n) * a.V * es;
+  r.q = n < g ? (const char*)a.q + ((int64_t)b * g + n) * a.V * es : nullptr;
+  const Run run = run_of<DT, VEC>(a.V, C * kProbWarps, rank * kProbWarps + warp);
+  int flags = sh.flags;
+  unsigned long long total = 0, before = 0;
+  bool cluster_any = false, cluster_odd = false;
+  // once, and again on p_n where the residual is empty
+  for (int pass = 0; pass < 2; ++pass) {
+    bool any = false, odd = false;
+    const unsigned long long mine = warp_sum(sum_run<DT, VEC>(r, run, any, odd));
+    any = __any_sync(0xffffffffu, any);
+    odd = __any_sync(0xffffffffu, odd);
+    if (lane == 0) {
+      sh.warp_total[warp] = mine;
+      if (any) sh.any = 1;
+      if (odd) sh.odd = 1;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const unsigned long long s = warp_sum(lane < kProbWarps ? sh.warp_total[lane] : 0ull);
+      if (lane == 0) sh.total = s;
+    }
+    cluster.sync();
+    total = before = 0;
+    cluster_any = false;
+    for (int c = 0; c < C; ++c) {
+      const ProbShared* o = cluster.map_shared_rank(&sh, c);
+      const unsigned long long s = o->total;
+      if (c < rank) before += s;
+      total += s;
+      cluster_any |= o->any != 0;
+      cluster_odd |= o->odd != 0;
+    }
+    cluster.sync();  // nobody leaves, or sums again, while its totals are read
+    if (cluster_any || !r.q) break;
+    flags |= SV_FLAG_RESIDUAL_FALLBACK;
+    r.q = nullptr;
+  }
+  float u = __ldg(a.u + (int64_t)b * (g + 1) + g);
+  if (!(u >= 0.0f && u < 1.0f)) {
+    flags |= SV_FLAG_NONFINITE;
+    u = u >= 1.0f ? 0x1.fffffep-1f : 0.0f;
+  }
+  if (cluster_odd) flags |= SV_FLAG_NONFINITE;
+  if (!cluster_any) flags |= SV_FLAG_ZERO_MASS;
+  const unsigned long long target = times(u, total);
+  int32_t* out = a.out_tokens + (int64_t)b * (g + 1);
+  for (int w = 0; w < warp; ++w) before += sh.warp_total[w];
+  if (total > 0 && before <= target && target < before + sh.warp_total[warp]) {
+    const int64_t t = find_in_run<DT, VEC>(r, run, before, target);
+    if (lane == 0) out[n] = (int32_t)(t < 0 ? 0 : t);
+  }
+  if (rank == 0) {
+    if (threadIdx.x <= g && (int)threadIdx.x != n)
+      out[threadIdx.x] = (int)threadIdx.x < n ? __ldg(a.x + (int64_t)b * g + threadIdx.x) : -1;
+    if (threadIdx.x == 0) {
+      if (total == 0) out[n] = 0;  // no mass (or none as large as a unit)
+      a.out_counts[b] = n;
+      if (a.out_flags) a.out_flags[b] = (uint8_t)flags;
+    }
+  }
+}
+
+template <int DT>
+cudaError_t launch_dt(const ProbArgs& a, int cluster, cudaStream_t stream) {
+  constexpr int es = DT == SV_F32 ? 4 : 2;
+  // 16-byte loads where every row starts on a 16-byte boundary
+  auto* k = (a.V * es) % 16 == 0 ? k_verify_probs<DT, true> : k_verify_probs<DT, false>;
+  return launch_pdl_cluster(k, dim3((unsigned)(a.B * cluster)), dim3(kProbThreads), 0,
+                            (unsigned)cluster, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_verify_probs(const void* p, const void* q, const int32_t* x, const float* u,
+                                int B, int gamma, int64_t V, int dtype, int32_t* out_tokens,
+                                int32_t* out_counts, uint8_t* out_flags, cudaStream_t stream) {
+  const ProbArgs a{p, q, x, u, B, gamma, V, out_tokens, out_counts, out_flags};
+  // CTAs per batch row: until the grid has two for each of 152 SMs, and while a
+  // CTA keeps at least 4096 entries.
+  int c = 1;
+  while (c < kProbMaxCluster && (int64_t)B * c < 304 && V / (2 * c) >= 4096) c *= 2;
+  return dtype == SV_F32 ? launch_dt<SV_F32>(a, c, stream) : launch_dt<SV_BF16>(a, c, stream);
+}
+
+}  // namespace sv

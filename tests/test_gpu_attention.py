@@ -1,0 +1,218 @@
+"""spec_chunk_attention against the definition in 64 bits."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import speculative_decoding_verification_21_gb300 as sv
+from tests._paged import Case, E4M3
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sv.load()
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, FP), (BF, E4M3), (FP, E4M3)])
+@pytest.mark.parametrize("lens", [
+    [(1, 1)], [(1, 129)], [(5, 5)], [(5, 128), (5, 127), (5, 300)], [(33, 400), (1, 1), (7, 257)],
+])
+def test_rounds(lens, dtype, cache):
+    Case(lens, dtype=dtype, cache=cache).check()
+
+
+@pytest.mark.parametrize("page", [1, 4, 8, 16, 24, 32, 64, 128, 256, 1024])
+@pytest.mark.parametrize("cache", [BF, E4M3])
+def test_page_sizes(page, cache):
+    """Pages that end inside a tile, and tiles that end inside a page."""
+    Case([(3, 2 * page + 1), (6, 130), (2, 515)], page=page, cache=cache, dim=128).check()
+
+
+@pytest.mark.parametrize("dim", [16, 32, 48, 64, 80, 96, 112, 128, 144, 256])
+@pytest.mark.parametrize("dtype,cache", [(FP, FP), (BF, E4M3)])
+def test_head_sizes(dim, dtype, cache):
+    Case([(4, 200), (70, 70)], dim=dim, dtype=dtype, cache=cache, layout="nhd").check()
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 8, 16, 31, 71, 128])
+@pytest.mark.parametrize("kv_heads", [1, 3])
+def test_groups(group, kv_heads):
+    """Grouped heads, from one query head per key head to all of them on one."""
+    Case([(1, 150), (9, 140), (40, 300)], group=group, kv_heads=kv_heads).check()
+
+
+@pytest.mark.parametrize("window", [1, 2, 17, 128, 129, 500])
+@pytest.mark.parametrize("cache", [BF, E4M3])
+def test_windows(window, cache):
+    Case([(1, 700), (5, 133), (90, 400), (200, 200)], cache=cache, dim=128).check(window=window)
+
+
+def test_prompts():
+    """Chunks of many tiles, whole prompts and stretches of them, packed."""
+    Case([(300, 300), (129, 1000), (1, 17), (513, 700)], dim=128, group=4).check()
+    Case([(257, 257), (64, 2000)], dim=64, group=7, dtype=FP).check(window=300)
+    Case([(200, 900), (3, 3)], dim=128, group=8, cache=E4M3).check()
+
+
+def test_long_cache_is_split_and_joined():
+    for cache in (FP, E4M3):
+        Case([(6, 50001)], kv_heads=1, group=8, dim=64, page=128, dtype=FP, cache=cache).check()
+    Case([(1, 9000), (1, 1), (1, 20000), (1, 3)], kv_heads=2, group=8, dim=128).check()
+
+
+def test_empty_sequences_and_rows_without_keys():
+    """No new tokens, no cached ones, and a chunk longer than its sequence: the rows before
+    position 0 see nothing."""
+    Case([(0, 40), (3, 3), (0, 0), (5, 2), (2, 0), (1, 77)]).check()
+    Case([(300, 100), (4, 0)], dim=128).check()
+    Case([(0, 10), (0, 0)]).attend()  # nothing to do
+
+
+def test_scales():
+    for scale in (0.0, 1.0, -0.3, 3.0):
+        Case([(5, 300), (60, 200)], dim=64).check(scale=scale)
+
+
+def test_many_sequences():
+    lens = [(1 + b % 4, 1 + (37 * b) % 400 + b % 4) for b in range(700)]
+    Case(lens, kv_heads=2, group=2).check()
+
+
+def test_wide_range_of_token_scales():
+    """Keys and values whose sizes differ by 2^12 from token to token."""
+    Case([(5, 700), (40, 150)], dim=128, cache=E4M3, scale_spread=6).check(scale=1e-3)
+
+
+def test_sharp_rows():
+    """Scores far apart: the running maximum rises by hundreds along the keys, and falls."""
+    for sign in (1.0, -1.0):
+        c = Case([(4, 1500), (130, 600)], dim=64, group=4)
+        for b, (n, L) in enumerate(c.lens):
+            ramp = sign * torch.linspace(-6, 6, L, device="cuda")[:, None, None]
+            k = (c.k64[b] * 0.1 + ramp).to(BF)
+            j = torch.arange(L, device="cuda")
+            p = torch.tensor(c.owned[b], device="cuda")[j // c.ps]
+            c.cache.k[p, :, j % c.ps] = k
+            c.k64[b] = k.double()
+        c.q.abs_()
+        c.check()
+
+
+def test_equal_scores_give_the_mean():
+    c = Case([(1, 1000)], dim=64)
+    c.q.zero_()
+    o = c.check()
+    assert torch.allclose(o["lse"], torch.full_like(o["lse"], math.log(1000.0)), atol=1e-6)
+
+
+def test_infinite_and_nan_values_reach_only_who_sees_them():
+    """A NaN and an infinity in the first tokens reach every query; the other sequence, the other
+    head and whoever's window is past them keep theirs."""
+    c = Case([(3, 400), (3, 400)], dim=64)
+    page, slot = c.owned[0][0], 2
+    c.cache.v[page, 0, slot, 5] = math.inf
+    c.cache.v[page, 0, slot, 6] = math.nan
+    clean = Case([(3, 400), (3, 400)], dim=64).attend()["out"]
+    o = c.attend()["out"]
+    assert bool(torch.isposinf(o[:3, :4, 5]).all()) and bool(torch.isnan(o[:3, :4, 6]).all())
+    assert torch.equal(o[3:], clean[3:]) and torch.equal(o[:, 4:], clean[:, 4:])
+    assert torch.equal(o[:3, :4, 7:], clean[:3, :4, 7:])
+    w = c.attend(window=200)["out"]
+    assert bool(torch.isfinite(w).all())
+
+
+def test_a_nan_key_reaches_its_sequence_and_head_only():
+    c = Case([(3, 400), (3, 300)], dim=64)
+    clean = c.attend()["out"].clone()
+    c.cache.k[c.owned[0][3], 1, 4, 9] = math.nan
+    o = c.attend()["out"]
+    assert bool(torch.isnan(o[:3, 4:]).all())
+    assert torch.equal(o[3:], clean[3:]) and torch.equal(o[:3, :4], clean[:3, :4])
+
+
+def test_offsets_past_32_bits():
+    """Pages whose byte offsets pass 2^32 (a pool of 6 GB a side)."""
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    Case([(5, 600), (2, 100)], kv_heads=2, dim=128, page=64, first_page=180000).check()
+
+
+def test_bad_pages_are_flagged_and_harm_nobody_else():
+    c = Case([(5, 300), (5, 300), (2, 40)], dim=64)
+    good = c.attend()["out"].clone()
+    for bad in (-1, c.pages, 2 ** 31 - 1, -2 ** 31):
+        c.table[1, 7] = bad
+        o = c.attend(want_flags=True)
+        assert o["flags"].tolist() == [0, sv.FLAG_BAD_PAGE, 0]
+        assert torch.equal(o["out"][:5], good[:5]) and torch.equal(o["out"][10:], good[10:])
+
+
+def test_bad_lengths_are_flagged_and_harm_nobody_else():
+    c = Case([(5, 300), (5, 300), (2, 40)], dim=64)
+    good = c.attend()["out"].clone()
+    for bad in (-1, -2 ** 31, 2 ** 31 - 1):
+        c.len[1] = bad
+        o = c.attend(want_flags=True)
+        assert o["flags"][0] == 0 and o["flags"][2] == 0
+        assert o["flags"][1].item() & sv.FLAG_BAD_LENGTH
+        assert torch.equal(o["out"][:5], good[:5]) and torch.equal(o["out"][10:], good[10:])
+    c.len[1] = 300
+    c.start[3] = 1000  # past the packed rows: the last sequence is skipped
+    o = c.attend(want_flags=True)
+    assert o["flags"].tolist() == [0, 0, sv.FLAG_BAD_LENGTH]
+    assert torch.equal(o["out"][:10], good[:10])
+
+
+def test_same_bits_every_time_and_on_another_stream():
+    c = Case([(5, 3000), (300, 700), (1, 9000)], dim=128, group=4)
+    a = c.attend()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        b = c.attend()
+    s.synchronize()
+    assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+def test_captured_into_a_graph_with_lengths_that_change():
+    c = Case([(5, 3000), (5, 700)], dim=128, group=4)
+    ws = torch.empty(max(256, sv.attention_workspace_bytes(c.cache, 8)), dtype=torch.uint8,
+                     device="cuda")
+    out = c.attend(workspace=ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.attend(workspace=ws, out=out)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            c.attend(workspace=ws, out=out)
+    for L in (3000, 129, 2047, 5):
+        c.len[0] = L
+        want = c.attend()
+        out["out"].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out["out"], want["out"]) and torch.equal(out["lse"], want["lse"])
+
+
+def test_refusals_of_the_binding():
+    c = Case([(2, 20)])
+    with pytest.raises(TypeError):
+        sv.spec_chunk_attention(c.q.float(), c.cache, c.table, c.start, c.len)
+    with pytest.raises(sv.SpecVerifyError):  # fp16 queries on a bf16 cache
+        sv.spec_chunk_attention(c.q.half(), c.cache, c.table, c.start, c.len)
+    with pytest.raises(ValueError):
+        sv.spec_chunk_attention(c.q[..., :32], c.cache, c.table, c.start, c.len)
+    with pytest.raises(ValueError):
+        sv.spec_chunk_attention(c.q, c.cache, c.table, c.start[:-1], c.len)
+    with pytest.raises(TypeError):
+        sv.spec_chunk_attention(c.q, c.cache, c.table.long(), c.start, c.len)
+    with pytest.raises(sv.SpecVerifyError):  # 7 query heads on 2 key heads
+        sv.spec_chunk_attention(c.q[:, :7], c.cache, c.table, c.start, c.len)
