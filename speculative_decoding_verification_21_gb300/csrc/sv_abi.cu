@@ -311,7 +311,7 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads) {
   if (check_cache(cache) != SV_OK || heads < 1 || heads % cache->kv_heads ||
       heads / cache->kv_heads > kMaxGroup)
     return 0;
-  return sv::attention_workspace_bytes(cache->head_dim);
+  return sv::attention_workspace_bytes(sv::cache_view(*cache), cache->dtype == SV_E4M3);
 }
 
 int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, const void* q,

@@ -1,5 +1,6 @@
-// sv_attention.cu -- spec_chunk_attention: causal attention of each sequence's
-// chunk of new tokens over its pages of the cache.
+// sv_attention.cu -- spec_chunk_attention for caches that the tile kernel does not
+// take (tiles_take): causal attention of each sequence's chunk of new tokens over
+// its pages, one query row per CTA.
 //
 //   s_j = scale q.k_j over the keys seen, m = max_j s_j, p_j = exp(s_j - m),
 //   out = (sum_j p_j v_j) / (sum_j p_j),  lse = m + log sum_j p_j
@@ -166,38 +167,32 @@ __global__ void __launch_bounds__(kRowWarps * 32) k_attend_rows(AttendArgs a) {
     a.lse[(int64_t)t * a.heads + hq] = L == 0.0f ? -kInf : (M == -kInf ? 0.0f : M) * kLn2 + logf(L);
 }
 
-// Flags of every sequence: its lengths, and the pages of the keys it sees.
 __global__ void __launch_bounds__(256) k_attend_flags(AttendArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
   const int b = (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
   if (b >= a.b.B) return;
-  const Seq q = load_seq(a.b, b, a.c.page_size);
-  bool bad = false;
-  if (q.n) {
-    const int first = q.pos0 + 1;
-    const int lo = a.window && first > a.window ? first - a.window : 0;
-    for (int p = lo / a.c.page_size + lane; (int64_t)p * a.c.page_size < q.len; p += 32) {
-      const int page = __ldg(a.b.table + (int64_t)b * a.b.max_pages + p);
-      bad |= page < 0 || page >= a.c.num_pages;
-    }
-  }
-  bad = __any_sync(0xffffffffu, bad);
-  if (lane == 0)
-    a.flags[b] = (uint8_t)((q.bad ? SV_FLAG_BAD_LENGTH : 0) | (bad ? SV_FLAG_BAD_PAGE : 0));
+  const uint8_t f = sequence_flags(a, b);
+  if ((threadIdx.x & 31) == 0) a.flags[b] = f;
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int) { return 0; }
+size_t attention_workspace_bytes(const CacheView& c, bool e4m3) {
+  return tiles_take(c, e4m3) ? attention_tiles_workspace(c.head_dim) : 0;
+}
 
 cudaError_t launch_attention(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream) {
-  if (a.flags && a.b.B) {
+  if (tiles_take(a.c, e4m3)) {
+    bool taken = false;
+    const cudaError_t e = launch_attention_tiles(a, dtype, e4m3, stream, &taken);
+    if (e != cudaSuccess || taken) return e;
+  }
+  if (a.flags) {
     const cudaError_t e = launch_pdl(k_attend_flags, dim3((a.b.B + 7) / 8), dim3(256), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
-  if (a.b.total == 0 || a.b.B == 0) return cudaSuccess;
+  if (a.b.total == 0) return cudaSuccess;
   auto* k = dtype == SV_BF16 ? (e4m3 ? k_attend_rows<SV_BF16, true> : k_attend_rows<SV_BF16, false>)
                              : (e4m3 ? k_attend_rows<SV_F16, true> : k_attend_rows<SV_F16, false>);
   return launch_pdl(k, dim3((unsigned)((int64_t)a.b.total * a.heads)), dim3(kRowWarps * 32), 0,

@@ -23,7 +23,37 @@ struct AttendArgs {
   char* ws;
 };
 
-size_t attention_workspace_bytes(int head_dim);
+// Whether the tile kernel takes a cache: head_dim up to 128, and pages that divide
+// a tile of 128 tokens or are whole tiles, at least 8 tokens (one swizzle group), or
+// 16 where their scale bytes are copied 16 at a time.  The row kernel takes the rest.
+inline bool tiles_take(const CacheView& c, bool e4m3) {
+  if (c.head_dim > 128 || c.num_pages == 0) return false;
+  if (!e4m3) return c.page_shift >= 3;
+  return c.page_shift >= 4 && ((uintptr_t)c.ks | (uintptr_t)c.vs) % 16 == 0;
+}
+
+// Flags of sequence b (one warp): its lengths, and the pages of the keys it sees.
+__device__ __forceinline__ uint8_t sequence_flags(const AttendArgs& a, int b) {
+  const Seq q = load_seq(a.b, b, a.c.page_size);
+  bool bad = false;
+  if (q.n) {
+    const int first = q.pos0 + 1;
+    const int lo = a.window && first > a.window ? first - a.window : 0;
+    for (int p = lo / a.c.page_size + (threadIdx.x & 31); (int64_t)p * a.c.page_size < q.len; p += 32) {
+      const int page = __ldg(a.b.table + (int64_t)b * a.b.max_pages + p);
+      bad |= page < 0 || page >= a.c.num_pages;
+    }
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  return (uint8_t)((q.bad ? SV_FLAG_BAD_LENGTH : 0) | (bad ? SV_FLAG_BAD_PAGE : 0));
+}
+
+size_t attention_workspace_bytes(const CacheView& c, bool e4m3);
+size_t attention_tiles_workspace(int head_dim);
 cudaError_t launch_attention(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream);
+
+// *taken = false: the cache cannot be described by a tensor map; nothing was queued.
+cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream,
+                                   bool* taken);
 
 }  // namespace sv

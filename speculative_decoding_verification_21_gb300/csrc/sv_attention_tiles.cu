@@ -1,0 +1,1133 @@
+// sv_attention_tiles.cu -- spec_chunk_attention on the tensor cores: tiles of 128
+// query rows against tiles of 128 keys.
+//
+//   S = Q K^T (tcgen05, fp32 in tensor memory), P = 2^(c S - m) with the running
+//   row maximum m, O += P V (P from tensor memory), l += row sums of P;
+//   out = O / l, lse = (m + log2 l) ln 2.
+//
+// Rows: the `group` query heads of a key head share its keys, so the rows of a
+// tile are (token, head of the group) pairs, floor(128 / group) tokens of them; a
+// key tile is read once for all of them.  An item is up to two such tiles of one
+// (sequence, key head); its keys are cut into tiles of 128 counted from token 0.
+//
+// Balance: all key tiles of all items form one line, cut into equal shares, one
+// per CTA (one CTA per SM).  An item cut by a share's end leaves partial (m, l, O)
+// in the workspace, at most two per CTA, which k_attend_join adds up; an item
+// inside a share is written at once.  Lengths live on the device, so every CTA
+// finds its own place in the line at its start.
+//
+// Two softmax warpgroups keep the tensor cores busy: while one works on its S,
+// the other's products run.  An item of two row tiles gives one to each; an item
+// of one row tile (a round's few tokens) gives them the key tiles alternately, and
+// their (m, l, O) are added up at its end.
+//
+// Roles: warp 0 fetches key and value pages (tensor copies, 128-byte swizzle),
+// warp 1 issues the products, warps 2-3 fetch queries, warps 4-11 are the softmax,
+// and for e4m3 caches warps 12-15 widen the codes to 16 bits between the copies
+// and the products.  Every wait is bounded; one that gives up ends the CTA's roles
+// and flags the call.
+//
+// Waits of one CTA, by barrier: full/empty (key and value tiles in 16 bits),
+// rawfull/rawempty (e4m3 codes), qfull/qempty (query tiles), sfull (S ready),
+// pfull (P written, so S is free), ofull (last product of a stage done), xbar
+// (the two warpgroups at the end of a one-tile item).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "specverify.h"
+#include "sv_attention.h"
+#include "sv_cache.cuh"
+#include "sv_device.cuh"
+#include "sv_launch.h"
+#include "sv_tma.cuh"
+#include "sv_umma.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kTile = 128;          // query rows and keys per tile
+constexpr int kSpan = 16384;        // 128 rows of one 128-byte swizzle span
+constexpr int kMaxCtas = 160;       // shares (GB300: 152 SMs)
+constexpr int kMaxRows = 2 * kTile;
+constexpr int kMaxStages = 10, kMaxRaw = 8;
+constexpr long long kWaitClocks = 1ll << 32;  // about two seconds
+constexpr size_t kSmemBytes = 227 * 1024;
+constexpr int kQBytes = 2 * kSpan;                // one query tile
+constexpr int kRing16 = 160 * 1024;               // 16-bit caches: 5 (or 10) key/value tiles
+constexpr int kRing8 = 96 * 1024;                 // e4m3: 3 (or 6) widened tiles ...
+constexpr int kRaw8 = 4 * kTile * (kTile + 1);    // ... and 4 or more tiles of codes and scales
+constexpr int kJoinThreads = 256;
+// The running maximum may lag by this many powers of two before O is rescaled: P
+// stays within 2^8, exact enough in 16-bit floats and far from their range.
+constexpr float kLag = 8.0f;
+
+struct TileArgs {
+  AttendArgs a;
+  int group, tpt;      // query heads per key head; tokens per row tile
+  int nhalf;           // swizzle spans per row: 1 (head_dim <= 64) or 2
+  int nst, nraw;       // ring slots
+  int box;             // tokens per copy: min(page_size, 128)
+  int flip;            // negative scale: the queries' signs are flipped
+  float c;             // |scale| log2 e
+  float* part;         // [2 * kMaxCtas][kMaxRows][head_dim]
+  float2* ml;          // [2 * kMaxCtas][kMaxRows]
+  struct Rec* rec;     // [kMaxCtas]
+  int* err;            // [kMaxCtas]
+};
+
+// What a CTA leaves for the join: the item that it began and did not end.
+struct Rec {
+  int more;            // further CTAs with a part of it (0: nothing to join)
+  int row0, ntok, h;   // first packed row, tokens, key head
+};
+
+// Control words of a CTA.
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages], rawfull[kMaxRaw], rawempty[kMaxRaw];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], xbar, fin;
+  uint32_t tmem;
+  int abort;
+  int b, h, qt, off;   // start of the CTA's share
+  long long left, share;
+  union {
+    long long warp_units[16];
+    float2 xch[2][kTile];  // (m, l) of the two warpgroups
+  };
+};
+
+// ---------------------------------------------------------------------------
+// The line of work.
+// ---------------------------------------------------------------------------
+struct Span {
+  int lo, hi;        // keys [lo, hi) that some row of the item sees
+  int first, count;  // key tiles; count >= 1 (a masked one if nothing is seen)
+};
+
+__device__ __forceinline__ Span item_span(const Seq& q, int per_item, int qt, int window) {
+  const int i0 = qt * per_item, i1 = min(q.n, i0 + per_item);
+  Span s;
+  s.hi = max(0, q.pos0 + i1);
+  s.lo = window ? max(0, q.pos0 + i0 + 1 - window) : 0;
+  if (s.hi <= s.lo) {
+    s.lo = s.hi = s.first = 0;
+    s.count = 1;
+  } else {
+    s.first = s.lo / kTile;
+    s.count = (s.hi + kTile - 1) / kTile - s.first;
+  }
+  return s;
+}
+
+__device__ __forceinline__ long long warp_sum64(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ long long warp_scan64(long long v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long w = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += w;
+  }
+  return v;
+}
+
+// Key tiles of one head of the lane's sequence (n = 0: none).  A sequence of many
+// items is summed by the whole warp.
+__device__ __forceinline__ long long head_units(const Seq& q, int per_item, int window) {
+  const int lane = threadIdx.x & 31;
+  const int nqt = (q.n + per_item - 1) / per_item;
+  long long u = 0;
+  if (nqt <= 4)
+    for (int t = 0; t < nqt; ++t) u += item_span(q, per_item, t, window).count;
+  unsigned big = __ballot_sync(0xffffffffu, nqt > 4);
+  while (big) {
+    const int src = __ffs(big) - 1;
+    big &= big - 1;
+    Seq s{};
+    s.n = __shfl_sync(0xffffffffu, q.n, src);
+    s.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
+    long long v = 0;
+    const int m = (s.n + per_item - 1) / per_item;
+    for (int t = lane; t < m; t += 32) v += item_span(s, per_item, t, window).count;
+    v = warp_sum64(v);
+    if (lane == src) u = v;
+  }
+  return u;
+}
+
+// The start of this CTA's share (all threads; ends with a barrier).
+__device__ void find_share(const TileArgs& t, Ctl& ctl) {
+  const BatchView& bv = t.a.b;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (int)(blockDim.x >> 5);
+  const int per_item = 2 * t.tpt, H = t.a.c.kv_heads, ps = t.a.c.page_size;
+  const int chunk = (bv.B + nw - 1) / nw;
+  const int b0 = min(bv.B, warp * chunk), b1 = min(bv.B, b0 + chunk);
+  long long sum = 0;
+  for (int base = b0; base < b1; base += 32) {
+    Seq q{};
+    if (base + lane < b1) q = load_seq(bv, base + lane, ps);
+    sum += warp_sum64(head_units(q, per_item, t.a.window) * H);
+  }
+  if (lane == 0) ctl.warp_units[warp] = sum;
+  if (threadIdx.x == 0) {
+    ctl.left = 0;
+    ctl.b = bv.B;
+    ctl.h = ctl.qt = ctl.off = 0;
+  }
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    const long long u = ctl.warp_units[w];
+    if (w < warp) before += u;
+    total += u;
+  }
+  const long long share = max(1ll, (total + gridDim.x - 1) / (long long)gridDim.x);
+  const long long start = share * blockIdx.x;
+  if (start >= before && start < before + sum) {  // this warp's sequences hold the start
+    for (int base = b0; base < b1; base += 32) {
+      Seq q{};
+      if (base + lane < b1) q = load_seq(bv, base + lane, ps);
+      const long long per_head = head_units(q, per_item, t.a.window);
+      const long long scan = warp_scan64(per_head * H);
+      const unsigned hit = __ballot_sync(0xffffffffu, start < before + scan);
+      if (!hit) {
+        before += __shfl_sync(0xffffffffu, scan, 31);
+        continue;
+      }
+      const int src = __ffs(hit) - 1;
+      Seq s{};
+      s.n = __shfl_sync(0xffffffffu, q.n, src);
+      s.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
+      const long long ph = __shfl_sync(0xffffffffu, per_head, src);
+      long long r = start - before - __shfl_sync(0xffffffffu, scan - per_head * H, src);
+      const int h = (int)(r / ph);
+      r -= h * ph;
+      const int m = (s.n + per_item - 1) / per_item;
+      for (int q0 = 0; q0 < m; q0 += 32) {
+        const long long c = q0 + lane < m ? item_span(s, per_item, q0 + lane, t.a.window).count : 0;
+        const long long sc = warp_scan64(c);
+        const unsigned in = __ballot_sync(0xffffffffu, r < sc);
+        if (!in) {
+          r -= __shfl_sync(0xffffffffu, sc, 31);
+          continue;
+        }
+        const int l = __ffs(in) - 1;
+        const long long off = r - __shfl_sync(0xffffffffu, sc - c, l);
+        if (lane == 0) {
+          ctl.b = base + src;
+          ctl.h = h;
+          ctl.qt = q0 + l;
+          ctl.off = (int)off;
+          ctl.left = min(share, total - start);
+        }
+        break;
+      }
+      break;
+    }
+  }
+  if (threadIdx.x == 0) ctl.share = share;
+  __syncthreads();
+}
+
+// One CTA's part of one item.
+struct Seg {
+  int b, h;
+  int row0, ntok;    // first packed row, tokens
+  int pos;           // position of the first token
+  int lo, hi;
+  int t0, n;         // key tiles t0 .. t0+n-1
+  bool two;          // two row tiles
+  int slot;          // -1: the whole item; else the partial slot of the CTA (0, 1)
+  int more;          // slot 1: further CTAs with a part of it
+};
+
+struct Walk {
+  int b, h, qt, off, nqt;
+  long long left;
+  Seq q;
+  bool loaded;
+
+  __device__ __forceinline__ Walk(const Ctl& c)
+      : b(c.b), h(c.h), qt(c.qt), off(c.off), nqt(0), left(c.left), loaded(false) {}
+
+  __device__ __forceinline__ bool next(const TileArgs& t, const Ctl& ctl, Seg& s) {
+    if (left <= 0) return false;
+    const int per_item = 2 * t.tpt;
+    while (!loaded) {
+      if (b >= t.a.b.B) return false;
+      q = load_seq(t.a.b, b, t.a.c.page_size);
+      nqt = (q.n + per_item - 1) / per_item;
+      if (nqt) loaded = true;
+      else ++b;
+    }
+    const Span sp = item_span(q, per_item, qt, t.a.window);
+    const int avail = sp.count - off;
+    s.b = b;
+    s.h = h;
+    s.row0 = q.tok0 + qt * per_item;
+    s.ntok = min(per_item, q.n - qt * per_item);
+    s.pos = q.pos0 + qt * per_item;
+    s.lo = sp.lo;
+    s.hi = sp.hi;
+    s.t0 = sp.first + off;
+    s.n = (int)min((long long)avail, left);
+    s.two = s.ntok > t.tpt;
+    s.slot = s.n == sp.count ? -1 : (off ? 0 : 1);
+    s.more = s.slot == 1 ? (int)((avail - s.n + ctl.share - 1) / ctl.share) : 0;
+    left -= s.n;
+    off = 0;
+    if (++qt == nqt) {
+      qt = 0;
+      if (++h == t.a.c.kv_heads) {
+        h = 0;
+        ++b;
+        loaded = false;
+      }
+    }
+    return true;
+  }
+};
+
+// Ring order of an item part's tiles: K0 K1 V0 K2 V1 ... V(n-1), as the products
+// need them when the next S is computed one product ahead.
+__device__ __forceinline__ int k_index(int i) { return i ? 2 * i - 1 : 0; }
+__device__ __forceinline__ int v_index(int i, int n) { return i == n - 1 ? 2 * n - 1 : 2 * i + 2; }
+__device__ __forceinline__ void tile_of(int idx, int n, bool& is_v, int& tile) {
+  is_v = idx == 2 * n - 1 || (idx > 0 && (idx & 1) == 0);
+  tile = is_v ? (idx == 2 * n - 1 ? n - 1 : idx / 2 - 1) : (idx + 1) / 2;
+}
+
+// ---------------------------------------------------------------------------
+// Waits.
+// ---------------------------------------------------------------------------
+// Which wait gave up first (1..), for whoever looks at the workspace after a timeout.
+enum WaitId { kWaitSlot = 1, kWaitQ, kWaitK, kWaitV, kWaitP, kWaitQFree, kWaitS, kWaitO, kWaitX, kWaitRaw,
+              kWaitWide };
+
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                         int id) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (clock64() - t0 < kWaitClocks) {
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  *abort_flag = id;
+  return false;
+}
+// A whole warp: lane 0 polls and decides for all lanes (a lane that tested the
+// barrier for itself could find it a phase further on and part from the others).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int id) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_one(bar, parity, abort_flag, id);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok != 0;
+}
+// What must have ended before the CTA may go, whether or not the call is aborted.
+__device__ __forceinline__ void wait_end(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity) && clock64() - t0 < kWaitClocks) {
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Softmax of one S tile row (this thread's), 128 scores in tensor memory.
+// ---------------------------------------------------------------------------
+// Scores that the row does not see become -inf; the row sees columns [first, first+span).
+template <bool MASK>
+__device__ __forceinline__ float row_max(uint32_t s_tm, int first, int span) {
+  float m = -kInf;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t r[32];
+    tmem_ld32_async(s_tm + 32 * k, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      float s = __uint_as_float(r[j]);
+      if (MASK) s = (unsigned)(32 * k + j - first) < (unsigned)span ? s : -kInf;
+      m = fmaxf(m, s);
+    }
+  }
+  return m;
+}
+
+// P = 2^(c s - m), written over S as pairs of 16-bit floats; returns the row sum.
+template <int PT, bool MASK>
+__device__ __forceinline__ float row_exp(uint32_t s_tm, int first, int span, float c, float m) {
+  const uint64_t cc = pack2(c, c), mm = pack2(-m, -m);
+  uint64_t acc0 = pack2(0.0f, 0.0f), acc1 = acc0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t r[32], w[16];
+    tmem_ld32_async(s_tm + 32 * k, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float x, y;
+      unpack2(ffma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), cc, mm), x, y);
+      x = ex2(x);
+      y = ex2(y);
+      if (MASK) {
+        x = (unsigned)(32 * k + 2 * j - first) < (unsigned)span ? x : 0.0f;
+        y = (unsigned)(32 * k + 2 * j + 1 - first) < (unsigned)span ? y : 0.0f;
+      }
+      if (j & 1) acc1 = fadd2(acc1, pack2(x, y));
+      else acc0 = fadd2(acc0, pack2(x, y));
+      w[j] = F16<PT>::down(x, y);
+    }
+    tmem_st16(s_tm + 16 * k, w);
+  }
+  float a, b, d, e;
+  unpack2(acc0, a, b);
+  unpack2(acc1, d, e);
+  return (a + b) + (d + e);
+}
+
+// O *= f (rows that need none have f = 1).
+__device__ __forceinline__ void rescale(uint32_t o_tm, int units, float f) {
+  for (int u = 0; u < units; ++u) {
+    uint32_t r[16];
+    __syncwarp();
+    tmem_ld16_async(o_tm + 16 * u, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+    tmem_st16(o_tm + 16 * u, r);
+  }
+  tmem_wait_st();
+}
+
+template <int DT>
+__device__ __forceinline__ void store16(char* at, const float* x) {
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = F16<DT>::down(x[2 * j], x[2 * j + 1]);
+  reinterpret_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void store16f(float* at, const float* x) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    reinterpret_cast<float4*>(at)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -kInf : ((m == -kInf ? 0.0f : m) + log2f(l)) * kLn2;
+}
+
+template <int DT, bool E4M3>
+__global__ void __launch_bounds__(E4M3 ? 512 : 384, 1)
+k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+               const __grid_constant__ TileArgs t) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int kRing = E4M3 ? kRing8 : kRing16;
+  constexpr int kPT = DT;
+  constexpr float kShift = kPT == SV_F16 ? 6.0f : 0.0f;  // fp16 P within 2^14: small ones keep bits
+  uint8_t* const qbuf = smem;
+  uint8_t* const ring = smem + 2 * kQBytes;
+  uint8_t* const raw = ring + kRing;  // e4m3 codes: [nraw][128 (D + 1)], scales behind the codes
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem + 2 * kQBytes + kRing + (E4M3 ? kRaw8 : 0));
+  static_assert(2 * kQBytes + kRing16 + sizeof(Ctl) <= kSmemBytes, "shared memory");
+  static_assert(2 * kQBytes + kRing8 + kRaw8 + sizeof(Ctl) <= kSmemBytes, "shared memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const AttendArgs& a = t.a;
+  const int D = a.c.head_dim, nst = t.nst, nraw = t.nraw;
+  const int stage_bytes = t.nhalf * kSpan, raw_bytes = kTile * (D + 1);
+  volatile int* const abort_flag = &ctl.abort;
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    ctl.abort = (smem_u32(smem) & 1023u) ? 1 : 0;  // the swizzle needs this alignment
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(ctl.full + i, E4M3 ? 4 : 1);
+      mbar_init(ctl.empty + i, 1);
+    }
+    for (int i = 0; i < kMaxRaw; ++i) {
+      mbar_init(ctl.rawfull + i, 1);
+      mbar_init(ctl.rawempty + i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(ctl.qfull + i, 2);
+      mbar_init(ctl.qempty + i, 1);
+      mbar_init(ctl.sfull + i, 1);
+      mbar_init(ctl.pfull + i, 4);
+      mbar_init(ctl.ofull + i, 1);
+    }
+    mbar_init(&ctl.xbar, 8);
+    mbar_init(&ctl.fin, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = ctl.tmem;
+  pdl_wait();
+  find_share(t, ctl);
+  const int wid = (int)blockIdx.x;
+  Walk walk(ctl);
+  Seg s;
+  bool ok = *abort_flag == 0;
+
+  if (warp == 0) {
+    // ---------------- fetch key and value pages ----------------
+    const uint64_t pol = l2_policy_evict_first();
+    uint32_t issued = 0;  // tiles
+    const int copies = kTile / t.box;                         // copies along a tile
+    const int part = E4M3 ? lane : (t.nhalf == 2 ? lane >> 1 : lane);  // this lane's copy ...
+    const int half = E4M3 ? 0 : (t.nhalf == 2 ? lane & 1 : 0);         // ... and span
+    while (ok && walk.next(t, ctl, s)) {
+      const int32_t* table = a.b.table + (int64_t)s.b * a.b.max_pages;
+      for (int idx = 0; ok && idx < 2 * s.n; ++idx, ++issued) {
+        bool is_v;
+        int tile;
+        tile_of(idx, s.n, is_v, tile);
+        const int key0 = (s.t0 + tile) * kTile;
+        const int from = max(0, s.lo - key0) / t.box;                         // copies that hold
+        const int upto = min(copies, (max(0, s.hi - key0) + t.box - 1) / t.box);  // keys seen
+        const int mine = key0 + part * t.box;
+        int page = -1;
+        if (part >= from && part < upto) page = __ldg(table + (mine >> a.c.page_shift));
+        const uint32_t ns = E4M3 ? nraw : nst;
+        const uint32_t slot = issued % ns, ph = (issued / ns) & 1u;
+        uint64_t* const fullb = (E4M3 ? ctl.rawfull : ctl.full) + slot;
+        if (!wait_warp((E4M3 ? ctl.rawempty : ctl.empty) + slot, ph ^ 1u, abort_flag, kWaitSlot)) {
+          ok = false;
+          break;
+        }
+        const int live = max(0, upto - from);
+        uint32_t bytes = (uint32_t)(live * t.box * (E4M3 ? D : t.nhalf * 128));
+        uint8_t* const dst8 = raw + (size_t)slot * raw_bytes;
+        uint8_t* const scales = dst8 + kTile * D + part * t.box;
+        // a page outside the pool arrives as zeros; so do its scales
+        const bool sound = page >= 0 && page < a.c.num_pages;
+        if (E4M3) {
+          bytes += __popc(__ballot_sync(0xffffffffu, sound)) * t.box;
+          if (part >= from && part < upto && !sound)
+            for (int e = 0; e < t.box; e += 16)
+              *reinterpret_cast<uint4*>(scales + e) = make_uint4(0, 0, 0, 0);
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(fullb, bytes);
+        __syncwarp();
+        if (part >= from && part < upto) {
+          const int slot_in_page = mine & (a.c.page_size - 1);
+          if (E4M3) {
+            tma_load_4d_hint(dst8 + part * t.box * D, is_v ? &mv : &mk, 0, slot_in_page, s.h, page,
+                             fullb, pol);
+            if (sound)
+              bulk_load(scales,
+                        (is_v ? a.c.vs : a.c.ks) +
+                            ((int64_t)page * a.c.kv_heads + s.h) * a.c.page_size + slot_in_page,
+                        (uint32_t)t.box, fullb);
+          } else {
+            uint8_t* const dst = ring + (size_t)slot * stage_bytes;
+            tma_load_4d_hint(dst + half * kSpan + part * t.box * 128, is_v ? &mv : &mk, 64 * half,
+                             slot_in_page, s.h, page, fullb, pol);
+          }
+        }
+      }
+    }
+    // every copy has landed before the CTA may exit
+    const uint32_t ns = E4M3 ? nraw : nst;
+    for (uint32_t i = 0; i < ns && i < issued; ++i) {
+      const uint32_t last = (issued - 1u) - ((issued - 1u - i) % ns);
+      if (lane == 0) wait_end((E4M3 ? ctl.rawfull : ctl.full) + i, (last / ns) & 1u);
+    }
+  } else if (warp == 1) {
+    // ---------------- issue the products ----------------
+    const uint32_t idesc_s = umma_idesc_16(DT == SV_BF16, kTile, kTile, false);
+    const uint32_t idesc_o = umma_idesc_16(kPT == SV_BF16, kTile, D, true);
+    const int ksteps = D / 16;
+    uint32_t base = 0, qn = 0;          // tiles and query tiles used so far
+    uint32_t pph[2] = {0, 0};
+    while (ok && walk.next(t, ctl, s)) {
+      const int jobs = s.two ? 2 * s.n : s.n;
+      const int shift = s.two ? 1 : 0;
+      // S of job j: stage j & 1
+      auto scores = [&](int j) -> bool {
+        const int i = j >> shift, st = j & 1;
+        const uint32_t k = base + (uint32_t)k_index(i), slot = k % (uint32_t)nst;
+        const uint32_t qb = (qn + (s.two ? (uint32_t)st : 0u)) & 1u;
+        if (j < 2) {
+          const uint32_t qk = qn + (s.two ? (uint32_t)st : 0u);
+          if (!wait_warp(ctl.qfull + qb, (qk >> 1) & 1u, abort_flag, kWaitQ)) return false;
+        }
+        if (!wait_warp(ctl.full + slot, (k / (uint32_t)nst) & 1u, abort_flag, kWaitK)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t ad = umma_smem_desc(smem_u32(qbuf + qb * kQBytes), 16, 1024);
+          const uint64_t bd = umma_smem_desc(smem_u32(ring + (size_t)slot * stage_bytes), 16, 1024);
+          for (int kk = 0; kk < ksteps; ++kk) {
+            const uint64_t o = (uint64_t)((kk >> 2) * (kSpan >> 4) + (kk & 3) * 2);
+            umma_bf16(tbase + st * kTile, ad + o, bd + o, idesc_s, kk != 0);
+          }
+          umma_commit(ctl.sfull + st);
+          if (!s.two || st) umma_commit(ctl.empty + slot);
+          if (s.two ? i == s.n - 1 : j == s.n - 1) umma_commit(ctl.qempty + qb);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int j = 0; ok && j < 2 && j < jobs; ++j) ok = scores(j);
+      for (int j = 0; ok && j < jobs; ++j) {
+        const int i = j >> shift, st = j & 1;
+        const uint32_t k = base + (uint32_t)v_index(i, s.n), slot = k % (uint32_t)nst;
+        uint8_t* const vt = ring + (size_t)slot * stage_bytes;
+        if (!wait_warp(ctl.full + slot, (k / (uint32_t)nst) & 1u, abort_flag, kWaitV)) {
+          ok = false;
+          break;
+        }
+        // keys of the tile that somebody sees, in steps of 16
+        const int key0 = (s.t0 + i) * kTile;
+        const int v0 = max(0, s.lo - key0), v1 = min(kTile, s.hi - key0);
+        const int s0 = v0 / 16, s1 = max(s0, (v1 + 15) / 16);
+        if (!E4M3 && !(s.two && st) && ((v0 & 15) || (v1 & 15)) && v1 > v0) {
+          // rows of the first and last step that nobody sees may hold anything: zeros
+          const int pre = v0 - s0 * 16, post = s1 * 16 - v1;
+          const int chunks = t.nhalf * 8;
+          for (int e = lane; e < (pre + post) * chunks; e += 32) {
+            const int r = e / chunks, ch = e - r * chunks;
+            const int row = r < pre ? s0 * 16 + r : v1 + r - pre;
+            *reinterpret_cast<uint4*>(vt + (ch >> 3) * kSpan + row * 128 + (ch & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        if (!wait_warp(ctl.pfull + st, pph[st], abort_flag, kWaitP)) {
+          ok = false;
+          break;
+        }
+        pph[st] ^= 1u;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t bd = umma_smem_desc(smem_u32(vt), kSpan, 1024);
+          const bool fresh = s.two ? i == 0 : j < 2;
+          for (int kk = s0; kk < s1; ++kk)
+            umma_f16_ts(tbase + 256 + st * kTile, tbase + st * kTile + kk * 8,
+                        bd + (uint64_t)(kk * 128), idesc_o, !(fresh && kk == s0));
+          if (!s.two || st) umma_commit(ctl.empty + slot);
+          if (j + 2 >= jobs) umma_commit(ctl.ofull + st);
+        }
+        __syncwarp();
+        if (j + 2 < jobs) ok = scores(j + 2);
+      }
+      base += 2u * (uint32_t)s.n;
+      qn += s.two ? 2u : 1u;
+    }
+    // all products complete before tensor memory is released
+    if (lane == 0) {
+      umma_commit(&ctl.fin);
+      wait_end(&ctl.fin, 0);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------- fetch query tiles ----------------
+    const int th = (int)threadIdx.x - 64;  // 0..63: four rows of 16 chunks at a time
+    const int ch = th & 15;
+    const uint32_t sign = t.flip ? 0x80008000u : 0u;
+    uint32_t qn = 0;
+    if (th == 0) t.rec[wid].more = 0;
+    while (ok && walk.next(t, ctl, s)) {
+      if (th == 0 && s.slot == 1) t.rec[wid] = Rec{s.more, s.row0, s.ntok, s.h};
+      for (int st = 0; ok && st < (s.two ? 2 : 1); ++st, ++qn) {
+        const uint32_t qb = qn & 1u;
+        if (!wait_warp(ctl.qempty + qb, ((qn >> 1) & 1u) ^ 1u, abort_flag, kWaitQFree)) {
+          ok = false;
+          break;
+        }
+        const int tok = s.row0 + st * t.tpt;
+        const int rows = min(t.tpt, s.ntok - st * t.tpt) * t.group;
+        const char* src = a.q + (int64_t)s.h * t.group * a.q_head;
+        uint8_t* dst = qbuf + qb * kQBytes + (ch >> 3) * kSpan;
+        if (ch * 8 < D) {
+          int tk = (th >> 4) / t.group, hd = (th >> 4) - tk * t.group;
+          const int step_t = 4 / t.group, step_h = 4 - step_t * t.group;
+#pragma unroll 4
+          for (int r = th >> 4; r < rows; r += 4) {
+            uint4 x = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(tok + tk) * a.q_token +
+                                                           (int64_t)hd * a.q_head) + ch);
+            x.x ^= sign;
+            x.y ^= sign;
+            x.z ^= sign;
+            x.w ^= sign;
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+            tk += step_t;
+            hd += step_h;
+            if (hd >= t.group) {
+              hd -= t.group;
+              ++tk;
+            }
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ctl.qfull + qb);
+      }
+    }
+  } else if (warp < 12) {
+    // ---------------- softmax and output ----------------
+    const int st = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
+    const uint32_t lanes = tbase + ((uint32_t)(32 * quad) << 16);
+    const uint32_t s_tm = lanes + st * kTile, o_tm = lanes + 256 + st * kTile;
+    const int units = D / 16;
+    const int my_tok = row / t.group, my_head = row - my_tok * t.group;
+    uint32_t sph = 0, oph = 0, xph = 0;
+    while (ok && walk.next(t, ctl, s)) {
+      const int shift = s.two ? 0 : 1;
+      const int jobs = s.two ? s.n : (s.n + 1 - st) >> 1;
+      const int tok_off = s.two ? st * t.tpt : 0;
+      const int ntok = min(t.tpt, s.ntok - tok_off);
+      const bool live = my_tok < ntok;
+      const bool warp_live = 32 * quad < ntok * t.group;
+      const int pos = s.pos + tok_off + my_tok;
+      const int see1 = live ? pos + 1 : 0;  // keys [see0, see1)
+      const int see0 = a.window ? max(0, see1 - a.window) : 0;
+      float m = -kInf, l = 0.0f;
+      for (int k = 0; ok && k < jobs; ++k) {
+        if (!wait_warp(ctl.sfull + st, sph, abort_flag, kWaitS)) {
+          ok = false;
+          break;
+        }
+        sph ^= 1u;
+        tc_fence_after();
+        if (warp_live) {
+          const int key0 = (s.t0 + (shift ? 2 * k + st : k)) * kTile;
+          const int first = max(0, see0 - key0), span = max(0, min(kTile, see1 - key0) - first);
+          const bool masked = __any_sync(0xffffffffu, live && span < kTile);
+          const float tm = (masked ? row_max<true>(s_tm, first, span) : row_max<false>(s_tm, 0, 0)) *
+                               t.c - kShift;
+          const bool rise = tm > m + kLag || (m == -kInf && tm > m);
+          if (__any_sync(0xffffffffu, rise)) {
+            const float nm = rise ? tm : m;
+            if (k) {
+              const float f = rise ? ex2(m - nm) : 1.0f;
+              l *= f;
+              rescale(o_tm, units, f);
+            }
+            m = nm;
+          }
+          const float mu = m == -kInf ? 0.0f : m;
+          l += masked ? row_exp<kPT, true>(s_tm, first, span, t.c, mu)
+                      : row_exp<kPT, false>(s_tm, 0, 0, t.c, mu);
+          tmem_wait_st();
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ctl.pfull + st);
+      }
+      if (!ok) break;
+      if (jobs) {
+        if (!wait_warp(ctl.ofull + st, oph, abort_flag, kWaitO)) {
+          ok = false;
+          break;
+        }
+        oph ^= 1u;
+        tc_fence_after();
+      }
+      const int64_t prow = ((int64_t)(2 * wid + (s.slot > 0 ? 1 : 0)) * kMaxRows + (s.two ? st * kTile : 0) + row);
+      const int64_t orow = (int64_t)(s.row0 + tok_off + my_tok) * a.heads + s.h * t.group + my_head;
+      if (s.two) {
+        if (warp_live) {
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          for (int u = 0; u < units; ++u) {
+            uint32_t r[16];
+            float x[16];
+            __syncwarp();  // the lanes parted at the stores
+            tmem_ld16_async(o_tm + 16 * u, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              x[j] = __uint_as_float(r[j]);
+              if (s.slot < 0) x[j] = l == 0.0f ? 0.0f : x[j] * inv;
+            }
+            if (live) {
+              if (s.slot < 0) store16<DT>(a.out + (orow * D + 16 * u) * 2, x);
+              else store16f(t.part + prow * D + 16 * u, x);
+            }
+          }
+          if (live) {
+            if (s.slot < 0) {
+              if (a.lse) a.lse[orow] = lse_of(m, l);
+            } else {
+              t.ml[prow] = make_float2(m, l);
+            }
+          }
+        }
+      } else {
+        ctl.xch[st][row] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.xbar);
+        if (!wait_warp(&ctl.xbar, xph, abort_flag, kWaitX)) {
+          ok = false;
+          break;
+        }
+        xph ^= 1u;
+        tc_fence_after();
+        if (warp_live) {
+          const float2 p0 = ctl.xch[0][row], p1 = ctl.xch[1][row];
+          const float M = fmaxf(p0.x, p1.x);
+          const float f0 = p0.y == 0.0f ? 0.0f : ex2(p0.x - (M == -kInf ? 0.0f : M));
+          const float f1 = p1.y == 0.0f ? 0.0f : ex2(p1.x - (M == -kInf ? 0.0f : M));
+          const float L = (p0.y == 0.0f ? 0.0f : f0 * p0.y) + (p1.y == 0.0f ? 0.0f : f1 * p1.y);
+          const float inv = s.slot >= 0 ? 1.0f : (L == 0.0f ? 0.0f : 1.0f / L);
+          const int u0 = st ? (units + 1) / 2 : 0, u1 = st ? units : (units + 1) / 2;
+          for (int u = u0; u < u1; ++u) {
+            uint32_t r0[16], r1[16];
+            float x[16];
+            __syncwarp();  // the lanes parted at the stores
+            tmem_ld16_async(lanes + 256 + 16 * u, r0);
+            tmem_ld16_async(lanes + 256 + kTile + 16 * u, r1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              // a stage without keys left its O as it was: not read
+              const float y0 = p0.y == 0.0f ? 0.0f : f0 * __uint_as_float(r0[j]);
+              const float y1 = p1.y == 0.0f ? 0.0f : f1 * __uint_as_float(r1[j]);
+              x[j] = (y0 + y1) * inv;
+            }
+            if (live) {
+              if (s.slot < 0) store16<DT>(a.out + (orow * D + 16 * u) * 2, x);
+              else store16f(t.part + prow * D + 16 * u, x);
+            }
+          }
+          if (live && st == 0) {
+            if (s.slot < 0) {
+              if (a.lse) a.lse[orow] = lse_of(M, L);
+            } else {
+              t.ml[prow] = make_float2(M, L);
+            }
+          }
+        }
+        // the other warpgroup has read this stage's O and (m, l)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.xbar);
+        if (!wait_warp(&ctl.xbar, xph, abort_flag, kWaitX)) {
+          ok = false;
+          break;
+        }
+        xph ^= 1u;
+        tc_fence_after();
+      }
+    }
+  } else if (E4M3) {
+    // ---------------- widen e4m3 codes ----------------
+    const int cw = warp - 12, ch = lane & 7, g = lane >> 3;  // 16 codes each, four rows at a time
+    uint32_t k = 0;
+    while (ok && walk.next(t, ctl, s)) {
+      for (int idx = 0; ok && idx < 2 * s.n; ++idx, ++k) {
+        bool is_v;
+        int tile;
+        tile_of(idx, s.n, is_v, tile);
+        const int key0 = (s.t0 + tile) * kTile;
+        const uint32_t rs = k % (uint32_t)nraw, slot = k % (uint32_t)nst;
+        if (!wait_warp(ctl.rawfull + rs, (k / (uint32_t)nraw) & 1u, abort_flag, kWaitRaw) ||
+            !wait_warp(ctl.empty + slot, ((k / (uint32_t)nst) & 1u) ^ 1u, abort_flag, kWaitWide)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = raw + (size_t)rs * raw_bytes;
+        uint8_t* dst = ring + (size_t)slot * stage_bytes + (ch >> 2) * kSpan;
+        const uint32_t scale = src[kTile * D + 32 * cw + lane];
+        const int c0 = (ch & 3) * 2;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int r = 32 * cw + 4 * p + g;
+          const float f = scale_of(__shfl_sync(0xffffffffu, scale, 4 * p + g));
+          const bool seen = key0 + r >= s.lo && key0 + r < s.hi;
+          if (ch * 16 < D) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (seen) x = *reinterpret_cast<const uint4*>(src + r * D + ch * 16);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 u = e4m3x2((uint16_t)w[j]), v = e4m3x2((uint16_t)(w[j] >> 16));
+              // rows that nobody sees are zeros whatever their scale
+              o[2 * j] = seen ? F16<DT>::down(u.x * f, u.y * f) : 0u;
+              o[2 * j + 1] = seen ? F16<DT>::down(v.x * f, v.y * f) : 0u;
+            }
+            const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
+            // the two spans' lanes write opposite chunks at a time (no bank conflict)
+            const int c1 = ch < 4 ? c0 : c0 + 1, c2 = ch < 4 ? c0 + 1 : c0;
+            *reinterpret_cast<uint4*>(dst + r * 128 + ((c1 ^ (r & 7)) << 4)) = ch < 4 ? lo4 : hi4;
+            *reinterpret_cast<uint4*>(dst + r * 128 + ((c2 ^ (r & 7)) << 4)) = ch < 4 ? hi4 : lo4;
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(ctl.full + slot);
+          mbar_arrive(ctl.rawempty + rs);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, 512);
+  if (threadIdx.x == 0) t.err[wid] = ctl.abort;
+}
+
+// ---------------------------------------------------------------------------
+// The join: items cut by a share's end, and the flags.
+// ---------------------------------------------------------------------------
+// One row from its parts: a warp takes every `stride`-th part from `first` on and
+// returns this lane's four columns (scaled to the maximum M of all parts).
+__device__ __forceinline__ float4 join_parts(const TileArgs& t, int c, int parts, int r, float M,
+                                             int first, int stride, float& L) {
+  const int lane = threadIdx.x & 31, D = t.a.c.head_dim;
+  float4 o = make_float4(0, 0, 0, 0);
+  L = 0.0f;
+#pragma unroll 4
+  for (int p = first; p < parts; p += stride) {
+    const int slot = p ? 2 * (c + p) : 2 * c + 1;
+    const int64_t at = (int64_t)slot * kMaxRows + r;
+    const float2 ml = __ldcg(t.ml + at);
+    if (ml.y == 0.0f) continue;  // sees nothing of that part
+    const float f = ex2(ml.x - M);
+    L += f * ml.y;
+    if (lane * 4 < D) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(t.part + at * D) + lane);
+      o.x += f * x.x;
+      o.y += f * x.y;
+      o.z += f * x.z;
+      o.w += f * x.w;
+    }
+  }
+  return o;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ TileArgs t,
+                                                              int ctas, int join_blocks) {
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ Rec rec[kMaxCtas];
+  __shared__ int rows_to[kMaxCtas];  // rows of records 0..c
+  __shared__ int warp_rows[kWarps];
+  __shared__ int most;
+  __shared__ float4 so[kWarps][32];
+  __shared__ float sl[kWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const AttendArgs& a = t.a;
+  if ((int)blockIdx.x >= join_blocks) {
+    const int b = ((int)blockIdx.x - join_blocks) * kWarps + warp;
+    if (b >= a.b.B) return;
+    bool late = false;
+    for (int c = lane; c < ctas; c += 32) late |= __ldcg(t.err + c) != 0;
+    late = __any_sync(0xffffffffu, late);
+    const uint8_t f = sequence_flags(a, b);
+    if (lane == 0) a.flags[b] = f | (late ? SV_FLAG_TIMEOUT : 0);
+    return;
+  }
+  // records, and the rows before each (kMaxCtas <= kJoinThreads)
+  static_assert(kMaxCtas <= kJoinThreads, "one record per thread");
+  if (threadIdx.x == 0) most = 0;
+  __syncthreads();
+  int n = 0;
+  if ((int)threadIdx.x < ctas) {
+    const Rec r = t.rec[threadIdx.x];
+    rec[threadIdx.x] = r;
+    n = r.more ? r.ntok * t.group : 0;
+    if (r.more) atomicMax(&most, r.more);
+  }
+  int scan = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) warp_rows[warp] = scan;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) scan += warp_rows[w];
+  if (threadIdx.x < kMaxCtas) rows_to[threadIdx.x] = scan;
+  __syncthreads();
+  const int total = rows_to[kMaxCtas - 1];
+  // few rows of many parts: a whole block to a row; else a warp to a row
+  const bool wide = most >= 8 && total <= 4 * join_blocks;
+  const int step = wide ? join_blocks : join_blocks * kWarps;
+  for (int j = wide ? (int)blockIdx.x : (int)blockIdx.x * kWarps + warp; j < total; j += step) {
+    int c = 0;
+    for (int half = 128; half; half >>= 1)
+      if (c + half <= ctas && rows_to[c + half - 1] <= j) c += half;
+    const Rec r = rec[c];
+    const int k = j - (c ? rows_to[c - 1] : 0);
+    const int tok = k / t.group, hd = k - tok * t.group;
+    const int row = tok / t.tpt * kTile + tok % t.tpt * t.group + hd;
+    const int parts = r.more + 1;
+    float M = -kInf;
+    for (int p = lane; p < parts; p += 32) {
+      const int slot = p ? 2 * (c + p) : 2 * c + 1;
+      M = fmaxf(M, __ldcg(t.ml + (int64_t)slot * kMaxRows + row).x);
+    }
+    M = warp_max(M);
+    if (M == -kInf) M = 0.0f;
+    float L;
+    float4 o = join_parts(t, c, parts, row, M, wide ? warp : 0, wide ? kWarps : 1, L);
+    if (wide) {
+      __syncthreads();
+      so[warp][lane] = o;
+      if (lane == 0) sl[warp] = L;
+      __syncthreads();
+      if (warp) continue;
+      for (int w = 1; w < kWarps; ++w) {
+        const float4 x = so[w][lane];
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
+        L += sl[w];
+      }
+    }
+    const int64_t orow = (int64_t)(r.row0 + tok) * a.heads + r.h * t.group + hd;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const int D = a.c.head_dim;
+    if (lane * 4 < D) {
+      const uint2 w = make_uint2(F16<DT>::down(o.x * inv, o.y * inv),
+                                 F16<DT>::down(o.z * inv, o.w * inv));
+      reinterpret_cast<uint2*>(a.out + orow * D * 2)[lane] = w;
+    }
+    if (lane == 0 && a.lse) a.lse[orow] = lse_of(M, L);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+std::mutex g_mu;
+EncodeTiled g_encode = nullptr;
+int g_sms[64] = {};
+
+cudaError_t device_ready(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!g_encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q);
+    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<EncodeTiled>(fn);
+  }
+  if (!g_sms[dev]) {
+    const int smem = (int)kSmemBytes;
+    for (const void* k : {(const void*)k_attend_tiles<SV_BF16, false>,
+                          (const void*)k_attend_tiles<SV_F16, false>,
+                          (const void*)k_attend_tiles<SV_BF16, true>,
+                          (const void*)k_attend_tiles<SV_F16, true>}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+    }
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    g_sms[dev] = n;
+  }
+  *sms = g_sms[dev];
+  return cudaSuccess;
+}
+
+// A pool [pages][kv_heads][page_size][dim] by its strides (in bytes), one box of
+// `span` entries and `box` tokens at a time.
+bool encode_pool(CUtensorMap* map, const CacheView& c, const void* base, CUtensorMapDataType type,
+                 CUtensorMapSwizzle swizzle, int span, int box) {
+  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
+                              (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
+  // a dimension of one entry is never stepped along: any legal stride will do
+  const cuuint64_t strides[3] = {(cuuint64_t)c.token_bytes,
+                                 (cuuint64_t)(c.kv_heads > 1 ? c.head_bytes : c.token_bytes),
+                                 (cuuint64_t)(c.num_pages > 1 ? c.page_bytes : c.token_bytes)};
+  const cuuint32_t bx[4] = {(cuuint32_t)span, (cuuint32_t)box, 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return g_encode(map, type, 4, const_cast<void*>(base), dims, strides, bx, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kRecBytes = 4096, kMlBytes = sizeof(float2) * 2 * kMaxCtas * kMaxRows;
+static_assert(kMaxCtas * (sizeof(Rec) + sizeof(int)) <= kRecBytes, "records");
+
+}  // namespace
+
+size_t attention_tiles_workspace(int head_dim) {
+  return kRecBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * (size_t)head_dim;
+}
+
+cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream,
+                                   bool* taken) {
+  int sms = 0;
+  cudaError_t e = device_ready(&sms);
+  if (e != cudaSuccess) return e;
+  const CacheView& c = a.c;
+  TileArgs t{};
+  t.a = a;
+  t.group = a.heads / c.kv_heads;
+  t.tpt = kTile / t.group;
+  t.nhalf = c.head_dim > 64 ? 2 : 1;
+  t.nst = (e4m3 ? kRing8 : kRing16) / (t.nhalf * kSpan);
+  t.nraw = kRaw8 / (kTile * (c.head_dim + 1));
+  if (t.nraw > kMaxRaw) t.nraw = kMaxRaw;
+  t.box = c.page_size < kTile ? c.page_size : kTile;
+  t.flip = a.scale_log2 < 0.0f;
+  // a scale of zero: every product times 1e-30 is zero beside 1, and the -inf of a
+  // key that is not seen stays one
+  t.c = a.scale_log2 == 0.0f ? 1e-30f : (t.flip ? -a.scale_log2 : a.scale_log2);
+  t.rec = reinterpret_cast<Rec*>(a.ws);
+  t.err = reinterpret_cast<int*>(a.ws + kMaxCtas * sizeof(Rec));
+  t.ml = reinterpret_cast<float2*>(a.ws + kRecBytes);
+  t.part = reinterpret_cast<float*>(a.ws + kRecBytes + kMlBytes);
+  alignas(64) CUtensorMap mk{}, mv{};
+  if (e4m3) {
+    *taken = encode_pool(&mk, c, c.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE,
+                         c.head_dim, t.box) &&
+             encode_pool(&mv, c, c.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE,
+                         c.head_dim, t.box);
+  } else {
+    *taken = encode_pool(&mk, c, c.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         CU_TENSOR_MAP_SWIZZLE_128B, 64, t.box) &&
+             encode_pool(&mv, c, c.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         CU_TENSOR_MAP_SWIZZLE_128B, 64, t.box);
+  }
+  if (!*taken) return cudaSuccess;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  auto* k = dtype == SV_BF16 ? (e4m3 ? k_attend_tiles<SV_BF16, true> : k_attend_tiles<SV_BF16, false>)
+                             : (e4m3 ? k_attend_tiles<SV_F16, true> : k_attend_tiles<SV_F16, false>);
+  e = launch_pdl(k, dim3(ctas), dim3(e4m3 ? 512 : 384), kSmemBytes, stream, mk, mv, t);
+  if (e != cudaSuccess) return e;
+  const int join_blocks = 2 * ctas;
+  const int flag_blocks = a.flags ? (a.b.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
+  auto* j = dtype == SV_BF16 ? k_attend_join<SV_BF16> : k_attend_join<SV_F16>;
+  return launch_pdl(j, dim3(join_blocks + flag_blocks), dim3(kJoinThreads), 0, stream, t, ctas,
+                    join_blocks);
+}
+
+}  // namespace sv
