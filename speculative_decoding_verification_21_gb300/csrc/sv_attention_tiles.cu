@@ -69,6 +69,7 @@ struct TileArgs {
   int group, tpt;      // query heads per key head; tokens per row tile
   int nhalf;           // swizzle spans per row: 1 (head_dim <= 64) or 2
   int nst, nraw;       // ring slots
+  uint32_t inv_nst, inv_nraw;  // ceil(2^32 / slots): slot and turn of tile k without a division
   int box;             // tokens per copy: min(page_size, 128)
   int flip;            // negative scale: the queries' signs are flipped
   float c;             // |scale| log2 e
@@ -302,6 +303,26 @@ __device__ __forceinline__ void tile_of(int idx, int n, bool& is_v, int& tile) {
   tile = is_v ? (idx == 2 * n - 1 ? n - 1 : idx / 2 - 1) : (idx + 1) / 2;
 }
 
+// Slot and phase of the k-th tile of a ring of n slots (k < 2^32 / n / 10).
+struct Slot {
+  uint32_t i, ph;
+  __device__ __forceinline__ Slot(uint32_t k, uint32_t n, uint32_t inv) {
+    const uint32_t turn = __umulhi(k, inv);
+    i = k - turn * n;
+    ph = turn & 1u;
+  }
+};
+
+// A value that is the same in all lanes, in a form that the compiler knows to be.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// Keys of a tile that some row sees, in steps of 16 (a product's depth).
+__device__ __forceinline__ void key_steps(int lo, int hi, int tile, int& s0, int& s1) {
+  const int key0 = tile * kTile;
+  s0 = max(0, lo - key0) / 16;
+  s1 = max(s0, (min(kTile, hi - key0) + 15) / 16);
+}
+
 // ---------------------------------------------------------------------------
 // Waits.
 // ---------------------------------------------------------------------------
@@ -309,28 +330,20 @@ __device__ __forceinline__ void tile_of(int idx, int n, bool& is_v, int& tile) {
 enum WaitId { kWaitSlot = 1, kWaitQ, kWaitK, kWaitV, kWaitP, kWaitQFree, kWaitS, kWaitO, kWaitX, kWaitRaw,
               kWaitWide };
 
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                         int id) {
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (clock64() - t0 < kWaitClocks) {
-    for (int i = 0; i < 16; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-  }
-  *abort_flag = id;
-  return false;
-}
-// A whole warp: lane 0 polls and decides for all lanes (a lane that tested the
-// barrier for itself could find it a phase further on and part from the others).
+// A whole warp.  All lanes test and go on together: one that went ahead could let
+// the barrier move a phase further before another tests it.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           int id) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = wait_one(bar, parity, abort_flag, id);
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  __syncwarp();
-  return ok != 0;
+  for (int i = 0; i < 64; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const bool late = clock64() - t0 >= kWaitClocks;
+    if (__any_sync(0xffffffffu, late)) *abort_flag = id;
+    if (__any_sync(0xffffffffu, late || *abort_flag != 0)) return false;
+  }
 }
 // What must have ended before the CTA may go, whether or not the call is aborted.
 __device__ __forceinline__ void wait_end(uint64_t* bar, uint32_t parity) {
@@ -343,22 +356,25 @@ __device__ __forceinline__ void wait_end(uint64_t* bar, uint32_t parity) {
 // Softmax of one S tile row (this thread's), 128 scores in tensor memory.
 // ---------------------------------------------------------------------------
 // Scores that the row does not see become -inf; the row sees columns [first, first+span).
+// Both passes are loops of 64 columns: straight-line code for all 128 would not
+// stay in the instruction caches beside the other roles'.
 template <bool MASK>
 __device__ __forceinline__ float row_max(uint32_t s_tm, int first, int span) {
-  float m = -kInf;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t r[32];
-    tmem_ld32_async(s_tm + 32 * k, r);
+  float m[4] = {-kInf, -kInf, -kInf, -kInf};
+#pragma unroll 1
+  for (int k = 0; k < kTile; k += 64) {
+    uint32_t r[64];
+    tmem_ld32_async(s_tm + k, r);
+    tmem_ld32_async(s_tm + k + 32, r + 32);
     tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < 64; ++j) {
       float s = __uint_as_float(r[j]);
-      if (MASK) s = (unsigned)(32 * k + j - first) < (unsigned)span ? s : -kInf;
-      m = fmaxf(m, s);
+      if (MASK) s = (unsigned)(k + j - first) < (unsigned)span ? s : -kInf;
+      m[j & 3] = fmaxf(m[j & 3], s);
     }
   }
-  return m;
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 // P = 2^(c s - m), written over S as pairs of 16-bit floats; returns the row sum.
@@ -366,26 +382,28 @@ template <int PT, bool MASK>
 __device__ __forceinline__ float row_exp(uint32_t s_tm, int first, int span, float c, float m) {
   const uint64_t cc = pack2(c, c), mm = pack2(-m, -m);
   uint64_t acc0 = pack2(0.0f, 0.0f), acc1 = acc0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t r[32], w[16];
-    tmem_ld32_async(s_tm + 32 * k, r);
+#pragma unroll 1
+  for (int k = 0; k < kTile; k += 64) {
+    uint32_t r[64], w[16];
+    tmem_ld32_async(s_tm + k, r);
+    tmem_ld32_async(s_tm + k + 32, r + 32);
     tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < 32; ++j) {
       float x, y;
       unpack2(ffma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), cc, mm), x, y);
       x = ex2(x);
       y = ex2(y);
       if (MASK) {
-        x = (unsigned)(32 * k + 2 * j - first) < (unsigned)span ? x : 0.0f;
-        y = (unsigned)(32 * k + 2 * j + 1 - first) < (unsigned)span ? y : 0.0f;
+        x = (unsigned)(k + 2 * j - first) < (unsigned)span ? x : 0.0f;
+        y = (unsigned)(k + 2 * j + 1 - first) < (unsigned)span ? y : 0.0f;
       }
       if (j & 1) acc1 = fadd2(acc1, pack2(x, y));
       else acc0 = fadd2(acc0, pack2(x, y));
-      w[j] = F16<PT>::down(x, y);
+      w[j & 15] = F16<PT>::down(x, y);
+      // columns k/2 .. of P lie over scores that were read in this or an earlier pass
+      if ((j & 15) == 15) tmem_st16(s_tm + k / 2 + (j & 16), w);
     }
-    tmem_st16(s_tm + 16 * k, w);
   }
   float a, b, d, e;
   unpack2(acc0, a, b);
@@ -501,8 +519,8 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         const int mine = key0 + part * t.box;
         int page = -1;
         if (part >= from && part < upto) page = __ldg(table + (mine >> a.c.page_shift));
-        const uint32_t ns = E4M3 ? nraw : nst;
-        const uint32_t slot = issued % ns, ph = (issued / ns) & 1u;
+        const Slot at(issued, (uint32_t)(E4M3 ? nraw : nst), E4M3 ? t.inv_nraw : t.inv_nst);
+        const uint32_t slot = at.i, ph = at.ph;
         uint64_t* const fullb = (E4M3 ? ctl.rawfull : ctl.full) + slot;
         if (!wait_warp((E4M3 ? ctl.rawempty : ctl.empty) + slot, ph ^ 1u, abort_flag, kWaitSlot)) {
           ok = false;
@@ -549,92 +567,73 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
   } else if (warp == 1) {
     // ---------------- issue the products ----------------
+    const uint32_t leader = elect_leader();
     const uint32_t idesc_s = umma_idesc_16(DT == SV_BF16, kTile, kTile, false);
     const uint32_t idesc_o = umma_idesc_16(kPT == SV_BF16, kTile, D, true);
     const int ksteps = D / 16;
+    const uint64_t qdesc = umma_smem_desc(smem_u32(qbuf), 16, 1024);
+    const uint64_t kdesc = umma_smem_desc(smem_u32(ring), 16, 1024);
+    const uint64_t vdesc = umma_smem_desc(smem_u32(ring), kSpan, 1024);
+    const uint32_t stage16 = (uint32_t)stage_bytes >> 4, tb = (uint32_t)uniform((int)tbase);
     uint32_t base = 0, qn = 0;          // tiles and query tiles used so far
-    uint32_t pph[2] = {0, 0};
+    uint32_t pph0 = 0, pph1 = 0;
     while (ok && walk.next(t, ctl, s)) {
-      const int jobs = s.two ? 2 * s.n : s.n;
-      const int shift = s.two ? 1 : 0;
+      const int n = uniform(s.n), two = uniform(s.two ? 1 : 0);
+      const int lo = uniform(s.lo), hi = uniform(s.hi), t0 = uniform(s.t0);
+      const int jobs = n << two;
       // S of job j: stage j & 1
       auto scores = [&](int j) -> bool {
-        const int i = j >> shift, st = j & 1;
-        const uint32_t k = base + (uint32_t)k_index(i), slot = k % (uint32_t)nst;
-        const uint32_t qb = (qn + (s.two ? (uint32_t)st : 0u)) & 1u;
-        if (j < 2) {
-          const uint32_t qk = qn + (s.two ? (uint32_t)st : 0u);
-          if (!wait_warp(ctl.qfull + qb, (qk >> 1) & 1u, abort_flag, kWaitQ)) return false;
-        }
-        if (!wait_warp(ctl.full + slot, (k / (uint32_t)nst) & 1u, abort_flag, kWaitK)) return false;
+        const int i = j >> two, st = j & 1;
+        const Slot k(base + (uint32_t)k_index(i), (uint32_t)nst, t.inv_nst);
+        const uint32_t qk = qn + (uint32_t)(two & st), qb = qk & 1u;
+        if (j < 2 && !wait_warp(ctl.qfull + qb, (qk >> 1) & 1u, abort_flag, kWaitQ)) return false;
+        if (!wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK)) return false;
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t ad = umma_smem_desc(smem_u32(qbuf + qb * kQBytes), 16, 1024);
-          const uint64_t bd = umma_smem_desc(smem_u32(ring + (size_t)slot * stage_bytes), 16, 1024);
-          for (int kk = 0; kk < ksteps; ++kk) {
-            const uint64_t o = (uint64_t)((kk >> 2) * (kSpan >> 4) + (kk & 3) * 2);
-            umma_bf16(tbase + st * kTile, ad + o, bd + o, idesc_s, kk != 0);
-          }
-          umma_commit(ctl.sfull + st);
-          if (!s.two || st) umma_commit(ctl.empty + slot);
-          if (s.two ? i == s.n - 1 : j == s.n - 1) umma_commit(ctl.qempty + qb);
+        const uint64_t ad = qdesc + qb * (kQBytes >> 4), bd = kdesc + k.i * stage16;
+        const uint32_t acc = tb + st * kTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t o = (uint64_t)((kk >> 2) * (kSpan >> 4) + (kk & 3) * 2);
+          if (kk < ksteps) umma_ss_if(leader, acc, ad + o, bd + o, idesc_s, kk != 0);
         }
-        __syncwarp();
+        umma_commit_if(leader, ctl.sfull + st);  // the softmax then frees the key and query tiles
         return true;
       };
       for (int j = 0; ok && j < 2 && j < jobs; ++j) ok = scores(j);
       for (int j = 0; ok && j < jobs; ++j) {
-        const int i = j >> shift, st = j & 1;
-        const uint32_t k = base + (uint32_t)v_index(i, s.n), slot = k % (uint32_t)nst;
-        uint8_t* const vt = ring + (size_t)slot * stage_bytes;
-        if (!wait_warp(ctl.full + slot, (k / (uint32_t)nst) & 1u, abort_flag, kWaitV)) {
+        const int i = j >> two, st = j & 1;
+        const Slot k(base + (uint32_t)v_index(i, n), (uint32_t)nst, t.inv_nst);
+        if (!wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitV) ||
+            !wait_warp(ctl.pfull + st, st ? pph1 : pph0, abort_flag, kWaitP)) {
           ok = false;
           break;
         }
-        // keys of the tile that somebody sees, in steps of 16
-        const int key0 = (s.t0 + i) * kTile;
-        const int v0 = max(0, s.lo - key0), v1 = min(kTile, s.hi - key0);
-        const int s0 = v0 / 16, s1 = max(s0, (v1 + 15) / 16);
-        if (!E4M3 && !(s.two && st) && ((v0 & 15) || (v1 & 15)) && v1 > v0) {
-          // rows of the first and last step that nobody sees may hold anything: zeros
-          const int pre = v0 - s0 * 16, post = s1 * 16 - v1;
-          const int chunks = t.nhalf * 8;
-          for (int e = lane; e < (pre + post) * chunks; e += 32) {
-            const int r = e / chunks, ch = e - r * chunks;
-            const int row = r < pre ? s0 * 16 + r : v1 + r - pre;
-            *reinterpret_cast<uint4*>(vt + (ch >> 3) * kSpan + row * 128 + (ch & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async();
-          __syncwarp();
-        }
-        if (!wait_warp(ctl.pfull + st, pph[st], abort_flag, kWaitP)) {
-          ok = false;
-          break;
-        }
-        pph[st] ^= 1u;
+        if (st) pph1 ^= 1u;
+        else pph0 ^= 1u;
         tc_fence_after();
-        if (lane == 0) {
-          const uint64_t bd = umma_smem_desc(smem_u32(vt), kSpan, 1024);
-          const bool fresh = s.two ? i == 0 : j < 2;
+        int s0, s1;
+        key_steps(lo, hi, t0 + i, s0, s1);
+        const uint64_t bd = vdesc + k.i * stage16;
+        const uint32_t acc = tb + 256 + st * kTile, p = tb + st * kTile;
+        const bool fresh = two ? i == 0 : j < 2;
+        if (s0 == 0 && s1 == 8) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts_if(leader, acc, p + kk * 8, bd + (uint64_t)(kk * 128), idesc_o, kk || !fresh);
+        } else {
           for (int kk = s0; kk < s1; ++kk)
-            umma_f16_ts(tbase + 256 + st * kTile, tbase + st * kTile + kk * 8,
-                        bd + (uint64_t)(kk * 128), idesc_o, !(fresh && kk == s0));
-          if (!s.two || st) umma_commit(ctl.empty + slot);
-          if (j + 2 >= jobs) umma_commit(ctl.ofull + st);
+            umma_ts_if(leader, acc, p + kk * 8, bd + (uint64_t)(kk * 128), idesc_o, kk != s0 || !fresh);
         }
-        __syncwarp();
+        if (!two || st) umma_commit_if(leader, ctl.empty + k.i);
+        if (j + 2 >= jobs) umma_commit_if(leader, ctl.ofull + st);
         if (j + 2 < jobs) ok = scores(j + 2);
       }
-      base += 2u * (uint32_t)s.n;
-      qn += s.two ? 2u : 1u;
+      base += 2u * (uint32_t)n;
+      qn += 1u + (uint32_t)two;
     }
     // all products complete before tensor memory is released
-    if (lane == 0) {
-      umma_commit(&ctl.fin);
-      wait_end(&ctl.fin, 0);
-    }
-    __syncwarp();
+    umma_commit_if(leader, &ctl.fin);
+    wait_end(&ctl.fin, 0);
   } else if (warp < 4) {
     // ---------------- fetch query tiles ----------------
     const int th = (int)threadIdx.x - 64;  // 0..63: four rows of 16 chunks at a time
@@ -687,7 +686,8 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     const int units = D / 16;
     const int my_tok = row / t.group, my_head = row - my_tok * t.group;
     uint32_t sph = 0, oph = 0, xph = 0;
-    while (ok && walk.next(t, ctl, s)) {
+    uint32_t base = 0, qn = 0;  // tiles and query tiles of the parts before
+    for (; ok && walk.next(t, ctl, s); base += 2u * (uint32_t)s.n, qn += s.two ? 2u : 1u) {
       const int shift = s.two ? 0 : 1;
       const int jobs = s.two ? s.n : (s.n + 1 - st) >> 1;
       const int tok_off = s.two ? st * t.tpt : 0;
@@ -705,8 +705,15 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         }
         sph ^= 1u;
         tc_fence_after();
+        const int i = shift ? 2 * k + st : k;  // key tile
+        if (quad == 0 && lane == 0) {  // S is done with its key tile, the last S with the queries
+          if (!s.two || st)
+            mbar_arrive(ctl.empty + Slot(base + (uint32_t)k_index(i), (uint32_t)nst, t.inv_nst).i);
+          if (i == s.n - 1) mbar_arrive(ctl.qempty + ((qn + (uint32_t)(s.two ? st : 0)) & 1u));
+        }
+        __syncwarp();
         if (warp_live) {
-          const int key0 = (s.t0 + (shift ? 2 * k + st : k)) * kTile;
+          const int key0 = (s.t0 + i) * kTile;
           const int first = max(0, see0 - key0), span = max(0, min(kTile, see1 - key0) - first);
           const bool masked = __any_sync(0xffffffffu, live && span < kTile);
           const float tm = (masked ? row_max<true>(s_tm, first, span) : row_max<false>(s_tm, 0, 0)) *
@@ -725,6 +732,28 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
           l += masked ? row_exp<kPT, true>(s_tm, first, span, t.c, mu)
                       : row_exp<kPT, false>(s_tm, 0, 0, t.c, mu);
           tmem_wait_st();
+        }
+        if (!E4M3 && !(s.two && st)) {
+          // value rows of the first and last step that nobody sees may hold anything:
+          // zeros (their P is 0, but 0 times infinity is not)
+          const int key0 = (s.t0 + i) * kTile;
+          const int v0 = max(0, s.lo - key0), v1 = min(kTile, s.hi - key0);
+          if (((v0 | v1) & 15) && v1 > v0) {
+            const Slot vk(base + (uint32_t)v_index(i, s.n), (uint32_t)nst, t.inv_nst);
+            if (!wait_warp(ctl.full + vk.i, vk.ph, abort_flag, kWaitV)) {
+              ok = false;
+              break;
+            }
+            uint8_t* const vt = ring + (size_t)vk.i * stage_bytes;
+            const int pre = v0 & 15, post = -v1 & 15, chunks = t.nhalf * 8;
+            for (int e = row; e < (pre + post) * chunks; e += kTile) {
+              const int r = e / chunks, ch = e - r * chunks;
+              const int vr = r < pre ? v0 - pre + r : v1 + r - pre;
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * kSpan + vr * 128 + (ch & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();
+          }
         }
         __syncwarp();
         tc_fence_before();
@@ -837,38 +866,47 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         int tile;
         tile_of(idx, s.n, is_v, tile);
         const int key0 = (s.t0 + tile) * kTile;
-        const uint32_t rs = k % (uint32_t)nraw, slot = k % (uint32_t)nst;
-        if (!wait_warp(ctl.rawfull + rs, (k / (uint32_t)nraw) & 1u, abort_flag, kWaitRaw) ||
-            !wait_warp(ctl.empty + slot, ((k / (uint32_t)nst) & 1u) ^ 1u, abort_flag, kWaitWide)) {
+        const Slot from(k, (uint32_t)nraw, t.inv_nraw), to(k, (uint32_t)nst, t.inv_nst);
+        const uint32_t rs = from.i, slot = to.i;
+        if (!wait_warp(ctl.rawfull + rs, from.ph, abort_flag, kWaitRaw) ||
+            !wait_warp(ctl.empty + slot, to.ph ^ 1u, abort_flag, kWaitWide)) {
           ok = false;
           break;
         }
-        const uint8_t* src = raw + (size_t)rs * raw_bytes;
-        uint8_t* dst = ring + (size_t)slot * stage_bytes + (ch >> 2) * kSpan;
-        const uint32_t scale = src[kTile * D + 32 * cw + lane];
-        const int c0 = (ch & 3) * 2;
+        const uint8_t* src = raw + (size_t)rs * raw_bytes + (32 * cw + g) * D + ch * 16;
+        uint8_t* dst = ring + (size_t)slot * stage_bytes + (ch >> 2) * kSpan + (32 * cw + g) * 128;
+        const uint32_t scale = raw[(size_t)rs * raw_bytes + kTile * D + 32 * cw + lane];
+        // rows 32 cw + 4 p + g; only the part's first and last tiles hold rows that
+        // nobody sees: those become zeros whatever they hold
+        const int row0 = key0 + 32 * cw;
+        const bool edge = row0 < s.lo || row0 + 32 > s.hi;
+        const bool on = ch * 16 < D;
+        uint4 x[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          x[p] = on ? *reinterpret_cast<const uint4*>(src + 4 * p * D) : make_uint4(0, 0, 0, 0);
+        // the two spans' lanes write opposite chunks at a time (no bank conflict)
+        const int c1 = (ch & 3) * 2 + (ch < 4 ? 0 : 1), c2 = c1 ^ 1;
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-          const int r = 32 * cw + 4 * p + g;
           const float f = scale_of(__shfl_sync(0xffffffffu, scale, 4 * p + g));
-          const bool seen = key0 + r >= s.lo && key0 + r < s.hi;
-          if (ch * 16 < D) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (seen) x = *reinterpret_cast<const uint4*>(src + r * D + ch * 16);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t o[8];
+          const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+          uint32_t o[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 u = e4m3x2((uint16_t)w[j]), v = e4m3x2((uint16_t)(w[j] >> 16));
-              // rows that nobody sees are zeros whatever their scale
-              o[2 * j] = seen ? F16<DT>::down(u.x * f, u.y * f) : 0u;
-              o[2 * j + 1] = seen ? F16<DT>::down(v.x * f, v.y * f) : 0u;
-            }
+          for (int j = 0; j < 4; ++j) {
+            const float2 u = e4m3x2((uint16_t)w[j]), v = e4m3x2((uint16_t)(w[j] >> 16));
+            o[2 * j] = F16<DT>::down(u.x * f, u.y * f);
+            o[2 * j + 1] = F16<DT>::down(v.x * f, v.y * f);
+          }
+          if (edge && !(row0 + 4 * p + g >= s.lo && row0 + 4 * p + g < s.hi)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = 0;
+          }
+          if (on) {
             const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
-            // the two spans' lanes write opposite chunks at a time (no bank conflict)
-            const int c1 = ch < 4 ? c0 : c0 + 1, c2 = ch < 4 ? c0 + 1 : c0;
-            *reinterpret_cast<uint4*>(dst + r * 128 + ((c1 ^ (r & 7)) << 4)) = ch < 4 ? lo4 : hi4;
-            *reinterpret_cast<uint4*>(dst + r * 128 + ((c2 ^ (r & 7)) << 4)) = ch < 4 ? hi4 : lo4;
+            const int sw = (4 * p + g) & 7;  // 32 cw leaves the row's swizzle alone
+            *reinterpret_cast<uint4*>(dst + 4 * p * 128 + ((c1 ^ sw) << 4)) = ch < 4 ? lo4 : hi4;
+            *reinterpret_cast<uint4*>(dst + 4 * p * 128 + ((c2 ^ sw) << 4)) = ch < 4 ? hi4 : lo4;
           }
         }
         fence_proxy_async();
@@ -1096,6 +1134,8 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
   t.nst = (e4m3 ? kRing8 : kRing16) / (t.nhalf * kSpan);
   t.nraw = kRaw8 / (kTile * (c.head_dim + 1));
   if (t.nraw > kMaxRaw) t.nraw = kMaxRaw;
+  t.inv_nst = (uint32_t)((0x100000000ull + t.nst - 1) / t.nst);
+  t.inv_nraw = (uint32_t)((0x100000000ull + t.nraw - 1) / t.nraw);
   t.box = c.page_size < kTile ? c.page_size : kTile;
   t.flip = a.scale_log2 < 0.0f;
   // a scale of zero: every product times 1e-30 is zero beside 1, and the -inf of a
