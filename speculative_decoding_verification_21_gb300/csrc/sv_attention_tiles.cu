@@ -23,7 +23,7 @@
 //
 // Roles: warp 0 fetches key and value pages (tensor copies, 128-byte swizzle),
 // warp 1 issues the products, warps 2-3 fetch queries, warps 4-11 are the softmax,
-// and for e4m3 caches warps 12-15 widen the codes to 16 bits between the copies
+// and for e4m3 caches warps 12-19 widen the codes to 16 bits between the copies
 // and the products.  Every wait is bounded; one that gives up ends the CTA's roles
 // and flags the call.
 //
@@ -63,6 +63,14 @@ constexpr int kJoinThreads = 256;
 // The running maximum may lag by this many powers of two before O is rescaled: P
 // stays within 2^8, exact enough in 16-bit floats and far from their range.
 constexpr float kLag = 8.0f;
+// Threads, and the registers a thread is launched with and then takes by role (the
+// roles' sum must not pass what the launch gave, or the takers would wait forever).
+constexpr int kThreads16 = 384, kThreads8 = 640;
+constexpr int kRegs16 = 168, kRegs8 = 96;
+constexpr int kHelpRegs16 = 88, kSoftRegs16 = 208;
+constexpr int kHelpRegs8 = 64, kSoftRegs8 = 136, kWideRegs8 = 72;
+static_assert(128 * kHelpRegs16 + 256 * kSoftRegs16 <= kThreads16 * kRegs16, "registers");
+static_assert(128 * kHelpRegs8 + 256 * kSoftRegs8 + 256 * kWideRegs8 <= kThreads8 * kRegs8, "registers");
 
 struct TileArgs {
   AttendArgs a;
@@ -94,7 +102,7 @@ struct Ctl {
   int b, h, qt, off;   // start of the CTA's share
   long long left, share;
   union {
-    long long warp_units[16];
+    long long warp_units[kThreads8 / 32];
     float2 xch[2][kTile];  // (m, l) of the two warpgroups
   };
 };
@@ -355,60 +363,60 @@ __device__ __forceinline__ void wait_end(uint64_t* bar, uint32_t parity) {
 // ---------------------------------------------------------------------------
 // Softmax of one S tile row (this thread's), 128 scores in tensor memory.
 // ---------------------------------------------------------------------------
-// Scores that the row does not see become -inf; the row sees columns [first, first+span).
-// Both passes are loops of 64 columns: straight-line code for all 128 would not
-// stay in the instruction caches beside the other roles'.
-template <bool MASK>
-__device__ __forceinline__ float row_max(uint32_t s_tm, int first, int span) {
-  float m[4] = {-kInf, -kInf, -kInf, -kInf};
-#pragma unroll 1
-  for (int k = 0; k < kTile; k += 64) {
-    uint32_t r[64];
-    tmem_ld32_async(s_tm + k, r);
-    tmem_ld32_async(s_tm + k + 32, r + 32);
-    tmem_wait_ld();
+// Scores of columns that the row does not see become -inf; it sees [first, first + span).
+template <int N>
+__device__ __forceinline__ void hide(uint32_t* r, int first, int span) {
 #pragma unroll
-    for (int j = 0; j < 64; ++j) {
-      float s = __uint_as_float(r[j]);
-      if (MASK) s = (unsigned)(k + j - first) < (unsigned)span ? s : -kInf;
-      m[j & 3] = fmaxf(m[j & 3], s);
-    }
-  }
+  for (int j = 0; j < N; ++j)
+    if ((unsigned)(j - first) >= (unsigned)span) r[j] = 0xff800000u;
+}
+template <int N>
+__device__ __forceinline__ float max_of(const uint32_t* r) {
+  float m[4] = {-kInf, -kInf, -kInf, -kInf};
+#pragma unroll
+  for (int j = 0; j < N; ++j) m[j & 3] = fmaxf(m[j & 3], __uint_as_float(r[j]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-
-// P = 2^(c s - m), written over S as pairs of 16-bit floats; returns the row sum.
-template <int PT, bool MASK>
-__device__ __forceinline__ float row_exp(uint32_t s_tm, int first, int span, float c, float m) {
+// P = 2^(c s - m) of N scores in pairs of 16-bit floats into tensor memory; adds to
+// the four pairs of sums.
+template <int PT, int N>
+__device__ __forceinline__ void exp_of(const uint32_t* r, float c, float m, uint32_t p_tm,
+                                       uint64_t* acc) {
   const uint64_t cc = pack2(c, c), mm = pack2(-m, -m);
-  uint64_t acc0 = pack2(0.0f, 0.0f), acc1 = acc0;
-#pragma unroll 1
-  for (int k = 0; k < kTile; k += 64) {
-    uint32_t r[64], w[16];
-    tmem_ld32_async(s_tm + k, r);
-    tmem_ld32_async(s_tm + k + 32, r + 32);
-    tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+  for (int k = 0; k < N; k += 32) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
       float x, y;
-      unpack2(ffma2(pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), cc, mm), x, y);
+      unpack2(ffma2(pack2(__uint_as_float(r[k + 2 * j]), __uint_as_float(r[k + 2 * j + 1])), cc, mm),
+              x, y);
       x = ex2(x);
       y = ex2(y);
-      if (MASK) {
-        x = (unsigned)(k + 2 * j - first) < (unsigned)span ? x : 0.0f;
-        y = (unsigned)(k + 2 * j + 1 - first) < (unsigned)span ? y : 0.0f;
-      }
-      if (j & 1) acc1 = fadd2(acc1, pack2(x, y));
-      else acc0 = fadd2(acc0, pack2(x, y));
-      w[j & 15] = F16<PT>::down(x, y);
-      // columns k/2 .. of P lie over scores that were read in this or an earlier pass
-      if ((j & 15) == 15) tmem_st16(s_tm + k / 2 + (j & 16), w);
+      acc[j & 3] = fadd2(acc[j & 3], pack2(x, y));
+      w[j] = F16<PT>::down(x, y);
     }
+    tmem_st16(p_tm + k / 2, w);
   }
-  float a, b, d, e;
-  unpack2(acc0, a, b);
-  unpack2(acc1, d, e);
-  return (a + b) + (d + e);
+}
+__device__ __forceinline__ float sum_of(const uint64_t* acc) {
+  float a, b;
+  unpack2(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), a, b);
+  return a + b;
+}
+
+// Two e4m3 values times 2^(sc - 127) in 16 bits.  bf16: the codes fit bf16 and a power
+// of two changes no digit, so the packed product is exact; fp16 rounds once from fp32.
+template <int DT>
+__device__ __forceinline__ uint32_t scaled(float2 v, uint32_t sc) {
+  if (DT == SV_F16) {
+    const float f = scale_of(sc);
+    return F16<DT>::down(v.x * f, v.y * f);
+  }
+  const uint32_t f2 = (sc << 7) | (sc << 23), c = F16<SV_BF16>::down(v.x, v.y);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(c), "r"(f2));
+  return r;
 }
 
 // O *= f (rows that need none have f = 1).
@@ -443,8 +451,17 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? -kInf : ((m == -kInf ? 0.0f : m) + log2f(l)) * kLn2;
 }
 
+template <int REGS>
+__device__ __forceinline__ void take_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void give_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
 template <int DT, bool E4M3>
-__global__ void __launch_bounds__(E4M3 ? 512 : 384, 1)
+__global__ void __launch_bounds__(E4M3 ? kThreads8 : kThreads16, 1)
 k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                const __grid_constant__ TileArgs t) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -467,12 +484,12 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   if (threadIdx.x == 0) {
     ctl.abort = (smem_u32(smem) & 1023u) ? 1 : 0;  // the swizzle needs this alignment
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(ctl.full + i, E4M3 ? 4 : 1);
+      mbar_init(ctl.full + i, E4M3 ? 8 : 1);
       mbar_init(ctl.empty + i, 1);
     }
     for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(ctl.rawfull + i, 1);
-      mbar_init(ctl.rawempty + i, 4);
+      mbar_init(ctl.rawempty + i, 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(ctl.qfull + i, 2);
@@ -499,6 +516,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   Walk walk(ctl);
   Seg s;
   bool ok = *abort_flag == 0;
+  if (warp < 4) give_regs<E4M3 ? kHelpRegs8 : kHelpRegs16>();
 
   if (warp == 0) {
     // ---------------- fetch key and value pages ----------------
@@ -576,46 +594,56 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     const uint64_t vdesc = umma_smem_desc(smem_u32(ring), kSpan, 1024);
     const uint32_t stage16 = (uint32_t)stage_bytes >> 4, tb = (uint32_t)uniform((int)tbase);
     uint32_t base = 0, qn = 0;          // tiles and query tiles used so far
-    uint32_t pph0 = 0, pph1 = 0;
+    uint32_t pph = 0;                   // phases of the two stages' P
     while (ok && walk.next(t, ctl, s)) {
       const int n = uniform(s.n), two = uniform(s.two ? 1 : 0);
       const int lo = uniform(s.lo), hi = uniform(s.hi), t0 = uniform(s.t0);
       const int jobs = n << two;
-      // S of job j: stage j & 1
-      auto scores = [&](int j) -> bool {
+      // S of job j (stage j & 1), once its tiles are there
+      auto key_slot = [&](int j) {
+        return Slot(base + (uint32_t)k_index(j >> two), (uint32_t)nst, t.inv_nst);
+      };
+      auto scores = [&](int j, uint32_t slot) {
         const int i = j >> two, st = j & 1;
-        const Slot k(base + (uint32_t)k_index(i), (uint32_t)nst, t.inv_nst);
-        const uint32_t qk = qn + (uint32_t)(two & st), qb = qk & 1u;
-        if (j < 2 && !wait_warp(ctl.qfull + qb, (qk >> 1) & 1u, abort_flag, kWaitQ)) return false;
-        if (!wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK)) return false;
-        tc_fence_after();
-        const uint64_t ad = qdesc + qb * (kQBytes >> 4), bd = kdesc + k.i * stage16;
+        const uint32_t qb = (qn + (uint32_t)(two & st)) & 1u;
+        const uint64_t ad = qdesc + qb * (kQBytes >> 4), bd = kdesc + slot * stage16;
         const uint32_t acc = tb + st * kTile;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint64_t o = (uint64_t)((kk >> 2) * (kSpan >> 4) + (kk & 3) * 2);
           if (kk < ksteps) umma_ss_if(leader, acc, ad + o, bd + o, idesc_s, kk != 0);
         }
-        umma_commit_if(leader, ctl.sfull + st);  // the softmax then frees the key and query tiles
-        return true;
+        umma_commit_if(leader, ctl.sfull + st);
+        if (!two || st) umma_commit_if(leader, ctl.empty + slot);
+        if (i == n - 1) umma_commit_if(leader, ctl.qempty + qb);
       };
-      for (int j = 0; ok && j < 2 && j < jobs; ++j) ok = scores(j);
+      for (int j = 0; j < 2 && j < jobs; ++j) {
+        const Slot k = key_slot(j);
+        const uint32_t qk = qn + (uint32_t)(two & j);
+        ok = wait_warp(ctl.qfull + (qk & 1u), (qk >> 1) & 1u, abort_flag, kWaitQ) &&
+             wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK);
+        if (!ok) break;
+        tc_fence_after();
+        scores(j, k.i);
+      }
       for (int j = 0; ok && j < jobs; ++j) {
         const int i = j >> two, st = j & 1;
-        const Slot k(base + (uint32_t)v_index(i, n), (uint32_t)nst, t.inv_nst);
-        if (!wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitV) ||
-            !wait_warp(ctl.pfull + st, st ? pph1 : pph0, abort_flag, kWaitP)) {
-          ok = false;
-          break;
-        }
-        if (st) pph1 ^= 1u;
-        else pph0 ^= 1u;
-        tc_fence_after();
+        const bool more = j + 2 < jobs;
+        const Slot v(base + (uint32_t)v_index(i, n), (uint32_t)nst, t.inv_nst);
+        const Slot k = key_slot(more ? j + 2 : j);
         int s0, s1;
         key_steps(lo, hi, t0 + i, s0, s1);
-        const uint64_t bd = vdesc + k.i * stage16;
+        const uint64_t bd = vdesc + v.i * stage16;
         const uint32_t acc = tb + 256 + st * kTile, p = tb + st * kTile;
         const bool fresh = two ? i == 0 : j < 2;
+        // P is awaited last: nothing then stands between it and the products.  (The key
+        // tile of job j + 2 does not depend on job j: its slot was freed by an earlier one.)
+        ok = wait_warp(ctl.full + v.i, v.ph, abort_flag, kWaitV) &&
+             (!more || wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK)) &&
+             wait_warp(ctl.pfull + st, (pph >> st) & 1u, abort_flag, kWaitP);
+        if (!ok) break;
+        pph ^= 1u << st;
+        tc_fence_after();
         if (s0 == 0 && s1 == 8) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
@@ -624,9 +652,9 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
           for (int kk = s0; kk < s1; ++kk)
             umma_ts_if(leader, acc, p + kk * 8, bd + (uint64_t)(kk * 128), idesc_o, kk != s0 || !fresh);
         }
-        if (!two || st) umma_commit_if(leader, ctl.empty + k.i);
-        if (j + 2 >= jobs) umma_commit_if(leader, ctl.ofull + st);
-        if (j + 2 < jobs) ok = scores(j + 2);
+        if (!two || st) umma_commit_if(leader, ctl.empty + v.i);
+        if (more) scores(j + 2, k.i);
+        else umma_commit_if(leader, ctl.ofull + st);
       }
       base += 2u * (uint32_t)n;
       qn += 1u + (uint32_t)two;
@@ -680,14 +708,15 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
   } else if (warp < 12) {
     // ---------------- softmax and output ----------------
+    take_regs<E4M3 ? kSoftRegs8 : kSoftRegs16>();
     const int st = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
     const uint32_t lanes = tbase + ((uint32_t)(32 * quad) << 16);
     const uint32_t s_tm = lanes + st * kTile, o_tm = lanes + 256 + st * kTile;
     const int units = D / 16;
     const int my_tok = row / t.group, my_head = row - my_tok * t.group;
     uint32_t sph = 0, oph = 0, xph = 0;
-    uint32_t base = 0, qn = 0;  // tiles and query tiles of the parts before
-    for (; ok && walk.next(t, ctl, s); base += 2u * (uint32_t)s.n, qn += s.two ? 2u : 1u) {
+    uint32_t base = 0;  // tiles of the parts before
+    for (; ok && walk.next(t, ctl, s); base += 2u * (uint32_t)s.n) {
       const int shift = s.two ? 0 : 1;
       const int jobs = s.two ? s.n : (s.n + 1 - st) >> 1;
       const int tok_off = s.two ? st * t.tpt : 0;
@@ -706,18 +735,24 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         sph ^= 1u;
         tc_fence_after();
         const int i = shift ? 2 * k + st : k;  // key tile
-        if (quad == 0 && lane == 0) {  // S is done with its key tile, the last S with the queries
-          if (!s.two || st)
-            mbar_arrive(ctl.empty + Slot(base + (uint32_t)k_index(i), (uint32_t)nst, t.inv_nst).i);
-          if (i == s.n - 1) mbar_arrive(ctl.qempty + ((qn + (uint32_t)(s.two ? st : 0)) & 1u));
-        }
-        __syncwarp();
         if (warp_live) {
           const int key0 = (s.t0 + i) * kTile;
           const int first = max(0, see0 - key0), span = max(0, min(kTile, see1 - key0) - first);
           const bool masked = __any_sync(0xffffffffu, live && span < kTile);
-          const float tm = (masked ? row_max<true>(s_tm, first, span) : row_max<false>(s_tm, 0, 0)) *
-                               t.c - kShift;
+          // beside the converters a thread has no room for all of its scores: it reads
+          // them twice, 64 at a time (P lies over scores that were read by then)
+          constexpr int kHeld = E4M3 ? 64 : kTile;
+          uint32_t r[kHeld];
+          float tm = -kInf;
+#pragma unroll 1
+          for (int c0 = 0; c0 < kTile; c0 += kHeld) {
+#pragma unroll
+            for (int c = 0; c < kHeld; c += 32) tmem_ld32_async(s_tm + c0 + c, r + c);
+            tmem_wait_ld();
+            if (masked) hide<kHeld>(r, first - c0, span);
+            tm = fmaxf(tm, max_of<kHeld>(r));
+          }
+          tm = tm * t.c - kShift;
           const bool rise = tm > m + kLag || (m == -kInf && tm > m);
           if (__any_sync(0xffffffffu, rise)) {
             const float nm = rise ? tm : m;
@@ -729,11 +764,21 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             m = nm;
           }
           const float mu = m == -kInf ? 0.0f : m;
-          l += masked ? row_exp<kPT, true>(s_tm, first, span, t.c, mu)
-                      : row_exp<kPT, false>(s_tm, 0, 0, t.c, mu);
+          uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll 1
+          for (int c0 = 0; c0 < kTile; c0 += kHeld) {
+            if (E4M3) {
+#pragma unroll
+              for (int c = 0; c < kHeld; c += 32) tmem_ld32_async(s_tm + c0 + c, r + c);
+              tmem_wait_ld();
+              if (masked) hide<kHeld>(r, first - c0, span);
+            }
+            exp_of<kPT, kHeld>(r, t.c, mu, s_tm + c0 / 2, acc);
+          }
+          l += sum_of(acc);
           tmem_wait_st();
         }
-        if (!E4M3 && !(s.two && st)) {
+        if (!E4M3 && !(s.two && st) && (i == 0 || i == s.n - 1)) {
           // value rows of the first and last step that nobody sees may hold anything:
           // zeros (their P is 0, but 0 times infinity is not)
           const int key0 = (s.t0 + i) * kTile;
@@ -858,7 +903,14 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
   } else if (E4M3) {
     // ---------------- widen e4m3 codes ----------------
-    const int cw = warp - 12, ch = lane & 7, g = lane >> 3;  // 16 codes each, four rows at a time
+    // A lane widens 16 codes of a row (two 16-byte chunks of a swizzle span).  Four
+    // lanes take one span of a row and the next four that span of the row below, so
+    // that the eight lanes of a store's phase write different banks; four rows at a
+    // time, 16 rows a warp.
+    give_regs<kWideRegs8>();
+    const int cw = warp - 12;
+    const int span = (lane >> 3) & 1, ch = (lane & 3) + 4 * span;
+    const int g = ((lane >> 2) & 1) + 2 * (lane >> 4);
     uint32_t k = 0;
     while (ok && walk.next(t, ctl, s)) {
       for (int idx = 0; ok && idx < 2 * s.n; ++idx, ++k) {
@@ -873,40 +925,40 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
           ok = false;
           break;
         }
-        const uint8_t* src = raw + (size_t)rs * raw_bytes + (32 * cw + g) * D + ch * 16;
-        uint8_t* dst = ring + (size_t)slot * stage_bytes + (ch >> 2) * kSpan + (32 * cw + g) * 128;
-        const uint32_t scale = raw[(size_t)rs * raw_bytes + kTile * D + 32 * cw + lane];
-        // rows 32 cw + 4 p + g; only the part's first and last tiles hold rows that
-        // nobody sees: those become zeros whatever they hold
-        const int row0 = key0 + 32 * cw;
-        const bool edge = row0 < s.lo || row0 + 32 > s.hi;
-        const bool on = ch * 16 < D;
-        uint4 x[8];
+        const uint8_t* src = raw + (size_t)rs * raw_bytes + (16 * cw + g) * D + ch * 16;
+        uint8_t* dst = ring + (size_t)slot * stage_bytes + span * kSpan + (16 * cw + g) * 128;
+        const uint8_t* scales = raw + (size_t)rs * raw_bytes + kTile * D + 16 * cw + g;
+        // only the part's first and last tiles hold rows that nobody sees: those
+        // become zeros whatever they hold
+        const int row0 = key0 + 16 * cw;
+        const bool edge = row0 < s.lo || row0 + 16 > s.hi;
+        if (ch * 16 < D) {
+          uint4 x[4];
+          uint32_t sc[4];
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
-          x[p] = on ? *reinterpret_cast<const uint4*>(src + 4 * p * D) : make_uint4(0, 0, 0, 0);
-        // the two spans' lanes write opposite chunks at a time (no bank conflict)
-        const int c1 = (ch & 3) * 2 + (ch < 4 ? 0 : 1), c2 = c1 ^ 1;
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const float f = scale_of(__shfl_sync(0xffffffffu, scale, 4 * p + g));
-          const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-          uint32_t o[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 u = e4m3x2((uint16_t)w[j]), v = e4m3x2((uint16_t)(w[j] >> 16));
-            o[2 * j] = F16<DT>::down(u.x * f, u.y * f);
-            o[2 * j + 1] = F16<DT>::down(v.x * f, v.y * f);
+          for (int p = 0; p < 4; ++p) {
+            x[p] = *reinterpret_cast<const uint4*>(src + 4 * p * D);
+            sc[p] = scales[4 * p];
           }
-          if (edge && !(row0 + 4 * p + g >= s.lo && row0 + 4 * p + g < s.hi)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = 0;
-          }
-          if (on) {
-            const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
-            const int sw = (4 * p + g) & 7;  // 32 cw leaves the row's swizzle alone
-            *reinterpret_cast<uint4*>(dst + 4 * p * 128 + ((c1 ^ sw) << 4)) = ch < 4 ? lo4 : hi4;
-            *reinterpret_cast<uint4*>(dst + 4 * p * 128 + ((c2 ^ sw) << 4)) = ch < 4 ? hi4 : lo4;
+          for (int p = 0; p < 4; ++p) {
+            const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 u = e4m3x2((uint16_t)w[j]), v = e4m3x2((uint16_t)(w[j] >> 16));
+              o[2 * j] = scaled<DT>(u, sc[p]);
+              o[2 * j + 1] = scaled<DT>(v, sc[p]);
+            }
+            if (edge && !(row0 + 4 * p + g >= s.lo && row0 + 4 * p + g < s.hi)) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] = 0;
+            }
+            const int sw = (4 * p + g) & 7, c1 = 2 * (lane & 3);  // 16 cw leaves the swizzle alone
+            *reinterpret_cast<uint4*>(dst + 4 * p * 128 + ((c1 ^ sw) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + 4 * p * 128 + (((c1 + 1) ^ sw) << 4)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
         fence_proxy_async();
@@ -1077,12 +1129,20 @@ cudaError_t device_ready(int* sms) {
     g_encode = reinterpret_cast<EncodeTiled>(fn);
   }
   if (!g_sms[dev]) {
-    const int smem = (int)kSmemBytes;
-    for (const void* k : {(const void*)k_attend_tiles<SV_BF16, false>,
-                          (const void*)k_attend_tiles<SV_F16, false>,
-                          (const void*)k_attend_tiles<SV_BF16, true>,
-                          (const void*)k_attend_tiles<SV_F16, true>}) {
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const struct {
+      const void* kernel;
+      int regs;
+    } all[] = {{(const void*)k_attend_tiles<SV_BF16, false>, kRegs16},
+               {(const void*)k_attend_tiles<SV_F16, false>, kRegs16},
+               {(const void*)k_attend_tiles<SV_BF16, true>, kRegs8},
+               {(const void*)k_attend_tiles<SV_F16, true>, kRegs8}};
+    for (const auto& k : all) {
+      cudaFuncAttributes attr{};
+      e = cudaFuncGetAttributes(&attr, k.kernel);
+      if (e != cudaSuccess) return e;
+      if (attr.numRegs < k.regs) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
+      e = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)kSmemBytes);
       if (e != cudaSuccess) return e;
     }
     int n = 0;
@@ -1161,7 +1221,7 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   auto* k = dtype == SV_BF16 ? (e4m3 ? k_attend_tiles<SV_BF16, true> : k_attend_tiles<SV_BF16, false>)
                              : (e4m3 ? k_attend_tiles<SV_F16, true> : k_attend_tiles<SV_F16, false>);
-  e = launch_pdl(k, dim3(ctas), dim3(e4m3 ? 512 : 384), kSmemBytes, stream, mk, mv, t);
+  e = launch_pdl(k, dim3(ctas), dim3(e4m3 ? kThreads8 : kThreads16), kSmemBytes, stream, mk, mv, t);
   if (e != cudaSuccess) return e;
   const int join_blocks = 2 * ctas;
   const int flag_blocks = a.flags ? (a.b.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
