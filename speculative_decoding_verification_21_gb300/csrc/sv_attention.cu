@@ -183,7 +183,7 @@ size_t attention_workspace_bytes(const CacheView& c, bool e4m3) {
 }
 
 cudaError_t launch_attention(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream) {
-  if (tiles_take(a.c, e4m3)) {
+  if (tiles_take(a.c, e4m3) && a.scale_log2 >= 0.0f) {
     bool taken = false;
     const cudaError_t e = launch_attention_tiles(a, dtype, e4m3, stream, &taken);
     if (e != cudaSuccess || taken) return e;

@@ -22,7 +22,7 @@
 // their (m, l, O) are added up at its end.
 //
 // Roles: warp 0 fetches key and value pages (tensor copies, 128-byte swizzle),
-// warp 1 issues the products, warps 2-3 fetch queries, warps 4-11 are the softmax,
+// warp 1 issues the products, warp 2 fetches queries, warps 4-11 are the softmax,
 // and for e4m3 caches warps 12-19 widen the codes to 16 bits between the copies
 // and the products.  Every wait is bounded; one that gives up ends the CTA's roles
 // and flags the call.
@@ -79,8 +79,8 @@ struct TileArgs {
   int nst, nraw;       // ring slots
   uint32_t inv_nst, inv_nraw;  // ceil(2^32 / slots): slot and turn of tile k without a division
   int box;             // tokens per copy: min(page_size, 128)
-  int flip;            // negative scale: the queries' signs are flipped
-  float c;             // |scale| log2 e
+  int wide;            // outputs sit on 32-byte boundaries
+  float c;             // scale log2 e, positive
   float* part;         // [2 * kMaxCtas][kMaxRows][head_dim]
   float2* ml;          // [2 * kMaxCtas][kMaxRows]
   struct Rec* rec;     // [kMaxCtas]
@@ -433,18 +433,28 @@ __device__ __forceinline__ void rescale(uint32_t o_tm, int units, float f) {
   tmem_wait_st();
 }
 
+// A lane's 16 outputs of one row: one 32-byte store (a whole sector) where that is aligned.
 template <int DT>
-__device__ __forceinline__ void store16(char* at, const float* x) {
+__device__ __forceinline__ void store16(char* at, const float* x, bool wide) {
   uint32_t w[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) w[j] = F16<DT>::down(x[2 * j], x[2 * j + 1]);
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+    return;
+  }
   reinterpret_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
   reinterpret_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
-__device__ __forceinline__ void store16f(float* at, const float* x) {
+__device__ __forceinline__ void store16f(float* at, const float* x) {  // 32-byte aligned
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    reinterpret_cast<float4*>(at)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+  for (int j = 0; j < 16; j += 8)
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at + j), "f"(x[j]),
+                 "f"(x[j + 1]), "f"(x[j + 2]), "f"(x[j + 3]), "f"(x[j + 4]), "f"(x[j + 5]),
+                 "f"(x[j + 6]), "f"(x[j + 7])
+                 : "memory");
 }
 
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -462,8 +472,8 @@ __device__ __forceinline__ void give_regs() {
 
 template <int DT, bool E4M3>
 __global__ void __launch_bounds__(E4M3 ? kThreads8 : kThreads16, 1)
-k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-               const __grid_constant__ TileArgs t) {
+k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, const __grid_constant__ TileArgs t) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int kRing = E4M3 ? kRing8 : kRing16;
   constexpr int kPT = DT;
@@ -492,7 +502,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       mbar_init(ctl.rawempty + i, 8);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(ctl.qfull + i, 2);
+      mbar_init(ctl.qfull + i, 1);
       mbar_init(ctl.qempty + i, 1);
       mbar_init(ctl.sfull + i, 1);
       mbar_init(ctl.pfull + i, 4);
@@ -663,48 +673,31 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     umma_commit_if(leader, &ctl.fin);
     wait_end(&ctl.fin, 0);
   } else if (warp < 4) {
-    // ---------------- fetch query tiles ----------------
-    const int th = (int)threadIdx.x - 64;  // 0..63: four rows of 16 chunks at a time
-    const int ch = th & 15;
-    const uint32_t sign = t.flip ? 0x80008000u : 0u;
-    uint32_t qn = 0;
-    if (th == 0) t.rec[wid].more = 0;
-    while (ok && walk.next(t, ctl, s)) {
-      if (th == 0 && s.slot == 1) t.rec[wid] = Rec{s.more, s.row0, s.ntok, s.h};
-      for (int st = 0; ok && st < (s.two ? 2 : 1); ++st, ++qn) {
-        const uint32_t qb = qn & 1u;
-        if (!wait_warp(ctl.qempty + qb, ((qn >> 1) & 1u) ^ 1u, abort_flag, kWaitQFree)) {
-          ok = false;
-          break;
-        }
-        const int tok = s.row0 + st * t.tpt;
-        const int rows = min(t.tpt, s.ntok - st * t.tpt) * t.group;
-        const char* src = a.q + (int64_t)s.h * t.group * a.q_head;
-        uint8_t* dst = qbuf + qb * kQBytes + (ch >> 3) * kSpan;
-        if (ch * 8 < D) {
-          int tk = (th >> 4) / t.group, hd = (th >> 4) - tk * t.group;
-          const int step_t = 4 / t.group, step_h = 4 - step_t * t.group;
-#pragma unroll 4
-          for (int r = th >> 4; r < rows; r += 4) {
-            uint4 x = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(tok + tk) * a.q_token +
-                                                           (int64_t)hd * a.q_head) + ch);
-            x.x ^= sign;
-            x.y ^= sign;
-            x.z ^= sign;
-            x.w ^= sign;
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
-            tk += step_t;
-            hd += step_h;
-            if (hd >= t.group) {
-              hd -= t.group;
-              ++tk;
-            }
+    // ---------------- fetch query tiles (warp 2) ----------------
+    // A copy takes tpt tokens by group heads, rows in the order of the tile.  Tokens
+    // behind the sequence's last are other sequences' or zeros: nobody reads their rows.
+    if (warp == 2) {
+      const uint64_t pol = l2_policy_evict_first();
+      uint32_t qn = 0;
+      if (lane == 0) t.rec[wid].more = 0;
+      while (ok && walk.next(t, ctl, s)) {
+        if (lane == 0 && s.slot == 1) t.rec[wid] = Rec{s.more, s.row0, s.ntok, s.h};
+        for (int st = 0; ok && st < (s.two ? 2 : 1); ++st, ++qn) {
+          const uint32_t qb = qn & 1u;
+          ok = wait_warp(ctl.qempty + qb, ((qn >> 1) & 1u) ^ 1u, abort_flag, kWaitQFree);
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(ctl.qfull + qb, (uint32_t)(t.nhalf * t.tpt * t.group * 128));
+            for (int h = 0; h < t.nhalf; ++h)
+              tma_load_3d_hint(qbuf + qb * kQBytes + h * kSpan, &mq, 64 * h, s.h * t.group,
+                               s.row0 + st * t.tpt, ctl.qfull + qb, pol);
           }
+          __syncwarp();
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ctl.qfull + qb);
       }
+      // every copy has landed before the CTA may exit
+      for (uint32_t i = qn > 2 ? qn - 2 : 0; i < qn; ++i)
+        if (lane == 0) wait_end(ctl.qfull + (i & 1u), (i >> 1) & 1u);
+      __syncwarp();
     }
   } else if (warp < 12) {
     // ---------------- softmax and output ----------------
@@ -831,7 +824,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
               if (s.slot < 0) x[j] = l == 0.0f ? 0.0f : x[j] * inv;
             }
             if (live) {
-              if (s.slot < 0) store16<DT>(a.out + (orow * D + 16 * u) * 2, x);
+              if (s.slot < 0) store16<DT>(a.out + (orow * D + 16 * u) * 2, x, t.wide);
               else store16f(t.part + prow * D + 16 * u, x);
             }
           }
@@ -877,7 +870,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
               x[j] = (y0 + y1) * inv;
             }
             if (live) {
-              if (s.slot < 0) store16<DT>(a.out + (orow * D + 16 * u) * 2, x);
+              if (s.slot < 0) store16<DT>(a.out + (orow * D + 16 * u) * 2, x, t.wide);
               else store16f(t.part + prow * D + 16 * u, x);
             }
           }
@@ -1171,6 +1164,22 @@ bool encode_pool(CUtensorMap* map, const CacheView& c, const void* base, CUtenso
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries [total][heads][dim] by their strides, tpt tokens by group heads at a time.
+bool encode_queries(CUtensorMap* map, const AttendArgs& a, int dim, int group, int tpt) {
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)a.heads, (cuuint64_t)a.b.total};
+  // a dimension of one entry is never stepped along: any legal stride will do
+  const cuuint64_t row = (cuuint64_t)dim * 2;
+  const cuuint64_t strides[2] = {a.heads > 1 ? (cuuint64_t)a.q_head : row,
+                                 a.b.total > 1 ? (cuuint64_t)a.q_token : row};
+  const cuuint32_t bx[3] = {64, (cuuint32_t)group, (cuuint32_t)tpt};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return a.b.total > 0 &&
+         g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<char*>(a.q), dims, strides,
+                  bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr size_t kRecBytes = 4096, kMlBytes = sizeof(float2) * 2 * kMaxCtas * kMaxRows;
 static_assert(kMaxCtas * (sizeof(Rec) + sizeof(int)) <= kRecBytes, "records");
 
@@ -1197,22 +1206,25 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
   t.inv_nst = (uint32_t)((0x100000000ull + t.nst - 1) / t.nst);
   t.inv_nraw = (uint32_t)((0x100000000ull + t.nraw - 1) / t.nraw);
   t.box = c.page_size < kTile ? c.page_size : kTile;
-  t.flip = a.scale_log2 < 0.0f;
+  t.wide = ((uintptr_t)a.out & 31) == 0;
   // a scale of zero: every product times 1e-30 is zero beside 1, and the -inf of a
   // key that is not seen stays one
-  t.c = a.scale_log2 == 0.0f ? 1e-30f : (t.flip ? -a.scale_log2 : a.scale_log2);
+  t.c = a.scale_log2 == 0.0f ? 1e-30f : a.scale_log2;
   t.rec = reinterpret_cast<Rec*>(a.ws);
   t.err = reinterpret_cast<int*>(a.ws + kMaxCtas * sizeof(Rec));
   t.ml = reinterpret_cast<float2*>(a.ws + kRecBytes);
   t.part = reinterpret_cast<float*>(a.ws + kRecBytes + kMlBytes);
-  alignas(64) CUtensorMap mk{}, mv{};
+  alignas(64) CUtensorMap mq{}, mk{}, mv{};
+  *taken = encode_queries(&mq, a, c.head_dim, t.group, t.tpt);
   if (e4m3) {
-    *taken = encode_pool(&mk, c, c.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE,
+    *taken = *taken &&
+             encode_pool(&mk, c, c.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE,
                          c.head_dim, t.box) &&
              encode_pool(&mv, c, c.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE,
                          c.head_dim, t.box);
   } else {
-    *taken = encode_pool(&mk, c, c.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+    *taken = *taken &&
+             encode_pool(&mk, c, c.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                          CU_TENSOR_MAP_SWIZZLE_128B, 64, t.box) &&
              encode_pool(&mv, c, c.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                          CU_TENSOR_MAP_SWIZZLE_128B, 64, t.box);
@@ -1221,7 +1233,7 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   auto* k = dtype == SV_BF16 ? (e4m3 ? k_attend_tiles<SV_BF16, true> : k_attend_tiles<SV_BF16, false>)
                              : (e4m3 ? k_attend_tiles<SV_F16, true> : k_attend_tiles<SV_F16, false>);
-  e = launch_pdl(k, dim3(ctas), dim3(e4m3 ? kThreads8 : kThreads16), kSmemBytes, stream, mk, mv, t);
+  e = launch_pdl(k, dim3(ctas), dim3(e4m3 ? kThreads8 : kThreads16), kSmemBytes, stream, mq, mk, mv, t);
   if (e != cudaSuccess) return e;
   const int join_blocks = 2 * ctas;
   const int flag_blocks = a.flags ? (a.b.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
