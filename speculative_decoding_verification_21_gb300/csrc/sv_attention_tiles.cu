@@ -52,13 +52,18 @@ constexpr int kTile = 128;          // query rows and keys per tile
 constexpr int kSpan = 16384;        // 128 rows of one 128-byte swizzle span
 constexpr int kMaxCtas = 160;       // shares (GB300: 152 SMs)
 constexpr int kMaxRows = 2 * kTile;
-constexpr int kMaxStages = 10, kMaxRaw = 8;
+constexpr int kMaxStages = 12, kMaxRaw = 8;
 constexpr long long kWaitClocks = 1ll << 32;  // about two seconds
 constexpr size_t kSmemBytes = 227 * 1024;
 constexpr int kQBytes = 2 * kSpan;                // one query tile
-constexpr int kRing16 = 160 * 1024;               // 16-bit caches: 5 (or 10) key/value tiles
-constexpr int kRing8 = 96 * 1024;                 // e4m3: 3 (or 6) widened tiles ...
-constexpr int kRaw8 = 4 * kTile * (kTile + 1);    // ... and 4 or more tiles of codes and scales
+// Shared memory: two query tiles, then 160 KB.  A 16-bit cache's ring of key and value
+// tiles (5 of 32 KB, or 10 of 16 KB) takes those; an e4m3 cache's codes take the first
+// 64 KB and the widened tiles (3 or 6) the rest.  In a call without an item of two row
+// tiles the second query tile is not used, and the first of the rings starts there:
+// with 6 tiles of codes in flight instead of 4 a round of 32 sequences took X us
+// instead of 505.
+constexpr int kCodes = 64 * 1024, kRing16 = 160 * 1024, kRing8 = 96 * 1024;
+constexpr int kScaleBytes = kMaxRaw * kTile;
 constexpr int kJoinThreads = 256;
 // The running maximum may lag by this many powers of two before O is rescaled: P
 // stays within 2^8, exact enough in 16-bit floats and far from their range.
@@ -68,16 +73,20 @@ constexpr float kLag = 8.0f;
 constexpr int kThreads16 = 384, kThreads8 = 640;
 constexpr int kRegs16 = 168, kRegs8 = 96;
 constexpr int kHelpRegs16 = 88, kSoftRegs16 = 208;
-constexpr int kHelpRegs8 = 64, kSoftRegs8 = 136, kWideRegs8 = 72;
+constexpr int kHelpRegs8 = 64, kSoftRegs8 = 120, kWideRegs8 = 88;
 static_assert(128 * kHelpRegs16 + 256 * kSoftRegs16 <= kThreads16 * kRegs16, "registers");
 static_assert(128 * kHelpRegs8 + 256 * kSoftRegs8 + 256 * kWideRegs8 <= kThreads8 * kRegs8, "registers");
+
+// Slots of a ring, and ceil(2^32 / slots): slot and turn of tile k without a division.
+struct Ring {
+  uint32_t n, inv;
+};
 
 struct TileArgs {
   AttendArgs a;
   int group, tpt;      // query heads per key head; tokens per row tile
   int nhalf;           // swizzle spans per row: 1 (head_dim <= 64) or 2
-  int nst, nraw;       // ring slots
-  uint32_t inv_nst, inv_nraw;  // ceil(2^32 / slots): slot and turn of tile k without a division
+  Ring tiles[2], codes[2];  // of 16-bit tiles and of codes, without and with items of two
   int box;             // tokens per copy: min(page_size, 128)
   int wide;            // outputs sit on 32-byte boundaries
   float c;             // scale log2 e, positive
@@ -99,11 +108,12 @@ struct Ctl {
   uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], xbar, fin;
   uint32_t tmem;
   int abort;
+  int two;             // some item of the call has two row tiles
   int b, h, qt, off;   // start of the CTA's share
   long long left, share;
   union {
     long long warp_units[kThreads8 / 32];
-    float2 xch[2][kTile];  // (m, l) of the two warpgroups
+    float2 xch[kTile];  // (m, l) from one warpgroup to the other
   };
 };
 
@@ -181,6 +191,7 @@ __device__ void find_share(const TileArgs& t, Ctl& ctl) {
     Seq q{};
     if (base + lane < b1) q = load_seq(bv, base + lane, ps);
     sum += warp_sum64(head_units(q, per_item, t.a.window) * H);
+    if (q.n > t.tpt) ctl.two = 1;
   }
   if (lane == 0) ctl.warp_units[warp] = sum;
   if (threadIdx.x == 0) {
@@ -311,12 +322,12 @@ __device__ __forceinline__ void tile_of(int idx, int n, bool& is_v, int& tile) {
   tile = is_v ? (idx == 2 * n - 1 ? n - 1 : idx / 2 - 1) : (idx + 1) / 2;
 }
 
-// Slot and phase of the k-th tile of a ring of n slots (k < 2^32 / n / 10).
+// Slot and phase of the k-th tile of a ring (k < 2^32 / 12).
 struct Slot {
   uint32_t i, ph;
-  __device__ __forceinline__ Slot(uint32_t k, uint32_t n, uint32_t inv) {
-    const uint32_t turn = __umulhi(k, inv);
-    i = k - turn * n;
+  __device__ __forceinline__ Slot(uint32_t k, const Ring& r) {
+    const uint32_t turn = __umulhi(k, r.inv);
+    i = k - turn * r.n;
     ph = turn & 1u;
   }
 };
@@ -475,23 +486,22 @@ __global__ void __launch_bounds__(E4M3 ? kThreads8 : kThreads16, 1)
 k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const __grid_constant__ TileArgs t) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int kRing = E4M3 ? kRing8 : kRing16;
   constexpr int kPT = DT;
   constexpr float kShift = kPT == SV_F16 ? 6.0f : 0.0f;  // fp16 P within 2^14: small ones keep bits
   uint8_t* const qbuf = smem;
-  uint8_t* const ring = smem + 2 * kQBytes;
-  uint8_t* const raw = ring + kRing;  // e4m3 codes: [nraw][128 (D + 1)], scales behind the codes
-  Ctl& ctl = *reinterpret_cast<Ctl*>(smem + 2 * kQBytes + kRing + (E4M3 ? kRaw8 : 0));
-  static_assert(2 * kQBytes + kRing16 + sizeof(Ctl) <= kSmemBytes, "shared memory");
-  static_assert(2 * kQBytes + kRing8 + kRaw8 + sizeof(Ctl) <= kSmemBytes, "shared memory");
+  uint8_t* const scale_area = smem + 2 * kQBytes + kRing16;  // e4m3: [kMaxRaw][128]
+  Ctl& ctl = *reinterpret_cast<Ctl*>(scale_area + kScaleBytes);
+  static_assert(2 * kQBytes + kRing16 + kScaleBytes + sizeof(Ctl) <= kSmemBytes, "shared memory");
+  static_assert(kCodes + kRing8 == kRing16, "shared memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AttendArgs& a = t.a;
-  const int D = a.c.head_dim, nst = t.nst, nraw = t.nraw;
-  const int stage_bytes = t.nhalf * kSpan, raw_bytes = kTile * (D + 1);
+  const int D = a.c.head_dim;
+  const int stage_bytes = t.nhalf * kSpan, raw_bytes = kTile * D;
   volatile int* const abort_flag = &ctl.abort;
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
+    ctl.two = 0;
     ctl.abort = (smem_u32(smem) & 1023u) ? 1 : 0;  // the swizzle needs this alignment
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(ctl.full + i, E4M3 ? 8 : 1);
@@ -523,6 +533,11 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   pdl_wait();
   find_share(t, ctl);
   const int wid = (int)blockIdx.x;
+  const int pair = ctl.two;                       // query tiles held: 1 + pair
+  const Ring rt = t.tiles[pair], rc = t.codes[pair];
+  uint8_t* const first = smem + (1 + pair) * kQBytes;
+  uint8_t* const raw = first;                     // e4m3: codes
+  uint8_t* const ring = E4M3 ? smem + 2 * kQBytes + kCodes : first;
   Walk walk(ctl);
   Seg s;
   bool ok = *abort_flag == 0;
@@ -547,7 +562,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int mine = key0 + part * t.box;
         int page = -1;
         if (part >= from && part < upto) page = __ldg(table + (mine >> a.c.page_shift));
-        const Slot at(issued, (uint32_t)(E4M3 ? nraw : nst), E4M3 ? t.inv_nraw : t.inv_nst);
+        const Slot at(issued, E4M3 ? rc : rt);
         const uint32_t slot = at.i, ph = at.ph;
         uint64_t* const fullb = (E4M3 ? ctl.rawfull : ctl.full) + slot;
         if (!wait_warp((E4M3 ? ctl.rawempty : ctl.empty) + slot, ph ^ 1u, abort_flag, kWaitSlot)) {
@@ -557,7 +572,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int live = max(0, upto - from);
         uint32_t bytes = (uint32_t)(live * t.box * (E4M3 ? D : t.nhalf * 128));
         uint8_t* const dst8 = raw + (size_t)slot * raw_bytes;
-        uint8_t* const scales = dst8 + kTile * D + part * t.box;
+        uint8_t* const scales = scale_area + slot * kTile + part * t.box;
         // a page outside the pool arrives as zeros; so do its scales
         const bool sound = page >= 0 && page < a.c.num_pages;
         if (E4M3) {
@@ -588,7 +603,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       }
     }
     // every copy has landed before the CTA may exit
-    const uint32_t ns = E4M3 ? nraw : nst;
+    const uint32_t ns = E4M3 ? rc.n : rt.n;
     for (uint32_t i = 0; i < ns && i < issued; ++i) {
       const uint32_t last = (issued - 1u) - ((issued - 1u - i) % ns);
       if (lane == 0) wait_end((E4M3 ? ctl.rawfull : ctl.full) + i, (last / ns) & 1u);
@@ -603,6 +618,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const uint64_t kdesc = umma_smem_desc(smem_u32(ring), 16, 1024);
     const uint64_t vdesc = umma_smem_desc(smem_u32(ring), kSpan, 1024);
     const uint32_t stage16 = (uint32_t)stage_bytes >> 4, tb = (uint32_t)uniform((int)tbase);
+    const int pr = uniform(pair);
     uint32_t base = 0, qn = 0;          // tiles and query tiles used so far
     uint32_t pph = 0;                   // phases of the two stages' P
     while (ok && walk.next(t, ctl, s)) {
@@ -611,11 +627,11 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       const int jobs = n << two;
       // S of job j (stage j & 1), once its tiles are there
       auto key_slot = [&](int j) {
-        return Slot(base + (uint32_t)k_index(j >> two), (uint32_t)nst, t.inv_nst);
+        return Slot(base + (uint32_t)k_index(j >> two), rt);
       };
       auto scores = [&](int j, uint32_t slot) {
         const int i = j >> two, st = j & 1;
-        const uint32_t qb = (qn + (uint32_t)(two & st)) & 1u;
+        const uint32_t qb = (qn + (uint32_t)(two & st)) & (uint32_t)pr;
         const uint64_t ad = qdesc + qb * (kQBytes >> 4), bd = kdesc + slot * stage16;
         const uint32_t acc = tb + st * kTile;
 #pragma unroll
@@ -630,7 +646,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       for (int j = 0; j < 2 && j < jobs; ++j) {
         const Slot k = key_slot(j);
         const uint32_t qk = qn + (uint32_t)(two & j);
-        ok = wait_warp(ctl.qfull + (qk & 1u), (qk >> 1) & 1u, abort_flag, kWaitQ) &&
+        ok = wait_warp(ctl.qfull + (qk & (uint32_t)pr), (qk >> pr) & 1u, abort_flag, kWaitQ) &&
              wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK);
         if (!ok) break;
         tc_fence_after();
@@ -639,7 +655,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       for (int j = 0; ok && j < jobs; ++j) {
         const int i = j >> two, st = j & 1;
         const bool more = j + 2 < jobs;
-        const Slot v(base + (uint32_t)v_index(i, n), (uint32_t)nst, t.inv_nst);
+        const Slot v(base + (uint32_t)v_index(i, n), rt);
         const Slot k = key_slot(more ? j + 2 : j);
         int s0, s1;
         key_steps(lo, hi, t0 + i, s0, s1);
@@ -647,9 +663,11 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const uint32_t acc = tb + 256 + st * kTile, p = tb + st * kTile;
         const bool fresh = two ? i == 0 : j < 2;
         // P is awaited last: nothing then stands between it and the products.  (The key
-        // tile of job j + 2 does not depend on job j: its slot was freed by an earlier one.)
+        // tile of job j + 2 does not depend on job j: its slot was freed by an earlier
+        // one.  Of an e4m3 cache's three slots that one is freed late: there the key
+        // tile is awaited behind the product with V.)
         ok = wait_warp(ctl.full + v.i, v.ph, abort_flag, kWaitV) &&
-             (!more || wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK)) &&
+             (E4M3 || !more || wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK)) &&
              wait_warp(ctl.pfull + st, (pph >> st) & 1u, abort_flag, kWaitP);
         if (!ok) break;
         pph ^= 1u << st;
@@ -663,6 +681,11 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             umma_ts_if(leader, acc, p + kk * 8, bd + (uint64_t)(kk * 128), idesc_o, kk != s0 || !fresh);
         }
         if (!two || st) umma_commit_if(leader, ctl.empty + v.i);
+        if (E4M3 && more) {
+          ok = wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK);
+          if (!ok) break;
+          tc_fence_after();
+        }
         if (more) scores(j + 2, k.i);
         else umma_commit_if(leader, ctl.ofull + st);
       }
@@ -683,8 +706,8 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       while (ok && walk.next(t, ctl, s)) {
         if (lane == 0 && s.slot == 1) t.rec[wid] = Rec{s.more, s.row0, s.ntok, s.h};
         for (int st = 0; ok && st < (s.two ? 2 : 1); ++st, ++qn) {
-          const uint32_t qb = qn & 1u;
-          ok = wait_warp(ctl.qempty + qb, ((qn >> 1) & 1u) ^ 1u, abort_flag, kWaitQFree);
+          const uint32_t qb = qn & (uint32_t)pair;
+          ok = wait_warp(ctl.qempty + qb, ((qn >> pair) & 1u) ^ 1u, abort_flag, kWaitQFree);
           if (ok && lane == 0) {
             mbar_arrive_expect_tx(ctl.qfull + qb, (uint32_t)(t.nhalf * t.tpt * t.group * 128));
             for (int h = 0; h < t.nhalf; ++h)
@@ -695,8 +718,9 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
       }
       // every copy has landed before the CTA may exit
-      for (uint32_t i = qn > 2 ? qn - 2 : 0; i < qn; ++i)
-        if (lane == 0) wait_end(ctl.qfull + (i & 1u), (i >> 1) & 1u);
+      const uint32_t held = 1u + (uint32_t)pair;
+      for (uint32_t i = qn > held ? qn - held : 0; i < qn; ++i)
+        if (lane == 0) wait_end(ctl.qfull + (i & (uint32_t)pair), (i >> pair) & 1u);
       __syncwarp();
     }
   } else if (warp < 12) {
@@ -777,7 +801,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           const int key0 = (s.t0 + i) * kTile;
           const int v0 = max(0, s.lo - key0), v1 = min(kTile, s.hi - key0);
           if (((v0 | v1) & 15) && v1 > v0) {
-            const Slot vk(base + (uint32_t)v_index(i, s.n), (uint32_t)nst, t.inv_nst);
+            const Slot vk(base + (uint32_t)v_index(i, s.n), rt);
             if (!wait_warp(ctl.full + vk.i, vk.ph, abort_flag, kWaitV)) {
               ok = false;
               break;
@@ -837,18 +861,21 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           }
         }
       } else {
-        ctl.xch[st][row] = make_float2(m, l);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.xbar);
-        if (!wait_warp(&ctl.xbar, xph, abort_flag, kWaitX)) {
-          ok = false;
-          break;
+        // stage 1's (m, l) to warpgroup 0, then stage 0's to warpgroup 1
+        float2 p0 = make_float2(m, l), p1 = p0;
+        for (int turn = 0; ok && turn < 2; ++turn) {
+          if (st != turn) ctl.xch[row] = make_float2(m, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.xbar);
+          ok = wait_warp(&ctl.xbar, xph, abort_flag, kWaitX);
+          xph ^= 1u;
+          if (st == turn) (st ? p0 : p1) = ctl.xch[row];
+          __syncwarp();
         }
-        xph ^= 1u;
+        if (!ok) break;
         tc_fence_after();
         if (warp_live) {
-          const float2 p0 = ctl.xch[0][row], p1 = ctl.xch[1][row];
           const float M = fmaxf(p0.x, p1.x);
           const float f0 = p0.y == 0.0f ? 0.0f : ex2(p0.x - (M == -kInf ? 0.0f : M));
           const float f1 = p1.y == 0.0f ? 0.0f : ex2(p1.x - (M == -kInf ? 0.0f : M));
@@ -899,7 +926,8 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     // A lane widens 16 codes of a row (two 16-byte chunks of a swizzle span).  Four
     // lanes take one span of a row and the next four that span of the row below, so
     // that the eight lanes of a store's phase write different banks; four rows at a
-    // time, 16 rows a warp.
+    // time, 16 rows a warp.  Every warp takes part in every tile: one that left out
+    // turns of a slot could mistake its barrier's phase.
     give_regs<kWideRegs8>();
     const int cw = warp - 12;
     const int span = (lane >> 3) & 1, ch = (lane & 3) + 4 * span;
@@ -911,7 +939,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         int tile;
         tile_of(idx, s.n, is_v, tile);
         const int key0 = (s.t0 + tile) * kTile;
-        const Slot from(k, (uint32_t)nraw, t.inv_nraw), to(k, (uint32_t)nst, t.inv_nst);
+        const Slot from(k, rc), to(k, rt);
         const uint32_t rs = from.i, slot = to.i;
         if (!wait_warp(ctl.rawfull + rs, from.ph, abort_flag, kWaitRaw) ||
             !wait_warp(ctl.empty + slot, to.ph ^ 1u, abort_flag, kWaitWide)) {
@@ -920,7 +948,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
         const uint8_t* src = raw + (size_t)rs * raw_bytes + (16 * cw + g) * D + ch * 16;
         uint8_t* dst = ring + (size_t)slot * stage_bytes + span * kSpan + (16 * cw + g) * 128;
-        const uint8_t* scales = raw + (size_t)rs * raw_bytes + kTile * D + 16 * cw + g;
+        const uint8_t* scales = scale_area + rs * kTile + 16 * cw + g;
         // only the part's first and last tiles hold rows that nobody sees: those
         // become zeros whatever they hold
         const int row0 = key0 + 16 * cw;
@@ -974,27 +1002,47 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 // ---------------------------------------------------------------------------
 // The join: items cut by a share's end, and the flags.
 // ---------------------------------------------------------------------------
-// One row from its parts: a warp takes every `stride`-th part from `first` on and
-// returns this lane's four columns (scaled to the maximum M of all parts).
-__device__ __forceinline__ float4 join_parts(const TileArgs& t, int c, int parts, int r, float M,
-                                             int first, int stride, float& L) {
+// One row from its parts (at most one per CTA).  The (m, l) of all parts are read at
+// once, a part per lane; the warp then adds up every `stride`-th part's O from `first`
+// on, 32 lanes by four columns.  Returns this lane's columns; M, L: of all parts.
+__device__ __forceinline__ float4 join_parts(const TileArgs& t, int c, int parts, int row, int first,
+                                             int stride, float& M, float& L) {
+  constexpr int kSets = (kMaxCtas + 31) / 32;
   const int lane = threadIdx.x & 31, D = t.a.c.head_dim;
-  float4 o = make_float4(0, 0, 0, 0);
+  auto place = [&](int p) { return (int64_t)(p ? 2 * (c + p) : 2 * c + 1) * kMaxRows + row; };
+  float2 ml[kSets];
+  M = -kInf;
+#pragma unroll
+  for (int k = 0; k < kSets; ++k) {
+    ml[k] = make_float2(-kInf, 0.0f);
+    if (32 * k + lane < parts) ml[k] = __ldcg(t.ml + place(32 * k + lane));
+    M = fmaxf(M, ml[k].x);
+  }
+  M = warp_max(M);
+  if (M == -kInf) M = 0.0f;
   L = 0.0f;
+  float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+  for (int k = 0; k < kSets; ++k) {
+    if (32 * k >= parts) break;
+    // (a part that sees nothing has l = 0, and its O was never written)
+    const float f = ml[k].y == 0.0f ? 0.0f : ex2(ml[k].x - M);
+    float l = ml[k].y == 0.0f ? 0.0f : f * ml[k].y;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    L += l;
+    const unsigned seen = __ballot_sync(0xffffffffu, ml[k].y != 0.0f);
+    const int last = min(32, parts - 32 * k);
 #pragma unroll 4
-  for (int p = first; p < parts; p += stride) {
-    const int slot = p ? 2 * (c + p) : 2 * c + 1;
-    const int64_t at = (int64_t)slot * kMaxRows + r;
-    const float2 ml = __ldcg(t.ml + at);
-    if (ml.y == 0.0f) continue;  // sees nothing of that part
-    const float f = ex2(ml.x - M);
-    L += f * ml.y;
-    if (lane * 4 < D) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(t.part + at * D) + lane);
-      o.x += f * x.x;
-      o.y += f * x.y;
-      o.z += f * x.z;
-      o.w += f * x.w;
+    for (int q = first; q < last; q += stride) {
+      const float g = __shfl_sync(0xffffffffu, f, q);
+      if (((seen >> q) & 1u) && lane * 4 < D) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(t.part + place(32 * k + q) * D) + lane);
+        o.x += g * x.x;
+        o.y += g * x.y;
+        o.z += g * x.z;
+        o.w += g * x.w;
+      }
     }
   }
   return o;
@@ -1009,7 +1057,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
   __shared__ int warp_rows[kWarps];
   __shared__ int most;
   __shared__ float4 so[kWarps][32];
-  __shared__ float sl[kWarps];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1059,19 +1106,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
     const int tok = k / t.group, hd = k - tok * t.group;
     const int row = tok / t.tpt * kTile + tok % t.tpt * t.group + hd;
     const int parts = r.more + 1;
-    float M = -kInf;
-    for (int p = lane; p < parts; p += 32) {
-      const int slot = p ? 2 * (c + p) : 2 * c + 1;
-      M = fmaxf(M, __ldcg(t.ml + (int64_t)slot * kMaxRows + row).x);
-    }
-    M = warp_max(M);
-    if (M == -kInf) M = 0.0f;
-    float L;
-    float4 o = join_parts(t, c, parts, row, M, wide ? warp : 0, wide ? kWarps : 1, L);
+    float M, L;
+    float4 o = join_parts(t, c, parts, row, wide ? warp : 0, wide ? kWarps : 1, M, L);
     if (wide) {
       __syncthreads();
       so[warp][lane] = o;
-      if (lane == 0) sl[warp] = L;
       __syncthreads();
       if (warp) continue;
       for (int w = 1; w < kWarps; ++w) {
@@ -1080,7 +1119,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
         o.y += x.y;
         o.z += x.z;
         o.w += x.w;
-        L += sl[w];
       }
     }
     const int64_t orow = (int64_t)(r.row0 + tok) * a.heads + r.h * t.group + hd;
@@ -1180,6 +1218,11 @@ bool encode_queries(CUtensorMap* map, const AttendArgs& a, int dim, int group, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+Ring make_ring(int n, int most) {
+  const uint32_t k = (uint32_t)(n < most ? n : most);
+  return Ring{k, (uint32_t)((0x100000000ull + k - 1) / k)};
+}
+
 constexpr size_t kRecBytes = 4096, kMlBytes = sizeof(float2) * 2 * kMaxCtas * kMaxRows;
 static_assert(kMaxCtas * (sizeof(Rec) + sizeof(int)) <= kRecBytes, "records");
 
@@ -1200,11 +1243,12 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
   t.group = a.heads / c.kv_heads;
   t.tpt = kTile / t.group;
   t.nhalf = c.head_dim > 64 ? 2 : 1;
-  t.nst = (e4m3 ? kRing8 : kRing16) / (t.nhalf * kSpan);
-  t.nraw = kRaw8 / (kTile * (c.head_dim + 1));
-  if (t.nraw > kMaxRaw) t.nraw = kMaxRaw;
-  t.inv_nst = (uint32_t)((0x100000000ull + t.nst - 1) / t.nst);
-  t.inv_nraw = (uint32_t)((0x100000000ull + t.nraw - 1) / t.nraw);
+  const int stage = t.nhalf * kSpan, codes = kTile * c.head_dim;
+  for (int two = 0; two < 2; ++two) {
+    const int spare = two ? 0 : kQBytes;
+    t.tiles[two] = make_ring(e4m3 ? kRing8 / stage : (kRing16 + spare) / stage, kMaxStages);
+    t.codes[two] = make_ring((kCodes + spare) / codes, kMaxRaw);
+  }
   t.box = c.page_size < kTile ? c.page_size : kTile;
   t.wide = ((uintptr_t)a.out & 31) == 0;
   // a scale of zero: every product times 1e-30 is zero beside 1, and the -inf of a
