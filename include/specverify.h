@@ -443,8 +443,8 @@ int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, con
  * q_n) (fp32 differences), from p_n if that has no positive entry, and from
  * p_gamma after a clean sweep, by the inverse transform: the smallest v with
  * w_0 + ... + w_v > u_gamma (w_0 + ... + w_{V-1}).  The sums are integers in
- * units of 2^-61 (each weight truncated to one), so they do not depend on the
- * order of summation.
+ * units of 2^-61 (each weight rounded to the nearest), so they do not depend on
+ * the order of summation.
  *   out_tokens, out_counts, out_flags as spec_verify.  A probability that is
  *   negative, not finite or above 2 counts as 0 and sets SV_FLAG_NONFINITE, as
  *   does a uniform outside [0, 1) (clamped into it; NaN as 0); a row whose sum

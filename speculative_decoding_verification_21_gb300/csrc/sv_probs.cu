@@ -12,6 +12,13 @@
 // (from L2) and stops inside it.  W is an integer in units of 2^-61, so the split
 // changes nothing, and the target floor(u W) is exact: u = m 2^-e with a 24-bit m,
 // so u W is a 128-bit product shifted right.
+//
+// Units without 64-bit conversions or shifts (those bound the kernel at three times
+// the time of its reads): adding a constant M rounds w to a multiple of M's last
+// place, and the sum's bits less M's are that multiple.  Three constants peel w into
+// multiples of 2^-21, 2^-44 and 2^-61; what each leaves is exact in fp32.  Two
+// entries share an instruction, and the three 32-bit sums of a batch of entries are
+// put together in 64 bits once a batch.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -51,9 +58,43 @@ __device__ __forceinline__ float sane(float p, bool& odd) {
   return ok ? p : 0.0f;
 }
 
-// w in units of 2^-61, 0 <= w <= 2 (the product is exact, the conversion truncates).
+// Constants whose last places are 2^-21, 2^-44 and 2^-61.
+constexpr float kM1 = 4.0f, kM2 = 1.5f * 0x1p-21f, kM3 = 1.5f * 0x1p-38f;
+
+// Sums of the three parts' bits over a batch; the constants' own bits are taken off
+// at its end.
+struct Parts {
+  uint32_t a = 0, b = 0, c = 0;
+};
+
+// Two weights 0 <= w <= 2 into the parts.
+__device__ __forceinline__ void add_parts(Parts& s, float w0, float w1) {
+  const uint64_t w = pack2(w0, w1), minus = pack2(-1.0f, -1.0f);
+  const uint64_t t1 = fadd2(w, pack2(kM1, kM1));
+  const uint64_t l1 = ffma2(fadd2(t1, pack2(-kM1, -kM1)), minus, w);
+  const uint64_t t2 = fadd2(l1, pack2(kM2, kM2));
+  const uint64_t l2 = ffma2(fadd2(t2, pack2(-kM2, -kM2)), minus, l1);
+  const uint64_t t3 = fadd2(l2, pack2(kM3, kM3));
+  float x, y;
+  unpack2(t1, x, y);
+  s.a += __float_as_uint(x) + __float_as_uint(y);
+  unpack2(t2, x, y);
+  s.b += __float_as_uint(x) + __float_as_uint(y);
+  unpack2(t3, x, y);
+  s.c += __float_as_uint(x) + __float_as_uint(y);
+}
+// The batch's sum in units of 2^-61 (n entries, n <= 64: no part passes 31 bits).
+__device__ __forceinline__ unsigned long long units(const Parts& s, int n) {
+  const int a = (int)(s.a - (uint32_t)n * __float_as_uint(kM1));
+  const int b = (int)(s.b - (uint32_t)n * __float_as_uint(kM2));
+  const int c = (int)(s.c - (uint32_t)n * __float_as_uint(kM3));
+  return (unsigned long long)(((long long)a << 40) + ((long long)b << 17) + c);
+}
+// One weight.
 __device__ __forceinline__ unsigned long long units(float w) {
-  return __float2ull_rz(w * 0x1p61f);
+  Parts s;
+  add_parts(s, w, 0.0f);
+  return units(s, 2);
 }
 
 // floor(u w) for 0 <= u < 1.
@@ -79,28 +120,62 @@ struct Piece {
   static constexpr int N = VEC ? VecInfo<DT>::kElems : 1;
 };
 
+// Raw vectors (or single entries) of p and q, and the weights that they hold.
+template <int DT, bool VEC>
+struct Entry;
+template <int DT>
+struct Entry<DT, true> {
+  uint4 p, q;
+  __device__ __forceinline__ void load(const Weights& r, int64_t i) {
+    constexpr int es = DT == SV_F32 ? 4 : 2;
+    p = ld_stream16((const char*)r.p + i * es);
+    q = r.q ? ld_stream16((const char*)r.q + i * es) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float* fp, float* fq) const {
+    unpack<DT>(p, fp);
+    unpack<DT>(q, fq);
+  }
+};
+template <int DT>
+struct Entry<DT, false> {
+  float p, q;
+  __device__ __forceinline__ void load(const Weights& r, int64_t i) {
+    p = load_logit<DT>(r.p, i);
+    q = r.q ? load_logit<DT>(r.q, i) : 0.0f;
+  }
+  __device__ __forceinline__ void get(float* fp, float* fq) const {
+    fp[0] = p;
+    fq[0] = q;
+  }
+};
+
+// max(0, p - q) of one entry's values.  A value is a probability for certain when
+// neither of its two highest bits is set (0 <= p < 2); only where some is set is each
+// looked at by itself.
+template <int N>
+__device__ __forceinline__ void weights_of(float* fp, float* fq, float* w, bool& odd) {
+  uint32_t all = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) all |= __float_as_uint(fp[j]) | __float_as_uint(fq[j]);
+  if (all & 0xC0000000u) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      fp[j] = sane(fp[j], odd);
+      fq[j] = sane(fq[j], odd);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) w[j] = fmaxf(0.0f, fp[j] - fq[j]);
+}
+
 template <int DT, bool VEC>
 __device__ __forceinline__ void load_weights(const Weights& r, int64_t i, float* w, bool& odd) {
   constexpr int N = Piece<DT, VEC>::N;
-  if (VEC) {
-    constexpr int es = DT == SV_F32 ? 4 : 2;
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>((const char*)r.p + i * es));
-    float fp[N];
-    unpack<DT>(a, fp);
-    float fq[N];
-    if (r.q) {
-      const uint4 b = __ldg(reinterpret_cast<const uint4*>((const char*)r.q + i * es));
-      unpack<DT>(b, fq);
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      w[j] = sane(fp[j], odd);
-      if (r.q) w[j] = fmaxf(0.0f, w[j] - sane(fq[j], odd));
-    }
-  } else {
-    w[0] = sane(load_logit<DT>(r.p, i), odd);
-    if (r.q) w[0] = fmaxf(0.0f, w[0] - sane(load_logit<DT>(r.q, i), odd));
-  }
+  Entry<DT, VEC> e;
+  float fp[N], fq[N];
+  e.load(r, i);
+  e.get(fp, fq);
+  weights_of<N>(fp, fq, w, odd);
 }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
@@ -160,31 +235,36 @@ __device__ __forceinline__ Run run_of(int64_t V, int parts, int part) {
 template <int DT, bool VEC>
 __device__ __forceinline__ unsigned long long sum_run(const Weights& r, Run run, bool& any,
                                                       bool& odd) {
-  constexpr int N = Piece<DT, VEC>::N, U = 4;
+  constexpr int N = Piece<DT, VEC>::N, U = VEC ? 2 : 8;  // entries of a batch in flight
   const int lane = threadIdx.x & 31;
   unsigned long long s = 0;
-  int64_t i = run.lo + (int64_t)lane * N;
-  for (; i + (U - 1) * 32 * N < run.hi; i += U * 32 * N) {
-    float w[U][N];
-#pragma unroll
-    for (int k = 0; k < U; ++k) load_weights<DT, VEC>(r, i + k * 32 * N, w[k], odd);
+  uint32_t some = 0;  // bits of any weight
+  for (int64_t i = run.lo + (int64_t)lane * N; i < run.hi; i += U * 32 * N) {
+    Entry<DT, VEC> e[U];
 #pragma unroll
     for (int k = 0; k < U; ++k)
+      if (k == 0 || i + k * 32 * N < run.hi) e[k].load(r, i + k * 32 * N);
+      else e[k] = Entry<DT, VEC>{};
+    Parts parts;
+    float last = 0.0f;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        s += units(w[k][j]);
-        any |= w[k][j] > 0.0f;
+    for (int k = 0; k < U; ++k) {
+      float fp[N], fq[N], w[N];
+      e[k].get(fp, fq);
+      weights_of<N>(fp, fq, w, odd);
+#pragma unroll
+      for (int j = 0; j < N; ++j) some |= __float_as_uint(w[j]);
+      if (N == 1) {  // two single entries make a pair
+        if (k & 1) add_parts(parts, last, w[0]);
+        last = w[0];
+      } else {
+#pragma unroll
+        for (int j = 0; j + 1 < N; j += 2) add_parts(parts, w[j], w[j + 1]);
       }
-  }
-  for (; i < run.hi; i += 32 * N) {
-    float w[N];
-    load_weights<DT, VEC>(r, i, w, odd);
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      s += units(w[j]);
-      any |= w[j] > 0.0f;
     }
+    s += units(parts, U * N);
   }
+  any |= some != 0;
   return s;
 }
 

@@ -57,7 +57,7 @@ def reference(p, q, x, u):
                 w = pn
         if not (w > 0).any():
             flags[b] |= sv.FLAG_ZERO_MASS
-        run = np.cumsum(np.floor(w.astype(np.float64) * 2.0 ** 61).astype(np.uint64))
+        run = np.cumsum(np.rint(w.astype(np.float64) * 2.0 ** 61).astype(np.uint64))
         ub = float(u[b, G])
         if not 0 <= ub < 1:
             odd = True
