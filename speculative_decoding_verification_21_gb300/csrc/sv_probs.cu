@@ -35,7 +35,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kProbWarps = 16;
+constexpr int kProbWarps = 8;
 constexpr int kProbThreads = kProbWarps * 32;
 constexpr int kProbMaxCluster = 8;
 
@@ -235,7 +235,7 @@ __device__ __forceinline__ Run run_of(int64_t V, int parts, int part) {
 template <int DT, bool VEC>
 __device__ __forceinline__ unsigned long long sum_run(const Weights& r, Run run, bool& any,
                                                       bool& odd) {
-  constexpr int N = Piece<DT, VEC>::N, U = VEC ? 2 : 8;  // entries of a batch in flight
+  constexpr int N = Piece<DT, VEC>::N, U = VEC ? 4 : 8;  // entries of a batch in flight
   const int lane = threadIdx.x & 31;
   unsigned long long s = 0;
   uint32_t some = 0;  // bits of any weight
@@ -269,54 +269,63 @@ __device__ __forceinline__ unsigned long long sum_run(const Weights& r, Run run,
 }
 
 // The first element of the run at which the running sum, `before` in front of
-// the run, passes `target`; -1 if none does.
+// the run, passes `target`; -1 if none does.  Four pieces are read at a time, so that
+// the search waits for memory once in 512 entries.
 template <int DT, bool VEC>
 __device__ int64_t find_in_run(const Weights& r, Run run, unsigned long long before,
                                unsigned long long target) {
-  constexpr int N = Piece<DT, VEC>::N;
+  constexpr int N = Piece<DT, VEC>::N, U = 4;
   const int lane = threadIdx.x & 31;
   bool odd = false;
-  for (int64_t base = run.lo; base < run.hi; base += 32 * N) {
-    const int64_t i = base + (int64_t)lane * N;
-    float w[N];
-    unsigned long long mine = 0;
-    const bool in = i < run.hi;
-    if (in) {
-      load_weights<DT, VEC>(r, i, w, odd);
+  for (int64_t base = run.lo; base < run.hi; base += U * 32 * N) {
+    Entry<DT, VEC> e[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t i = base + (k * 32 + lane) * N;
+      if (i < run.hi) e[k].load(r, i);
+      else e[k] = Entry<DT, VEC>{};
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      float fp[N], fq[N], w[N];
+      e[k].get(fp, fq);
+      weights_of<N>(fp, fq, w, odd);
+      unsigned long long mine = 0;
 #pragma unroll
       for (int j = 0; j < N; ++j) mine += units(w[j]);
-    }
-    unsigned long long scan = mine;  // inclusive over the lanes
+      unsigned long long scan = mine;  // inclusive over the lanes
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long v = __shfl_up_sync(0xffffffffu, scan, o);
-      if (lane >= o) scan += v;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + scan > target);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      int at = 0;
-      if (lane == l) {
-        unsigned long long c = before + scan - mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long v = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + scan > target);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        int at = 0;
+        if (lane == l) {
+          unsigned long long c = before + scan - mine;
+          bool found = false;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          c += units(w[j]);
-          if (c > target) {
-            at = j;
-            break;
+          for (int j = 0; j < N; ++j) {
+            c += units(w[j]);
+            if (!found && c > target) {
+              at = j;
+              found = true;
+            }
           }
         }
+        at = __shfl_sync(0xffffffffu, at, l);
+        return base + (int64_t)(k * 32 + l) * N + at;
       }
-      at = __shfl_sync(0xffffffffu, at, l);
-      return base + (int64_t)l * N + at;
+      before += __shfl_sync(0xffffffffu, scan, 31);
     }
-    before += __shfl_sync(0xffffffffu, scan, 31);
   }
   return -1;
 }
 
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kProbThreads, 2) k_verify_probs(ProbArgs a) {
+__global__ void __launch_bounds__(kProbThreads, 4) k_verify_probs(ProbArgs a) {
   __shared__ ProbShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -366,8 +375,9 @@ __global__ void __launch_bounds__(kProbThreads, 2) k_verify_probs(ProbArgs a) {
       cluster_any |= o->any != 0;
       cluster_odd |= o->odd != 0;
     }
-    cluster.sync();  // nobody leaves, or sums again, while its totals are read
+    cluster.barrier_arrive();  // its totals are read: the wait stands where they change or end
     if (cluster_any || !r.q) break;
+    cluster.barrier_wait();
     flags |= SV_FLAG_RESIDUAL_FALLBACK;
     r.q = nullptr;
   }
@@ -394,6 +404,7 @@ __global__ void __launch_bounds__(kProbThreads, 2) k_verify_probs(ProbArgs a) {
       if (a.out_flags) a.out_flags[b] = (uint8_t)flags;
     }
   }
+  cluster.barrier_wait();
 }
 
 template <int DT>
@@ -411,10 +422,12 @@ cudaError_t launch_verify_probs(const void* p, const void* q, const int32_t* x, 
                                 int B, int gamma, int64_t V, int dtype, int32_t* out_tokens,
                                 int32_t* out_counts, uint8_t* out_flags, cudaStream_t stream) {
   const ProbArgs a{p, q, x, u, B, gamma, V, out_tokens, out_counts, out_flags};
-  // CTAs per batch row: until the grid has two for each of 152 SMs, and while a
-  // CTA keeps at least 4096 entries.
+  // CTAs per batch row: as many as give each of 152 SMs a dozen (a batch of 256 rows of
+  // 152064: 72 us with 2048 CTAs of 256 threads, 100 us with 512; an SM then has rows of
+  // one and of two vectors to read, and others' reads while one searches), while a CTA
+  // keeps at least 2048 entries.
   int c = 1;
-  while (c < kProbMaxCluster && (int64_t)B * c < 304 && V / (2 * c) >= 4096) c *= 2;
+  while (c < kProbMaxCluster && (int64_t)B * c < 2048 && V / (2 * c) >= 2048) c *= 2;
   return dtype == SV_F32 ? launch_dt<SV_F32>(a, c, stream) : launch_dt<SV_BF16>(a, c, stream);
 }
 
