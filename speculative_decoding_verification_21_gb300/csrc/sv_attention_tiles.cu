@@ -21,16 +21,20 @@
 // of one row tile (a round's few tokens) gives them the key tiles alternately, and
 // their (m, l, O) are added up at its end.
 //
-// Roles: warp 0 fetches key and value pages (tensor copies, 128-byte swizzle),
+// Roles: warps 0 and 3 fetch key and value pages (tensor copies, 128-byte swizzle),
 // warp 1 issues the products, warp 2 fetches queries, warps 4-11 are the softmax,
-// and for e4m3 caches warps 12-19 widen the codes to 16 bits between the copies
+// and for e4m3 caches warps 12-27 widen the codes to 16 bits between the copies
 // and the products.  Every wait is bounded; one that gives up ends the CTA's roles
 // and flags the call.
 //
 // Waits of one CTA, by barrier: full/empty (key and value tiles in 16 bits),
 // rawfull/rawempty (e4m3 codes), qfull/qempty (query tiles), sfull (S ready),
 // pfull (P written, so S is free), ofull (last product of a stage done), xbar
-// (the two warpgroups at the end of a one-tile item).
+// (the two warpgroups at the end of a one-tile item).  Two warps (or two groups of
+// converters) that take a ring's tiles in turn leave out turns of a slot, and a
+// waiter who leaves out turns can take one phase of a barrier for another; so the
+// barriers that such waiters wait on are those of a ring of twice the slots, whose
+// every place belongs to one of the two.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -70,12 +74,12 @@ constexpr int kJoinThreads = 256;
 constexpr float kLag = 8.0f;
 // Threads, and the registers a thread is launched with and then takes by role (the
 // roles' sum must not pass what the launch gave, or the takers would wait forever).
-constexpr int kThreads16 = 384, kThreads8 = 640;
-constexpr int kRegs16 = 168, kRegs8 = 96;
+constexpr int kThreads16 = 384, kThreads8 = 896;
+constexpr int kRegs16 = 168, kRegs8 = 72;
 constexpr int kHelpRegs16 = 88, kSoftRegs16 = 208;
-constexpr int kHelpRegs8 = 64, kSoftRegs8 = 120, kWideRegs8 = 88;
+constexpr int kHelpRegs8 = 56, kSoftRegs8 = 112, kWideRegs8 = 56;
 static_assert(128 * kHelpRegs16 + 256 * kSoftRegs16 <= kThreads16 * kRegs16, "registers");
-static_assert(128 * kHelpRegs8 + 256 * kSoftRegs8 + 256 * kWideRegs8 <= kThreads8 * kRegs8, "registers");
+static_assert(128 * kHelpRegs8 + 256 * kSoftRegs8 + 512 * kWideRegs8 <= kThreads8 * kRegs8, "registers");
 
 // Slots of a ring, and ceil(2^32 / slots): slot and turn of tile k without a division.
 struct Ring {
@@ -87,6 +91,7 @@ struct TileArgs {
   int group, tpt;      // query heads per key head; tokens per row tile
   int nhalf;           // swizzle spans per row: 1 (head_dim <= 64) or 2
   Ring tiles[2], codes[2];  // of 16-bit tiles and of codes, without and with items of two
+  Ring tiles2[2], codes2[2];  // twice their slots (see the barriers)
   int box;             // tokens per copy: min(page_size, 128)
   int wide;            // outputs sit on 32-byte boundaries
   float c;             // scale log2 e, positive
@@ -104,7 +109,7 @@ struct Rec {
 
 // Control words of a CTA.
 struct Ctl {
-  uint64_t full[kMaxStages], empty[kMaxStages], rawfull[kMaxRaw], rawempty[kMaxRaw];
+  uint64_t full[kMaxStages], empty[2 * kMaxStages], rawfull[2 * kMaxRaw], rawempty[2 * kMaxRaw];
   uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], xbar, fin;
   uint32_t tmem;
   int abort;
@@ -503,11 +508,9 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   if (threadIdx.x == 0) {
     ctl.two = 0;
     ctl.abort = (smem_u32(smem) & 1023u) ? 1 : 0;  // the swizzle needs this alignment
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(ctl.full + i, E4M3 ? 8 : 1);
-      mbar_init(ctl.empty + i, 1);
-    }
-    for (int i = 0; i < kMaxRaw; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(ctl.full + i, E4M3 ? 8 : 1);
+    for (int i = 0; i < 2 * kMaxStages; ++i) mbar_init(ctl.empty + i, 1);
+    for (int i = 0; i < 2 * kMaxRaw; ++i) {
       mbar_init(ctl.rawfull + i, 1);
       mbar_init(ctl.rawempty + i, 8);
     }
@@ -534,7 +537,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   find_share(t, ctl);
   const int wid = (int)blockIdx.x;
   const int pair = ctl.two;                       // query tiles held: 1 + pair
-  const Ring rt = t.tiles[pair], rc = t.codes[pair];
+  const Ring rt = t.tiles[pair], rc = t.codes[pair], rt2 = t.tiles2[pair], rc2 = t.codes2[pair];
   uint8_t* const first = smem + (1 + pair) * kQBytes;
   uint8_t* const raw = first;                     // e4m3: codes
   uint8_t* const ring = E4M3 ? smem + 2 * kQBytes + kCodes : first;
@@ -543,71 +546,85 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   bool ok = *abort_flag == 0;
   if (warp < 4) give_regs<E4M3 ? kHelpRegs8 : kHelpRegs16>();
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // ---------------- fetch key and value pages ----------------
+    // The two warps take the tiles in turn: one alone (page numbers, a wait, up to 16
+    // copies a tile) is slower than HBM.  The lanes hold a tile's copies; its page
+    // numbers are read a tile ahead.
     const uint64_t pol = l2_policy_evict_first();
-    uint32_t issued = 0;  // tiles
-    const int copies = kTile / t.box;                         // copies along a tile
+    const uint32_t turn = warp == 3 ? 1u : 0u;
+    const Ring rs = E4M3 ? rc : rt, rs2 = E4M3 ? rc2 : rt2;
+    uint64_t* const freeb = E4M3 ? ctl.rawempty : ctl.empty;
+    uint32_t issued = 0, done = 0;  // tiles before the part; behind this warp's last
+    const int copies = kTile / t.box;                                  // along a tile
     const int part = E4M3 ? lane : (t.nhalf == 2 ? lane >> 1 : lane);  // this lane's copy ...
     const int half = E4M3 ? 0 : (t.nhalf == 2 ? lane & 1 : 0);         // ... and span
-    while (ok && walk.next(t, ctl, s)) {
+    for (; ok && walk.next(t, ctl, s); issued += 2u * (uint32_t)s.n) {
       const int32_t* table = a.b.table + (int64_t)s.b * a.b.max_pages;
-      for (int idx = 0; ok && idx < 2 * s.n; ++idx, ++issued) {
-        bool is_v;
+      // the copies of a tile that hold keys somebody sees, and this lane's page
+      auto look = [&](int idx, int& key0, int& from, int& upto, bool& is_v) {
         int tile;
         tile_of(idx, s.n, is_v, tile);
-        const int key0 = (s.t0 + tile) * kTile;
-        const int from = max(0, s.lo - key0) / t.box;                         // copies that hold
-        const int upto = min(copies, (max(0, s.hi - key0) + t.box - 1) / t.box);  // keys seen
+        key0 = (s.t0 + tile) * kTile;
+        from = max(0, s.lo - key0) / t.box;
+        upto = min(copies, (max(0, s.hi - key0) + t.box - 1) / t.box);
         const int mine = key0 + part * t.box;
-        int page = -1;
-        if (part >= from && part < upto) page = __ldg(table + (mine >> a.c.page_shift));
-        const Slot at(issued, E4M3 ? rc : rt);
-        const uint32_t slot = at.i, ph = at.ph;
-        uint64_t* const fullb = (E4M3 ? ctl.rawfull : ctl.full) + slot;
-        if (!wait_warp((E4M3 ? ctl.rawempty : ctl.empty) + slot, ph ^ 1u, abort_flag, kWaitSlot)) {
-          ok = false;
-          break;
-        }
+        return part >= from && part < upto ? __ldg(table + (mine >> a.c.page_shift)) : -1;
+      };
+      int key0, from, upto;
+      bool is_v;
+      int idx = (int)((issued ^ turn) & 1u);  // 2 n tiles: always two turns' worth
+      int page = look(idx, key0, from, upto, is_v);
+      for (; ok && idx < 2 * s.n; idx += 2) {
+        const uint32_t k = issued + (uint32_t)idx, slot = Slot(k, rs).i;
+        const Slot at2(k, rs2);
+        uint64_t* const fullb = E4M3 ? ctl.rawfull + at2.i : ctl.full + slot;
+        ok = wait_warp(freeb + at2.i, at2.i < rs.n ? at2.ph ^ 1u : at2.ph, abort_flag, kWaitSlot);
+        if (!ok) break;
         const int live = max(0, upto - from);
+        const bool mine = part >= from && part < upto;
+        const int in_page = (key0 + part * t.box) & (a.c.page_size - 1);
         uint32_t bytes = (uint32_t)(live * t.box * (E4M3 ? D : t.nhalf * 128));
-        uint8_t* const dst8 = raw + (size_t)slot * raw_bytes;
-        uint8_t* const scales = scale_area + slot * kTile + part * t.box;
-        // a page outside the pool arrives as zeros; so do its scales
-        const bool sound = page >= 0 && page < a.c.num_pages;
         if (E4M3) {
+          // a page outside the pool arrives as zeros; so do its scales
+          uint8_t* const dst = raw + (size_t)slot * raw_bytes + part * t.box * D;
+          uint8_t* const scales = scale_area + slot * kTile + part * t.box;
+          const bool sound = page >= 0 && page < a.c.num_pages;
           bytes += __popc(__ballot_sync(0xffffffffu, sound)) * t.box;
-          if (part >= from && part < upto && !sound)
+          if (mine && !sound)
             for (int e = 0; e < t.box; e += 16)
               *reinterpret_cast<uint4*>(scales + e) = make_uint4(0, 0, 0, 0);
           __syncwarp();
-        }
-        if (lane == 0) mbar_arrive_expect_tx(fullb, bytes);
-        __syncwarp();
-        if (part >= from && part < upto) {
-          const int slot_in_page = mine & (a.c.page_size - 1);
-          if (E4M3) {
-            tma_load_4d_hint(dst8 + part * t.box * D, is_v ? &mv : &mk, 0, slot_in_page, s.h, page,
-                             fullb, pol);
+          if (lane == 0) mbar_arrive_expect_tx(fullb, bytes);
+          __syncwarp();
+          if (mine) {
+            tma_load_4d_hint(dst, is_v ? &mv : &mk, 0, in_page, s.h, page, fullb, pol);
             if (sound)
               bulk_load(scales,
                         (is_v ? a.c.vs : a.c.ks) +
-                            ((int64_t)page * a.c.kv_heads + s.h) * a.c.page_size + slot_in_page,
+                            ((int64_t)page * a.c.kv_heads + s.h) * a.c.page_size + in_page,
                         (uint32_t)t.box, fullb);
-          } else {
-            uint8_t* const dst = ring + (size_t)slot * stage_bytes;
-            tma_load_4d_hint(dst + half * kSpan + part * t.box * 128, is_v ? &mv : &mk, 64 * half,
-                             slot_in_page, s.h, page, fullb, pol);
           }
+        } else {
+          uint8_t* const dst =
+              ring + (size_t)slot * stage_bytes + half * kSpan + part * t.box * 128;
+          if (lane == 0) mbar_arrive_expect_tx(fullb, bytes);
+          __syncwarp();
+          if (mine)
+            tma_load_4d_hint(dst, is_v ? &mv : &mk, 64 * half, in_page, s.h, page, fullb, pol);
         }
+        __syncwarp();
+        done = k + 1;
+        if (idx + 2 < 2 * s.n) page = look(idx + 2, key0, from, upto, is_v);
       }
     }
     // every copy has landed before the CTA may exit
-    const uint32_t ns = E4M3 ? rc.n : rt.n;
-    for (uint32_t i = 0; i < ns && i < issued; ++i) {
-      const uint32_t last = (issued - 1u) - ((issued - 1u - i) % ns);
-      if (lane == 0) wait_end((E4M3 ? ctl.rawfull : ctl.full) + i, (last / ns) & 1u);
+    const uint32_t end = ok ? issued : done;
+    for (uint32_t k = end > rs.n ? end - rs.n : 0; k < end; ++k) {
+      const Slot at(k, E4M3 ? rc2 : rt);
+      if (lane == 0 && (k & 1u) == turn) wait_end((E4M3 ? ctl.rawfull : ctl.full) + at.i, at.ph);
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------- issue the products ----------------
     const uint32_t leader = elect_leader();
@@ -629,6 +646,8 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       auto key_slot = [&](int j) {
         return Slot(base + (uint32_t)k_index(j >> two), rt);
       };
+      // whoever waits for tile k's slot waits for tile k + n, the slot's next
+      auto freed = [&](uint32_t k) { return ctl.empty + Slot(k + rt.n, rt2).i; };
       auto scores = [&](int j, uint32_t slot) {
         const int i = j >> two, st = j & 1;
         const uint32_t qb = (qn + (uint32_t)(two & st)) & (uint32_t)pr;
@@ -640,7 +659,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           if (kk < ksteps) umma_ss_if(leader, acc, ad + o, bd + o, idesc_s, kk != 0);
         }
         umma_commit_if(leader, ctl.sfull + st);
-        if (!two || st) umma_commit_if(leader, ctl.empty + slot);
+        if (!two || st) umma_commit_if(leader, freed(base + (uint32_t)k_index(i)));
         if (i == n - 1) umma_commit_if(leader, ctl.qempty + qb);
       };
       for (int j = 0; j < 2 && j < jobs; ++j) {
@@ -680,7 +699,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           for (int kk = s0; kk < s1; ++kk)
             umma_ts_if(leader, acc, p + kk * 8, bd + (uint64_t)(kk * 128), idesc_o, kk != s0 || !fresh);
         }
-        if (!two || st) umma_commit_if(leader, ctl.empty + v.i);
+        if (!two || st) umma_commit_if(leader, freed(base + (uint32_t)v_index(i, n)));
         if (E4M3 && more) {
           ok = wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK);
           if (!ok) break;
@@ -695,34 +714,32 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     // all products complete before tensor memory is released
     umma_commit_if(leader, &ctl.fin);
     wait_end(&ctl.fin, 0);
-  } else if (warp < 4) {
-    // ---------------- fetch query tiles (warp 2) ----------------
+  } else if (warp == 2) {
+    // ---------------- fetch query tiles ----------------
     // A copy takes tpt tokens by group heads, rows in the order of the tile.  Tokens
     // behind the sequence's last are other sequences' or zeros: nobody reads their rows.
-    if (warp == 2) {
-      const uint64_t pol = l2_policy_evict_first();
-      uint32_t qn = 0;
-      if (lane == 0) t.rec[wid].more = 0;
-      while (ok && walk.next(t, ctl, s)) {
-        if (lane == 0 && s.slot == 1) t.rec[wid] = Rec{s.more, s.row0, s.ntok, s.h};
-        for (int st = 0; ok && st < (s.two ? 2 : 1); ++st, ++qn) {
-          const uint32_t qb = qn & (uint32_t)pair;
-          ok = wait_warp(ctl.qempty + qb, ((qn >> pair) & 1u) ^ 1u, abort_flag, kWaitQFree);
-          if (ok && lane == 0) {
-            mbar_arrive_expect_tx(ctl.qfull + qb, (uint32_t)(t.nhalf * t.tpt * t.group * 128));
-            for (int h = 0; h < t.nhalf; ++h)
-              tma_load_3d_hint(qbuf + qb * kQBytes + h * kSpan, &mq, 64 * h, s.h * t.group,
-                               s.row0 + st * t.tpt, ctl.qfull + qb, pol);
-          }
-          __syncwarp();
+    const uint64_t pol = l2_policy_evict_first();
+    uint32_t qn = 0;
+    if (lane == 0) t.rec[wid].more = 0;
+    while (ok && walk.next(t, ctl, s)) {
+      if (lane == 0 && s.slot == 1) t.rec[wid] = Rec{s.more, s.row0, s.ntok, s.h};
+      for (int st = 0; ok && st < (s.two ? 2 : 1); ++st, ++qn) {
+        const uint32_t qb = qn & (uint32_t)pair;
+        ok = wait_warp(ctl.qempty + qb, ((qn >> pair) & 1u) ^ 1u, abort_flag, kWaitQFree);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(ctl.qfull + qb, (uint32_t)(t.nhalf * t.tpt * t.group * 128));
+          for (int h = 0; h < t.nhalf; ++h)
+            tma_load_3d_hint(qbuf + qb * kQBytes + h * kSpan, &mq, 64 * h, s.h * t.group,
+                             s.row0 + st * t.tpt, ctl.qfull + qb, pol);
         }
+        __syncwarp();
       }
-      // every copy has landed before the CTA may exit
-      const uint32_t held = 1u + (uint32_t)pair;
-      for (uint32_t i = qn > held ? qn - held : 0; i < qn; ++i)
-        if (lane == 0) wait_end(ctl.qfull + (i & (uint32_t)pair), (i >> pair) & 1u);
-      __syncwarp();
     }
+    // every copy has landed before the CTA may exit
+    const uint32_t held = 1u + (uint32_t)pair;
+    for (uint32_t i = qn > held ? qn - held : 0; i < qn; ++i)
+      if (lane == 0) wait_end(ctl.qfull + (i & (uint32_t)pair), (i >> pair) & 1u);
+    __syncwarp();
   } else if (warp < 12) {
     // ---------------- softmax and output ----------------
     take_regs<E4M3 ? kSoftRegs8 : kSoftRegs16>();
@@ -923,26 +940,29 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     }
   } else if (E4M3) {
     // ---------------- widen e4m3 codes ----------------
+    // Two groups of eight warps take the tiles in turn, so that one tile's loads and
+    // stores stand beside the other's arithmetic.
     // A lane widens 16 codes of a row (two 16-byte chunks of a swizzle span).  Four
     // lanes take one span of a row and the next four that span of the row below, so
     // that the eight lanes of a store's phase write different banks; four rows at a
-    // time, 16 rows a warp.  Every warp takes part in every tile: one that left out
-    // turns of a slot could mistake its barrier's phase.
+    // time, 16 rows a warp.
     give_regs<kWideRegs8>();
-    const int cw = warp - 12;
+    const int cw = (warp - 12) & 7;
+    const uint32_t group = (uint32_t)(warp - 12) >> 3;
     const int span = (lane >> 3) & 1, ch = (lane & 3) + 4 * span;
     const int g = ((lane >> 2) & 1) + 2 * (lane >> 4);
     uint32_t k = 0;
     while (ok && walk.next(t, ctl, s)) {
       for (int idx = 0; ok && idx < 2 * s.n; ++idx, ++k) {
+        if ((k & 1u) != group) continue;
         bool is_v;
         int tile;
         tile_of(idx, s.n, is_v, tile);
         const int key0 = (s.t0 + tile) * kTile;
-        const Slot from(k, rc), to(k, rt);
-        const uint32_t rs = from.i, slot = to.i;
-        if (!wait_warp(ctl.rawfull + rs, from.ph, abort_flag, kWaitRaw) ||
-            !wait_warp(ctl.empty + slot, to.ph ^ 1u, abort_flag, kWaitWide)) {
+        const uint32_t rs = Slot(k, rc).i, slot = Slot(k, rt).i;
+        const Slot from(k, rc2), to(k, rt2);
+        if (!wait_warp(ctl.rawfull + from.i, from.ph, abort_flag, kWaitRaw) ||
+            !wait_warp(ctl.empty + to.i, to.i < rt.n ? to.ph ^ 1u : to.ph, abort_flag, kWaitWide)) {
           ok = false;
           break;
         }
@@ -986,7 +1006,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(ctl.full + slot);
-          mbar_arrive(ctl.rawempty + rs);
+          mbar_arrive(ctl.rawempty + Slot(k + rc.n, rc2).i);
         }
       }
     }
@@ -1248,6 +1268,8 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
     const int spare = two ? 0 : kQBytes;
     t.tiles[two] = make_ring(e4m3 ? kRing8 / stage : (kRing16 + spare) / stage, kMaxStages);
     t.codes[two] = make_ring((kCodes + spare) / codes, kMaxRaw);
+    t.tiles2[two] = make_ring(2 * t.tiles[two].n, 2 * kMaxStages);
+    t.codes2[two] = make_ring(2 * t.codes[two].n, 2 * kMaxRaw);
   }
   t.box = c.page_size < kTile ? c.page_size : kTile;
   t.wide = ((uintptr_t)a.out & 31) == 0;
