@@ -93,6 +93,7 @@ struct TileArgs {
   Ring tiles[2], codes[2];  // of 16-bit tiles and of codes, without and with items of two
   Ring tiles2[2], codes2[2];  // twice their slots (see the barriers)
   int box;             // tokens per copy: min(page_size, 128)
+  int fetchers;        // warps that fetch key and value tiles
   int wide;            // outputs sit on 32-byte boundaries
   float c;             // scale log2 e, positive
   float* part;         // [2 * kMaxCtas][kMaxRows][head_dim]
@@ -184,18 +185,37 @@ __device__ __forceinline__ long long head_units(const Seq& q, int per_item, int 
   return u;
 }
 
-// The start of this CTA's share (all threads; ends with a barrier).
+// a / b and a % b of non-negative numbers, in 32 bits where they fit (a 64-bit division
+// is a long subroutine).
+__device__ __forceinline__ long long divide(long long a, long long b, long long& rest) {
+  if (((a | b) >> 32) == 0) {
+    const uint32_t q = (uint32_t)a / (uint32_t)b;
+    rest = (uint32_t)a - q * (uint32_t)b;
+    return q;
+  }
+  const long long q = a / b;
+  rest = a - q * b;
+  return q;
+}
+
+// The start of this CTA's share (all threads; ends with a barrier).  Each warp looks
+// at its stretch of the sequences, 32 at a time.
 __device__ void find_share(const TileArgs& t, Ctl& ctl) {
   const BatchView& bv = t.a.b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (int)(blockDim.x >> 5);
   const int per_item = 2 * t.tpt, H = t.a.c.kv_heads, ps = t.a.c.page_size;
   const int chunk = (bv.B + nw - 1) / nw;
   const int b0 = min(bv.B, warp * chunk), b1 = min(bv.B, b0 + chunk);
-  long long sum = 0;
-  for (int base = b0; base < b1; base += 32) {
-    Seq q{};
+  Seq q{};
+  long long per_head = 0, sum = 0;
+  auto look = [&](int base) {
+    q = Seq{};
     if (base + lane < b1) q = load_seq(bv, base + lane, ps);
-    sum += warp_sum64(head_units(q, per_item, t.a.window) * H);
+    per_head = head_units(q, per_item, t.a.window);
+  };
+  for (int base = b0; base < b1; base += 32) {
+    look(base);
+    sum += warp_sum64(per_head * H);
     if (q.n > t.tpt) ctl.two = 1;
   }
   if (lane == 0) ctl.warp_units[warp] = sum;
@@ -205,19 +225,16 @@ __device__ void find_share(const TileArgs& t, Ctl& ctl) {
     ctl.h = ctl.qt = ctl.off = 0;
   }
   __syncthreads();
-  long long before = 0, total = 0;
-  for (int w = 0; w < nw; ++w) {
-    const long long u = ctl.warp_units[w];
-    if (w < warp) before += u;
-    total += u;
-  }
-  const long long share = max(1ll, (total + gridDim.x - 1) / (long long)gridDim.x);
+  // the units of the warps before this one, and of all
+  const long long mine = lane < nw ? ctl.warp_units[lane] : 0;
+  const long long total = warp_sum64(mine);
+  long long before = __shfl_sync(0xffffffffu, warp_scan64(mine) - mine, warp);
+  long long rest;
+  const long long share = max(1ll, divide(total + gridDim.x - 1, (long long)gridDim.x, rest));
   const long long start = share * blockIdx.x;
   if (start >= before && start < before + sum) {  // this warp's sequences hold the start
     for (int base = b0; base < b1; base += 32) {
-      Seq q{};
-      if (base + lane < b1) q = load_seq(bv, base + lane, ps);
-      const long long per_head = head_units(q, per_item, t.a.window);
+      if (b1 - b0 > 32) look(base);  // (else they are still here)
       const long long scan = warp_scan64(per_head * H);
       const unsigned hit = __ballot_sync(0xffffffffu, start < before + scan);
       if (!hit) {
@@ -230,8 +247,7 @@ __device__ void find_share(const TileArgs& t, Ctl& ctl) {
       s.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
       const long long ph = __shfl_sync(0xffffffffu, per_head, src);
       long long r = start - before - __shfl_sync(0xffffffffu, scan - per_head * H, src);
-      const int h = (int)(r / ph);
-      r -= h * ph;
+      const int h = (int)divide(r, ph, r);
       const int m = (s.n + per_item - 1) / per_item;
       for (int q0 = 0; q0 < m; q0 += 32) {
         const long long c = q0 + lane < m ? item_span(s, per_item, q0 + lane, t.a.window).count : 0;
@@ -546,9 +562,9 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   bool ok = *abort_flag == 0;
   if (warp < 4) give_regs<E4M3 ? kHelpRegs8 : kHelpRegs16>();
 
-  if (warp == 0 || warp == 3) {
+  if (warp == 0 || (warp == 3 && t.fetchers == 2)) {
     // ---------------- fetch key and value pages ----------------
-    // The two warps take the tiles in turn: one alone (page numbers, a wait, up to 16
+    // Two warps take the tiles in turn where one alone (page numbers, a wait, up to 16
     // copies a tile) is slower than HBM.  The lanes hold a tile's copies; its page
     // numbers are read a tile ahead.
     const uint64_t pol = l2_policy_evict_first();
@@ -573,9 +589,9 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       };
       int key0, from, upto;
       bool is_v;
-      int idx = (int)((issued ^ turn) & 1u);  // 2 n tiles: always two turns' worth
+      int idx = (int)turn;  // (a part has 2 n tiles: issued is even)
       int page = look(idx, key0, from, upto, is_v);
-      for (; ok && idx < 2 * s.n; idx += 2) {
+      for (; ok && idx < 2 * s.n; idx += t.fetchers) {
         const uint32_t k = issued + (uint32_t)idx, slot = Slot(k, rs).i;
         const Slot at2(k, rs2);
         uint64_t* const fullb = E4M3 ? ctl.rawfull + at2.i : ctl.full + slot;
@@ -615,14 +631,14 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
         __syncwarp();
         done = k + 1;
-        if (idx + 2 < 2 * s.n) page = look(idx + 2, key0, from, upto, is_v);
+        if (idx + t.fetchers < 2 * s.n) page = look(idx + t.fetchers, key0, from, upto, is_v);
       }
     }
     // every copy has landed before the CTA may exit
     const uint32_t end = ok ? issued : done;
     for (uint32_t k = end > rs.n ? end - rs.n : 0; k < end; ++k) {
       const Slot at(k, E4M3 ? rc2 : rt);
-      if (lane == 0 && (k & 1u) == turn) wait_end((E4M3 ? ctl.rawfull : ctl.full) + at.i, at.ph);
+      if (lane == 0 && (t.fetchers == 1 || (k & 1u) == turn)) wait_end((E4M3 ? ctl.rawfull : ctl.full) + at.i, at.ph);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -740,7 +756,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     for (uint32_t i = qn > held ? qn - held : 0; i < qn; ++i)
       if (lane == 0) wait_end(ctl.qfull + (i & (uint32_t)pair), (i >> pair) & 1u);
     __syncwarp();
-  } else if (warp < 12) {
+  } else if (warp >= 4 && warp < 12) {
     // ---------------- softmax and output ----------------
     take_regs<E4M3 ? kSoftRegs8 : kSoftRegs16>();
     const int st = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
@@ -850,8 +866,8 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       }
       const int64_t prow = ((int64_t)(2 * wid + (s.slot > 0 ? 1 : 0)) * kMaxRows + (s.two ? st * kTile : 0) + row);
       const int64_t orow = (int64_t)(s.row0 + tok_off + my_tok) * a.heads + s.h * t.group + my_head;
-      if (s.two) {
-        if (warp_live) {
+      if (s.two || s.n == 1) {  // (of a single key tile, all is warpgroup 0's)
+        if (warp_live && (s.two || st == 0)) {
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
           for (int u = 0; u < units; ++u) {
             uint32_t r[16];
@@ -938,7 +954,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         tc_fence_after();
       }
     }
-  } else if (E4M3) {
+  } else if (E4M3 && warp >= 12) {
     // ---------------- widen e4m3 codes ----------------
     // Two groups of eight warps take the tiles in turn, so that one tile's loads and
     // stores stand beside the other's arithmetic.
@@ -1053,7 +1069,7 @@ __device__ __forceinline__ float4 join_parts(const TileArgs& t, int c, int parts
     L += l;
     const unsigned seen = __ballot_sync(0xffffffffu, ml[k].y != 0.0f);
     const int last = min(32, parts - 32 * k);
-#pragma unroll 4
+#pragma unroll 8
     for (int q = first; q < last; q += stride) {
       const float g = __shfl_sync(0xffffffffu, f, q);
       if (((seen >> q) & 1u) && lane * 4 < D) {
@@ -1115,7 +1131,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
   __syncthreads();
   const int total = rows_to[kMaxCtas - 1];
   // few rows of many parts: a whole block to a row; else a warp to a row
-  const bool wide = most >= 8 && total <= 4 * join_blocks;
+  const bool wide = most >= 8 && total <= 2 * join_blocks;
   const int step = wide ? join_blocks : join_blocks * kWarps;
   for (int j = wide ? (int)blockIdx.x : (int)blockIdx.x * kWarps + warp; j < total; j += step) {
     int c = 0;
@@ -1273,6 +1289,10 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
   }
   t.box = c.page_size < kTile ? c.page_size : kTile;
   t.wide = ((uintptr_t)a.out & 31) == 0;
+  // a second warp fetches from four copies a tile on (32 sequences of e4m3 in pages of
+  // 64: 552 -> 466 us; one sequence of 64-wide heads in pages of 128: 36 us with one
+  // warp, 40 with two)
+  t.fetchers = kTile / t.box * (e4m3 ? 2 : t.nhalf) >= 4 ? 2 : 1;
   // a scale of zero: every product times 1e-30 is zero beside 1, and the -inf of a
   // key that is not seen stays one
   t.c = a.scale_log2 == 0.0f ? 1e-30f : a.scale_log2;
@@ -1301,7 +1321,9 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
                              : (e4m3 ? k_attend_tiles<SV_F16, true> : k_attend_tiles<SV_F16, false>);
   e = launch_pdl(k, dim3(ctas), dim3(e4m3 ? kThreads8 : kThreads16), kSmemBytes, stream, mq, mk, mv, t);
   if (e != cudaSuccess) return e;
-  const int join_blocks = 2 * ctas;
+  // all that fit (a warp's row is a chain of three loads), but no more blocks than rows
+  const int64_t rows = (int64_t)a.b.total * a.heads;
+  const int join_blocks = (int)(rows < 6 * ctas ? rows : 6 * ctas);
   const int flag_blocks = a.flags ? (a.b.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
   auto* j = dtype == SV_BF16 ? k_attend_join<SV_BF16> : k_attend_join<SV_F16>;
   return launch_pdl(j, dim3(join_blocks + flag_blocks), dim3(kJoinThreads), 0, stream, t, ctas,
