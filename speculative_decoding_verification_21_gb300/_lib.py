@@ -133,9 +133,15 @@ def status_string(status: int) -> str:
     return load().sv_status_string(int(status)).decode()
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -432,12 +438,29 @@ def alloc_kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
 
 
 def _row_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return SV_BF16
-    if t.dtype == torch.float16:
-        return SV_F16
-    raise TypeError(f"rows must be bfloat16 or float16, got {t.dtype}")
+    code = _row_codes.get(t.dtype)
+    if code is None:
+        torch = _torch()
+        _row_codes[torch.bfloat16], _row_codes[torch.float16] = SV_BF16, SV_F16
+        code = _row_codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"rows must be bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+_row_codes = {}  # torch dtype -> dtype code
+
+
+def _address(t):
+    """A tensor's address as the plain int that a pointer argument takes."""
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(stream, device) -> int:
+    """The raw stream that a call is queued on: `stream`, or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch().cuda.current_stream(device).cuda_stream
 
 
 def _check_rows(t, heads, cache, what):
@@ -452,7 +475,8 @@ def _check_rows(t, heads, cache, what):
 def _check_index(block_table, start, length):
     torch = _torch()
     _check_cuda(block_table, start, length)
-    if block_table.dtype != torch.int32 or start.dtype != torch.int32 or length.dtype != torch.int32:
+    i32 = torch.int32
+    if block_table.dtype != i32 or start.dtype != i32 or length.dtype != i32:
         raise TypeError("block_table, q_start and lengths must be int32")
     B = length.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] != B or tuple(start.shape) != (B + 1,):
@@ -467,19 +491,20 @@ def spec_kv_append(cache: KVCache, new_k, new_v, block_table, q_start, kv_len, *
     cache's pages: sequence b's rows q_start[b] .. q_start[b+1]-1 become its last
     tokens before kv_len[b].  Returns a dict with flags [B] uint8 (if want_flags)."""
     torch = _torch()
-    L = load()
+    L = _lib or load()
     _check_rows(new_k, cache.kv_heads, cache, "new_k")
     if new_v.shape != new_k.shape or new_v.dtype != new_k.dtype or new_v.stride() != new_k.stride():
         raise ValueError("new_v must match new_k in shape, type and strides")
     B = _check_index(block_table, q_start, kv_len)
+    dev = new_k.device
     o = dict(out or {})
     if want_flags:
-        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=new_k.device))
+        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
     batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
                          new_k.shape[0], B, block_table.shape[1])
-    rc = L.spec_kv_append(cache._ref, ctypes.addressof(batch), _ptr(new_k), _ptr(new_v),
+    rc = L.spec_kv_append(cache._ref, ctypes.addressof(batch), _address(new_k), _address(new_v),
                           _row_code(new_k), new_k.stride(0), new_k.stride(1),
-                          _ptr(o.get("flags")), _stream_handle(stream))
+                          _address(o.get("flags")), _stream_of(stream, dev))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_kv_append")
     return o
@@ -492,7 +517,7 @@ def spec_kv_read(cache: KVCache, block_table, first, out_start, total: int, *, d
     16-bit type (default bfloat16) for a float8_e4m3fn cache.  Returns a dict:
     k, v [total, kv_heads, head_dim], flags [B] uint8 (if want_flags)."""
     torch = _torch()
-    L = load()
+    L = _lib or load()
     B = _check_index(block_table, out_start, first)
     if dtype is None:
         dtype = torch.bfloat16 if cache.dtype == torch.float8_e4m3fn else cache.dtype
@@ -508,9 +533,9 @@ def spec_kv_read(cache: KVCache, block_table, first, out_start, total: int, *, d
         if tuple(o[name].shape) != (total, cache.kv_heads, cache.head_dim) or \
                 o[name].dtype != dtype:
             raise ValueError("out k, v: [total, kv_heads, head_dim] of the asked type")
-    rc = L.spec_kv_read(cache._ref, _ptr(block_table), _ptr(first), _ptr(out_start), B,
-                        block_table.shape[1], int(total), _ptr(o["k"]), _ptr(o["v"]),
-                        _row_code(o["k"]), _ptr(o.get("flags")), _stream_handle(stream))
+    rc = L.spec_kv_read(cache._ref, _address(block_table), _address(first), _address(out_start), B,
+                        block_table.shape[1], int(total), _address(o["k"]), _address(o["v"]),
+                        _row_code(o["k"]), _address(o.get("flags")), _stream_of(stream, dev))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_kv_read")
     return o
@@ -534,7 +559,7 @@ def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, sca
     out [total, heads, head_dim], lse [total, heads] float32 (if want_lse),
     flags [B] uint8 (if want_flags)."""
     torch = _torch()
-    L = load()
+    L = _lib or load()
     _check_rows(q, 0, cache, "q")
     B = _check_index(block_table, q_start, kv_len)
     total, heads, dim = q.shape
@@ -549,16 +574,16 @@ def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, sca
     if want_flags:
         o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
     _check_cuda(o["out"], o.get("lse"))
-    sh = _stream_handle(stream)
+    sh = _stream_of(stream, dev)
     need = attention_workspace_bytes(cache, heads)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value)
+    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh)
     batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), total, B,
                          block_table.shape[1])
-    rc = L.spec_chunk_attention(cache._ref, ctypes.addressof(batch), _ptr(q), _row_code(q), heads,
+    rc = L.spec_chunk_attention(cache._ref, ctypes.addressof(batch), _address(q), _row_code(q), heads,
                                 q.stride(0), q.stride(1),
                                 dim ** -0.5 if scale is None else float(scale), int(window),
-                                _ptr(o["out"]), _ptr(o.get("lse")), _ptr(o.get("flags")),
-                                _ptr(ws), ws.numel(), sh)
+                                _address(o["out"]), _address(o.get("lse")), _address(o.get("flags")),
+                                _address(ws), ws.numel(), sh)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_chunk_attention")
     return o
@@ -570,7 +595,7 @@ def spec_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, *,
     [B, gamma+1] float32 (the accept tests', then the draw's).  Returns a dict:
     tokens [B, g+1] int32, counts [B] int32, flags [B] uint8 (if want_flags)."""
     torch = _torch()
-    L = load()
+    L = _lib or load()
     B, g1, V = target_probs.shape
     g = g1 - 1
     if tuple(draft_probs.shape) != (B, g, V) or tuple(draft_tokens.shape) != (B, g) or \
@@ -590,10 +615,10 @@ def spec_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, *,
         o["counts"] = torch.empty((B,), dtype=torch.int32, device=dev)
     if want_flags:
         o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
-    rc = L.spec_verify_probs(_ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens),
-                             _ptr(uniforms), B, g, V, _dtype_code(target_probs),
-                             _ptr(o["tokens"]), _ptr(o["counts"]), _ptr(o.get("flags")),
-                             _stream_handle(stream))
+    rc = L.spec_verify_probs(_address(target_probs), _address(draft_probs), _address(draft_tokens),
+                             _address(uniforms), B, g, V, _dtype_code(target_probs),
+                             _address(o["tokens"]), _address(o["counts"]), _address(o.get("flags")),
+                             _stream_of(stream, dev))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_probs")
     return o
