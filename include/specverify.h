@@ -361,7 +361,7 @@ typedef struct {
   const int32_t* kv_len;       /* [B]            */
   int64_t total;               /* rows of the packed arrays (>= q_start[B])    */
   int32_t B;
-  int32_t max_pages;
+  int32_t max_pages;           /* max_pages * page_size <= 2^31 - 1024 */
 } sv_kv_batch;
 
 /*
@@ -418,9 +418,10 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  *             SV_FLAG_TIMEOUT on every sequence if a bounded device-side wait
  *             gave up (outputs are then unspecified)
  * A query that sees no key (kv_len shorter than the chunk) gets out = 0 and
- * lse = -inf.  Slots behind kv_len may hold anything.  A key or value inside
- * kv_len that is not finite may reach queries of the same chunk that do not see
- * it (their weight for it is 0).
+ * lse = -inf.  Slots behind kv_len, and in front of every window of the chunk, may
+ * hold anything.  A value inside that is not finite may reach queries of the same
+ * chunk that do not see it (their weight for it is 0, and 0 times infinity is NaN).
+ * Outputs are the same bits every time.
  *   workspace >= sv_attention_workspace_bytes(cache, heads), 256-byte aligned
  */
 int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, const void* q,

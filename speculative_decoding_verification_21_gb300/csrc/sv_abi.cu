@@ -82,6 +82,7 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxGroup = 128;                    // query heads per key head
 constexpr int64_t kMaxRows = (int64_t)1 << 31;    // rows of a packed array
+constexpr int64_t kMaxTokens = kMaxRows - 1024;   // tokens of a sequence: a tile past the end stays an int
 
 // A cache whose shape, type and strides the kernels can walk.
 int check_cache(const sv_kv_cache* c) {
@@ -104,7 +105,7 @@ int check_cache(const sv_kv_cache* c) {
 int check_batch(const int32_t* table, const int32_t* start, const int32_t* len, int B,
                 int max_pages, int64_t total, int page_size) {
   if (B < 0 || max_pages < 0 || total < 0 || total >= kMaxRows) return SV_ERR_ARG;
-  if ((int64_t)max_pages * page_size >= kMaxRows) return SV_ERR_ARG;
+  if ((int64_t)max_pages * page_size > kMaxTokens) return SV_ERR_ARG;
   if (B == 0) return SV_OK;
   if (!start || !len || (!table && max_pages > 0)) return SV_ERR_ARG;
   if (!aligned(table, 4) || !aligned(start, 4) || !aligned(len, 4)) return SV_ERR_ALIGN;

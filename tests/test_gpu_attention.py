@@ -216,3 +216,68 @@ def test_refusals_of_the_binding():
         sv.spec_chunk_attention(c.q, c.cache, c.table.long(), c.start, c.len)
     with pytest.raises(sv.SpecVerifyError):  # 7 query heads on 2 key heads
         sv.spec_chunk_attention(c.q[:, :7], c.cache, c.table, c.start, c.len)
+
+
+@pytest.mark.parametrize("page", [4, 16, 128])
+@pytest.mark.parametrize("cache", [BF, E4M3])
+def test_a_nan_key_of_a_later_token_stays_away(page, cache):
+    """The last token's key is NaN: the chunk's earlier queries keep their bits."""
+    c = Case([(6, 300), (200, 260)], dim=64, page=page, cache=cache)
+    clean = c.attend()["out"].clone()
+    for b, (n, L) in enumerate(c.lens):
+        at = (c.owned[b][(L - 1) // page], slice(None), (L - 1) % page)
+        if cache == E4M3:
+            c.cache.k.view(torch.uint8)[at] = 0x7f
+        else:
+            c.cache.k[at] = math.nan
+    o = c.attend()["out"]
+    for b, (n, L) in enumerate(c.lens):
+        last = c.start_list[b + 1] - 1
+        assert torch.equal(o[c.start_list[b]:last], clean[c.start_list[b]:last])
+        assert bool(torch.isnan(o[last]).all())
+
+
+@pytest.mark.parametrize("cache", [BF, E4M3])
+@pytest.mark.parametrize("page", [4, 16, 128])
+def test_what_lies_in_front_of_the_window_is_not_read(page, cache):
+    """Pages that were given back (their table entries are wild), and NaN in the slots in front
+    of the first one seen."""
+    c = Case([(5, 700), (40, 333)], dim=64, page=page, cache=cache)
+    window = 100
+    clean = c.attend(window=window)["out"].clone()
+    for b, (n, L) in enumerate(c.lens):
+        lo = L - n + 1 - window
+        first = lo // page
+        for s in range(lo % page):
+            at = (c.owned[b][first], slice(None), s)
+            for pool, scale in ((c.cache.k, c.cache.k_scale), (c.cache.v, c.cache.v_scale)):
+                if cache == E4M3:
+                    pool.view(torch.uint8)[at] = 0xff
+                    scale[at] = 255
+                else:
+                    pool[at] = math.nan
+        c.table[b, :first] = 2 ** 31 - 1
+    o = c.attend(window=window, want_flags=True)
+    assert torch.equal(o["out"], clean) and not bool(o["flags"].any())
+
+
+@pytest.mark.parametrize("lens", [[(1, 40)], [(5, 3000), (70, 200)]])
+def test_outputs_and_queries_on_16_byte_boundaries(lens):
+    c = Case(lens, dim=128, group=4)
+    want = c.attend()["out"]
+    room = torch.zeros(c.total * 8 * 128 + 8, dtype=BF, device="cuda")
+    out = room[8:].view(c.total, 8, 128)
+    qs = torch.zeros(c.total * 8 * 128 + 8, dtype=BF, device="cuda")[8:].view(c.total, 8, 128)
+    qs.copy_(c.q)
+    sv.spec_chunk_attention(qs, c.cache, c.table, c.start, c.len, out={"out": out})
+    assert torch.equal(out, want) and not bool(room[:8].any())
+
+
+def test_queries_shared_by_all_tokens():
+    """A query tensor expanded along the tokens (stride 0)."""
+    c = Case([(7, 90), (3, 200)], dim=64)
+    one = c.q[:1].contiguous().expand(c.total, -1, -1)
+    # (two kernels: each off by 2^-8 of the value and of the weights' mass on |v| < 6)
+    a = sv.spec_chunk_attention(one, c.cache, c.table, c.start, c.len)["out"]
+    b = sv.spec_chunk_attention(one.contiguous(), c.cache, c.table, c.start, c.len)["out"]
+    assert bool(((a.double() - b.double()).abs() <= 2.0 ** -7 * (6 + b.double().abs())).all())
