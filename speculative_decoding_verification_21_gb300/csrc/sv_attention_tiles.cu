@@ -27,6 +27,21 @@
 // and the products.  Every wait is bounded; one that gives up ends the CTA's roles
 // and flags the call.
 //
+// What bounds it, measured on GB300 (152 SMs, one CTA each):
+//   a round (5 tokens, 64 sequences up to 8192, 32/8 heads of 128, bf16): HBM; 203 to
+//     209 us for 1.27 GB, 6.1 TB/s, 0.90 of a copy's rate;
+//   a prompt chunk (4096 and 1605 tokens, 32/8 heads of 128, bf16): the chain softmax,
+//     P V, Q K^T of a stage (about 3200 clocks for 2048 of products) and the power
+//     limit; 455 us, 1.3 PFLOP/s, 0.67 of a large library product's rate;
+//   a round on e4m3 (9 tokens, 32 sequences up to 40000, 64/8 heads of 128): issue slots
+//     and the three slots of widened tiles; 459 us, 3.3 TB/s of codes, 0.49 of a copy's.
+//     Per tile of 128 keys and values an SM issues about 2200 instructions a scheduler
+//     (half of them widen codes), and has 1370 clocks at HBM's rate.
+//   small calls: the chain lengths, page numbers, copies, products, join; 16 us for one
+//     token on 777, of them 3 to find the shares, 3 to the first scores, 5 for the join.
+// The 128 x 128 tile keeps S, P and O of two stages in tensor memory's 512 columns; the
+// operands leave room for five tiles of 32 KB in flight, what HBM's latency asks for.
+//
 // Waits of one CTA, by barrier: full/empty (key and value tiles in 16 bits),
 // rawfull/rawempty (e4m3 codes), qfull/qempty (query tiles), sfull (S ready),
 // pfull (P written, so S is free), ofull (last product of a stage done), xbar
@@ -63,9 +78,8 @@ constexpr int kQBytes = 2 * kSpan;                // one query tile
 // Shared memory: two query tiles, then 160 KB.  A 16-bit cache's ring of key and value
 // tiles (5 of 32 KB, or 10 of 16 KB) takes those; an e4m3 cache's codes take the first
 // 64 KB and the widened tiles (3 or 6) the rest.  In a call without an item of two row
-// tiles the second query tile is not used, and the first of the rings starts there:
-// with 6 tiles of codes in flight instead of 4 a round of 32 sequences took X us
-// instead of 505.
+// tiles the second query tile is not used, and the first of the rings starts there (a
+// round of 64 sequences of bf16, 6 tiles in flight instead of 5: 203 us instead of 212).
 constexpr int kCodes = 64 * 1024, kRing16 = 160 * 1024, kRing8 = 96 * 1024;
 constexpr int kScaleBytes = kMaxRaw * kTile;
 constexpr int kJoinThreads = 256;

@@ -11,6 +11,10 @@
 // e4m3: with amax = f 2^e, 1 <= f < 2, the largest code 448 = 1.75 2^8 holds
 // amax / 2^k for k = e - 8 if f <= 1.75 and k = e - 7 else; x 2^-k is exact in
 // fp32 (k >= -120 keeps 2^-k finite), so each code is rounded once.
+//
+// Measured on GB300: 84 thousand tokens of 8 heads of 128 into e4m3 94 us, 5.5 TB/s
+// (0.81 of a copy's rate; what is missing is the arithmetic between loads and stores);
+// 174 thousand out of e4m3 171 us, 6.3 TB/s (0.93); 320 tokens 4 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
