@@ -1,7 +1,7 @@
 """The target's side of speculative decoding, round by round, on a toy model.
 
-A one-layer attention model with random weights is the target; its own embeddings are the
-draft (the next token from the last one alone).  Prompts of different lengths enter the paged
+A one-layer attention model with random weights is the target; the same model without its
+attention is the draft (the next token from the last one alone).  Prompts of different lengths enter the paged
 cache as one chunk; every round then
 
   1. writes the chunk's keys and values into the cache (spec_kv_append),
@@ -27,7 +27,7 @@ import speculative_decoding_verification_21_gb300 as sv  # noqa: E402
 
 
 class ToyTarget:
-    """Embedding, one grouped-head attention layer over a paged cache, tied output head."""
+    """Embedding, one grouped-head attention layer over a paged cache, output head."""
 
     def __init__(self, vocab=512, heads=8, kv_heads=2, head_dim=64, seed=0, device="cuda"):
         g = torch.Generator(device=device)
@@ -39,10 +39,11 @@ class ToyTarget:
         self.w_qkv = (randn(width, (heads + 2 * kv_heads) * head_dim) * width ** -0.5 * 3).to(
             torch.bfloat16)
         self.w_out = (randn(width, width) * width ** -0.5).to(torch.bfloat16)
+        self.head = (randn(width, vocab) * 0.3).to(torch.bfloat16)
 
     def draft_logits(self, tokens):
         """The draft model: logits of the next token from the last token's embedding."""
-        return (self.embed[tokens].float() @ self.embed.float().T) * 0.5
+        return self.embed[tokens].float() @ self.head.float()
 
     def chunk(self, tokens, cache, table, q_start, kv_len):
         """Logits [total, vocab] of a packed chunk of new tokens, whose keys and values enter
@@ -53,7 +54,7 @@ class ToyTarget:
         sv.spec_kv_append(cache, k, v, table, q_start, kv_len)
         a = sv.spec_chunk_attention(q, cache, table, q_start, kv_len, want_lse=False)["out"]
         y = x + a.reshape(len(tokens), -1) @ self.w_out
-        return y.float() @ self.embed.float().T
+        return y.float() @ self.head.float()
 
 
 class Rounds:

@@ -34,6 +34,7 @@ def test_rounds_keep_what_they_accepted(e4m3):
     for _ in range(6):
         t = r.round()
         assert bool((t[:, 0] >= 0).all())  # every round emits a token
+    assert 0 < r.accepted < 6 * 3 * len(prompts)  # some drafts were kept, some forgotten
     k, v, start = r.cached()
     for b, tokens in enumerate(r.tokens):
         n = int(r.kv_len[b])
