@@ -10,8 +10,8 @@
 // key tile is read once for all of them.  An item is up to two such tiles of one
 // (sequence, key head); its keys are cut into tiles of 128 counted from token 0.
 //
-// Balance: all key tiles of all items form one line, cut into equal shares, one
-// per CTA (one CTA per SM).  An item cut by a share's end leaves partial (m, l, O)
+// Balance: all key tiles of all items form one line, an item's start worth kItemUnits
+// tiles more, cut into equal shares, one per CTA (one CTA per SM).  An item cut by a share's end leaves partial (m, l, O)
 // in the workspace, at most two per CTA, which k_attend_join adds up; an item
 // inside a share is written at once.  Lengths live on the device, so every CTA
 // finds its own place in the line at its start.
@@ -82,6 +82,10 @@ constexpr int kQBytes = 2 * kSpan;                // one query tile
 // round of 64 sequences of bf16, 6 tiles in flight instead of 5: 203 us instead of 212).
 constexpr int kCodes = 64 * 1024, kRing16 = 160 * 1024, kRing8 = 96 * 1024;
 constexpr int kScaleBytes = kMaxRaw * kTile;
+// What an item costs beside its key tiles (its queries, the end of its pipeline, its
+// outputs), in key tiles.  (Shares of key tiles alone: a round of 64 sequences 203 us,
+// with 1, 2, 3, 4 a start 201, 198, 197, 197; the prompt chunk 449 and 443, 439, 439, 440.)
+constexpr int kItemUnits = 3;
 constexpr int kJoinThreads = 256;
 // The running maximum may lag by this many powers of two before O is rescaled: P
 // stays within 2^8, exact enough in 16-bit floats and far from their range.
@@ -129,7 +133,7 @@ struct Ctl {
   uint32_t tmem;
   int abort;
   int two;             // some item of the call has two row tiles
-  int b, h, qt, off;   // start of the CTA's share
+  int b, h, qt, off;   // start of the CTA's share (off in units)
   long long left, share;
   union {
     long long warp_units[kThreads8 / 32];
@@ -175,14 +179,14 @@ __device__ __forceinline__ long long warp_scan64(long long v) {  // inclusive
   return v;
 }
 
-// Key tiles of one head of the lane's sequence (n = 0: none).  A sequence of many
+// Units of one head of the lane's sequence (n = 0: none).  A sequence of many
 // items is summed by the whole warp.
 __device__ __forceinline__ long long head_units(const Seq& q, int per_item, int window) {
   const int lane = threadIdx.x & 31;
   const int nqt = (q.n + per_item - 1) / per_item;
   long long u = 0;
   if (nqt <= 4)
-    for (int t = 0; t < nqt; ++t) u += item_span(q, per_item, t, window).count;
+    for (int t = 0; t < nqt; ++t) u += kItemUnits + item_span(q, per_item, t, window).count;
   unsigned big = __ballot_sync(0xffffffffu, nqt > 4);
   while (big) {
     const int src = __ffs(big) - 1;
@@ -192,7 +196,7 @@ __device__ __forceinline__ long long head_units(const Seq& q, int per_item, int 
     s.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
     long long v = 0;
     const int m = (s.n + per_item - 1) / per_item;
-    for (int t = lane; t < m; t += 32) v += item_span(s, per_item, t, window).count;
+    for (int t = lane; t < m; t += 32) v += kItemUnits + item_span(s, per_item, t, window).count;
     v = warp_sum64(v);
     if (lane == src) u = v;
   }
@@ -264,7 +268,8 @@ __device__ void find_share(const TileArgs& t, Ctl& ctl) {
       const int h = (int)divide(r, ph, r);
       const int m = (s.n + per_item - 1) / per_item;
       for (int q0 = 0; q0 < m; q0 += 32) {
-        const long long c = q0 + lane < m ? item_span(s, per_item, q0 + lane, t.a.window).count : 0;
+        const long long c =
+            q0 + lane < m ? kItemUnits + item_span(s, per_item, q0 + lane, t.a.window).count : 0;
         const long long sc = warp_scan64(c);
         const unsigned in = __ballot_sync(0xffffffffu, r < sc);
         if (!in) {
@@ -321,7 +326,12 @@ struct Walk {
       else ++b;
     }
     const Span sp = item_span(q, per_item, qt, t.a.window);
-    const int avail = sp.count - off;
+    // units off .. off + take of the item: its start, then a unit a tile
+    const int avail = sp.count + kItemUnits - off;
+    const int take = (int)min((long long)avail, left);
+    const int t0 = max(0, off - kItemUnits), t1 = off + take - kItemUnits;
+    left -= take;
+    if (t1 <= t0) return false;  // the share ends in front of the item's first tile
     s.b = b;
     s.h = h;
     s.row0 = q.tok0 + qt * per_item;
@@ -329,12 +339,11 @@ struct Walk {
     s.pos = q.pos0 + qt * per_item;
     s.lo = sp.lo;
     s.hi = sp.hi;
-    s.t0 = sp.first + off;
-    s.n = (int)min((long long)avail, left);
+    s.t0 = sp.first + t0;
+    s.n = t1 - t0;
     s.two = s.ntok > t.tpt;
-    s.slot = s.n == sp.count ? -1 : (off ? 0 : 1);
-    s.more = s.slot == 1 ? (int)((avail - s.n + ctl.share - 1) / ctl.share) : 0;
-    left -= s.n;
+    s.slot = s.n == sp.count ? -1 : (t0 ? 0 : 1);
+    s.more = s.slot == 1 ? (int)((avail - take + ctl.share - 1) / ctl.share) : 0;
     off = 0;
     if (++qt == nqt) {
       qt = 0;
