@@ -196,9 +196,12 @@ struct ProbShared {
   int n, flags;
 };
 
-// The accept tests of batch row b (one warp): n, and the flags they raise.
+// The accept tests of batch row b (one warp): n, and the flags they raise (lane 0's).
+struct Accept {
+  int n, flags;
+};
 template <int DT>
-__device__ void accept_tests(const ProbArgs& a, int b, ProbShared& sh) {
+__device__ Accept accept_tests(const ProbArgs& a, int b) {
   const int lane = threadIdx.x & 31, g = a.gamma;
   bool ok = false, bad_token = false, odd = false;
   if (lane < g) {
@@ -219,10 +222,20 @@ __device__ void accept_tests(const ProbArgs& a, int b, ProbShared& sh) {
   const unsigned seen = n >= 31 ? 0xffffffffu : (2u << n) - 1u;
   const unsigned bt = __ballot_sync(0xffffffffu, bad_token) & seen;
   const unsigned od = __ballot_sync(0xffffffffu, odd) & seen;
-  if (lane == 0) {
-    sh.n = n;
-    sh.flags = (bt ? SV_FLAG_BAD_TOKEN : 0) | (od ? SV_FLAG_NONFINITE : 0);
-  }
+  return Accept{n, (bt ? SV_FLAG_BAD_TOKEN : 0) | (od ? SV_FLAG_NONFINITE : 0)};
+}
+
+// The accept tests of all rows ahead of the rows' reads, one warp to a row: out_counts
+// holds n and, above 8 bits, the flags, until the row's own CTAs have ended.
+constexpr int kAcceptWarps = 4;
+template <int DT>
+__global__ void __launch_bounds__(kAcceptWarps * 32) k_accept(ProbArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = (int)blockIdx.x * kAcceptWarps + (int)(threadIdx.x >> 5);
+  if (b >= a.B) return;
+  const Accept t = accept_tests<DT>(a, b);
+  if ((threadIdx.x & 31) == 0) a.out_counts[b] = t.n | t.flags << 8;
 }
 
 // This warp's run of the row: its share of the CTA's slice.
@@ -328,7 +341,7 @@ __device__ int64_t find_in_run(const Weights& r, Run run, unsigned long long bef
   return -1;
 }
 
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool AHEAD>
 __global__ void __launch_bounds__(kProbThreads, 4) k_verify_probs(ProbArgs a) {
   __shared__ ProbShared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -341,7 +354,19 @@ __global__ void __launch_bounds__(kProbThreads, 4) k_verify_probs(ProbArgs a) {
     sh.any = 0;
     sh.odd = 0;
   }
-  if (warp == 0) accept_tests<DT>(a, b, sh);
+  if (AHEAD) {
+    if (threadIdx.x == 0) {
+      const int packed = a.out_counts[b];
+      sh.n = packed & 255;
+      sh.flags = packed >> 8;
+    }
+  } else if (warp == 0) {
+    const Accept t = accept_tests<DT>(a, b);
+    if (lane == 0) {
+      sh.n = t.n;
+      sh.flags = t.flags;
+    }
+  }
   __syncthreads();
   const int n = sh.n;
   constexpr int es = DT == SV_F32 ? 4 : 2;
@@ -415,7 +440,19 @@ template <int DT>
 cudaError_t launch_dt(const ProbArgs& a, int cluster, cudaStream_t stream) {
   constexpr int es = DT == SV_F32 ? 4 : 2;
   // 16-byte loads where every row starts on a 16-byte boundary
-  auto* k = (a.V * es) % 16 == 0 ? k_verify_probs<DT, true> : k_verify_probs<DT, false>;
+  const bool vec = (a.V * es) % 16 == 0;
+  // More CTAs than stand at once (four to an SM): each would begin with the accept tests'
+  // three dependent loads while its share of the memory idles, so they go ahead in a
+  // kernel of their own (256 rows of 152064: 68 us without it, 65 with; one row takes 6 us
+  // either way, but the call a launch more: 18.7 us of the host instead of 17.7).
+  const bool ahead = (int64_t)a.B * cluster > 4 * 152;
+  if (ahead) {
+    const cudaError_t e = launch_pdl(k_accept<DT>, dim3((a.B + kAcceptWarps - 1) / kAcceptWarps),
+                                     dim3(kAcceptWarps * 32), 0, stream, a);
+    if (e != cudaSuccess) return e;
+  }
+  auto* k = vec ? (ahead ? k_verify_probs<DT, true, true> : k_verify_probs<DT, true, false>)
+                : (ahead ? k_verify_probs<DT, false, true> : k_verify_probs<DT, false, false>);
   return launch_pdl_cluster(k, dim3((unsigned)(a.B * cluster)), dim3(kProbThreads), 0,
                             (unsigned)cluster, stream, a);
 }
