@@ -478,6 +478,12 @@ int sv_set_timing_events(void* const* events, int n);
  * until changed; not thread-safe.  Returns 0. */
 int sv_test_lmhead_stall(int job, uint32_t wait_limit);
 
+/* Test only: the same for spec_chunk_attention's tile kernel.  The next calls withhold the
+ * first scores that CTA `cta` (< 0: none) computes, and every bounded wait gives up after
+ * `wait_clocks` SM clocks (<= 0: the default, about two seconds); the call returns SV_OK
+ * and every sequence carries SV_FLAG_TIMEOUT.  Not thread-safe.  Returns 0. */
+int sv_test_attention_stall(int cta, int64_t wait_clocks);
+
 /* Human-readable name of a status code. */
 const char* sv_status_string(int status);
 

@@ -10,8 +10,8 @@ from ._lib import (FLAG_BAD_LENGTH, FLAG_BAD_PAGE, FLAG_BAD_TOKEN, FLAG_NONFINIT
                    alloc_kv_cache, alloc_workspace, attention_workspace_bytes, library_path, load,
                    spec_chunk_attention, spec_kv_append, spec_kv_read, spec_lmhead_draft,
                    spec_lmhead_verify, spec_lmhead_verify_drafted, spec_verify,
-                   spec_verify_greedy, spec_verify_probs, status_string, test_lmhead_stall,
-                   workspace_bytes)
+                   spec_verify_greedy, spec_verify_probs, status_string, test_attention_stall,
+                   test_lmhead_stall, workspace_bytes)
 
 __all__ = ["spec_verify", "spec_verify_greedy", "spec_lmhead_verify", "spec_lmhead_draft",
            "spec_lmhead_verify_drafted", "spec_kv_append", "spec_kv_read", "spec_chunk_attention",
@@ -19,4 +19,4 @@ __all__ = ["spec_verify", "spec_verify_greedy", "spec_lmhead_verify", "spec_lmhe
            "workspace_bytes",
            "alloc_workspace", "load", "library_path", "status_string", "SpecVerifyError",
            "FLAG_ZERO_MASS", "FLAG_NONFINITE", "FLAG_RESIDUAL_FALLBACK", "FLAG_TIMEOUT",
-           "FLAG_BAD_TOKEN", "FLAG_BAD_PAGE", "FLAG_BAD_LENGTH", "test_lmhead_stall"]
+           "FLAG_BAD_TOKEN", "FLAG_BAD_PAGE", "FLAG_BAD_LENGTH", "test_lmhead_stall", "test_attention_stall"]

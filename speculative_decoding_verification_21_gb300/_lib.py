@@ -23,7 +23,7 @@ EXPORTS = ("sv_workspace_bytes", "sv_workspace_init", "spec_verify", "spec_verif
            "spec_verify_greedy", "spec_lmhead_verify", "spec_lmhead_draft",
            "spec_lmhead_verify_drafted", "spec_kv_append", "spec_kv_read", "spec_chunk_attention",
            "spec_verify_probs", "sv_attention_workspace_bytes",
-           "sv_set_timing_events", "sv_test_lmhead_stall", "sv_status_string", "sv_version")
+           "sv_set_timing_events", "sv_test_lmhead_stall", "sv_test_attention_stall", "sv_status_string", "sv_version")
 
 
 class Options(ctypes.Structure):
@@ -114,6 +114,8 @@ def load(build_if_missing: bool = True):
         L.sv_set_timing_events.restype = I
         L.sv_test_lmhead_stall.argtypes = [I, ctypes.c_uint32]
         L.sv_test_lmhead_stall.restype = I
+        L.sv_test_attention_stall.argtypes = [I, I64]
+        L.sv_test_attention_stall.restype = I
         L.sv_status_string.argtypes = [I]
         L.sv_status_string.restype = ctypes.c_char_p
         L.sv_version.argtypes = []
@@ -127,6 +129,12 @@ def test_lmhead_stall(job: int, wait_limit: int = 0) -> None:
     (job < 0: none) and give up every bounded wait after `wait_limit` tries (0: the
     default); see sv_test_lmhead_stall in include/specverify.h."""
     load().sv_test_lmhead_stall(int(job), int(wait_limit))
+
+
+def test_attention_stall(cta: int, wait_clocks: int = 0) -> None:
+    """Test only: the same for spec_chunk_attention; see sv_test_attention_stall in
+    include/specverify.h."""
+    load().sv_test_attention_stall(int(cta), int(wait_clocks))
 
 
 def status_string(status: int) -> str:

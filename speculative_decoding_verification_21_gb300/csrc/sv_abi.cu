@@ -357,6 +357,11 @@ int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, con
              : SV_ERR_CUDA;
 }
 
+int sv_test_attention_stall(int cta, int64_t wait_clocks) {
+  sv::set_attention_stall(cta, wait_clocks);
+  return SV_OK;
+}
+
 int spec_verify_probs(const void* target_probs, const void* draft_probs,
                       const int32_t* draft_tokens, const float* uniforms, int B, int gamma,
                       int64_t V, int dtype, int32_t* out_tokens, int32_t* out_counts,

@@ -53,6 +53,9 @@ size_t attention_workspace_bytes(const CacheView& c, bool e4m3);
 size_t attention_tiles_workspace(int head_dim);
 cudaError_t launch_attention(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream);
 
+// Test only (sv_test_attention_stall).
+void set_attention_stall(int cta, long long clocks);
+
 // *taken = false: the cache cannot be described by a tensor map; nothing was queued.
 cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream,
                                    bool* taken);

@@ -73,6 +73,10 @@ constexpr int kMaxCtas = 160;       // shares (GB300: 152 SMs)
 constexpr int kMaxRows = 2 * kTile;
 constexpr int kMaxStages = 12, kMaxRaw = 8;
 constexpr long long kWaitClocks = 1ll << 32;  // about two seconds
+// The wait limit and the CTA whose first scores are never handed over in the next calls
+// (a failure test sets them through sv_test_attention_stall; not thread-safe).
+long long g_wait_clocks = kWaitClocks;
+int g_stall_cta = -1;
 constexpr size_t kSmemBytes = 227 * 1024;
 constexpr int kQBytes = 2 * kSpan;                // one query tile
 // Shared memory: two query tiles, then 160 KB.  A 16-bit cache's ring of key and value
@@ -112,6 +116,8 @@ struct TileArgs {
   Ring tiles2[2], codes2[2];  // twice their slots (see the barriers)
   int box;             // tokens per copy: min(page_size, 128)
   int fetchers;        // warps that fetch key and value tiles
+  int stall;           // test only: the CTA whose first scores are withheld (-1: none)
+  long long wait_clocks;
   int wide;            // outputs sit on 32-byte boundaries
   float c;             // scale log2 e, positive
   float* part;         // [2 * kMaxCtas][kMaxRows][head_dim]
@@ -395,23 +401,26 @@ enum WaitId { kWaitSlot = 1, kWaitQ, kWaitK, kWaitV, kWaitP, kWaitQFree, kWaitS,
 
 // A whole warp.  All lanes test and go on together: one that went ahead could let
 // the barrier move a phase further before another tests it.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          int id) {
+struct Guard {
+  volatile int* flag;  // the CTA's abort flag
+  long long clocks;    // limit of a wait
+};
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Guard& guard, int id) {
   for (int i = 0; i < 64; ++i)
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
   for (;;) {
     for (int i = 0; i < 16; ++i)
       if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const bool late = clock64() - t0 >= kWaitClocks;
-    if (__any_sync(0xffffffffu, late)) *abort_flag = id;
-    if (__any_sync(0xffffffffu, late || *abort_flag != 0)) return false;
+    const bool late = clock64() - t0 >= guard.clocks;
+    if (__any_sync(0xffffffffu, late)) *guard.flag = id;
+    if (__any_sync(0xffffffffu, late || *guard.flag != 0)) return false;
   }
 }
 // What must have ended before the CTA may go, whether or not the call is aborted.
-__device__ __forceinline__ void wait_end(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ void wait_end(uint64_t* bar, uint32_t parity, const Guard& guard) {
   const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity) && clock64() - t0 < kWaitClocks) {
+  while (!mbar_try_wait(bar, parity) && clock64() - t0 < guard.clocks) {
   }
 }
 
@@ -541,7 +550,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   const AttendArgs& a = t.a;
   const int D = a.c.head_dim;
   const int stage_bytes = t.nhalf * kSpan, raw_bytes = kTile * D;
-  volatile int* const abort_flag = &ctl.abort;
+  const Guard guard{&ctl.abort, t.wait_clocks};
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -582,7 +591,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   uint8_t* const ring = E4M3 ? smem + 2 * kQBytes + kCodes : first;
   Walk walk(ctl);
   Seg s;
-  bool ok = *abort_flag == 0;
+  bool ok = *guard.flag == 0;
   if (warp < 4) give_regs<E4M3 ? kHelpRegs8 : kHelpRegs16>();
 
   if (warp == 0 || (warp == 3 && t.fetchers == 2)) {
@@ -618,7 +627,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const uint32_t k = issued + (uint32_t)idx, slot = Slot(k, rs).i;
         const Slot at2(k, rs2);
         uint64_t* const fullb = E4M3 ? ctl.rawfull + at2.i : ctl.full + slot;
-        ok = wait_warp(freeb + at2.i, at2.i < rs.n ? at2.ph ^ 1u : at2.ph, abort_flag, kWaitSlot);
+        ok = wait_warp(freeb + at2.i, at2.i < rs.n ? at2.ph ^ 1u : at2.ph, guard, kWaitSlot);
         if (!ok) break;
         const int live = max(0, upto - from);
         const bool mine = part >= from && part < upto;
@@ -661,7 +670,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const uint32_t end = ok ? issued : done;
     for (uint32_t k = end > rs.n ? end - rs.n : 0; k < end; ++k) {
       const Slot at(k, E4M3 ? rc2 : rt);
-      if (lane == 0 && (t.fetchers == 1 || (k & 1u) == turn)) wait_end((E4M3 ? ctl.rawfull : ctl.full) + at.i, at.ph);
+      if (lane == 0 && (t.fetchers == 1 || (k & 1u) == turn)) wait_end((E4M3 ? ctl.rawfull : ctl.full) + at.i, at.ph, guard);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -687,7 +696,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       };
       // whoever waits for tile k's slot waits for tile k + n, the slot's next
       auto freed = [&](uint32_t k) { return ctl.empty + Slot(k + rt.n, rt2).i; };
-      auto scores = [&](int j, uint32_t slot) {
+      auto scores = [&](int j, uint32_t slot, uint32_t tell) {
         const int i = j >> two, st = j & 1;
         const uint32_t qb = (qn + (uint32_t)(two & st)) & (uint32_t)pr;
         const uint64_t ad = qdesc + qb * (kQBytes >> 4), bd = kdesc + slot * stage16;
@@ -697,18 +706,19 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           const uint64_t o = (uint64_t)((kk >> 2) * (kSpan >> 4) + (kk & 3) * 2);
           if (kk < ksteps) umma_ss_if(leader, acc, ad + o, bd + o, idesc_s, kk != 0);
         }
-        umma_commit_if(leader, ctl.sfull + st);
+        umma_commit_if(tell, ctl.sfull + st);
         if (!two || st) umma_commit_if(leader, freed(base + (uint32_t)k_index(i)));
         if (i == n - 1) umma_commit_if(leader, ctl.qempty + qb);
       };
       for (int j = 0; j < 2 && j < jobs; ++j) {
         const Slot k = key_slot(j);
         const uint32_t qk = qn + (uint32_t)(two & j);
-        ok = wait_warp(ctl.qfull + (qk & (uint32_t)pr), (qk >> pr) & 1u, abort_flag, kWaitQ) &&
-             wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK);
+        ok = wait_warp(ctl.qfull + (qk & (uint32_t)pr), (qk >> pr) & 1u, guard, kWaitQ) &&
+             wait_warp(ctl.full + k.i, k.ph, guard, kWaitK);
         if (!ok) break;
         tc_fence_after();
-        scores(j, k.i);
+        // (a test may withhold a CTA's first scores: the softmax's wait then runs out)
+        scores(j, k.i, t.stall == wid && base == 0 && j == 0 ? 0u : leader);
       }
       for (int j = 0; ok && j < jobs; ++j) {
         const int i = j >> two, st = j & 1;
@@ -724,9 +734,9 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         // tile of job j + 2 does not depend on job j: its slot was freed by an earlier
         // one.  Of an e4m3 cache's three slots that one is freed late: there the key
         // tile is awaited behind the product with V.)
-        ok = wait_warp(ctl.full + v.i, v.ph, abort_flag, kWaitV) &&
-             (E4M3 || !more || wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK)) &&
-             wait_warp(ctl.pfull + st, (pph >> st) & 1u, abort_flag, kWaitP);
+        ok = wait_warp(ctl.full + v.i, v.ph, guard, kWaitV) &&
+             (E4M3 || !more || wait_warp(ctl.full + k.i, k.ph, guard, kWaitK)) &&
+             wait_warp(ctl.pfull + st, (pph >> st) & 1u, guard, kWaitP);
         if (!ok) break;
         pph ^= 1u << st;
         tc_fence_after();
@@ -740,11 +750,11 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
         if (!two || st) umma_commit_if(leader, freed(base + (uint32_t)v_index(i, n)));
         if (E4M3 && more) {
-          ok = wait_warp(ctl.full + k.i, k.ph, abort_flag, kWaitK);
+          ok = wait_warp(ctl.full + k.i, k.ph, guard, kWaitK);
           if (!ok) break;
           tc_fence_after();
         }
-        if (more) scores(j + 2, k.i);
+        if (more) scores(j + 2, k.i, leader);
         else umma_commit_if(leader, ctl.ofull + st);
       }
       base += 2u * (uint32_t)n;
@@ -752,7 +762,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     }
     // all products complete before tensor memory is released
     umma_commit_if(leader, &ctl.fin);
-    wait_end(&ctl.fin, 0);
+    wait_end(&ctl.fin, 0, guard);
   } else if (warp == 2) {
     // ---------------- fetch query tiles ----------------
     // A copy takes tpt tokens by group heads, rows in the order of the tile.  Tokens
@@ -764,8 +774,9 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       if (lane == 0 && s.slot == 1) t.rec[wid] = Rec{s.more, s.row0, s.ntok, s.h};
       for (int st = 0; ok && st < (s.two ? 2 : 1); ++st, ++qn) {
         const uint32_t qb = qn & (uint32_t)pair;
-        ok = wait_warp(ctl.qempty + qb, ((qn >> pair) & 1u) ^ 1u, abort_flag, kWaitQFree);
-        if (ok && lane == 0) {
+        ok = wait_warp(ctl.qempty + qb, ((qn >> pair) & 1u) ^ 1u, guard, kWaitQFree);
+        if (!ok) break;
+        if (lane == 0) {
           mbar_arrive_expect_tx(ctl.qfull + qb, (uint32_t)(t.nhalf * t.tpt * t.group * 128));
           for (int h = 0; h < t.nhalf; ++h)
             tma_load_3d_hint(qbuf + qb * kQBytes + h * kSpan, &mq, 64 * h, s.h * t.group,
@@ -777,7 +788,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     // every copy has landed before the CTA may exit
     const uint32_t held = 1u + (uint32_t)pair;
     for (uint32_t i = qn > held ? qn - held : 0; i < qn; ++i)
-      if (lane == 0) wait_end(ctl.qfull + (i & (uint32_t)pair), (i >> pair) & 1u);
+      if (lane == 0) wait_end(ctl.qfull + (i & (uint32_t)pair), (i >> pair) & 1u, guard);
     __syncwarp();
   } else if (warp >= 4 && warp < 12) {
     // ---------------- softmax and output ----------------
@@ -801,7 +812,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       const int see0 = a.window ? max(0, see1 - a.window) : 0;
       float m = -kInf, l = 0.0f;
       for (int k = 0; ok && k < jobs; ++k) {
-        if (!wait_warp(ctl.sfull + st, sph, abort_flag, kWaitS)) {
+        if (!wait_warp(ctl.sfull + st, sph, guard, kWaitS)) {
           ok = false;
           break;
         }
@@ -858,7 +869,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           const int v0 = max(0, s.lo - key0), v1 = min(kTile, s.hi - key0);
           if (((v0 | v1) & 15) && v1 > v0) {
             const Slot vk(base + (uint32_t)v_index(i, s.n), rt);
-            if (!wait_warp(ctl.full + vk.i, vk.ph, abort_flag, kWaitV)) {
+            if (!wait_warp(ctl.full + vk.i, vk.ph, guard, kWaitV)) {
               ok = false;
               break;
             }
@@ -880,7 +891,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       }
       if (!ok) break;
       if (jobs) {
-        if (!wait_warp(ctl.ofull + st, oph, abort_flag, kWaitO)) {
+        if (!wait_warp(ctl.ofull + st, oph, guard, kWaitO)) {
           ok = false;
           break;
         }
@@ -924,7 +935,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl.xbar);
-          ok = wait_warp(&ctl.xbar, xph, abort_flag, kWaitX);
+          ok = wait_warp(&ctl.xbar, xph, guard, kWaitX);
           xph ^= 1u;
           if (st == turn) (st ? p0 : p1) = ctl.xch[row];
           __syncwarp();
@@ -969,7 +980,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.xbar);
-        if (!wait_warp(&ctl.xbar, xph, abort_flag, kWaitX)) {
+        if (!wait_warp(&ctl.xbar, xph, guard, kWaitX)) {
           ok = false;
           break;
         }
@@ -1000,8 +1011,8 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int key0 = (s.t0 + tile) * kTile;
         const uint32_t rs = Slot(k, rc).i, slot = Slot(k, rt).i;
         const Slot from(k, rc2), to(k, rt2);
-        if (!wait_warp(ctl.rawfull + from.i, from.ph, abort_flag, kWaitRaw) ||
-            !wait_warp(ctl.empty + to.i, to.i < rt.n ? to.ph ^ 1u : to.ph, abort_flag, kWaitWide)) {
+        if (!wait_warp(ctl.rawfull + from.i, from.ph, guard, kWaitRaw) ||
+            !wait_warp(ctl.empty + to.i, to.i < rt.n ? to.ph ^ 1u : to.ph, guard, kWaitWide)) {
           ok = false;
           break;
         }
@@ -1287,6 +1298,11 @@ static_assert(kMaxCtas * (sizeof(Rec) + sizeof(int)) <= kRecBytes, "records");
 
 }  // namespace
 
+void set_attention_stall(int cta, long long clocks) {
+  g_stall_cta = cta;
+  g_wait_clocks = clocks > 0 ? clocks : kWaitClocks;
+}
+
 size_t attention_tiles_workspace(int head_dim) {
   return kRecBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * (size_t)head_dim;
 }
@@ -1312,6 +1328,8 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
   }
   t.box = c.page_size < kTile ? c.page_size : kTile;
   t.wide = ((uintptr_t)a.out & 31) == 0;
+  t.stall = g_stall_cta;
+  t.wait_clocks = g_wait_clocks;
   // a second warp fetches from four copies a tile on (32 sequences of e4m3 in pages of
   // 64: 552 -> 466 us; one sequence of 64-wide heads in pages of 128: 36 us with one
   // warp, 40 with two)
