@@ -23,18 +23,18 @@
 //
 // Roles: warps 0 and 3 fetch key and value pages (tensor copies, 128-byte swizzle),
 // warp 1 issues the products, warp 2 fetches queries, warps 4-11 are the softmax,
-// and for e4m3 caches warps 12-27 widen the codes to 16 bits between the copies
+// and for e4m3 caches warps 12-19 widen the codes to 16 bits between the copies
 // and the products.  Every wait is bounded; one that gives up ends the CTA's roles
 // and flags the call.
 //
 // What bounds it, measured on GB300 (152 SMs, one CTA each):
-//   a round (5 tokens, 64 sequences up to 8192, 32/8 heads of 128, bf16): HBM; 203 to
-//     209 us for 1.27 GB, 6.1 TB/s, 0.90 of a copy's rate;
+//   a round (5 tokens, 64 sequences up to 8192, 32/8 heads of 128, bf16): HBM; 197 to
+//     203 us for 1.27 GB, 6.3 TB/s, 0.93 of a copy's rate;
 //   a prompt chunk (4096 and 1605 tokens, 32/8 heads of 128, bf16): the chain softmax,
 //     P V, Q K^T of a stage (about 3200 clocks for 2048 of products) and the power
-//     limit; 455 us, 1.3 PFLOP/s, 0.67 of a large library product's rate;
+//     limit; 440 to 460 us, 1.3 PFLOP/s, 0.67 of a large library product's rate;
 //   a round on e4m3 (9 tokens, 32 sequences up to 40000, 64/8 heads of 128): issue slots
-//     and the three slots of widened tiles; 459 us, 3.3 TB/s of codes, 0.49 of a copy's.
+//     and the three slots of widened tiles; 445 us, 3.4 TB/s of codes, 0.51 of a copy's.
 //     Per tile of 128 keys and values an SM issues about 2200 instructions a scheduler
 //     (half of them widen codes), and has 1370 clocks at HBM's rate.
 //   small calls: the chain lengths, page numbers, copies, products, join; 16 us for one
@@ -96,12 +96,12 @@ constexpr int kJoinThreads = 256;
 constexpr float kLag = 8.0f;
 // Threads, and the registers a thread is launched with and then takes by role (the
 // roles' sum must not pass what the launch gave, or the takers would wait forever).
-constexpr int kThreads16 = 384, kThreads8 = 896;
-constexpr int kRegs16 = 168, kRegs8 = 72;
+constexpr int kThreads16 = 384, kWideWarps = 4, kThreads8 = 384 + 64 * kWideWarps;
+constexpr int kRegs16 = 168, kRegs8 = 96;
 constexpr int kHelpRegs16 = 88, kSoftRegs16 = 208;
-constexpr int kHelpRegs8 = 56, kSoftRegs8 = 112, kWideRegs8 = 56;
+constexpr int kHelpRegs8 = 64, kSoftRegs8 = 128, kWideRegs8 = 80;
 static_assert(128 * kHelpRegs16 + 256 * kSoftRegs16 <= kThreads16 * kRegs16, "registers");
-static_assert(128 * kHelpRegs8 + 256 * kSoftRegs8 + 512 * kWideRegs8 <= kThreads8 * kRegs8, "registers");
+static_assert(128 * kHelpRegs8 + 256 * kSoftRegs8 + 64 * kWideWarps * kWideRegs8 <= kThreads8 * kRegs8, "registers");
 
 // Slots of a ring, and ceil(2^32 / slots): slot and turn of tile k without a division.
 struct Ring {
@@ -556,11 +556,11 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   if (threadIdx.x == 0) {
     ctl.two = 0;
     ctl.abort = (smem_u32(smem) & 1023u) ? 1 : 0;  // the swizzle needs this alignment
-    for (int i = 0; i < kMaxStages; ++i) mbar_init(ctl.full + i, E4M3 ? 8 : 1);
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(ctl.full + i, E4M3 ? kWideWarps : 1);
     for (int i = 0; i < 2 * kMaxStages; ++i) mbar_init(ctl.empty + i, 1);
     for (int i = 0; i < 2 * kMaxRaw; ++i) {
       mbar_init(ctl.rawfull + i, 1);
-      mbar_init(ctl.rawempty + i, 8);
+      mbar_init(ctl.rawempty + i, kWideWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(ctl.qfull + i, 1);
@@ -990,15 +990,18 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     }
   } else if (E4M3 && warp >= 12) {
     // ---------------- widen e4m3 codes ----------------
-    // Two groups of eight warps take the tiles in turn, so that one tile's loads and
-    // stores stand beside the other's arithmetic.
+    // Two groups of four warps take the tiles in turn, so that one tile's loads and
+    // stores stand beside the other's arithmetic.  (Groups of eight leave 72 registers
+    // a thread instead of 96 and hide no more: round 448 us instead of 445, window 141
+    // instead of 137; converters with 64 registers and softmax with 144: 465 us.)
     // A lane widens 16 codes of a row (two 16-byte chunks of a swizzle span).  Four
     // lanes take one span of a row and the next four that span of the row below, so
-    // that the eight lanes of a store's phase write different banks; four rows at a
-    // time, 16 rows a warp.
+    // that the eight lanes of a store's phase write different banks; four loads at a
+    // time, 16 rows a warp and step.
     give_regs<kWideRegs8>();
-    const int cw = (warp - 12) & 7;
-    const uint32_t group = (uint32_t)(warp - 12) >> 3;
+    constexpr int kRows = kTile / kWideWarps;  // of a warp
+    const int cw = (warp - 12) % kWideWarps;
+    const uint32_t group = (uint32_t)(warp - 12) / kWideWarps;
     const int span = (lane >> 3) & 1, ch = (lane & 3) + 4 * span;
     const int g = ((lane >> 2) & 1) + 2 * (lane >> 4);
     uint32_t k = 0;
@@ -1016,40 +1019,43 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
           ok = false;
           break;
         }
-        const uint8_t* src = raw + (size_t)rs * raw_bytes + (16 * cw + g) * D + ch * 16;
-        uint8_t* dst = ring + (size_t)slot * stage_bytes + span * kSpan + (16 * cw + g) * 128;
-        const uint8_t* scales = scale_area + rs * kTile + 16 * cw + g;
         // only the part's first and last tiles hold rows that nobody sees: those
         // become zeros whatever they hold
-        const int row0 = key0 + 16 * cw;
-        const bool edge = row0 < s.lo || row0 + 16 > s.hi;
+        const int row0 = key0 + kRows * cw;
+        const bool edge = row0 < s.lo || row0 + kRows > s.hi;
         if (ch * 16 < D) {
-          uint4 x[4];
-          uint32_t sc[4];
+#pragma unroll 1
+          for (int q = kRows * cw + g; q < kRows * (cw + 1); q += 16) {
+            const uint8_t* src = raw + (size_t)rs * raw_bytes + q * D + ch * 16;
+            uint8_t* dst = ring + (size_t)slot * stage_bytes + span * kSpan + q * 128;
+            const uint8_t* scales = scale_area + rs * kTile + q;
+            uint4 x[4];
+            uint32_t sc[4];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            x[p] = *reinterpret_cast<const uint4*>(src + 4 * p * D);
-            sc[p] = scales[4 * p];
-          }
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 u = e4m3x2((uint16_t)w[j]), v = e4m3x2((uint16_t)(w[j] >> 16));
-              o[2 * j] = scaled<DT>(u, sc[p]);
-              o[2 * j + 1] = scaled<DT>(v, sc[p]);
+            for (int p = 0; p < 4; ++p) {
+              x[p] = *reinterpret_cast<const uint4*>(src + 4 * p * D);
+              sc[p] = scales[4 * p];
             }
-            if (edge && !(row0 + 4 * p + g >= s.lo && row0 + 4 * p + g < s.hi)) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] = 0;
+            for (int p = 0; p < 4; ++p) {
+              const uint32_t w[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 u = e4m3x2((uint16_t)w[j]), v = e4m3x2((uint16_t)(w[j] >> 16));
+                o[2 * j] = scaled<DT>(u, sc[p]);
+                o[2 * j + 1] = scaled<DT>(v, sc[p]);
+              }
+              if (edge && (key0 + q + 4 * p < s.lo || key0 + q + 4 * p >= s.hi)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = 0;
+              }
+              const int sw = (4 * p + g) & 7, c1 = 2 * (lane & 3);  // (q is g and a multiple of 16)
+              *reinterpret_cast<uint4*>(dst + 4 * p * 128 + ((c1 ^ sw) << 4)) =
+                  make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(dst + 4 * p * 128 + (((c1 + 1) ^ sw) << 4)) =
+                  make_uint4(o[4], o[5], o[6], o[7]);
             }
-            const int sw = (4 * p + g) & 7, c1 = 2 * (lane & 3);  // 16 cw leaves the swizzle alone
-            *reinterpret_cast<uint4*>(dst + 4 * p * 128 + ((c1 ^ sw) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + 4 * p * 128 + (((c1 + 1) ^ sw) << 4)) =
-                make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
         fence_proxy_async();
