@@ -418,9 +418,8 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  *             SV_FLAG_TIMEOUT on every sequence if a bounded device-side wait
  *             gave up (outputs are then unspecified)
  * A query that sees no key (kv_len shorter than the chunk) gets out = 0 and
- * lse = -inf.  Slots behind kv_len, and in front of every window of the chunk, may
- * hold anything.  A value inside that is not finite may reach queries of the same
- * chunk that do not see it (their weight for it is 0, and 0 times infinity is NaN).
+ * lse = -inf.  What a query does not see (later tokens of its chunk, slots behind
+ * kv_len, tokens in front of its window) never reaches it, and may be NaN or infinite.
  * Outputs are the same bits every time.
  *   workspace >= sv_attention_workspace_bytes(cache, heads), 256-byte aligned
  */

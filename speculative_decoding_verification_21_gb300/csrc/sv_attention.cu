@@ -13,6 +13,7 @@
 
 #include "specverify.h"
 #include "sv_attention.h"
+#include "sv_attention_row.cuh"
 #include "sv_cache.cuh"
 #include "sv_device.cuh"
 #include "sv_launch.h"
@@ -54,88 +55,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) k_attend_rows(AttendArgs a) {
     sq[2 * d + 1] = f.y * a.scale_log2;
   }
   __syncthreads();
-  const int32_t* table = a.b.table + (int64_t)b * a.b.max_pages;
   float m = -kInf, l = 0.0f, o[8] = {};
-  for (int j0 = lo / 32 * 32 + warp * 32; j0 < hi; j0 += kRowWarps * 32) {
-    const int j = j0 + lane;
-    const bool seen = j >= lo && j < hi;
-    int page = -1, slot = 0;
-    if (seen) {
-      page_of(c, j, page, slot);
-      page = __ldg(table + page);
-      if (page < 0 || page >= c.num_pages) page = -1;
-    }
-    const int64_t at = (int64_t)page * c.page_bytes + (int64_t)h * c.head_bytes +
-                       (int64_t)slot * c.token_bytes;
-    const int64_t sat = ((int64_t)page * c.kv_heads + h) * c.page_size + slot;
-    float s = seen ? 0.0f : -kInf, vs = 1.0f;
-    if (page >= 0) {
-      if (E4M3) {
-        vs = scale_of(__ldg(c.vs + sat));
-        const float ks = scale_of(__ldg(c.ks + sat));
-        for (int d = 0; d < D; d += 16) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(c.k + at + d));
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 f = e4m3x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-            const float2 r = F16<DT>::up(F16<DT>::down(f.x * ks, f.y * ks));
-            s = fmaf(r.x, sq[d + 2 * e], s);
-            s = fmaf(r.y, sq[d + 2 * e + 1], s);
-          }
-        }
-      } else {
-        for (int d = 0; d < D; d += 8) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(c.k + at + 2 * d));
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 r = F16<DT>::up(w[e]);
-            s = fmaf(r.x, sq[d + 2 * e], s);
-            s = fmaf(r.y, sq[d + 2 * e + 1], s);
-          }
-        }
-      }
-    }
-    const float bm = fmaxf(m, warp_max(s));
-    if (bm > m) {
-      const float f = m == -kInf ? 0.0f : ex2(m - bm);
-      l *= f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] *= f;
-      m = bm;
-    }
-    // a NaN score (fmaxf passes it over) keeps its NaN here
-    const float p = seen ? (m == -kInf ? (s == s ? 0.0f : s) : ex2(s - m)) : 0.0f;
-    l += p;
-    const int first = max(0, lo - j0), last = min(32, hi - j0);
-    for (int e = first; e < last; ++e) {
-      const int64_t vat = __shfl_sync(0xffffffffu, at, e);
-      const int vpage = __shfl_sync(0xffffffffu, page, e);
-      const float pe = __shfl_sync(0xffffffffu, p, e), ve = __shfl_sync(0xffffffffu, vs, e);
-      if (vpage < 0 || lane * 8 >= D) continue;
-      if (E4M3) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(c.v + vat) + lane);
-        const uint32_t w[2] = {x.x, x.y};
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const float2 f = e4m3x2((uint16_t)(w[d >> 1] >> (16 * (d & 1))));
-          const float2 r = F16<DT>::up(F16<DT>::down(f.x * ve, f.y * ve));
-          o[2 * d] = fmaf(pe, r.x, o[2 * d]);
-          o[2 * d + 1] = fmaf(pe, r.y, o[2 * d + 1]);
-        }
-      } else {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(c.v + vat) + lane);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const float2 r = F16<DT>::up(w[d]);
-          o[2 * d] = fmaf(pe, r.x, o[2 * d]);
-          o[2 * d + 1] = fmaf(pe, r.y, o[2 * d + 1]);
-        }
-      }
-    }
-  }
+  attend_blocks<DT, E4M3, 4>(a, b, h, lo, hi, sq, warp, kRowWarps, m, l, o);
 #pragma unroll
   for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
   if (lane == 0) {

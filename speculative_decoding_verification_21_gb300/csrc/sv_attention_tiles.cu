@@ -58,6 +58,7 @@
 
 #include "specverify.h"
 #include "sv_attention.h"
+#include "sv_attention_row.cuh"
 #include "sv_cache.cuh"
 #include "sv_device.cuh"
 #include "sv_launch.h"
@@ -123,8 +124,10 @@ struct TileArgs {
   float* part;         // [2 * kMaxCtas][kMaxRows][head_dim]
   float2* ml;          // [2 * kMaxCtas][kMaxRows]
   struct Rec* rec;     // [kMaxCtas]
-  int* err;            // [kMaxCtas]
+  int* err;            // [kMaxCtas]: kLate, kMend
 };
+
+constexpr int kLate = 1, kMend = 2;
 
 // What a CTA leaves for the join: the item that it began and did not end.
 struct Rec {
@@ -138,6 +141,7 @@ struct Ctl {
   uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], xbar, fin;
   uint32_t tmem;
   int abort;
+  int mend;            // a row written by this CTA holds something that is not finite
   int two;             // some item of the call has two row tiles
   int b, h, qt, off;   // start of the CTA's share (off in units)
   long long left, share;
@@ -521,6 +525,15 @@ __device__ __forceinline__ void store16f(float* at, const float* x) {  // 32-byt
                  : "memory");
 }
 
+// (not finite if one of them is not)
+__device__ __forceinline__ float sum16(const float* x) {
+  uint64_t s[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    s[j] = fadd2(pack2(x[4 * j], x[4 * j + 1]), pack2(x[4 * j + 2], x[4 * j + 3]));
+  return sum_of(s);
+}
+
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.0f ? -kInf : ((m == -kInf ? 0.0f : m) + log2f(l)) * kLn2;
 }
@@ -555,6 +568,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     ctl.two = 0;
+    ctl.mend = 0;
     ctl.abort = (smem_u32(smem) & 1023u) ? 1 : 0;  // the swizzle needs this alignment
     for (int i = 0; i < kMaxStages; ++i) mbar_init(ctl.full + i, E4M3 ? kWideWarps : 1);
     for (int i = 0; i < 2 * kMaxStages; ++i) mbar_init(ctl.empty + i, 1);
@@ -915,8 +929,12 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
               if (s.slot < 0) x[j] = l == 0.0f ? 0.0f : x[j] * inv;
             }
             if (live) {
-              if (s.slot < 0) store16<DT>(a.out + (orow * D + 16 * u) * 2, x, t.wide);
-              else store16f(t.part + prow * D + 16 * u, x);
+              if (s.slot < 0) {
+                if (!(fabsf(sum16(x)) < kInf)) ctl.mend = kMend;
+                store16<DT>(a.out + (orow * D + 16 * u) * 2, x, t.wide);
+              } else {
+                store16f(t.part + prow * D + 16 * u, x);
+              }
             }
           }
           if (live) {
@@ -964,8 +982,12 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
               x[j] = (y0 + y1) * inv;
             }
             if (live) {
-              if (s.slot < 0) store16<DT>(a.out + (orow * D + 16 * u) * 2, x, t.wide);
-              else store16f(t.part + prow * D + 16 * u, x);
+              if (s.slot < 0) {
+                if (!(fabsf(sum16(x)) < kInf)) ctl.mend = kMend;
+                store16<DT>(a.out + (orow * D + 16 * u) * 2, x, t.wide);
+              } else {
+                store16f(t.part + prow * D + 16 * u, x);
+              }
             }
           }
           if (live && st == 0) {
@@ -1072,7 +1094,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tbase, 512);
-  if (threadIdx.x == 0) t.err[wid] = ctl.abort;
+  if (threadIdx.x == 0) t.err[wid] = (ctl.abort ? kLate : 0) | ctl.mend;
 }
 
 // ---------------------------------------------------------------------------
@@ -1124,7 +1146,57 @@ __device__ __forceinline__ float4 join_parts(const TileArgs& t, int c, int parts
   return o;
 }
 
-template <int DT>
+// The products of a tile weigh every value of it, and 0 times an infinity is NaN: a value
+// that is not finite reaches rows that do not see it.  So what is not finite in a row's
+// outputs is found again, one warp to the row, from the keys that it sees alone.  sq:
+// shared memory for the warp's query.
+template <int DT, bool E4M3>
+__device__ __forceinline__ void mend_row(const AttendArgs& a, int t, int hq, float* sq) {
+  const int lane = threadIdx.x & 31, D = a.c.head_dim;
+  __syncwarp();  // the row's stores
+  uint4 w = make_uint4(0, 0, 0, 0);
+  uint4* at = reinterpret_cast<uint4*>(a.out + ((int64_t)t * a.heads + hq) * D * 2) + lane;
+  if (lane * 8 < D) w = __ldcg(at);
+  uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  bool odd = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = F16<DT>::up(v[e]);
+    odd |= !(fabsf(f.x) < kInf && fabsf(f.y) < kInf);
+  }
+  if (!__any_sync(0xffffffffu, odd)) return;
+  const int b = owner_of(a.b.q_start, a.b.B, t);
+  if (b >= a.b.B) return;
+  const Seq q = load_seq(a.b, b, a.c.page_size);
+  const int i = t - q.tok0;
+  if (i < 0 || i >= q.n) return;
+  const int hi = max(0, q.pos0 + i + 1);
+  const int lo = a.window && hi > a.window ? hi - a.window : 0;
+  const char* qrow = a.q + (int64_t)t * a.q_token + (int64_t)hq * a.q_head;
+  for (int d = lane; d < D / 2; d += 32) {
+    const float2 f = F16<DT>::up(__ldg(reinterpret_cast<const uint32_t*>(qrow) + d));
+    sq[2 * d] = f.x * a.scale_log2;
+    sq[2 * d + 1] = f.y * a.scale_log2;
+  }
+  __syncwarp();
+  float m = -kInf, l = 0.0f, o[8] = {};
+  attend_blocks<DT, E4M3, 1>(a, b, hq / (a.heads / a.c.kv_heads), lo, hi, sq, 0, 1, m, l, o);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+  __syncwarp();
+  if (lane * 8 >= D) return;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = F16<DT>::up(v[e]);
+    const uint32_t y = F16<DT>::down(o[2 * e] * inv, o[2 * e + 1] * inv);
+    if (!(fabsf(f.x) < kInf)) v[e] = (v[e] & 0xffff0000u) | (y & 0xffffu);
+    if (!(fabsf(f.y) < kInf)) v[e] = (v[e] & 0xffffu) | (y & 0xffff0000u);
+  }
+  *at = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <int DT, bool E4M3>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ TileArgs t,
                                                               int ctas, int join_blocks) {
   constexpr int kWarps = kJoinThreads / 32;
@@ -1141,7 +1213,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
     const int b = ((int)blockIdx.x - join_blocks) * kWarps + warp;
     if (b >= a.b.B) return;
     bool late = false;
-    for (int c = lane; c < ctas; c += 32) late |= __ldcg(t.err + c) != 0;
+    for (int c = lane; c < ctas; c += 32) late |= (__ldcg(t.err + c) & kLate) != 0;
     late = __any_sync(0xffffffffu, late);
     const uint8_t f = sequence_flags(a, b);
     if (lane == 0) a.flags[b] = f | (late ? SV_FLAG_TIMEOUT : 0);
@@ -1151,9 +1223,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
   static_assert(kMaxCtas <= kJoinThreads, "one record per thread");
   if (threadIdx.x == 0) most = 0;
   __syncthreads();
-  int n = 0;
+  int n = 0, err = 0;
   if ((int)threadIdx.x < ctas) {
     const Rec r = t.rec[threadIdx.x];
+    err = __ldcg(t.err + threadIdx.x);
     rec[threadIdx.x] = r;
     n = r.more ? r.ntok * t.group : 0;
     if (r.more) atomicMax(&most, r.more);
@@ -1173,13 +1246,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
   // few rows of many parts: a whole block to a row; else a warp to a row
   const bool wide = most >= 8 && total <= 2 * join_blocks;
   const int step = wide ? join_blocks : join_blocks * kWarps;
-  for (int j = wide ? (int)blockIdx.x : (int)blockIdx.x * kWarps + warp; j < total; j += step) {
-    int c = 0;
+  const int begin = wide ? (int)blockIdx.x : (int)blockIdx.x * kWarps + warp;
+  auto locate = [&](int j, int& c, int& tok, int& hd) {
+    c = 0;
     for (int half = 128; half; half >>= 1)
       if (c + half <= ctas && rows_to[c + half - 1] <= j) c += half;
-    const Rec r = rec[c];
     const int k = j - (c ? rows_to[c - 1] : 0);
-    const int tok = k / t.group, hd = k - tok * t.group;
+    tok = k / t.group;
+    hd = k - tok * t.group;
+  };
+  bool odd = false;
+  for (int j = begin; j < total; j += step) {
+    int c, tok, hd;
+    locate(j, c, tok, hd);
+    const Rec r = rec[c];
     const int row = tok / t.tpt * kTile + tok % t.tpt * t.group + hd;
     const int parts = r.more + 1;
     float M, L;
@@ -1201,11 +1281,31 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     const int D = a.c.head_dim;
     if (lane * 4 < D) {
+      odd |= !(fabsf(o.x * inv + o.y * inv + o.z * inv + o.w * inv) < kInf);
       const uint2 w = make_uint2(F16<DT>::down(o.x * inv, o.y * inv),
                                  F16<DT>::down(o.z * inv, o.w * inv));
       reinterpret_cast<uint2*>(a.out + orow * D * 2)[lane] = w;
     }
     if (lane == 0 && a.lse) a.lse[orow] = lse_of(M, L);
+  }
+  if (!__syncthreads_or(odd || (err & kMend))) return;
+  // rare: the rows joined here, and those that the tile kernel wrote itself
+  float* sq = reinterpret_cast<float*>(so[warp]);
+  if (!wide || !warp)
+    for (int j = begin; j < total; j += step) {
+      int c, tok, hd;
+      locate(j, c, tok, hd);
+      mend_row<DT, E4M3>(a, rec[c].row0 + tok, rec[c].h * t.group + hd, sq);
+    }
+  if (!__syncthreads_or(err & kMend)) return;
+  const int64_t rows = (int64_t)a.b.total * a.heads;
+  for (int64_t j = (int64_t)blockIdx.x * kWarps + warp; j < rows; j += (int64_t)join_blocks * kWarps) {
+    const int tok = (int)(j / a.heads), hq = (int)(j - (int64_t)tok * a.heads);
+    bool cut = false;
+    for (int c = lane; c < ctas; c += 32)
+      cut |= rec[c].more && rec[c].h == hq / t.group && tok >= rec[c].row0 &&
+             tok - rec[c].row0 < rec[c].ntok;
+    if (!__any_sync(0xffffffffu, cut)) mend_row<DT, E4M3>(a, tok, hq, sq);
   }
 }
 
@@ -1368,11 +1468,15 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
                              : (e4m3 ? k_attend_tiles<SV_F16, true> : k_attend_tiles<SV_F16, false>);
   e = launch_pdl(k, dim3(ctas), dim3(e4m3 ? kThreads8 : kThreads16), kSmemBytes, stream, mq, mk, mv, t);
   if (e != cudaSuccess) return e;
-  // all that fit (a warp's row is a chain of three loads), but no more blocks than rows
+  // Blocks of the join: two rounds of the three that fit an SM, or for e4m3, whose mending
+  // leaves room for two, one round (round of 64: 197 us, with two an SM 200; e4m3 round 449,
+  // with four 452), but no more blocks than rows.
   const int64_t rows = (int64_t)a.b.total * a.heads;
-  const int join_blocks = (int)(rows < 6 * ctas ? rows : 6 * ctas);
+  const int most = (e4m3 ? 2 : 6) * ctas;
+  const int join_blocks = (int)(rows < most ? rows : most);
   const int flag_blocks = a.flags ? (a.b.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
-  auto* j = dtype == SV_BF16 ? k_attend_join<SV_BF16> : k_attend_join<SV_F16>;
+  auto* j = dtype == SV_BF16 ? (e4m3 ? k_attend_join<SV_BF16, true> : k_attend_join<SV_BF16, false>)
+                             : (e4m3 ? k_attend_join<SV_F16, true> : k_attend_join<SV_F16, false>);
   return launch_pdl(j, dim3(join_blocks + flag_blocks), dim3(kJoinThreads), 0, stream, t, ctas,
                     join_blocks);
 }

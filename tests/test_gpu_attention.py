@@ -281,3 +281,70 @@ def test_queries_shared_by_all_tokens():
     a = sv.spec_chunk_attention(one, c.cache, c.table, c.start, c.len)["out"]
     b = sv.spec_chunk_attention(one.contiguous(), c.cache, c.table, c.start, c.len)["out"]
     assert bool(((a.double() - b.double()).abs() <= 2.0 ** -7 * (6 + b.double().abs())).all())
+
+
+@pytest.mark.parametrize("cache", [BF, FP, E4M3])
+@pytest.mark.parametrize("page", [4, 16])
+@pytest.mark.parametrize("lens,dim,group,window", [
+    ([(6, 300), (200, 260), (1, 9)], 64, 4, 0),           # all items cut
+    ([(1500, 1700), (3, 40)], 128, 4, 0),                 # items of two row tiles
+    ([(1500, 1700), (130, 500)], 96, 2, 150),
+    ([(2 + b % 4, 6 + (37 * b) % 400) for b in range(400)], 128, 2, 0),  # whole items
+    ([(2 + b % 4, 6 + (37 * b) % 400) for b in range(400)], 64, 7, 50),
+])
+def test_values_that_are_not_finite_reach_only_queries_that_see_them(cache, page, lens, dim, group,
+                                                                     window):
+    """The value of every chunk's last but one token is infinite in one column and NaN in another,
+    and with a window so is that of the token 3 places before the chunk: the queries that see
+    neither keep within the bounds everywhere, the others in the other columns."""
+    dtype = FP if cache == FP else BF
+    c = Case(lens, kv_heads=2, dim=dim, group=group, page=page, dtype=dtype, cache=cache)
+    out, lse, tol, ltol = c.reference(window)  # (of the finite cache)
+    sees = torch.zeros(c.total, dtype=torch.bool)
+    for b, (n, L) in enumerate(c.lens):
+        for j in (L - 2, L - n - 3 if window else -1):
+            if j < 0:
+                continue
+            at = (c.owned[b][j // page], slice(None), j % page)
+            if cache == E4M3:  # (the code has no infinity)
+                c.cache.v.view(torch.uint8)[at + (slice(5, 7),)] = 0x7f
+            else:
+                c.cache.v[at + (5,)] = math.inf
+                c.cache.v[at + (6,)] = math.nan
+            pos = L - n + torch.arange(n)
+            seen = (j <= pos) & ((j > pos - window) if window else True)
+            sees[c.start_list[b]:c.start_list[b + 1]] |= seen
+    sees = sees.cuda()
+    o = c.attend(window=window, want_flags=True)
+    ok = (o["out"].double() - out).abs() <= tol
+    assert bool(ok[~sees].all())
+    assert bool(ok[:, :, :5].all()) and bool(ok[:, :, 7:].all())
+    assert not bool(torch.isfinite(o["out"][sees][:, :, 5:7]).any())
+    assert bool(((o["lse"].double() - lse).abs() <= ltol).all()) and not bool(o["flags"].any())
+
+
+def test_an_infinite_later_value_inside_a_graph():
+    """A captured call mends rows as the eager one does, and only while there is something to."""
+    c = Case([(6, 300), (300, 700)], dim=128)
+    clean = c.attend()["out"].clone()
+    out = {"out": torch.empty_like(clean)}
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        c.attend(out=out)
+        s.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            c.attend(out=out)
+    at = (c.owned[1][(700 - 1) // c.ps], slice(None), (700 - 1) % c.ps)
+    kept = c.cache.v[at].clone()
+    for value in (math.inf, math.nan):
+        c.cache.v[at] = value
+        g.replay()
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(out["out"][:-1]).all())
+        assert not bool(torch.isfinite(out["out"][-1]).any())
+        assert torch.equal(out["out"][:6], clean[:6])
+    c.cache.v[at] = kept
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out["out"], clean)
