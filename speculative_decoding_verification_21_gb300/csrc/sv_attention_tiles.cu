@@ -34,7 +34,7 @@
 //     P V, Q K^T of a stage (about 3200 clocks for 2048 of products) and the power
 //     limit; 440 to 460 us, 1.3 PFLOP/s, 0.67 of a large library product's rate;
 //   a round on e4m3 (9 tokens, 32 sequences up to 40000, 64/8 heads of 128): issue slots
-//     and the three slots of widened tiles; 445 us, 3.4 TB/s of codes, 0.51 of a copy's.
+//     and the three slots of widened tiles; 449 us, 3.4 TB/s of codes, 0.50 of a copy's.
 //     Per tile of 128 keys and values an SM issues about 2200 instructions a scheduler
 //     (half of them widen codes), and has 1370 clocks at HBM's rate.
 //   small calls: the chain lengths, page numbers, copies, products, join; 16 us for one
