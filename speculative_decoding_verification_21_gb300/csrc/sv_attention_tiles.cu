@@ -35,7 +35,7 @@
 //     limit; 440 to 460 us, 1.3 PFLOP/s, 0.67 of a large library product's rate;
 //   a round on e4m3 (9 tokens, 32 sequences up to 40000, 64/8 heads of 128): issue slots
 //     and the three slots of widened tiles; 449 us, 3.4 TB/s of codes, 0.50 of a copy's.
-//     Per tile of 128 keys and values an SM issues about 2200 instructions a scheduler
+//     Per tile of 128 keys and values an SM issues about 1800 instructions a scheduler
 //     (half of them widen codes), and has 1370 clocks at HBM's rate.
 //   small calls: the chain lengths, page numbers, copies, products, join; 16 us for one
 //     token on 777, of them 3 to find the shares, 3 to the first scores, 5 for the join.
