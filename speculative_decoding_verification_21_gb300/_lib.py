@@ -4,6 +4,10 @@ Every step of the verify path runs in the CUDA library; this module turns torch
 tensors into device pointers, allocates outputs and the workspace with torch
 when the caller does not pass them, and raises on a non-OK status.  There is
 no CPU fallback: if the library is missing or fails to load, the call raises.
+
+`stream` (every call): the torch stream that the call is queued on, by default the
+current one.  What the call allocates is taken for that stream; order the tensors that
+are handed in before it, and keep them until it has passed (Tensor.record_stream).
 """
 from __future__ import annotations
 
@@ -180,6 +184,23 @@ def _check_cuda(*ts):
             raise ValueError("all tensors must be contiguous")
 
 
+def _empty(shape, dtype, device, stream=None):
+    """Uninitialised memory for a call queued on `stream` (None: the current one).
+    torch hands memory out again in the order of the stream it was taken under, so
+    it is taken under the call's; the current stream, which the caller will mostly
+    read outputs on, is noted as its user too."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if current.cuda_stream == stream.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 class _WorkspaceCache:
     """Workspaces, one per (device, stream), grown on demand.  Calls queued on
     one stream may share a workspace; the library needs no initial contents."""
@@ -187,12 +208,11 @@ class _WorkspaceCache:
     def __init__(self):
         self._bufs = {}
 
-    def get(self, nbytes: int, device, stream_key):
-        torch = _torch()
+    def get(self, nbytes: int, device, stream_key, stream=None):
         key = (str(device), stream_key)
         buf = self._bufs.get(key)
         if buf is None or buf.numel() < nbytes:
-            buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+            buf = _empty((max(nbytes, 256),), _torch().uint8, device, stream)
             self._bufs[key] = buf
         return buf
 
@@ -235,19 +255,19 @@ def spec_verify(target_logits, draft_logits, draft_tokens, *, temperature: float
     dev = target_logits.device
     o = dict(out or {})
     if "tokens" not in o:
-        o["tokens"] = torch.empty((B, g1), dtype=torch.int32, device=dev)
+        o["tokens"] = _empty((B, g1), torch.int32, dev, stream)
     if "counts" not in o:
-        o["counts"] = torch.empty((B,), dtype=torch.int32, device=dev)
+        o["counts"] = _empty((B,), torch.int32, dev, stream)
     if want_pq:
-        o.setdefault("p", torch.empty((B, g), dtype=torch.float32, device=dev))
-        o.setdefault("q", torch.empty((B, g), dtype=torch.float32, device=dev))
+        o.setdefault("p", _empty((B, g), torch.float32, dev, stream))
+        o.setdefault("q", _empty((B, g), torch.float32, dev, stream))
     if want_alpha:
-        o.setdefault("alpha", torch.empty((B,), dtype=torch.float32, device=dev))
+        o.setdefault("alpha", _empty((B,), torch.float32, dev, stream))
     if want_flags:
-        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
     sh = _stream_handle(stream)
     need = workspace_bytes(B, g, V, SV_MODE_SAMPLE)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value)
+    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
     opts = Options(float(lenience), int(top_k), float(top_p), SAMPLERS[sampler])
     rc = L.spec_verify_opts(_ptr(target_logits), _ptr(draft_logits), _ptr(draft_tokens), B, g,
                             V, _dtype_code(target_logits), float(temperature),
@@ -272,11 +292,11 @@ def spec_verify_greedy(target_logits, draft_tokens, *, out=None, workspace=None,
     _check_cuda(target_logits, draft_tokens)
     dev = target_logits.device
     o = dict(out or {})
-    o.setdefault("tokens", torch.empty((B, g1), dtype=torch.int32, device=dev))
-    o.setdefault("counts", torch.empty((B,), dtype=torch.int32, device=dev))
+    o.setdefault("tokens", _empty((B, g1), torch.int32, dev, stream))
+    o.setdefault("counts", _empty((B,), torch.int32, dev, stream))
     sh = _stream_handle(stream)
     need = workspace_bytes(B, g, V, SV_MODE_GREEDY)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value)
+    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
     rc = L.spec_verify_greedy(_ptr(target_logits), _ptr(draft_tokens), B, g, V,
                               _dtype_code(target_logits), _ptr(o["tokens"]), _ptr(o["counts"]),
                               _ptr(ws), ws.numel(), sh)
@@ -301,16 +321,16 @@ def spec_lmhead_verify(h_target, W_target, h_draft, W_draft, draft_tokens, *, B:
     _check_cuda(h_target, W_target, h_draft, W_draft, draft_tokens, debug_logits)
     dev = h_target.device
     o = dict(out or {})
-    o.setdefault("tokens", torch.empty((B, gamma + 1), dtype=torch.int32, device=dev))
-    o.setdefault("counts", torch.empty((B,), dtype=torch.int32, device=dev))
+    o.setdefault("tokens", _empty((B, gamma + 1), torch.int32, dev, stream))
+    o.setdefault("counts", _empty((B,), torch.int32, dev, stream))
     if want_pq:
-        o.setdefault("p", torch.empty((B, gamma), dtype=torch.float32, device=dev))
-        o.setdefault("q", torch.empty((B, gamma), dtype=torch.float32, device=dev))
+        o.setdefault("p", _empty((B, gamma), torch.float32, dev, stream))
+        o.setdefault("q", _empty((B, gamma), torch.float32, dev, stream))
     if want_flags:
-        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
     sh = _stream_handle(stream)
     need = workspace_bytes(B, gamma, V, SV_MODE_LMHEAD)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value)
+    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
     rc = L.spec_lmhead_verify(_ptr(h_target), _ptr(W_target), Ht, _ptr(h_draft), _ptr(W_draft),
                               Hd, _ptr(draft_tokens), B, gamma, V, float(temperature),
                               int(seed) & (2**64 - 1), int(round) & (2**64 - 1),
@@ -342,16 +362,16 @@ def spec_lmhead_verify_drafted(h_target, W_target, h_draft, W_draft, draft_token
                 debug_logits)
     dev = h_target.device
     o = dict(out or {})
-    o.setdefault("tokens", torch.empty((B, gamma + 1), dtype=torch.int32, device=dev))
-    o.setdefault("counts", torch.empty((B,), dtype=torch.int32, device=dev))
+    o.setdefault("tokens", _empty((B, gamma + 1), torch.int32, dev, stream))
+    o.setdefault("counts", _empty((B,), torch.int32, dev, stream))
     if want_pq:
-        o.setdefault("p", torch.empty((B, gamma), dtype=torch.float32, device=dev))
-        o.setdefault("q", torch.empty((B, gamma), dtype=torch.float32, device=dev))
+        o.setdefault("p", _empty((B, gamma), torch.float32, dev, stream))
+        o.setdefault("q", _empty((B, gamma), torch.float32, dev, stream))
     if want_flags:
-        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
     sh = _stream_handle(stream)
     need = workspace_bytes(B, gamma, V, SV_MODE_LMHEAD)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value)
+    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
     rc = L.spec_lmhead_verify_drafted(
         _ptr(h_target), _ptr(W_target), Ht, _ptr(h_draft), _ptr(W_draft), Hd,
         _ptr(draft_tokens), _ptr(draft_lse), _ptr(draft_logit), B, gamma, V,
@@ -377,13 +397,13 @@ def spec_lmhead_draft(h_draft, W_draft, *, pos: int, temperature: float = 1.0, s
     _check_cuda(h_draft, W_draft, debug_logits)
     dev = h_draft.device
     o = dict(out or {})
-    o.setdefault("tokens", torch.empty((B,), dtype=torch.int32, device=dev))
-    o.setdefault("q", torch.empty((B,), dtype=torch.float32, device=dev))
-    o.setdefault("lse", torch.empty((B,), dtype=torch.float32, device=dev))
-    o.setdefault("logit", torch.empty((B,), dtype=torch.float32, device=dev))
+    o.setdefault("tokens", _empty((B,), torch.int32, dev, stream))
+    o.setdefault("q", _empty((B,), torch.float32, dev, stream))
+    o.setdefault("lse", _empty((B,), torch.float32, dev, stream))
+    o.setdefault("logit", _empty((B,), torch.float32, dev, stream))
     sh = _stream_handle(stream)
     need = workspace_bytes(B, 1, V, SV_MODE_DRAFT)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value)
+    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
     rc = L.spec_lmhead_draft(_ptr(h_draft), _ptr(W_draft), Hd, B, V, float(temperature),
                              int(seed) & (2**64 - 1), int(round) & (2**64 - 1), int(pos),
                              _ptr(o["tokens"]), _ptr(o["q"]), _ptr(o["lse"]), _ptr(o["logit"]),
@@ -507,7 +527,7 @@ def spec_kv_append(cache: KVCache, new_k, new_v, block_table, q_start, kv_len, *
     dev = new_k.device
     o = dict(out or {})
     if want_flags:
-        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
     batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
                          new_k.shape[0], B, block_table.shape[1])
     rc = L.spec_kv_append(cache._ref, ctypes.addressof(batch), _address(new_k), _address(new_v),
@@ -533,9 +553,9 @@ def spec_kv_read(cache: KVCache, block_table, first, out_start, total: int, *, d
     o = dict(out or {})
     for name in ("k", "v"):
         if name not in o:
-            o[name] = torch.empty((total, cache.kv_heads, cache.head_dim), dtype=dtype, device=dev)
+            o[name] = _empty((total, cache.kv_heads, cache.head_dim), dtype, dev, stream)
     if want_flags:
-        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
     _check_cuda(o["k"], o["v"])
     for name in ("k", "v"):
         if tuple(o[name].shape) != (total, cache.kv_heads, cache.head_dim) or \
@@ -574,17 +594,17 @@ def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, sca
     dev = q.device
     o = dict(out or {})
     if "out" not in o:
-        o["out"] = torch.empty((total, heads, dim), dtype=q.dtype, device=dev)
+        o["out"] = _empty((total, heads, dim), q.dtype, dev, stream)
     elif tuple(o["out"].shape) != (total, heads, dim) or o["out"].dtype != q.dtype:
         raise ValueError("out: [total, heads, head_dim] of q's type")
     if want_lse and "lse" not in o:
-        o["lse"] = torch.empty((total, heads), dtype=torch.float32, device=dev)
+        o["lse"] = _empty((total, heads), torch.float32, dev, stream)
     if want_flags:
-        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
     _check_cuda(o["out"], o.get("lse"))
     sh = _stream_of(stream, dev)
     need = attention_workspace_bytes(cache, heads)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh)
+    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh, stream)
     batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), total, B,
                          block_table.shape[1])
     rc = L.spec_chunk_attention(cache._ref, ctypes.addressof(batch), _address(q), _row_code(q), heads,
@@ -618,11 +638,11 @@ def spec_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, *,
     dev = target_probs.device
     o = dict(out or {})
     if "tokens" not in o:
-        o["tokens"] = torch.empty((B, g1), dtype=torch.int32, device=dev)
+        o["tokens"] = _empty((B, g1), torch.int32, dev, stream)
     if "counts" not in o:
-        o["counts"] = torch.empty((B,), dtype=torch.int32, device=dev)
+        o["counts"] = _empty((B,), torch.int32, dev, stream)
     if want_flags:
-        o.setdefault("flags", torch.empty((B,), dtype=torch.uint8, device=dev))
+        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
     rc = L.spec_verify_probs(_address(target_probs), _address(draft_probs), _address(draft_tokens),
                              _address(uniforms), B, g, V, _dtype_code(target_probs),
                              _address(o["tokens"]), _address(o["counts"]), _address(o.get("flags")),

@@ -351,3 +351,15 @@ def test_an_infinite_later_value_inside_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out["out"], clean)
+
+
+def test_queued_on_a_stream_that_is_not_the_current_one():
+    """The first call on a stream, and one that needs a larger workspace there, with cut items."""
+    s = torch.cuda.Stream()
+    for dim in (64, 128):
+        c = Case([(5, 3000), (300, 700), (1, 9000)], dim=dim)
+        want = c.attend()
+        s.wait_stream(torch.cuda.current_stream())
+        got = c.attend(stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
