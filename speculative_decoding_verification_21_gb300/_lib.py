@@ -203,15 +203,22 @@ def _empty(shape, dtype, device, stream=None):
 
 class _WorkspaceCache:
     """Workspaces, one per (device, stream), grown on demand.  Calls queued on
-    one stream may share a workspace; the library needs no initial contents."""
+    one stream may share a workspace; the library needs no initial contents.  One
+    that became too small is kept: a graph captured with it will use it again.  (So
+    a graph that runs beside calls of its capture's stream needs a workspace of its
+    own, passed as workspace=.)"""
 
     def __init__(self):
         self._bufs = {}
+        self._outgrown = []
 
     def get(self, nbytes: int, device, stream_key, stream=None):
         key = (str(device), stream_key)
         buf = self._bufs.get(key)
         if buf is None or buf.numel() < nbytes:
+            if buf is not None:  # twice the size at least: what is kept adds up to less than it
+                self._outgrown.append(buf)
+                nbytes = max(nbytes, 2 * buf.numel())
             buf = _empty((max(nbytes, 256),), _torch().uint8, device, stream)
             self._bufs[key] = buf
         return buf

@@ -1,8 +1,12 @@
-"""What the binding does on the host before a call is queued: memory by stream (no GPU)."""
+"""What the binding does on the host before a call is queued: memory by stream, workspaces that
+grow (no GPU)."""
+import weakref
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
+from speculative_decoding_verification_21_gb300 import _lib
 from tests import _fake_cuda as fake
 
 
@@ -36,3 +40,22 @@ def test_memory_of_a_call_on_the_current_stream(cuda, name):
         call()
         call(stream=side)
     assert all(t.made_under is side and not t.filled and not t.recorded for t in cuda.made)
+
+
+def test_an_outgrown_workspace_is_kept():
+    """A captured graph, or a call that another stream has not passed, may still use it."""
+    cache, cpu = _lib._WorkspaceCache(), torch.device("cpu")
+    sizes = [1000, 1001, 3000, 50000]
+    bufs = [weakref.ref(cache.get(n, cpu, 7)) for n in sizes]
+    assert all(b() is not None and b().numel() >= n for b, n in zip(bufs, sizes))
+    assert cache.get(10, cpu, 7) is bufs[-1]()  # calls share the largest
+    assert cache.get(10, cpu, 8) is not bufs[-1]()
+
+
+def test_outgrown_workspaces_take_no_more_than_the_one_in_use():
+    cache, cpu = _lib._WorkspaceCache(), torch.device("cpu")
+    seen = {}
+    for n in range(300, 40000, 97):
+        b = cache.get(n, cpu, 7)
+        seen[b.data_ptr()] = b.numel()
+    assert sum(seen.values()) <= 2 * b.numel()

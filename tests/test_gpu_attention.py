@@ -363,3 +363,24 @@ def test_queued_on_a_stream_that_is_not_the_current_one():
         got = c.attend(stream=s)
         torch.cuda.current_stream().wait_stream(s)
         assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+
+
+def test_a_graph_keeps_its_workspace_when_a_later_call_needs_a_larger_one():
+    """Captured without workspace=; then heads of 128 on the same stream, and memory taken anew."""
+    c = Case([(5, 3000), (300, 700)], dim=64)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        out = c.attend()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            c.attend(out=out)
+        wide = Case([(5, 3000), (300, 700)], dim=128)
+        wide.attend()
+        taken = [torch.full((1 << 22,), math.nan, device="cuda") for _ in range(8)]
+        want = c.attend()
+        out["out"].zero_()
+        g.replay()
+        s.synchronize()
+    assert torch.equal(out["out"], want["out"]) and torch.equal(out["lse"], want["lse"])
+    assert all(bool(torch.isnan(t).all()) for t in taken)  # the replay wrote to nobody's memory
