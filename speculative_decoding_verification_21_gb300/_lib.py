@@ -12,6 +12,7 @@ are handed in before it, and keep them until it has passed (Tensor.record_stream
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -201,6 +202,35 @@ def _empty(shape, dtype, device, stream=None):
     return t
 
 
+def _output(o, name, shape, dtype, device, stream, want=True, any_shape=False):
+    """o[name], made if it is missing and wanted.  One that was handed in has to be
+    contiguous, on the inputs' device, and of this shape and type (any_shape: of as
+    many bytes): the call writes all of it."""
+    if name not in o:
+        if want:
+            o[name] = _empty(shape, dtype, device, stream)
+        return
+    t = o[name]
+    if t is None:
+        return
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"out {name}: contiguous and on the inputs' device ({device})")
+    if any_shape:
+        if t.numel() * t.element_size() < math.prod(shape) * dtype.itemsize:
+            raise ValueError(f"out {name}: too small for {shape} of {dtype}")
+    elif tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"out {name}: {shape} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+
+
+def _workspace(workspace, nbytes, device, stream_key, stream):
+    """The workspace of a call: the caller's, or the stream's."""
+    if workspace is None:
+        return _ws_cache.get(nbytes, device, stream_key, stream)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: contiguous and on the inputs' device ({device})")
+    return workspace
+
+
 class _WorkspaceCache:
     """Workspaces, one per (device, stream), grown on demand.  Calls queued on
     one stream may share a workspace; the library needs no initial contents.  One
@@ -261,20 +291,15 @@ def spec_verify(target_logits, draft_logits, draft_tokens, *, temperature: float
     _check_cuda(target_logits, draft_logits, draft_tokens, row_temperature)
     dev = target_logits.device
     o = dict(out or {})
-    if "tokens" not in o:
-        o["tokens"] = _empty((B, g1), torch.int32, dev, stream)
-    if "counts" not in o:
-        o["counts"] = _empty((B,), torch.int32, dev, stream)
-    if want_pq:
-        o.setdefault("p", _empty((B, g), torch.float32, dev, stream))
-        o.setdefault("q", _empty((B, g), torch.float32, dev, stream))
-    if want_alpha:
-        o.setdefault("alpha", _empty((B,), torch.float32, dev, stream))
-    if want_flags:
-        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
+    _output(o, "tokens", (B, g1), torch.int32, dev, stream, any_shape=True)
+    _output(o, "counts", (B,), torch.int32, dev, stream, any_shape=True)
+    _output(o, "p", (B, g), torch.float32, dev, stream, want_pq, any_shape=True)
+    _output(o, "q", (B, g), torch.float32, dev, stream, want_pq, any_shape=True)
+    _output(o, "alpha", (B,), torch.float32, dev, stream, want_alpha, any_shape=True)
+    _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags, any_shape=True)
     sh = _stream_handle(stream)
     need = workspace_bytes(B, g, V, SV_MODE_SAMPLE)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
+    ws = _workspace(workspace, need, dev, sh.value, stream)
     opts = Options(float(lenience), int(top_k), float(top_p), SAMPLERS[sampler])
     rc = L.spec_verify_opts(_ptr(target_logits), _ptr(draft_logits), _ptr(draft_tokens), B, g,
                             V, _dtype_code(target_logits), float(temperature),
@@ -299,11 +324,11 @@ def spec_verify_greedy(target_logits, draft_tokens, *, out=None, workspace=None,
     _check_cuda(target_logits, draft_tokens)
     dev = target_logits.device
     o = dict(out or {})
-    o.setdefault("tokens", _empty((B, g1), torch.int32, dev, stream))
-    o.setdefault("counts", _empty((B,), torch.int32, dev, stream))
+    _output(o, "tokens", (B, g1), torch.int32, dev, stream, any_shape=True)
+    _output(o, "counts", (B,), torch.int32, dev, stream, any_shape=True)
     sh = _stream_handle(stream)
     need = workspace_bytes(B, g, V, SV_MODE_GREEDY)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
+    ws = _workspace(workspace, need, dev, sh.value, stream)
     rc = L.spec_verify_greedy(_ptr(target_logits), _ptr(draft_tokens), B, g, V,
                               _dtype_code(target_logits), _ptr(o["tokens"]), _ptr(o["counts"]),
                               _ptr(ws), ws.numel(), sh)
@@ -328,16 +353,14 @@ def spec_lmhead_verify(h_target, W_target, h_draft, W_draft, draft_tokens, *, B:
     _check_cuda(h_target, W_target, h_draft, W_draft, draft_tokens, debug_logits)
     dev = h_target.device
     o = dict(out or {})
-    o.setdefault("tokens", _empty((B, gamma + 1), torch.int32, dev, stream))
-    o.setdefault("counts", _empty((B,), torch.int32, dev, stream))
-    if want_pq:
-        o.setdefault("p", _empty((B, gamma), torch.float32, dev, stream))
-        o.setdefault("q", _empty((B, gamma), torch.float32, dev, stream))
-    if want_flags:
-        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
+    _output(o, "tokens", (B, gamma + 1), torch.int32, dev, stream, any_shape=True)
+    _output(o, "counts", (B,), torch.int32, dev, stream, any_shape=True)
+    _output(o, "p", (B, gamma), torch.float32, dev, stream, want_pq, any_shape=True)
+    _output(o, "q", (B, gamma), torch.float32, dev, stream, want_pq, any_shape=True)
+    _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags, any_shape=True)
     sh = _stream_handle(stream)
     need = workspace_bytes(B, gamma, V, SV_MODE_LMHEAD)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
+    ws = _workspace(workspace, need, dev, sh.value, stream)
     rc = L.spec_lmhead_verify(_ptr(h_target), _ptr(W_target), Ht, _ptr(h_draft), _ptr(W_draft),
                               Hd, _ptr(draft_tokens), B, gamma, V, float(temperature),
                               int(seed) & (2**64 - 1), int(round) & (2**64 - 1),
@@ -369,16 +392,14 @@ def spec_lmhead_verify_drafted(h_target, W_target, h_draft, W_draft, draft_token
                 debug_logits)
     dev = h_target.device
     o = dict(out or {})
-    o.setdefault("tokens", _empty((B, gamma + 1), torch.int32, dev, stream))
-    o.setdefault("counts", _empty((B,), torch.int32, dev, stream))
-    if want_pq:
-        o.setdefault("p", _empty((B, gamma), torch.float32, dev, stream))
-        o.setdefault("q", _empty((B, gamma), torch.float32, dev, stream))
-    if want_flags:
-        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
+    _output(o, "tokens", (B, gamma + 1), torch.int32, dev, stream, any_shape=True)
+    _output(o, "counts", (B,), torch.int32, dev, stream, any_shape=True)
+    _output(o, "p", (B, gamma), torch.float32, dev, stream, want_pq, any_shape=True)
+    _output(o, "q", (B, gamma), torch.float32, dev, stream, want_pq, any_shape=True)
+    _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags, any_shape=True)
     sh = _stream_handle(stream)
     need = workspace_bytes(B, gamma, V, SV_MODE_LMHEAD)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
+    ws = _workspace(workspace, need, dev, sh.value, stream)
     rc = L.spec_lmhead_verify_drafted(
         _ptr(h_target), _ptr(W_target), Ht, _ptr(h_draft), _ptr(W_draft), Hd,
         _ptr(draft_tokens), _ptr(draft_lse), _ptr(draft_logit), B, gamma, V,
@@ -404,13 +425,13 @@ def spec_lmhead_draft(h_draft, W_draft, *, pos: int, temperature: float = 1.0, s
     _check_cuda(h_draft, W_draft, debug_logits)
     dev = h_draft.device
     o = dict(out or {})
-    o.setdefault("tokens", _empty((B,), torch.int32, dev, stream))
-    o.setdefault("q", _empty((B,), torch.float32, dev, stream))
-    o.setdefault("lse", _empty((B,), torch.float32, dev, stream))
-    o.setdefault("logit", _empty((B,), torch.float32, dev, stream))
+    _output(o, "tokens", (B,), torch.int32, dev, stream, any_shape=True)
+    _output(o, "q", (B,), torch.float32, dev, stream, any_shape=True)
+    _output(o, "lse", (B,), torch.float32, dev, stream, any_shape=True)
+    _output(o, "logit", (B,), torch.float32, dev, stream, any_shape=True)
     sh = _stream_handle(stream)
     need = workspace_bytes(B, 1, V, SV_MODE_DRAFT)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh.value, stream)
+    ws = _workspace(workspace, need, dev, sh.value, stream)
     rc = L.spec_lmhead_draft(_ptr(h_draft), _ptr(W_draft), Hd, B, V, float(temperature),
                              int(seed) & (2**64 - 1), int(round) & (2**64 - 1), int(pos),
                              _ptr(o["tokens"]), _ptr(o["q"]), _ptr(o["lse"]), _ptr(o["logit"]),
@@ -533,8 +554,7 @@ def spec_kv_append(cache: KVCache, new_k, new_v, block_table, q_start, kv_len, *
     B = _check_index(block_table, q_start, kv_len)
     dev = new_k.device
     o = dict(out or {})
-    if want_flags:
-        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
+    _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags)
     batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
                          new_k.shape[0], B, block_table.shape[1])
     rc = L.spec_kv_append(cache._ref, ctypes.addressof(batch), _address(new_k), _address(new_v),
@@ -559,15 +579,8 @@ def spec_kv_read(cache: KVCache, block_table, first, out_start, total: int, *, d
     dev = block_table.device
     o = dict(out or {})
     for name in ("k", "v"):
-        if name not in o:
-            o[name] = _empty((total, cache.kv_heads, cache.head_dim), dtype, dev, stream)
-    if want_flags:
-        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
-    _check_cuda(o["k"], o["v"])
-    for name in ("k", "v"):
-        if tuple(o[name].shape) != (total, cache.kv_heads, cache.head_dim) or \
-                o[name].dtype != dtype:
-            raise ValueError("out k, v: [total, kv_heads, head_dim] of the asked type")
+        _output(o, name, (total, cache.kv_heads, cache.head_dim), dtype, dev, stream)
+    _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags)
     rc = L.spec_kv_read(cache._ref, _address(block_table), _address(first), _address(out_start), B,
                         block_table.shape[1], int(total), _address(o["k"]), _address(o["v"]),
                         _row_code(o["k"]), _address(o.get("flags")), _stream_of(stream, dev))
@@ -600,18 +613,12 @@ def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, sca
     total, heads, dim = q.shape
     dev = q.device
     o = dict(out or {})
-    if "out" not in o:
-        o["out"] = _empty((total, heads, dim), q.dtype, dev, stream)
-    elif tuple(o["out"].shape) != (total, heads, dim) or o["out"].dtype != q.dtype:
-        raise ValueError("out: [total, heads, head_dim] of q's type")
-    if want_lse and "lse" not in o:
-        o["lse"] = _empty((total, heads), torch.float32, dev, stream)
-    if want_flags:
-        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
-    _check_cuda(o["out"], o.get("lse"))
+    _output(o, "out", (total, heads, dim), q.dtype, dev, stream)
+    _output(o, "lse", (total, heads), torch.float32, dev, stream, want_lse)
+    _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags)
     sh = _stream_of(stream, dev)
     need = attention_workspace_bytes(cache, heads)
-    ws = workspace if workspace is not None else _ws_cache.get(need, dev, sh, stream)
+    ws = _workspace(workspace, need, dev, sh, stream)
     batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), total, B,
                          block_table.shape[1])
     rc = L.spec_chunk_attention(cache._ref, ctypes.addressof(batch), _address(q), _row_code(q), heads,
@@ -644,12 +651,9 @@ def spec_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, *,
     _check_cuda(target_probs, draft_probs, draft_tokens, uniforms)
     dev = target_probs.device
     o = dict(out or {})
-    if "tokens" not in o:
-        o["tokens"] = _empty((B, g1), torch.int32, dev, stream)
-    if "counts" not in o:
-        o["counts"] = _empty((B,), torch.int32, dev, stream)
-    if want_flags:
-        o.setdefault("flags", _empty((B,), torch.uint8, dev, stream))
+    _output(o, "tokens", (B, g1), torch.int32, dev, stream)
+    _output(o, "counts", (B,), torch.int32, dev, stream)
+    _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags)
     rc = L.spec_verify_probs(_address(target_probs), _address(draft_probs), _address(draft_tokens),
                              _address(uniforms), B, g, V, _dtype_code(target_probs),
                              _address(o["tokens"]), _address(o["counts"]), _address(o.get("flags")),

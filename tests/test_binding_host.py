@@ -1,5 +1,5 @@
 """What the binding does on the host before a call is queued: memory by stream, workspaces that
-grow (no GPU)."""
+grow, refusals (no GPU)."""
 import weakref
 
 import pytest
@@ -59,3 +59,78 @@ def test_outgrown_workspaces_take_no_more_than_the_one_in_use():
         b = cache.get(n, cpu, 7)
         seen[b.data_ptr()] = b.numel()
     assert sum(seen.values()) <= 2 * b.numel()
+
+
+def attention_outputs(**change):
+    o = {"out": fake.Tensor((6, 8, 64), fake.BF), "lse": fake.Tensor((6, 8), fake.F32),
+         "flags": fake.Tensor((2,), torch.uint8)}
+    return {**o, **change}
+
+
+def probs_outputs(**change):
+    o = {"tokens": fake.Tensor((2, 5), fake.I32), "counts": fake.Tensor((2,), fake.I32),
+         "flags": fake.Tensor((2,), torch.uint8)}
+    return {**o, **change}
+
+
+def rows_outputs(**change):
+    o = {"k": fake.Tensor((6, 2, 64), fake.BF), "v": fake.Tensor((6, 2, 64), fake.BF),
+         "flags": fake.Tensor((2,), torch.uint8)}
+    return {**o, **change}
+
+
+def flags_only(**change):
+    return {"flags": fake.Tensor((2,), torch.uint8), **change}
+
+
+NEW = {"spec_chunk_attention": attention_outputs, "spec_verify_probs": probs_outputs,
+       "spec_kv_read": rows_outputs, "spec_kv_append": flags_only}
+
+
+@pytest.mark.parametrize("name", NEW)
+def test_outputs_that_are_handed_in_are_looked_at(cuda, name):
+    """A short tensor, or one of a narrower type, would be written past its end."""
+    call, outputs = fake.calls()[name], NEW[name]
+    r = call(out=outputs(), want_flags=True)
+    assert set(r) == set(outputs()) and len(cuda.library.calls) == 1
+    for key, good in outputs().items():
+        shape, dtype = tuple(good.shape), good.dtype
+        wrong_type = torch.int8 if dtype != torch.int8 else torch.uint8
+        for bad in (fake.Tensor((shape[0] - 1,) + shape[1:], dtype),          # short
+                    fake.Tensor(shape[:-1] + (shape[-1] + 1,), dtype),        # another shape
+                    fake.Tensor(shape + (1,), dtype),
+                    fake.Tensor(shape, torch.float64 if dtype != torch.float64 else dtype),
+                    fake.Tensor(shape, wrong_type),                           # narrower
+                    fake.Tensor(shape, dtype, strides=[2 * s for s in good.stride()]),
+                    fake.Tensor(shape, dtype, "cpu")):
+            with pytest.raises((ValueError, TypeError)):
+                call(out=outputs(**{key: bad}))
+    assert len(cuda.library.calls) == 1
+
+
+@pytest.mark.parametrize("name", [n for n in fake.NAMES if n not in NEW])
+def test_older_calls_refuse_outputs_without_room(cuda, name):
+    call = fake.calls()[name]
+    full = call(**fake.FLAGS[name])
+    n = len(cuda.library.calls)
+    call(out=full)
+    for key, t in full.items():
+        size = t.numel()
+        call(out={**full, key: fake.Tensor((size,), t.dtype)})  # (any shape will do)
+        for bad in (fake.Tensor((size - 1,), t.dtype), fake.Tensor((size,), t.dtype, "cpu"),
+                    fake.Tensor((size,), t.dtype, strides=(2,))):
+            with pytest.raises(ValueError):
+                call(out={**full, key: bad})
+    assert len(cuda.library.calls) == n + 1 + len(full)
+
+
+def test_workspaces_that_are_handed_in_are_looked_at(cuda):
+    for name, call in fake.calls().items():
+        if name in ("spec_kv_append", "spec_kv_read", "spec_verify_probs"):
+            continue  # (need none)
+        call(workspace=fake.Tensor((5000,), torch.uint8))
+        assert cuda.library.calls[-1][1][-2] == 5000
+        for bad in (fake.Tensor((5000,), torch.uint8, "cpu"),
+                    fake.Tensor((5000,), torch.uint8, strides=(2,))):
+            with pytest.raises(ValueError):
+                call(workspace=bad)
