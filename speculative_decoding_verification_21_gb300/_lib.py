@@ -161,11 +161,26 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream_handle(stream):
-    torch = _torch()
+def _stream_of(stream, device) -> int:
+    """The raw stream that a call is queued on: `stream`, or the device's current one."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _torch().cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors of {device}")
+    return stream.cuda_stream
+
+
+def _stream_handle(stream, device):
+    return ctypes.c_void_p(_stream_of(stream, device))
+
+
+def _queue(entry, device, *args):
+    """entry(*args) with the tensors' device current: the library launches on that."""
+    cuda = _torch().cuda
+    if cuda.current_device() == device.index:
+        return entry(*args)
+    with cuda.device(device):
+        return entry(*args)
 
 
 def _dtype_code(t) -> int:
@@ -177,12 +192,18 @@ def _dtype_code(t) -> int:
     raise TypeError(f"logits must be float32 or bfloat16, got {t.dtype}")
 
 
-def _check_cuda(*ts):
+def _check_cuda(*ts, device=None):
+    """Contiguous tensors of one CUDA device (`device`, or the first one's)."""
     for t in ts:
-        if t is not None and not t.is_cuda:
+        if t is None:
+            continue
+        if not t.is_cuda:
             raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
-        if t is not None and not t.is_contiguous():
+        if not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
+        device = device or t.device
+        if t.device != device:
+            raise ValueError(f"all tensors must be on one device, got {device} and {t.device}")
 
 
 def _empty(shape, dtype, device, stream=None):
@@ -297,17 +318,16 @@ def spec_verify(target_logits, draft_logits, draft_tokens, *, temperature: float
     _output(o, "q", (B, g), torch.float32, dev, stream, want_pq, any_shape=True)
     _output(o, "alpha", (B,), torch.float32, dev, stream, want_alpha, any_shape=True)
     _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags, any_shape=True)
-    sh = _stream_handle(stream)
+    sh = _stream_handle(stream, dev)
     need = workspace_bytes(B, g, V, SV_MODE_SAMPLE)
     ws = _workspace(workspace, need, dev, sh.value, stream)
     opts = Options(float(lenience), int(top_k), float(top_p), SAMPLERS[sampler])
-    rc = L.spec_verify_opts(_ptr(target_logits), _ptr(draft_logits), _ptr(draft_tokens), B, g,
-                            V, _dtype_code(target_logits), float(temperature),
-                            _ptr(row_temperature), int(seed) & (2**64 - 1),
-                            int(round) & (2**64 - 1), _ptr(o["tokens"]), _ptr(o["counts"]),
-                            _ptr(o.get("p")), _ptr(o.get("q")), _ptr(o.get("alpha")),
-                            _ptr(o.get("flags")), ctypes.addressof(opts), _ptr(ws), ws.numel(),
-                            sh)
+    rc = _queue(L.spec_verify_opts, dev, _ptr(target_logits), _ptr(draft_logits),
+                _ptr(draft_tokens), B, g, V, _dtype_code(target_logits), float(temperature),
+                _ptr(row_temperature), int(seed) & (2**64 - 1), int(round) & (2**64 - 1),
+                _ptr(o["tokens"]), _ptr(o["counts"]), _ptr(o.get("p")), _ptr(o.get("q")),
+                _ptr(o.get("alpha")), _ptr(o.get("flags")), ctypes.addressof(opts), _ptr(ws),
+                ws.numel(), sh)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify")
     return o
@@ -326,12 +346,12 @@ def spec_verify_greedy(target_logits, draft_tokens, *, out=None, workspace=None,
     o = dict(out or {})
     _output(o, "tokens", (B, g1), torch.int32, dev, stream, any_shape=True)
     _output(o, "counts", (B,), torch.int32, dev, stream, any_shape=True)
-    sh = _stream_handle(stream)
+    sh = _stream_handle(stream, dev)
     need = workspace_bytes(B, g, V, SV_MODE_GREEDY)
     ws = _workspace(workspace, need, dev, sh.value, stream)
-    rc = L.spec_verify_greedy(_ptr(target_logits), _ptr(draft_tokens), B, g, V,
-                              _dtype_code(target_logits), _ptr(o["tokens"]), _ptr(o["counts"]),
-                              _ptr(ws), ws.numel(), sh)
+    rc = _queue(L.spec_verify_greedy, dev, _ptr(target_logits), _ptr(draft_tokens), B, g, V,
+                _dtype_code(target_logits), _ptr(o["tokens"]), _ptr(o["counts"]), _ptr(ws),
+                ws.numel(), sh)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_greedy")
     return o
@@ -358,15 +378,14 @@ def spec_lmhead_verify(h_target, W_target, h_draft, W_draft, draft_tokens, *, B:
     _output(o, "p", (B, gamma), torch.float32, dev, stream, want_pq, any_shape=True)
     _output(o, "q", (B, gamma), torch.float32, dev, stream, want_pq, any_shape=True)
     _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags, any_shape=True)
-    sh = _stream_handle(stream)
+    sh = _stream_handle(stream, dev)
     need = workspace_bytes(B, gamma, V, SV_MODE_LMHEAD)
     ws = _workspace(workspace, need, dev, sh.value, stream)
-    rc = L.spec_lmhead_verify(_ptr(h_target), _ptr(W_target), Ht, _ptr(h_draft), _ptr(W_draft),
-                              Hd, _ptr(draft_tokens), B, gamma, V, float(temperature),
-                              int(seed) & (2**64 - 1), int(round) & (2**64 - 1),
-                              _ptr(o["tokens"]), _ptr(o["counts"]), _ptr(o.get("p")),
-                              _ptr(o.get("q")), _ptr(o.get("flags")), _ptr(debug_logits),
-                              _ptr(ws), ws.numel(), sh)
+    rc = _queue(L.spec_lmhead_verify, dev, _ptr(h_target), _ptr(W_target), Ht, _ptr(h_draft),
+                _ptr(W_draft), Hd, _ptr(draft_tokens), B, gamma, V, float(temperature),
+                int(seed) & (2**64 - 1), int(round) & (2**64 - 1), _ptr(o["tokens"]),
+                _ptr(o["counts"]), _ptr(o.get("p")), _ptr(o.get("q")), _ptr(o.get("flags")),
+                _ptr(debug_logits), _ptr(ws), ws.numel(), sh)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_lmhead_verify")
     return o
@@ -397,15 +416,15 @@ def spec_lmhead_verify_drafted(h_target, W_target, h_draft, W_draft, draft_token
     _output(o, "p", (B, gamma), torch.float32, dev, stream, want_pq, any_shape=True)
     _output(o, "q", (B, gamma), torch.float32, dev, stream, want_pq, any_shape=True)
     _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags, any_shape=True)
-    sh = _stream_handle(stream)
+    sh = _stream_handle(stream, dev)
     need = workspace_bytes(B, gamma, V, SV_MODE_LMHEAD)
     ws = _workspace(workspace, need, dev, sh.value, stream)
-    rc = L.spec_lmhead_verify_drafted(
-        _ptr(h_target), _ptr(W_target), Ht, _ptr(h_draft), _ptr(W_draft), Hd,
-        _ptr(draft_tokens), _ptr(draft_lse), _ptr(draft_logit), B, gamma, V,
-        float(temperature), int(seed) & (2**64 - 1), int(round) & (2**64 - 1),
-        _ptr(o["tokens"]), _ptr(o["counts"]), _ptr(o.get("p")), _ptr(o.get("q")),
-        _ptr(o.get("flags")), _ptr(debug_logits), _ptr(ws), ws.numel(), sh)
+    rc = _queue(L.spec_lmhead_verify_drafted, dev, _ptr(h_target), _ptr(W_target), Ht,
+                _ptr(h_draft), _ptr(W_draft), Hd, _ptr(draft_tokens), _ptr(draft_lse),
+                _ptr(draft_logit), B, gamma, V, float(temperature), int(seed) & (2**64 - 1),
+                int(round) & (2**64 - 1), _ptr(o["tokens"]), _ptr(o["counts"]), _ptr(o.get("p")),
+                _ptr(o.get("q")), _ptr(o.get("flags")), _ptr(debug_logits), _ptr(ws), ws.numel(),
+                sh)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_lmhead_verify_drafted")
     return o
@@ -429,13 +448,13 @@ def spec_lmhead_draft(h_draft, W_draft, *, pos: int, temperature: float = 1.0, s
     _output(o, "q", (B,), torch.float32, dev, stream, any_shape=True)
     _output(o, "lse", (B,), torch.float32, dev, stream, any_shape=True)
     _output(o, "logit", (B,), torch.float32, dev, stream, any_shape=True)
-    sh = _stream_handle(stream)
+    sh = _stream_handle(stream, dev)
     need = workspace_bytes(B, 1, V, SV_MODE_DRAFT)
     ws = _workspace(workspace, need, dev, sh.value, stream)
-    rc = L.spec_lmhead_draft(_ptr(h_draft), _ptr(W_draft), Hd, B, V, float(temperature),
-                             int(seed) & (2**64 - 1), int(round) & (2**64 - 1), int(pos),
-                             _ptr(o["tokens"]), _ptr(o["q"]), _ptr(o["lse"]), _ptr(o["logit"]),
-                             _ptr(debug_logits), _ptr(ws), ws.numel(), sh)
+    rc = _queue(L.spec_lmhead_draft, dev, _ptr(h_draft), _ptr(W_draft), Hd, B, V,
+                float(temperature), int(seed) & (2**64 - 1), int(round) & (2**64 - 1), int(pos),
+                _ptr(o["tokens"]), _ptr(o["q"]), _ptr(o["lse"]), _ptr(o["logit"]),
+                _ptr(debug_logits), _ptr(ws), ws.numel(), sh)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_lmhead_draft")
     return o
@@ -467,12 +486,12 @@ class KVCache:
             for s in (k_scale, v_scale):
                 if s.dtype != torch.uint8 or tuple(s.shape) != tuple(k.shape[:3]):
                     raise ValueError("scales: uint8 [num_pages, kv_heads, page_size]")
-        _check_cuda(k_scale, v_scale)
         if not (k.is_cuda and v.device == k.device):
-            raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
+            raise ValueError("k and v must be CUDA tensors of one device (the library has no CPU path)")
+        _check_cuda(k_scale, v_scale, device=k.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
-        self.dtype = k.dtype
+        self.dtype, self.device = k.dtype, k.device
         self._struct = _CacheStruct(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
             v_scale.data_ptr() if e4m3 else None, k.shape[0], k.stride(0), k.stride(1),
@@ -512,25 +531,19 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_of(stream, device) -> int:
-    """The raw stream that a call is queued on: `stream`, or the device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _torch().cuda.current_stream(device).cuda_stream
-
-
 def _check_rows(t, heads, cache, what):
     if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads and t.shape[1] != heads):
         raise ValueError(f"{what}: [total, heads, head_dim]")
-    if not t.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
+    if t.device != cache.device:
+        raise ValueError(f"{what} is on {t.device}, the cache on {cache.device} "
+                         "(the library has no CPU path)")
     if t.stride(2) != 1:
         raise ValueError(f"{what}: the head dimension must be contiguous")
 
 
-def _check_index(block_table, start, length):
+def _check_index(block_table, start, length, device):
     torch = _torch()
-    _check_cuda(block_table, start, length)
+    _check_cuda(block_table, start, length, device=device)
     i32 = torch.int32
     if block_table.dtype != i32 or start.dtype != i32 or length.dtype != i32:
         raise TypeError("block_table, q_start and lengths must be int32")
@@ -549,17 +562,18 @@ def spec_kv_append(cache: KVCache, new_k, new_v, block_table, q_start, kv_len, *
     torch = _torch()
     L = _lib or load()
     _check_rows(new_k, cache.kv_heads, cache, "new_k")
+    _check_rows(new_v, cache.kv_heads, cache, "new_v")
     if new_v.shape != new_k.shape or new_v.dtype != new_k.dtype or new_v.stride() != new_k.stride():
         raise ValueError("new_v must match new_k in shape, type and strides")
-    B = _check_index(block_table, q_start, kv_len)
+    B = _check_index(block_table, q_start, kv_len, cache.device)
     dev = new_k.device
     o = dict(out or {})
     _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags)
     batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
                          new_k.shape[0], B, block_table.shape[1])
-    rc = L.spec_kv_append(cache._ref, ctypes.addressof(batch), _address(new_k), _address(new_v),
-                          _row_code(new_k), new_k.stride(0), new_k.stride(1),
-                          _address(o.get("flags")), _stream_of(stream, dev))
+    rc = _queue(L.spec_kv_append, dev, cache._ref, ctypes.addressof(batch), _address(new_k),
+                _address(new_v), _row_code(new_k), new_k.stride(0), new_k.stride(1),
+                _address(o.get("flags")), _stream_of(stream, dev))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_kv_append")
     return o
@@ -573,17 +587,18 @@ def spec_kv_read(cache: KVCache, block_table, first, out_start, total: int, *, d
     k, v [total, kv_heads, head_dim], flags [B] uint8 (if want_flags)."""
     torch = _torch()
     L = _lib or load()
-    B = _check_index(block_table, out_start, first)
+    B = _check_index(block_table, out_start, first, cache.device)
     if dtype is None:
         dtype = torch.bfloat16 if cache.dtype == torch.float8_e4m3fn else cache.dtype
-    dev = block_table.device
+    dev = cache.device
     o = dict(out or {})
     for name in ("k", "v"):
         _output(o, name, (total, cache.kv_heads, cache.head_dim), dtype, dev, stream)
     _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags)
-    rc = L.spec_kv_read(cache._ref, _address(block_table), _address(first), _address(out_start), B,
-                        block_table.shape[1], int(total), _address(o["k"]), _address(o["v"]),
-                        _row_code(o["k"]), _address(o.get("flags")), _stream_of(stream, dev))
+    rc = _queue(L.spec_kv_read, dev, cache._ref, _address(block_table), _address(first),
+                _address(out_start), B, block_table.shape[1], int(total), _address(o["k"]),
+                _address(o["v"]), _row_code(o["k"]), _address(o.get("flags")),
+                _stream_of(stream, dev))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_kv_read")
     return o
@@ -609,7 +624,7 @@ def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, sca
     torch = _torch()
     L = _lib or load()
     _check_rows(q, 0, cache, "q")
-    B = _check_index(block_table, q_start, kv_len)
+    B = _check_index(block_table, q_start, kv_len, cache.device)
     total, heads, dim = q.shape
     dev = q.device
     o = dict(out or {})
@@ -621,11 +636,10 @@ def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, sca
     ws = _workspace(workspace, need, dev, sh, stream)
     batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), total, B,
                          block_table.shape[1])
-    rc = L.spec_chunk_attention(cache._ref, ctypes.addressof(batch), _address(q), _row_code(q), heads,
-                                q.stride(0), q.stride(1),
-                                dim ** -0.5 if scale is None else float(scale), int(window),
-                                _address(o["out"]), _address(o.get("lse")), _address(o.get("flags")),
-                                _address(ws), ws.numel(), sh)
+    rc = _queue(L.spec_chunk_attention, dev, cache._ref, ctypes.addressof(batch), _address(q),
+                _row_code(q), heads, q.stride(0), q.stride(1),
+                dim ** -0.5 if scale is None else float(scale), int(window), _address(o["out"]),
+                _address(o.get("lse")), _address(o.get("flags")), _address(ws), ws.numel(), sh)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_chunk_attention")
     return o
@@ -654,10 +668,10 @@ def spec_verify_probs(target_probs, draft_probs, draft_tokens, uniforms, *,
     _output(o, "tokens", (B, g1), torch.int32, dev, stream)
     _output(o, "counts", (B,), torch.int32, dev, stream)
     _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags)
-    rc = L.spec_verify_probs(_address(target_probs), _address(draft_probs), _address(draft_tokens),
-                             _address(uniforms), B, g, V, _dtype_code(target_probs),
-                             _address(o["tokens"]), _address(o["counts"]), _address(o.get("flags")),
-                             _stream_of(stream, dev))
+    rc = _queue(L.spec_verify_probs, dev, _address(target_probs), _address(draft_probs),
+                _address(draft_tokens), _address(uniforms), B, g, V, _dtype_code(target_probs),
+                _address(o["tokens"]), _address(o["counts"]), _address(o.get("flags")),
+                _stream_of(stream, dev))
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_probs")
     return o

@@ -134,3 +134,42 @@ def test_workspaces_that_are_handed_in_are_looked_at(cuda):
                     fake.Tensor((5000,), torch.uint8, strides=(2,))):
             with pytest.raises(ValueError):
                 call(workspace=bad)
+
+
+@pytest.mark.parametrize("name", fake.NAMES)
+def test_tensors_of_two_devices_are_refused(cuda, name):
+    for device, other in (("cuda:0", "cuda:1"), ("cuda:1", "cuda:0")):
+        with pytest.raises(ValueError):
+            fake.calls(device, other)[name]()
+    with pytest.raises(ValueError):
+        fake.calls()[name](stream=fake.Stream("elsewhere", "cuda:1"))
+    t, q_start, kv_len = fake.index_arrays()
+    k, v = (fake.Tensor((6, 2, 64), fake.BF, d) for d in ("cuda:0", "cuda:1"))
+    for new in ((k, v), (v, k), (v, v)):
+        with pytest.raises(ValueError):
+            _lib.spec_kv_append(fake.cache(), *new, t, q_start, kv_len)
+    assert not cuda.library.calls
+
+
+def test_a_cache_has_one_device(cuda):
+    k, far = (fake.Tensor((10, 2, 16, 64), fake.BF, d) for d in ("cuda:0", "cuda:1"))
+    with pytest.raises(ValueError):
+        _lib.KVCache(k, far)
+    codes = [fake.Tensor((10, 2, 16, 64), torch.float8_e4m3fn) for _ in range(2)]
+    near, far = (fake.Tensor((10, 2, 16), torch.uint8, d) for d in ("cuda:0", "cuda:1"))
+    for scales in ((near, far), (far, near), (far, far)):
+        with pytest.raises(ValueError):
+            _lib.KVCache(*codes, *scales)
+    _lib.KVCache(*codes, near, near)
+
+
+@pytest.mark.parametrize("name", fake.NAMES)
+def test_a_call_is_queued_on_its_tensors_device(cuda, name):
+    """The library launches on the current device."""
+    call = fake.calls("cuda:1")[name]
+    call()
+    entry, args, device = cuda.library.calls[-1]
+    assert device == 1 and cuda.device_index == 0
+    handle = getattr(args[-1], "value", args[-1])
+    assert handle == cuda.default[1].cuda_stream
+    assert all(t.made_under is cuda.default[1] for t in cuda.made)
