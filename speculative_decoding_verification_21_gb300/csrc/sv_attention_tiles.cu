@@ -162,8 +162,9 @@ struct Span {
 __device__ __forceinline__ Span item_span(const Seq& q, int per_item, int qt, int window) {
   const int i0 = qt * per_item, i1 = min(q.n, i0 + per_item);
   Span s;
+  const int seen = q.pos0 + i0 + 1;  // keys up to the first row's own; negative in front of token 0
   s.hi = max(0, q.pos0 + i1);
-  s.lo = window ? max(0, q.pos0 + i0 + 1 - window) : 0;
+  s.lo = window && seen > window ? seen - window : 0;
   if (s.hi <= s.lo) {
     s.lo = s.hi = s.first = 0;
     s.count = 1;
@@ -823,7 +824,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
       const bool warp_live = 32 * quad < ntok * t.group;
       const int pos = s.pos + tok_off + my_tok;
       const int see1 = live ? pos + 1 : 0;  // keys [see0, see1)
-      const int see0 = a.window ? max(0, see1 - a.window) : 0;
+      const int see0 = a.window && see1 > a.window ? see1 - a.window : 0;
       float m = -kInf, l = 0.0f;
       for (int k = 0; ok && k < jobs; ++k) {
         if (!wait_warp(ctl.sfull + st, sph, guard, kWaitS)) {

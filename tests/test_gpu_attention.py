@@ -384,3 +384,12 @@ def test_a_graph_keeps_its_workspace_when_a_later_call_needs_a_larger_one():
         s.synchronize()
     assert torch.equal(out["out"], want["out"]) and torch.equal(out["lse"], want["lse"])
     assert all(bool(torch.isnan(t).all()) for t in taken)  # the replay wrote to nobody's memory
+
+
+@pytest.mark.parametrize("window", [50, 2 ** 31 - 1])
+@pytest.mark.parametrize("cache", [BF, E4M3])
+@pytest.mark.parametrize("page", [4, 16])
+def test_windows_over_chunks_longer_than_their_cache(window, cache, page):
+    """Rows in front of token 0 beside rows that see keys; the largest window hides nothing."""
+    Case([(300, 100), (5, 2), (4, 0), (200, 150)], dim=128, cache=cache, page=page).check(
+        window=window)
