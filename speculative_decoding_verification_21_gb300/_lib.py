@@ -618,7 +618,8 @@ def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, sca
     """Causal attention of each sequence's chunk q [total, heads, head_dim]
     (bfloat16 or float16, any token and head strides) over its pages; the chunk's
     own keys and values must be in the cache (spec_kv_append).  scale defaults to
-    head_dim^-1/2; window w > 0 shows a query only its last w keys.  Returns a dict:
+    head_dim^-1/2; window w > 0 shows a query only its last w keys (0: all; no
+    sequence reaches 2^31 of them).  Returns a dict:
     out [total, heads, head_dim], lse [total, heads] float32 (if want_lse),
     flags [B] uint8 (if want_flags)."""
     torch = _torch()
@@ -626,6 +627,9 @@ def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, sca
     _check_rows(q, 0, cache, "q")
     B = _check_index(block_table, q_start, kv_len, cache.device)
     total, heads, dim = q.shape
+    window = min(int(window), 2**31 - 1)
+    if window < 0:
+        raise ValueError("window: 0 or the number of keys that a query sees")
     dev = q.device
     o = dict(out or {})
     _output(o, "out", (total, heads, dim), q.dtype, dev, stream)
@@ -638,7 +642,7 @@ def spec_chunk_attention(q, cache: KVCache, block_table, q_start, kv_len, *, sca
                          block_table.shape[1])
     rc = _queue(L.spec_chunk_attention, dev, cache._ref, ctypes.addressof(batch), _address(q),
                 _row_code(q), heads, q.stride(0), q.stride(1),
-                dim ** -0.5 if scale is None else float(scale), int(window), _address(o["out"]),
+                dim ** -0.5 if scale is None else float(scale), window, _address(o["out"]),
                 _address(o.get("lse")), _address(o.get("flags")), _address(ws), ws.numel(), sh)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_chunk_attention")

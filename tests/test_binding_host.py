@@ -173,3 +173,15 @@ def test_a_call_is_queued_on_its_tensors_device(cuda, name):
     handle = getattr(args[-1], "value", args[-1])
     assert handle == cuda.default[1].cuda_stream
     assert all(t.made_under is cuda.default[1] for t in cuda.made)
+
+
+def test_a_window_past_32_bits_hides_nothing(cuda):
+    """(It would be cut to its low 32 bits on the way to the library.)"""
+    attend = fake.calls()["spec_chunk_attention"]
+    for window, passed in ((0, 0), (5, 5), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                           (2 ** 32 + 5, 2 ** 31 - 1), (10 ** 12, 2 ** 31 - 1)):
+        attend(window=window)
+        assert cuda.library.calls[-1][1][8] == passed
+    for window in (-1, -2 ** 31, -2 ** 32 - 5):
+        with pytest.raises(ValueError):
+            attend(window=window)
