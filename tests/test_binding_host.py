@@ -182,6 +182,6 @@ def test_a_window_past_32_bits_hides_nothing(cuda):
                            (2 ** 32 + 5, 2 ** 31 - 1), (10 ** 12, 2 ** 31 - 1)):
         attend(window=window)
         assert cuda.library.calls[-1][1][8] == passed
-    for window in (-1, -2 ** 31, -2 ** 32 - 5):
-        with pytest.raises(ValueError):
-            attend(window=window)
+    for window in (-1, -2 ** 31, -2 ** 32 - 5):  # the library refuses what is negative
+        attend(window=window)
+        assert cuda.library.calls[-1][1][8] == -1
