@@ -1441,9 +1441,9 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
   // 64: 552 -> 466 us; one sequence of 64-wide heads in pages of 128: 36 us with one
   // warp, 40 with two)
   t.fetchers = kTile / t.box * (e4m3 ? 2 : t.nhalf) >= 4 ? 2 : 1;
-  // a scale of zero: every product times 1e-30 is zero beside 1, and the -inf of a
+  // a scale of zero: every finite product times 2^-149 is below 2^-20, and the -inf of a
   // key that is not seen stays one
-  t.c = a.scale_log2 == 0.0f ? 1e-30f : a.scale_log2;
+  t.c = a.scale_log2 == 0.0f ? 0x1p-149f : a.scale_log2;
   t.rec = reinterpret_cast<Rec*>(a.ws);
   t.err = reinterpret_cast<int*>(a.ws + kMaxCtas * sizeof(Rec));
   t.ml = reinterpret_cast<float2*>(a.ws + kRecBytes);

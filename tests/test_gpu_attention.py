@@ -393,3 +393,13 @@ def test_windows_over_chunks_longer_than_their_cache(window, cache, page):
     """Rows in front of token 0 beside rows that see keys; the largest window hides nothing."""
     Case([(300, 100), (5, 2), (4, 0), (200, 150)], dim=128, cache=cache, page=page).check(
         window=window)
+
+
+@pytest.mark.parametrize("page", [4, 16])
+def test_a_scale_of_zero_with_large_scores(page):
+    """Products of 2^106 times zero: every weight is the same."""
+    c = Case([(5, 300), (60, 200)], page=page)
+    c.q.mul_(2.0 ** 50)
+    c.cache.k.mul_(2.0 ** 50)
+    c.k64 = [k * 2.0 ** 50 for k in c.k64]
+    c.check(scale=0.0)
