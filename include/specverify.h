@@ -405,7 +405,8 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  *             own type, or either for an SV_E4M3 cache); strides as new_k's above
  *   heads     a multiple of kv_heads; query head h reads key head
  *             h / (heads / kv_heads); at most 128 query heads to a key head
- *   scale     factor of the scores, finite; head_dim^-1/2 is usual
+ *   scale     factor of the scores, below 2.35e38 in magnitude (scale log2 e is a
+ *             float); head_dim^-1/2 is usual
  *   window    0: a query at position t sees keys 0..t.  w > 0: keys t-w+1..t
  * The chunk's own keys and values are read from the cache: append them first.
  * out = sum_j p_j v_j with p = softmax(scale q.k_j over the keys seen), the

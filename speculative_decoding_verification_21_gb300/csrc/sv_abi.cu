@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <limits>
 #include <cstdint>
 #include <mutex>
 
@@ -328,7 +329,10 @@ int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, con
     st = check_batch(batch->block_table, batch->q_start, batch->kv_len, batch->B, batch->max_pages,
                      batch->total, cache->page_size);
   if (st != SV_OK) return st;
-  if (heads < 1 || heads % cache->kv_heads || window < 0 || !std::isfinite(scale))
+  // scores are kept in log2 units
+  const double scale_log2 = (double)scale * 1.4426950408889634;
+  if (heads < 1 || heads % cache->kv_heads || window < 0 ||
+      !(std::fabs(scale_log2) <= (double)std::numeric_limits<float>::max()))
     return SV_ERR_ARG;
   if (heads / cache->kv_heads > kMaxGroup || batch->total * heads >= kMaxRows)
     return SV_ERR_UNSUPPORTED;
@@ -345,7 +349,7 @@ int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, con
   a.q_token = token_stride * 2;
   a.q_head = head_stride * 2;
   a.heads = heads;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = (float)scale_log2;
   a.window = window;
   a.out = (char*)out;
   a.lse = out_lse;

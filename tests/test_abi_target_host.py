@@ -138,3 +138,10 @@ def test_flags_are_distinct_bits():
     f = [sv.FLAG_ZERO_MASS, sv.FLAG_NONFINITE, sv.FLAG_RESIDUAL_FALLBACK, sv.FLAG_TIMEOUT,
          sv.FLAG_BAD_TOKEN, sv.FLAG_BAD_PAGE, sv.FLAG_BAD_LENGTH]
     assert sorted(f) == [1 << i for i in range(7)]
+
+
+def test_a_scale_that_leaves_the_range_in_log2_units_is_refused():
+    """(Scores are kept in log2 units: scale log2 e has to be a float.)"""
+    for scale in (3e38, -3e38, 2.36e38):
+        assert attend(cache(), batch(), scale=scale) == ARG
+    assert attend(cache(), batch(B=0), scale=2.35e38) == 0
