@@ -404,7 +404,8 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  *   q         [total][heads][head_dim] of `dtype` (SV_BF16 or SV_F16; the cache's
  *             own type, or either for an SV_E4M3 cache); strides as new_k's above
  *   heads     a multiple of kv_heads; query head h reads key head
- *             h / (heads / kv_heads); at most 128 query heads to a key head
+ *             h / (heads / kv_heads); at most 128 query heads to a key head, and
+ *             total * heads <= 2^31 - 1024
  *   scale     factor of the scores, below 2.35e38 in magnitude (scale log2 e is a
  *             float); head_dim^-1/2 is usual
  *   window    0: a query at position t sees keys 0..t.  w > 0: keys t-w+1..t

@@ -83,7 +83,8 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxGroup = 128;                    // query heads per key head
 constexpr int64_t kMaxRows = (int64_t)1 << 31;    // rows of a packed array
-constexpr int64_t kMaxTokens = kMaxRows - 1024;   // tokens of a sequence: a tile past the end stays an int
+// tokens of a sequence, and (token, head) rows of an attention: a tile past the end stays an int
+constexpr int64_t kMaxTokens = kMaxRows - 1024;
 
 // A cache whose shape, type and strides the kernels can walk.
 int check_cache(const sv_kv_cache* c) {
@@ -334,7 +335,7 @@ int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, con
   if (heads < 1 || heads % cache->kv_heads || window < 0 ||
       !(std::fabs(scale_log2) <= (double)std::numeric_limits<float>::max()))
     return SV_ERR_ARG;
-  if (heads / cache->kv_heads > kMaxGroup || batch->total * heads >= kMaxRows)
+  if (heads / cache->kv_heads > kMaxGroup || batch->total * heads > kMaxTokens)
     return SV_ERR_UNSUPPORTED;
   if (batch->B == 0) return SV_OK;
   if (batch->total > 0 && (!q || !out)) return SV_ERR_ARG;

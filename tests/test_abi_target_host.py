@@ -145,3 +145,10 @@ def test_a_scale_that_leaves_the_range_in_log2_units_is_refused():
     for scale in (3e38, -3e38, 2.36e38):
         assert attend(cache(), batch(), scale=scale) == ARG
     assert attend(cache(), batch(B=0), scale=2.35e38) == 0
+
+
+def test_rows_whose_last_tile_passes_31_bits_are_refused():
+    for total in (2 ** 31 - 1, 2 ** 31 - 100, 2 ** 31 - 1023):
+        assert attend(cache(kv_heads=1), batch(total=total), heads=1) == UNSUP
+    assert attend(cache(), batch(total=2 ** 30 - 1), heads=2) == UNSUP
+    assert attend(cache(kv_heads=1), batch(total=2 ** 31 - 1024, B=0), heads=1) == 0
