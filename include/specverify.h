@@ -91,8 +91,9 @@ enum {
   SV_FLAG_BAD_PAGE = 32,         /* a page index that the call needed lies outside the pool:
                                     nothing is written there, and it reads as zeros       */
   SV_FLAG_BAD_LENGTH = 64        /* q_start falls or leaves [0, total] (the sequence is then
-                                    skipped), or kv_len lies outside what its pages hold
-                                    (it is then clamped)                                  */
+                                    skipped: its rows are not read and not written), or
+                                    kv_len lies outside what its pages hold (it is then
+                                    clamped)                                              */
 };
 
 enum { SV_MODE_SAMPLE = 0, SV_MODE_GREEDY = 1, SV_MODE_LMHEAD = 2, SV_MODE_DRAFT = 3 };
@@ -354,7 +355,9 @@ typedef struct {
  * are rows q_start[b] .. q_start[b+1]-1 of the packed arrays, and kv_len[b] is
  * its length with them, so that new token i sits at position
  * kv_len[b] - (q_start[b+1] - q_start[b]) + i.  All three arrays are on the
- * device; table entries behind a sequence's last token are not read. */
+ * device; table entries behind a sequence's last token are not read.  A row that
+ * two sequences claim (some entry of q_start between theirs falls) is taken by one
+ * of them. */
 typedef struct {
   const int32_t* block_table;  /* [B][max_pages] */
   const int32_t* q_start;      /* [B+1]          */

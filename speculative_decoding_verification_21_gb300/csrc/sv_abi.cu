@@ -4,8 +4,8 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <limits>
 #include <cstdint>
+#include <limits>
 #include <mutex>
 
 #include "specverify.h"

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) k_attend_rows(AttendArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int D = c.head_dim;
   const int t = (int)(blockIdx.x / a.heads), hq = (int)(blockIdx.x - (unsigned)t * a.heads);
-  const int b = owner_of(a.b.q_start, a.b.B, t);
+  const int b = owner_of(a.b.q_start, a.b.B, t, a.b.total);
   if (b >= a.b.B) return;
   const Seq q = load_seq(a.b, b, c.page_size);
   const int i = t - q.tok0;

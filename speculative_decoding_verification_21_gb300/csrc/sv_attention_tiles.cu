@@ -1166,7 +1166,7 @@ __device__ __forceinline__ void mend_row(const AttendArgs& a, int t, int hq, flo
     odd |= !(fabsf(f.x) < kInf && fabsf(f.y) < kInf);
   }
   if (!__any_sync(0xffffffffu, odd)) return;
-  const int b = owner_of(a.b.q_start, a.b.B, t);
+  const int b = owner_of(a.b.q_start, a.b.B, t, a.b.total);
   if (b >= a.b.B) return;
   const Seq q = load_seq(a.b, b, a.c.page_size);
   const int i = t - q.tok0;

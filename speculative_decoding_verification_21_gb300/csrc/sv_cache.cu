@@ -190,14 +190,14 @@ __global__ void __launch_bounds__(kMoveWarps * 32, batch_of(E4M3, APPEND) > 1 ? 
   if (first >= a.total) return;
   const int t0 = (int)first, n = min(per, a.total - t0);
   // the sequence of the first token, and mostly of all
-  const int b0 = owner_of(a.start, a.B, t0);
+  const int b0 = owner_of(a.start, a.B, t0, a.total);
   const bool same = n == 1 || (b0 < a.B && t0 + n <= __ldg(a.start + b0 + 1));
   Place mine{-2, 0};
   if (same) {
     if (lane < n) mine = place_of<APPEND>(a, b0, t0 + lane, held);
   } else {
     for (int j = 0; j < n; ++j) {
-      const int b = owner_of(a.start, a.B, t0 + j);
+      const int b = owner_of(a.start, a.B, t0 + j, a.total);
       if (lane == j) mine = place_of<APPEND>(a, b, t0 + j, held);
     }
   }

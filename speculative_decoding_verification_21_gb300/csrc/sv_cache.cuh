@@ -74,17 +74,28 @@ __device__ __forceinline__ Seq load_seq(const BatchView& bv, int b, int page_siz
                   (int64_t)bv.max_pages * page_size);
 }
 
-// The sequence that owns packed row t: the number of entries of start[1..B] that
-// are <= t (one warp, all its lanes; B where none does).  The entries of a
-// well-formed start rise; for others the caller checks what it gets.
-__device__ __forceinline__ int owner_of(const int32_t* start, int B, int t) {
+// The sequence that owns packed row t < total (one warp, all its lanes; B where none
+// does).  The entries of a well-formed start rise, so it is the number of entries of
+// start[1..B] that are <= t.  Where that sequence does not hold the row, some entry is
+// bad: the first sequence whose own two entries hold it is looked for, so that a bad
+// entry costs the two sequences beside it their rows and nobody else.
+__device__ __forceinline__ int owner_of(const int32_t* start, int B, int t, int total) {
   const int lane = threadIdx.x & 31;
+  auto holds = [&](int b) {
+    const int s0 = __ldg(start + b), s1 = __ldg(start + b + 1);
+    return s0 >= 0 && s0 <= t && t < s1 && s1 <= total;
+  };
   int n = 0;
   for (int j = 0; j < B; j += 32) {
     const bool le = j + lane < B && __ldg(start + 1 + j + lane) <= t;
     n += __popc(__ballot_sync(0xffffffffu, le));
   }
-  return n;
+  if (n == B || holds(n)) return n;  // (all of start[1..B] are <= t: nobody's)
+  for (int j = 0; j < B; j += 32) {
+    const unsigned in = __ballot_sync(0xffffffffu, j + lane < B && holds(j + lane));
+    if (in) return j + __ffs(in) - 1;
+  }
+  return B;
 }
 
 __device__ __forceinline__ void page_of(const CacheView& c, int pos, int& page, int& slot) {

@@ -403,3 +403,40 @@ def test_a_scale_of_zero_with_large_scores(page):
     c.cache.k.mul_(2.0 ** 50)
     c.k64 = [k * 2.0 ** 50 for k in c.k64]
     c.check(scale=0.0)
+
+
+@pytest.mark.parametrize("bad", [2 ** 30, -1, -2 ** 31])
+@pytest.mark.parametrize("page", [4, 16])
+def test_a_bad_start_costs_only_the_sequences_beside_it(page, bad):
+    B = 70
+    c = Case([(1 + b % 3, 20 + b) for b in range(B)], page=page)
+    want = c.attend()
+    for at in (0, 1, 33, 69):
+        start = c.start.clone()
+        start[at] = bad
+        o = sv.spec_chunk_attention(c.q, c.cache, c.table, start, c.len, want_flags=True)
+        skipped = [b for b in (at - 1, at) if b >= 0]
+        assert o["flags"].nonzero().flatten().tolist() == skipped
+        for b in range(B):
+            if b not in skipped:
+                r = slice(c.start_list[b], c.start_list[b + 1])
+                assert torch.equal(o["out"][r], want["out"][r]), (at, b)
+                assert torch.equal(o["lse"][r], want["lse"][r]), (at, b)
+
+
+def test_a_bad_start_beside_an_infinite_value():
+    """Rows are mended by what they see there too."""
+    lens = [(2 + b % 4, 6 + (37 * b) % 400) for b in range(200)]
+    c = Case(lens, group=2, dim=128)
+    c.start[77] = 2 ** 30
+    clean = {k: v.clone() for k, v in c.attend().items()}
+    for b, (n, L) in enumerate(lens):  # what the last token alone sees
+        c.cache.v[c.owned[b][(L - 1) // c.ps], :, (L - 1) % c.ps, 5] = math.inf
+    o = c.attend()
+    for b in range(200):
+        if b not in (76, 77):
+            r = slice(c.start_list[b], c.start_list[b + 1] - 1)
+            # (mended: fp32 weights instead of rounded ones)
+            d = (o["out"][r].double() - clean["out"][r].double()).abs()
+            assert bool((d <= 2.0 ** -7 * (6 + clean["out"][r].double().abs())).all()), b
+            assert bool(torch.isposinf(o["out"][c.start_list[b + 1] - 1, :, 5]).all()), b

@@ -229,3 +229,37 @@ def test_refusals_of_the_binding():
         sv.KVCache(e.k, e.v)
     with pytest.raises(ValueError):
         sv.KVCache(e.k, e.v, e.k_scale[:2], e.v_scale[:2])
+
+
+@pytest.mark.parametrize("cache", [BF, E4M3])
+@pytest.mark.parametrize("bad", [2 ** 30, -1, -2 ** 31])
+@pytest.mark.parametrize("repeat", [1, 120])  # one token a warp, and four
+def test_a_bad_start_costs_only_the_sequences_beside_it(cache, bad, repeat):
+    B = 70
+    c = Case([(repeat * (1 + b % 3), repeat * (1 + b % 3) + b) for b in range(B)], cache=cache)
+    k, v = rows(c)
+    first = torch.tensor([L - n for n, L in c.lens], dtype=torch.int32, device="cuda")
+    sv.spec_kv_append(c.cache, k, v, c.table, c.start, c.len)
+    want = sv.spec_kv_read(c.cache, c.table, first, c.start, c.total)
+    held = raw(c.cache.k).clone(), raw(c.cache.v).clone()
+    r, p, s = (torch.tensor(z, device="cuda") for z in zip(*places(c)))
+    owner = torch.repeat_interleave(torch.arange(B), torch.tensor([n for n, _ in c.lens])).cuda()
+    for at in (0, 1, 33, 69):
+        start = c.start.clone()
+        start[at] = bad
+        skipped = [b for b in (at - 1, at) if b >= 0]
+        kept = (owner[:, None] != torch.tensor(skipped, device="cuda")).all(1)
+        o = {x: torch.full_like(want[x], math.nan) for x in ("k", "v")}
+        f = sv.spec_kv_read(c.cache, c.table, first, start, c.total, out=o, want_flags=True)["flags"]
+        assert f.nonzero().flatten().tolist() == skipped
+        for x in ("k", "v"):
+            assert torch.equal(o[x][kept], want[x][kept])
+            assert bool(torch.isnan(o[x][~kept]).all())  # not written
+        for pool in (c.cache.k, c.cache.v):
+            raw(pool).zero_()
+        f = sv.spec_kv_append(c.cache, k, v, c.table, start, c.len, want_flags=True)["flags"]
+        assert f.nonzero().flatten().tolist() == skipped
+        for pool, all_ in zip((c.cache.k, c.cache.v), held):
+            got = raw(pool)[p, :, s]
+            assert torch.equal(got[kept], all_[p, :, s][kept]) and not bool(got[~kept].any())
+            raw(pool).copy_(all_)
