@@ -376,8 +376,10 @@ typedef struct {
  * token and head, s = 2^k with the smallest k >= -120 that keeps the largest
  * finite |x| / s within 448, and codes rounded to nearest, ties to even; NaN and
  * infinities become the NaN code.  No two of the new tokens may share a slot.
+ * A new token whose position lies in front of token 0 or behind what the table's
+ * pages hold is dropped; positions follow kv_len as it is given (not clamped).
  *   out_flags     [B] uint8 or NULL: SV_FLAG_BAD_PAGE, SV_FLAG_BAD_LENGTH (here
- *                 also where a new token's position is negative: it is dropped)
+ *                 also where a token is dropped)
  */
 int spec_kv_append(const sv_kv_cache* cache, const sv_kv_batch* batch, const void* new_k,
                    const void* new_v, int dtype, int64_t token_stride, int64_t head_stride,

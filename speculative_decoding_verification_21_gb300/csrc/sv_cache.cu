@@ -46,16 +46,22 @@ struct MoveArgs {
   int move_blocks;        // blocks that move tokens; the rest write flags
 };
 
-// Position of the first row of sequence b, and whether its entries are sound.
+// Rows tok0 .. tok0+n-1 of sequence b, the position of the first (as the lengths say,
+// wherever that is: a row whose position lies outside the pages has no place), and
+// whether the entries are sound.
+struct MoveSeq {
+  int tok0, n;
+  int64_t pos0;
+  bool bad;
+};
 template <bool APPEND>
-__device__ __forceinline__ Seq move_seq(const MoveArgs& a, int b) {
+__device__ __forceinline__ MoveSeq move_seq(const MoveArgs& a, int b) {
   const int s0 = __ldg(a.start + b), s1 = __ldg(a.start + b + 1), at = __ldg(a.at + b);
   const int64_t held = (int64_t)a.max_pages * a.c.page_size;
-  if (APPEND) return make_seq(s0, s1, at, a.total, held);
-  Seq q = make_seq(s0, s1, 0, a.total, held);
-  q.pos0 = at;
-  q.bad = q.bad || (q.n && (at < 0 || (int64_t)at + q.n > held));
-  return q;
+  const Seq q = make_seq(s0, s1, APPEND ? at : 0, a.total, held);
+  MoveSeq m{q.tok0, q.n, APPEND ? (int64_t)at - q.n : at, q.bad};
+  m.bad |= m.n && (m.pos0 < 0 || m.pos0 + m.n > held);
+  return m;
 }
 
 __device__ __forceinline__ bool in_pages(int64_t pos, int64_t held) { return pos >= 0 && pos < held; }
@@ -64,10 +70,9 @@ __device__ __forceinline__ bool in_pages(int64_t pos, int64_t held) { return pos
 template <bool APPEND>
 __device__ void write_flags(const MoveArgs& a, int b) {
   const int lane = threadIdx.x & 31;
-  const Seq q = move_seq<APPEND>(a, b);
+  const MoveSeq q = move_seq<APPEND>(a, b);
   const int64_t held = (int64_t)a.max_pages * a.c.page_size;
   int64_t lo = q.pos0, hi = lo + q.n;
-  bool bad = q.bad || (q.n && lo < 0);
   lo = lo < 0 ? 0 : lo;
   hi = hi > held ? held : hi;
   bool page_bad = false;
@@ -80,7 +85,7 @@ __device__ void write_flags(const MoveArgs& a, int b) {
   }
   const bool any = __any_sync(0xffffffffu, page_bad);
   if (lane == 0)
-    a.flags[b] = (uint8_t)((bad ? SV_FLAG_BAD_LENGTH : 0) | (any ? SV_FLAG_BAD_PAGE : 0));
+    a.flags[b] = (uint8_t)((q.bad ? SV_FLAG_BAD_LENGTH : 0) | (any ? SV_FLAG_BAD_PAGE : 0));
 }
 
 // 16 values as codes: the row's largest finite |x| over its group of lanes, the
@@ -150,10 +155,10 @@ template <bool APPEND>
 __device__ __forceinline__ Place place_of(const MoveArgs& a, int b, int t, int64_t held) {
   Place p{-2, 0};
   if (b >= a.B) return p;  // rows behind the last sequence
-  const Seq q = move_seq<APPEND>(a, b);
+  const MoveSeq q = move_seq<APPEND>(a, b);
   const int i = t - q.tok0;
   if (i < 0 || i >= q.n) return p;  // start does not rise
-  const int64_t pos = (int64_t)q.pos0 + i;
+  const int64_t pos = q.pos0 + i;
   p.page = -1;
   if (!in_pages(pos, held)) return p;
   int index;

@@ -263,3 +263,27 @@ def test_a_bad_start_costs_only_the_sequences_beside_it(cache, bad, repeat):
             got = raw(pool)[p, :, s]
             assert torch.equal(got[kept], all_[p, :, s][kept]) and not bool(got[~kept].any())
             raw(pool).copy_(all_)
+
+
+@pytest.mark.parametrize("cache", [BF, E4M3])
+@pytest.mark.parametrize("length", [33, 34, 36, 40, 2 ** 31 - 1, 0, 2, -1, -2 ** 31])
+def test_new_tokens_outside_the_pages_are_dropped_and_others_kept(cache, length):
+    """A table of two pages of 16 and chunks of 4: positions below 0 and from 32 on have no place,
+    and the tokens that are there already stay."""
+    c = Case([(4, 32), (4, 32)], cache=cache)
+    c.table = c.table[:, :2].contiguous()
+    c.len[0] = length
+    k, v = rows(c)
+    before = [raw(x).clone() for x in (c.cache.k, c.cache.v)]
+    f = sv.spec_kv_append(c.cache, k, v, c.table, c.start, c.len, want_flags=True)["flags"]
+    assert f.tolist() == [sv.FLAG_BAD_LENGTH, 0]
+    at = [(i, length - 4 + i) for i in range(4) if 0 <= length - 4 + i < 32]
+    at = [(i, c.owned[0][q // 16], q % 16) for i, q in at]
+    at += [(4 + i, c.owned[1][1], 12 + i) for i in range(4)]
+    r, p, s = (torch.tensor(z, device="cuda") for z in zip(*at))
+    for pool, want, new in zip((c.cache.k, c.cache.v), before, (k, v)):
+        if cache == E4M3:
+            want[p, :, s] = quantise64(new)[0].float().to(E4M3).view(torch.uint8)[r]
+        else:
+            want[p, :, s] = new[r].view(torch.int16)
+        assert torch.equal(raw(pool), want)
