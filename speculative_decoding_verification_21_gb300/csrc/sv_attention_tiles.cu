@@ -931,7 +931,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
             if (live) {
               if (s.slot < 0) {
-                if (!(fabsf(sum16(x)) < kInf)) ctl.mend = kMend;
+                if (l == l && !(fabsf(sum16(x)) < kInf)) ctl.mend = kMend;
                 store16<DT>(a.out + (orow * D + 16 * u) * 2, x, t.wide);
               } else {
                 store16f(t.part + prow * D + 16 * u, x);
@@ -984,7 +984,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
             if (live) {
               if (s.slot < 0) {
-                if (!(fabsf(sum16(x)) < kInf)) ctl.mend = kMend;
+                if (L == L && !(fabsf(sum16(x)) < kInf)) ctl.mend = kMend;
                 store16<DT>(a.out + (orow * D + 16 * u) * 2, x, t.wide);
               } else {
                 store16f(t.part + prow * D + 16 * u, x);
@@ -1149,12 +1149,18 @@ __device__ __forceinline__ float4 join_parts(const TileArgs& t, int c, int parts
 
 // The products of a tile weigh every value of it, and 0 times an infinity is NaN: a value
 // that is not finite reaches rows that do not see it.  So what is not finite in a row's
-// outputs is found again, one warp to the row, from the keys that it sees alone.  sq:
+// outputs is found again, one warp to the row, from the keys that it sees alone.  (Not
+// where the sum of the weights is NaN, from the query or a key that the row does see: its
+// outputs are NaN by the definition.  Rows like that alone set off no mending.)  sq:
 // shared memory for the warp's query.
 template <int DT, bool E4M3>
 __device__ __forceinline__ void mend_row(const AttendArgs& a, int t, int hq, float* sq) {
   const int lane = threadIdx.x & 31, D = a.c.head_dim;
   __syncwarp();  // the row's stores
+  if (a.lse) {
+    const float lse = __ldcg(a.lse + (int64_t)t * a.heads + hq);
+    if (lse != lse) return;
+  }
   uint4 w = make_uint4(0, 0, 0, 0);
   uint4* at = reinterpret_cast<uint4*>(a.out + ((int64_t)t * a.heads + hq) * D * 2) + lane;
   if (lane * 8 < D) w = __ldcg(at);
@@ -1282,7 +1288,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     const int D = a.c.head_dim;
     if (lane * 4 < D) {
-      odd |= !(fabsf(o.x * inv + o.y * inv + o.z * inv + o.w * inv) < kInf);
+      odd |= L == L && !(fabsf(o.x * inv + o.y * inv + o.z * inv + o.w * inv) < kInf);
       const uint2 w = make_uint2(F16<DT>::down(o.x * inv, o.y * inv),
                                  F16<DT>::down(o.z * inv, o.w * inv));
       reinterpret_cast<uint2*>(a.out + orow * D * 2)[lane] = w;

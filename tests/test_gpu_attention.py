@@ -440,3 +440,58 @@ def test_a_bad_start_beside_an_infinite_value():
             d = (o["out"][r].double() - clean["out"][r].double()).abs()
             assert bool((d <= 2.0 ** -7 * (6 + clean["out"][r].double().abs())).all()), b
             assert bool(torch.isposinf(o["out"][c.start_list[b + 1] - 1, :, 5]).all()), b
+
+
+def best_ms(call):
+    times = []
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times)
+
+
+@pytest.mark.parametrize("want_lse", [True, False])
+@pytest.mark.parametrize("cache", [FP, E4M3])
+def test_a_row_that_is_rightly_nan_delays_nobody(cache, want_lse):
+    """One NaN in a query, one in a key that a whole sequence sees: no row is computed again (that
+    took hundreds of times the call's time)."""
+    lens = [(6, 100001), (300, 900), (1, 40)]
+    c = Case(lens, kv_heads=1, group=8, dim=64, page=128, dtype=FP, cache=cache)
+    clean = {k: v.clone() for k, v in c.attend(want_lse=want_lse).items()}
+    ms = best_ms(lambda: c.attend(want_lse=want_lse))
+    c.q[2, 3, 5] = math.nan
+    page = c.owned[1][0]
+    if cache == E4M3:
+        c.cache.k.view(torch.uint8)[page, :, 7, 9] = 0x7f
+    else:
+        c.cache.k[page, :, 7, 9] = math.nan
+    o = c.attend(want_lse=want_lse)
+    nan = torch.zeros((c.total, 8), dtype=torch.bool, device="cuda")
+    nan[2, 3] = True
+    nan[6:306] = True
+    assert bool(torch.isnan(o["out"][nan]).all())
+    assert torch.equal(o["out"][~nan], clean["out"][~nan])
+    if want_lse:
+        assert bool(torch.isnan(o["lse"][nan]).all())
+        assert torch.equal(o["lse"][~nan], clean["lse"][~nan])
+    assert best_ms(lambda: c.attend(want_lse=want_lse)) < 10 * ms + 0.2
+
+
+@pytest.mark.parametrize("want_lse", [True, False])
+def test_rows_that_are_rightly_nan_beside_rows_to_mend(want_lse):
+    c = Case([(6, 300), (200, 260), (40, 40)], dim=128)
+    out, _, tol, _ = c.reference()  # (of the finite cache)
+    c.q[3, 2, 1] = math.nan
+    for b, (n, L) in enumerate(c.lens):
+        c.cache.v[c.owned[b][(L - 1) // c.ps], :, (L - 1) % c.ps] = math.nan
+    o = c.attend(want_lse=want_lse)["out"]
+    last = torch.zeros(c.total, dtype=torch.bool, device="cuda")
+    last[[s - 1 for s in c.start_list[1:]]] = True
+    nan = last[:, None].expand(-1, 8).clone()
+    nan[3, 2] = True
+    assert bool(torch.isnan(o[nan]).all())
+    assert bool(((o.double() - out).abs() <= tol)[~nan].all())
