@@ -124,7 +124,7 @@ struct TileArgs {
   float* part;         // [2 * kMaxCtas][kMaxRows][head_dim]
   float2* ml;          // [2 * kMaxCtas][kMaxRows]
   struct Rec* rec;     // [kMaxCtas]
-  int* err;            // [kMaxCtas]: kLate, kMend
+  int* err;            // [kMaxCtas]: kLate, kMend; above 8 bits a wait that gave up
 };
 
 constexpr int kLate = 1, kMend = 2;
@@ -400,7 +400,7 @@ __device__ __forceinline__ void key_steps(int lo, int hi, int tile, int& s0, int
 // ---------------------------------------------------------------------------
 // Waits.
 // ---------------------------------------------------------------------------
-// Which wait gave up first (1..), for whoever looks at the workspace after a timeout.
+// Which wait gave up, in the CTA's err word, for whoever looks at the workspace after a timeout.
 enum WaitId { kWaitSlot = 1, kWaitQ, kWaitK, kWaitV, kWaitP, kWaitQFree, kWaitS, kWaitO, kWaitX, kWaitRaw,
               kWaitWide };
 
@@ -1095,7 +1095,7 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tbase, 512);
-  if (threadIdx.x == 0) t.err[wid] = (ctl.abort ? kLate : 0) | ctl.mend;
+  if (threadIdx.x == 0) t.err[wid] = (ctl.abort ? kLate | ctl.abort << 8 : 0) | ctl.mend;
 }
 
 // ---------------------------------------------------------------------------

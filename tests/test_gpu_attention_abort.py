@@ -40,3 +40,20 @@ def test_stalled_scores_time_out_and_the_context_survives(lens, cache):
         again = c.attend(want_flags=True)
         assert torch.equal(again["out"], want["out"]) and torch.equal(again["lse"], want["lse"])
         assert not bool(again["flags"].any())
+
+
+def test_the_workspace_names_the_cta_and_the_wait_that_gave_up():
+    c = Case([(5, 4000), (200, 900)], dim=128)
+    ws = torch.zeros(sv.attention_workspace_bytes(c.cache, 8), dtype=torch.uint8, device="cuda")
+    err = ws[160 * 16:160 * 20].view(torch.int32)  # (behind 160 records of 16 bytes)
+    c.attend(workspace=ws)
+    assert not bool(err.any())
+    sv.test_attention_stall(3, 1 << 22)
+    try:
+        c.attend(workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        sv.test_attention_stall(-1, 0)
+    e = err.tolist()
+    assert e[3] & 1 and 1 <= e[3] >> 8 <= 11
+    assert not any(e[:3] + e[4:])
