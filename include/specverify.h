@@ -84,9 +84,9 @@ enum {
                                     outputs of the row are then in range but unspecified  */
   SV_FLAG_RESIDUAL_FALLBACK = 4, /* max(0, p_n - q_n) had no positive entry in floating
                                     point; the token was drawn from p_n                   */
-  SV_FLAG_TIMEOUT = 8,           /* a bounded device-side wait of the fused LM head gave up
-                                    (a tile that never arrived); the row's outputs are then
-                                    unspecified                                          */
+  SV_FLAG_TIMEOUT = 8,           /* a bounded device-side wait of the fused LM head or of
+                                    the attention gave up (a tile that never arrived); the
+                                    row's outputs are then unspecified                   */
   SV_FLAG_BAD_TOKEN = 16,        /* a draft token outside [0, V): treated as p = q = 0    */
   SV_FLAG_BAD_PAGE = 32,         /* a page index that the call needed lies outside the pool:
                                     nothing is written there, and it reads as zeros       */
@@ -331,7 +331,12 @@ int spec_lmhead_verify_drafted(const void* h_target, const void* W_target, int H
  * (4 exponent bits, 3 of mantissa, largest value 448) times a power of two of
  * its own, held as one byte s that stands for 2^(s - 127), 1 <= s <= 254.  A
  * power of two loses nothing against an arbitrary factor, because the codes are
- * floating point themselves, and makes every dequantised value exact in bf16.
+ * floating point themselves, and makes every dequantised value exact in bf16 (of
+ * scales from 2^-120 on, which spec_kv_append keeps to; below, it is rounded).  In
+ * either 16-bit type a value past the largest one reads as an infinity.  The
+ * largest values of a row's own type can become that: codes are rounded to
+ * nearest, and from 63488 in fp16 and 248 2^120 in bf16 on that is up to 2^16 and
+ * to 2^128.
  * ------------------------------------------------------------------------- */
 
 /* The pool: element (page, head, token, i) of k is at
@@ -418,7 +423,8 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  * out = sum_j p_j v_j with p = softmax(scale q.k_j over the keys seen), the
  * scores, the softmax's maximum and sum and the products' sums in fp32; p may be
  * rounded to `dtype` for the product with v, and an SV_E4M3 cache is dequantised
- * to `dtype` (exact in SV_BF16).
+ * to `dtype` (exact in SV_BF16; in SV_F16 to nearest, so that what lies beyond 65504
+ * becomes an infinity and what lies below 2^-25 a zero).
  *   out       [total][heads][head_dim] of `dtype`, contiguous, 16-byte aligned
  *   out_lse   [total][heads] float or NULL: log sum_j exp(scale q.k_j)
  *   out_flags [B] uint8 or NULL: SV_FLAG_BAD_PAGE, SV_FLAG_BAD_LENGTH, and
@@ -444,7 +450,8 @@ int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, con
  *   draft_probs   [B][gamma][V]   dtype
  *   draft_tokens  [B][gamma] int32
  *   uniforms      [B][gamma+1] float in [0, 1): u_0..u_{gamma-1} of the accept
- *                 tests, then the draw's
+ *                 tests, then the draw's.  An accept test's is compared as it
+ *                 stands (NaN rejects)
  * Draft i is accepted iff u_i <= p_i(x_i) / q_i(x_i) (IEEE fp32 quotient; 0/0
  * rejects).  The token at the first rejection n is drawn from w = max(0, p_n -
  * q_n) (fp32 differences), from p_n if that has no positive entry, and from
@@ -454,8 +461,9 @@ int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, con
  * the order of summation.
  *   out_tokens, out_counts, out_flags as spec_verify.  A probability that is
  *   negative, not finite or above 2 counts as 0 and sets SV_FLAG_NONFINITE, as
- *   does a uniform outside [0, 1) (clamped into it; NaN as 0); a row whose sum
- *   is 4 or more gives an unspecified token in range.  No workspace.
+ *   does a uniform outside [0, 1) that was used (the draw's is clamped into it, NaN
+ *   as 0).  A row whose sum is 4 or more gives an unspecified token in range, one
+ *   whose weights are all below 2^-62 token 0.  No workspace.
  */
 int spec_verify_probs(const void* target_probs, const void* draft_probs,
                       const int32_t* draft_tokens, const float* uniforms, int B, int gamma,

@@ -287,3 +287,20 @@ def test_new_tokens_outside_the_pages_are_dropped_and_others_kept(cache, length)
         else:
             want[p, :, s] = new[r].view(torch.int16)
         assert torch.equal(raw(pool), want)
+
+
+@pytest.mark.parametrize("dtype,last", [(FP, 63456.0), (BF, 247.0 * 2.0 ** 120)])
+def test_the_largest_values_of_a_type_round_up_to_infinity(dtype, last):
+    """Codes are rounded to nearest: 248 times the scale becomes 256, past the type's range; what
+    lies below that border stays finite."""
+    top = torch.finfo(dtype).max
+    c = Case([(2, 2)], dim=64, dtype=dtype, cache=E4M3)
+    k, v = rows(c)
+    k[0, 0, 0], k[0, 0, 1], k[0, 1, 0], k[0, 1, 1] = top, last, -top, -last
+    sv.spec_kv_append(c.cache, k, v, c.table, c.start, c.len)
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = sv.spec_kv_read(c.cache, c.table, zero, c.start, c.total, dtype=dtype)["k"]
+    scale = 2.0 ** (8 if dtype == FP else 120)
+    assert got[0, :, 0].tolist() == [math.inf, -math.inf]
+    assert got[0, :, 1].tolist() == [240 * scale, -240 * scale]
+    assert bool(torch.isfinite(got[1]).all())

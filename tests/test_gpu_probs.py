@@ -198,3 +198,17 @@ def test_refusals_of_the_binding():
         sv.spec_verify_probs(p, q, x, u.double())
     with pytest.raises(ValueError):
         sv.spec_verify_probs(p, q, x, u[:, :2])
+
+
+def test_uniforms_of_the_accept_tests_are_compared_as_they_stand():
+    """p/q = 1.25: 1.2 accepts, 1.5 rejects, NaN rejects, -3 accepts; each is flagged.  Behind the
+    first rejection nothing is looked at."""
+    p = torch.tensor([0.5, 0.5], device="cuda").expand(5, 3, 2).contiguous()
+    q = torch.tensor([0.4, 0.6], device="cuda").expand(5, 2, 2).contiguous()
+    x = torch.zeros((5, 2), dtype=torch.int32, device="cuda")
+    u = torch.full((5, 3), 0.5, device="cuda")
+    u[:4, 0] = torch.tensor([1.2, 1.5, float("nan"), -3.0])
+    x[4, 0], u[4, 0], u[4, 1] = 1, 0.9, float("nan")  # 0.9 > 0.5 / 0.6
+    o = check(p, q, x, u)
+    assert o["counts"].tolist() == [2, 0, 0, 2, 0]
+    assert o["flags"].tolist() == [sv.FLAG_NONFINITE] * 4 + [0]
