@@ -23,9 +23,9 @@ struct AttendArgs {
   char* ws;
 };
 
-// Whether the tile kernel takes a cache: head_dim up to 128, and pages that divide
-// a tile of 128 tokens or are whole tiles, at least 8 tokens (one swizzle group), or
-// 16 where their scale bytes are copied 16 at a time.  The row kernel takes the rest,
+// Whether the tile kernel takes a cache: head_dim up to 128, and pages of a power of two
+// of tokens (they divide a tile of 128 or are whole tiles), at least 8 (one swizzle
+// group), or 16 where their scale bytes are copied 16 at a time.  The row kernel takes the rest,
 // and negative scales (a row's maximum is then not its largest product).
 inline bool tiles_take(const CacheView& c, bool e4m3) {
   if (c.head_dim > 128 || c.num_pages == 0) return false;

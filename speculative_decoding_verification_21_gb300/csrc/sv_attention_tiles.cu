@@ -32,11 +32,14 @@
 //     203 us for 1.27 GB, 6.3 TB/s, 0.93 of a copy's rate;
 //   a prompt chunk (4096 and 1605 tokens, 32/8 heads of 128, bf16): the chain softmax,
 //     P V, Q K^T of a stage (about 3200 clocks for 2048 of products) and the power
-//     limit; 440 to 460 us, 1.3 PFLOP/s, 0.67 of a large library product's rate;
-//   a round on e4m3 (9 tokens, 32 sequences up to 40000, 64/8 heads of 128): issue slots
-//     and the three slots of widened tiles; 449 us, 3.4 TB/s of codes, 0.50 of a copy's.
-//     Per tile of 128 keys and values an SM issues about 1800 instructions a scheduler
-//     (half of them widen codes), and has 1370 clocks at HBM's rate.
+//     limit; 440 to 500 us, 1.2 to 1.35 PFLOP/s, 0.62 to 0.70 of a large library
+//     product's rate;
+//   a round on e4m3 (9 tokens, 32 sequences up to 40000, 64/8 heads of 128): the widening
+//     of codes, by its length rather than by a full unit; 449 to 455 us, 3.4 TB/s of codes,
+//     0.50 of a copy's.  Per tile of 128 keys and values an SM issues about 1800
+//     instructions a scheduler (half of them widen codes), and has 1370 clocks at HBM's
+//     rate; 60% of the issue slots are used and no pipe more than 41%, while the tiles'
+//     three widened slots are waited for on both sides.
 //   small calls: the chain lengths, page numbers, copies, products, join; 16 us for one
 //     token on 777, of them 3 to find the shares, 3 to the first scores, 5 for the join.
 // The 128 x 128 tile keeps S, P and O of two stages in tensor memory's 512 columns; the
@@ -98,6 +101,8 @@ constexpr float kLag = 8.0f;
 // Threads, and the registers a thread is launched with and then takes by role (the
 // roles' sum must not pass what the launch gave, or the takers would wait forever).
 constexpr int kThreads16 = 384, kWideWarps = 4, kThreads8 = 384 + 64 * kWideWarps;
+// (At these counts a thread spills 12 to 50 words, around an item's start and end: 0.1 to
+// 0.7% of the instructions issued touch them.)
 constexpr int kRegs16 = 168, kRegs8 = 96;
 constexpr int kHelpRegs16 = 88, kSoftRegs16 = 208;
 constexpr int kHelpRegs8 = 64, kSoftRegs8 = 128, kWideRegs8 = 80;
@@ -447,7 +452,11 @@ __device__ __forceinline__ float max_of(const uint32_t* r) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 // P = 2^(c s - m) of N scores in pairs of 16-bit floats into tensor memory; adds to
-// the four pairs of sums.
+// the four pairs of sums.  P is rounded to the values' type because the product takes
+// both operands in one 16-bit type, and a second product for what the rounding leaves
+// would double the time of P V; the sums are of the unrounded weights.  Measured against
+// 64 bits: an error of 2.1e-3 to 2.3e-3 in bf16, where rounding the output alone leaves
+// 1.7e-3, and 2.9e-4 in fp16, of 2.1e-4.
 template <int PT, int N>
 __device__ __forceinline__ void exp_of(const uint32_t* r, float c, float m, uint32_t p_tm,
                                        uint64_t* acc) {
