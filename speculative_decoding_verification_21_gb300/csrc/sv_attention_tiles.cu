@@ -101,8 +101,8 @@ constexpr float kLag = 8.0f;
 // Threads, and the registers a thread is launched with and then takes by role (the
 // roles' sum must not pass what the launch gave, or the takers would wait forever).
 constexpr int kThreads16 = 384, kWideWarps = 4, kThreads8 = 384 + 64 * kWideWarps;
-// (At these counts a thread spills 12 to 50 words, around an item's start and end: 0.1 to
-// 0.7% of the instructions issued touch them.)
+// (At these counts the kernels spill 28 to 50 words a thread, outside the loops over key
+// tiles: eight times the keys leave the number of their loads and stores the same.)
 constexpr int kRegs16 = 168, kRegs8 = 96;
 constexpr int kHelpRegs16 = 88, kSoftRegs16 = 208;
 constexpr int kHelpRegs8 = 64, kSoftRegs8 = 128, kWideRegs8 = 80;
