@@ -174,13 +174,19 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(_stream_of(stream, device))
 
 
+_queue_lock = threading.Lock()
+
+
 def _queue(entry, device, *args):
-    """entry(*args) with the tensors' device current: the library launches on that."""
+    """entry(*args) with the tensors' device current: the library launches on that.
+    One call at a time: the kernels of two calls on one stream, queued by two threads
+    (ctypes lets others run meanwhile), would mix in the workspace that they share."""
     cuda = _torch().cuda
-    if cuda.current_device() == device.index:
-        return entry(*args)
-    with cuda.device(device):
-        return entry(*args)
+    with _queue_lock:
+        if cuda.current_device() == device.index:
+            return entry(*args)
+        with cuda.device(device):
+            return entry(*args)
 
 
 def _dtype_code(t) -> int:
@@ -262,17 +268,19 @@ class _WorkspaceCache:
     def __init__(self):
         self._bufs = {}
         self._outgrown = []
+        self._lock = threading.Lock()
 
     def get(self, nbytes: int, device, stream_key, stream=None):
         key = (str(device), stream_key)
-        buf = self._bufs.get(key)
-        if buf is None or buf.numel() < nbytes:
-            if buf is not None:  # twice the size at least: what is kept adds up to less than it
-                self._outgrown.append(buf)
-                nbytes = max(nbytes, 2 * buf.numel())
-            buf = _empty((max(nbytes, 256),), _torch().uint8, device, stream)
-            self._bufs[key] = buf
-        return buf
+        with self._lock:
+            buf = self._bufs.get(key)
+            if buf is None or buf.numel() < nbytes:
+                if buf is not None:  # twice the size at least: what is kept adds up to less than it
+                    self._outgrown.append(buf)
+                    nbytes = max(nbytes, 2 * buf.numel())
+                buf = _empty((max(nbytes, 256),), _torch().uint8, device, stream)
+                self._bufs[key] = buf
+            return buf
 
 
 _ws_cache = _WorkspaceCache()

@@ -1,5 +1,7 @@
 """What the binding does on the host before a call is queued: memory by stream, workspaces that
 grow, refusals (no GPU)."""
+import threading
+import time
 import weakref
 
 import pytest
@@ -185,3 +187,30 @@ def test_a_window_past_32_bits_hides_nothing(cuda):
     for window in (-1, -2 ** 31, -2 ** 32 - 5):  # the library refuses what is negative
         attend(window=window)
         assert cuda.library.calls[-1][1][8] == -1
+
+
+def test_calls_of_two_threads_do_not_interleave_on_the_device(cuda, monkeypatch):
+    """Calls of a stream share its workspace, and one call queues several kernels: another's in
+    between would use the workspace too.  (ctypes lets other threads run during a call.)"""
+    inside, most = [], []
+
+    class Slow(fake.Library):
+        def __getattr__(self, name):
+            def entry(*args):
+                if name.endswith("workspace_bytes"):
+                    return 5000
+                inside.append(name)
+                most.append(len(inside))
+                time.sleep(0.002)
+                inside.pop()
+                return 0
+            return entry
+
+    monkeypatch.setattr(_lib, "_lib", Slow(cuda))
+    calls = [fake.calls()[n] for n in ("spec_chunk_attention", "spec_verify", "spec_kv_append")]
+    threads = [threading.Thread(target=lambda c=c: [c() for _ in range(10)]) for c in calls * 2]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(most) == 60 and max(most) == 1
