@@ -65,6 +65,8 @@ class Rounds:
         self.model, self.gamma, self.tokens = model, gamma, [list(p) for p in prompts]
         dev = model.embed.device
         B, pages = len(prompts), -(-room // page_size)
+        self.room = pages * page_size
+        self.check_room(-1)
         dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
         self.cache = sv.alloc_kv_cache(B * pages, model.kv_heads, page_size, model.head_dim,
                                        dtype=dtype, device=dev)
@@ -83,9 +85,16 @@ class Rounds:
             model.chunk(flat, self.cache, self.table, start, self.kv_len)
         self.last = torch.tensor([p[-1] for p in prompts], device=dev)
 
+    def check_room(self, more):
+        """Every sequence's tokens and `more` have to fit its pages (the cache would drop the rest
+        and flag it)."""
+        if max(len(t) for t in self.tokens) + more > self.room:
+            raise ValueError(f"a sequence has no room left in its {self.room} cached tokens")
+
     def round(self):
         """One round; returns the tokens it emitted, -1 behind them [B, gamma+1]."""
         m, B, g = self.model, len(self.tokens), self.gamma
+        self.check_room(g)
         dev = self.last.device
         drafts, q, x = [], [], self.last
         for _ in range(g):

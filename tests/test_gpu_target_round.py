@@ -80,3 +80,20 @@ def test_the_example_runs(capsys, monkeypatch):
     monkeypatch.setattr("sys.argv", ["target_round.py", "--rounds", "2", "--e4m3"])
     ex.main()
     assert "drafts accepted" in capsys.readouterr().out
+
+
+def test_a_full_cache_ends_the_rounds():
+    """The last round that fits leaves its tokens in the cache; the next is refused."""
+    m = ToyTarget(vocab=50)
+    with pytest.raises(ValueError):
+        Rounds(m, [[1] * 34, [2]], gamma=3, room=32)
+    r = Rounds(m, [[1] * 25, [2]], gamma=3, room=32)
+    done = 0
+    while len(r.tokens[0]) + 3 <= 32:
+        r.round()
+        done += 1
+    assert done and int(r.kv_len.max()) <= 32
+    before = [list(t) for t in r.tokens]
+    with pytest.raises(ValueError):
+        r.round()
+    assert r.tokens == before and r.cached()[2][-1] == sum(len(t) - 1 for t in before)
