@@ -203,13 +203,15 @@ def _check_cuda(*ts, device=None):
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
+        at = t.device
+        if at != device:
+            if not t.is_cuda:
+                raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
+            if device is not None:
+                raise ValueError(f"all tensors must be on one device, got {device} and {at}")
+            device = at
         if not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
-        device = device or t.device
-        if t.device != device:
-            raise ValueError(f"all tensors must be on one device, got {device} and {t.device}")
 
 
 def _empty(shape, dtype, device, stream=None):
@@ -570,9 +572,9 @@ def spec_kv_append(cache: KVCache, new_k, new_v, block_table, q_start, kv_len, *
     torch = _torch()
     L = _lib or load()
     _check_rows(new_k, cache.kv_heads, cache, "new_k")
-    _check_rows(new_v, cache.kv_heads, cache, "new_v")
-    if new_v.shape != new_k.shape or new_v.dtype != new_k.dtype or new_v.stride() != new_k.stride():
-        raise ValueError("new_v must match new_k in shape, type and strides")
+    if new_v.shape != new_k.shape or new_v.dtype != new_k.dtype or \
+            new_v.stride() != new_k.stride() or new_v.device != cache.device:
+        raise ValueError("new_v must match new_k in shape, type, strides and device")
     B = _check_index(block_table, q_start, kv_len, cache.device)
     dev = new_k.device
     o = dict(out or {})
