@@ -73,7 +73,7 @@ typedef enum {
                               support (stated at that entry point)                     */
 } sv_status;
 
-typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2, SV_E4M3 = 3 } sv_dtype;
+typedef enum { SV_F32 = 0, SV_BF16 = 1, SV_F16 = 2, SV_E4M3 = 3, SV_U4 = 5 } sv_dtype;
 
 /* Per-batch-row flags written to out_flags[b] (bitwise OR). */
 enum {
@@ -337,23 +337,37 @@ int spec_lmhead_verify_drafted(const void* h_target, const void* W_target, int H
  * largest values of a row's own type can become that: codes are rounded to
  * nearest, and from 63488 in fp16 and 248 2^120 in bf16 on that is up to 2^16 and
  * to 2^128.
+ *
+ * A cache of type SV_U4 holds each head's vector of a token as 4-bit codes c in 0..15
+ * with a step s and a zero z of its own, two bf16 numbers; a code stands for z + s c
+ * (fp32; s c is exact there).  A row enters it as
+ *   z = bf16(its smallest value), s = max(bf16((largest / 2 - z / 2) fl(2/15)), 2^-120),
+ *   c = the integer nearest to (x - z) / s (ties to even), within 0..15,
+ * in fp32, the halves because a difference may pass the largest float; fl(2/15) is
+ * the fp32 number nearest to 1/7.5.  The zero follows rows that are not centred (keys
+ * mostly are not), which a step alone would pay for with a bit.  A row that holds NaN or
+ * an infinity gets z = s = NaN and reads as NaN throughout: there is no code for one.
+ * What reaches the end of its type can read as an infinity there, because z and s are
+ * rounded: fp16 values from 65280 on, bf16 ones of a row that spans 1.99 of the largest.
  * ------------------------------------------------------------------------- */
 
 /* The pool: element (page, head, token, i) of k is at
  * k[page * page_stride + head * head_stride + token * token_stride + i], and the
  * same in v; strides are in elements, so pages may be head-major or token-major.
- * k and v are 16-byte aligned and the strides whole multiples of 16 bytes. */
+ * k and v are 16-byte aligned and the strides whole multiples of 16 bytes.  SV_U4 has
+ * two elements to a byte, the even one in its low half: strides are even, and element
+ * i of a row at byte offset (page * page_stride + ...) / 2 + i / 2. */
 typedef struct {
   void* k;
   void* v;
-  uint8_t* k_scale;     /* SV_E4M3: [num_pages][kv_heads][page_size]; else NULL */
-  uint8_t* v_scale;
+  uint8_t* k_scale;     /* SV_E4M3: [num_pages][kv_heads][page_size]; SV_U4: bf16    */
+  uint8_t* v_scale;     /* [num_pages][kv_heads][page_size][2], step then zero; else NULL */
   int64_t num_pages;    /* < 2^31                                              */
   int64_t page_stride, head_stride, token_stride;
   int32_t kv_heads;
   int32_t page_size;
-  int32_t head_dim;     /* a multiple of 16, at most 256                       */
-  int32_t dtype;        /* SV_BF16, SV_F16 or SV_E4M3                          */
+  int32_t head_dim;     /* a multiple of 16 (SV_U4: of 32), at most 256        */
+  int32_t dtype;        /* SV_BF16, SV_F16, SV_E4M3 or SV_U4                   */
 } sv_kv_cache;
 
 /* B sequences and their chunks, packed one after another: sequence b's new tokens
@@ -380,7 +394,8 @@ typedef struct {
  * A 16-bit cache has the same dtype and gets copies.  An SV_E4M3 cache gets, per
  * token and head, s = 2^k with the smallest k >= -120 that keeps the largest
  * finite |x| / s within 448, and codes rounded to nearest, ties to even; NaN and
- * infinities become the NaN code.  No two of the new tokens may share a slot.
+ * infinities become the NaN code.  An SV_U4 cache gets codes, steps and zeros as
+ * described above.  No two of the new tokens may share a slot.
  * A new token whose position lies in front of token 0 or behind what the table's
  * pages hold is dropped; positions follow kv_len as it is given (not clamped).
  *   out_flags     [B] uint8 or NULL: SV_FLAG_BAD_PAGE, SV_FLAG_BAD_LENGTH (here
@@ -390,6 +405,42 @@ int spec_kv_append(const sv_kv_cache* cache, const sv_kv_batch* batch, const voi
                    const void* new_v, int dtype, int64_t token_stride, int64_t head_stride,
                    uint8_t* out_flags, void* cuda_stream);
 
+/* Rotary positions: row t of the table belongs to position t and holds rot_dim / 2
+ * cosines, then as many sines, of the angles by which the pairs of a head's first
+ * rot_dim elements are turned; the others stay.  What the angles are (base, scaling, a
+ * common factor) is the caller's. */
+typedef struct {
+  const float* cos_sin;  /* [positions][rot_dim], 16-byte aligned, on the device */
+  int64_t positions;     /* rows of the table, < 2^31                            */
+  int32_t rot_dim;       /* a multiple of 16, at most head_dim                   */
+  int32_t interleaved;   /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1)   */
+} sv_rope;
+
+/*
+ * spec_kv_append_rope -- spec_kv_append of a chunk whose queries and keys still lack
+ * their positions: both are rotated on the way.
+ * Of a pair (x, y) of a token at position t, with (c, s) its cosine and sine from row t,
+ *   x' = x c - y s,  y' = y c + x s
+ * in fp32, each product and their sum rounded.  The rotated keys are rounded to a 16-bit
+ * cache's type, or quantised as they stand (in fp32) into SV_E4M3 or SV_U4; values are
+ * not rotated.
+ *   q             [total][heads][head_dim] of `dtype`, strides as new_k's; NULL where
+ *                 heads is 0 (keys and values alone)
+ *   out_q         [total][heads][head_dim] of `dtype`, contiguous, 16-byte aligned: the
+ *                 rotated queries, rounded once.  May be q itself where q is contiguous,
+ *                 and must not overlap it otherwise
+ *   out_flags     [B] uint8 or NULL, as spec_kv_append
+ * A new token whose position lies outside the rotations' table is dropped and flagged
+ * (SV_FLAG_BAD_LENGTH) as one outside the pages is, and its rotated queries are zeros.
+ * A token that has no place in the pages alone gets its queries.  Rows that no sequence
+ * has are left as they are.
+ */
+int spec_kv_append_rope(const sv_kv_cache* cache, const sv_kv_batch* batch,
+                        const sv_rope* rope, const void* new_k, const void* new_v, int dtype,
+                        int64_t token_stride, int64_t head_stride, const void* q, int heads,
+                        int64_t q_token_stride, int64_t q_head_stride, void* out_q,
+                        uint8_t* out_flags, void* cuda_stream);
+
 /*
  * spec_kv_read -- tokens out of the pages into packed arrays.
  *   first         [B] int32 on the device: sequence b's tokens first[b] ..
@@ -397,7 +448,8 @@ int spec_kv_append(const sv_kv_cache* cache, const sv_kv_batch* batch, const voi
  *   out_start     [B+1] int32 on the device, as q_start of sv_kv_batch
  *   out_k, out_v  [total][kv_heads][head_dim] of `dtype` (SV_BF16 or SV_F16: the
  *                 cache's own, or either for an SV_E4M3 cache: exact in SV_BF16,
- *                 rounded to nearest in SV_F16), 16-byte aligned
+ *                 rounded to nearest in SV_F16; or either for an SV_U4 cache: z + s c
+ *                 in fp32, then rounded to nearest), 16-byte aligned
  *   out_flags     [B] uint8 or NULL, as spec_kv_append; what a flagged token would
  *                 have held is written as zeros
  */
@@ -412,7 +464,7 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
 /*
  * spec_chunk_attention -- causal attention of each sequence's chunk over its pages.
  *   q         [total][heads][head_dim] of `dtype` (SV_BF16 or SV_F16; the cache's
- *             own type, or either for an SV_E4M3 cache); strides as new_k's above
+ *             own type, or either for an SV_E4M3 or SV_U4 cache); strides as new_k's above
  *   heads     a multiple of kv_heads; query head h reads key head
  *             h / (heads / kv_heads); at most 128 query heads to a key head, and
  *             total * heads <= 2^31 - 1024
@@ -424,7 +476,10 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  * scores, the softmax's maximum and sum and the products' sums in fp32; p may be
  * rounded to `dtype` for the product with v, and an SV_E4M3 cache is dequantised
  * to `dtype` (exact in SV_BF16; in SV_F16 to nearest, so that what lies beyond 65504
- * becomes an infinity and what lies below 2^-25 a zero).
+ * becomes an infinity and what lies below 2^-25 a zero).  An SV_U4 cache is not
+ * dequantised: q.k_j = z_j sum(q) + s_j (q.c_j) in fp32, out = sum_j (p_j s_j) c_j +
+ * sum_j p_j z_j with p_j s_j in fp16, relative to the largest step that the sequence's
+ * key head has shown so far (weights below 2^-37 of that step are lost).
  *   out       [total][heads][head_dim] of `dtype`, contiguous, 16-byte aligned
  *   out_lse   [total][heads] float or NULL: log sum_j exp(scale q.k_j)
  *   out_flags [B] uint8 or NULL: SV_FLAG_BAD_PAGE, SV_FLAG_BAD_LENGTH, and

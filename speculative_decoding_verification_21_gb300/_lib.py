@@ -19,14 +19,14 @@ import threading
 from . import build as _build
 
 SV_OK = 0
-SV_F32, SV_BF16, SV_F16, SV_E4M3 = 0, 1, 2, 3
+SV_F32, SV_BF16, SV_F16, SV_E4M3, SV_U4 = 0, 1, 2, 3, 5
 SV_MODE_SAMPLE, SV_MODE_GREEDY, SV_MODE_LMHEAD, SV_MODE_DRAFT = 0, 1, 2, 3
 FLAG_ZERO_MASS, FLAG_NONFINITE, FLAG_RESIDUAL_FALLBACK, FLAG_TIMEOUT, FLAG_BAD_TOKEN = 1, 2, 4, 8, 16
 FLAG_BAD_PAGE, FLAG_BAD_LENGTH = 32, 64
 
 EXPORTS = ("sv_workspace_bytes", "sv_workspace_init", "spec_verify", "spec_verify_opts",
            "spec_verify_greedy", "spec_lmhead_verify", "spec_lmhead_draft",
-           "spec_lmhead_verify_drafted", "spec_kv_append", "spec_kv_read", "spec_chunk_attention",
+           "spec_lmhead_verify_drafted", "spec_kv_append", "spec_kv_append_rope", "spec_kv_read", "spec_chunk_attention",
            "spec_verify_probs", "sv_attention_workspace_bytes",
            "sv_set_timing_events", "sv_test_lmhead_stall", "sv_test_attention_stall", "sv_status_string", "sv_version")
 
@@ -52,6 +52,12 @@ class _BatchStruct(ctypes.Structure):
     _fields_ = [("block_table", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
                 ("kv_len", ctypes.c_void_p), ("total", ctypes.c_int64), ("B", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32)]
+
+
+class _RopeStruct(ctypes.Structure):
+    """sv_rope of include/specverify.h."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 SV_SAMPLER_GUMBEL, SV_SAMPLER_INVERSE = 0, 1
@@ -107,6 +113,8 @@ def load(build_if_missing: bool = True):
         L.spec_lmhead_draft.restype = I
         L.spec_kv_append.argtypes = [P, P, P, P, I, I64, I64, P, P]
         L.spec_kv_append.restype = I
+        L.spec_kv_append_rope.argtypes = [P, P, P, P, P, I, I64, I64, P, I, I64, I64, P, P, P]
+        L.spec_kv_append_rope.restype = I
         L.spec_kv_read.argtypes = [P, P, P, P, I, I, I64, P, P, I, P, P]
         L.spec_kv_read.restype = I
         L.sv_attention_workspace_bytes.argtypes = [P, I]
@@ -475,45 +483,65 @@ class KVCache:
     k, v [num_pages, kv_heads, page_size, head_dim] in bfloat16, float16 or
     float8_e4m3fn, the last dimension contiguous (a token-major pool is passed as
     its transpose), and for float8_e4m3fn k_scale, v_scale [num_pages, kv_heads,
-    page_size] uint8, a byte s standing for 2^(s - 127).  Sequences find their
+    page_size] uint8, a byte s standing for 2^(s - 127).  A cache of 4-bit codes has
+    uint8 pools [num_pages, kv_heads, page_size, head_dim / 2], the even element of a
+    byte in its low half, and k_scale, v_scale [num_pages, kv_heads, page_size, 2]
+    bfloat16, step and zero of each row.  Sequences find their
     pages through a block_table [B, max_pages] int32.  The tensors are the
     caller's; this object only names them."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         torch = _torch()
-        codes = {torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3}
+        codes = {torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3,
+                 torch.uint8: SV_U4}
         if k.dtype not in codes:
-            raise TypeError(f"a cache is bfloat16, float16 or float8_e4m3fn, got {k.dtype}")
+            raise TypeError("a cache is bfloat16, float16, float8_e4m3fn or (4-bit codes) uint8, "
+                            f"got {k.dtype}")
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
             raise ValueError("k and v: [num_pages, kv_heads, page_size, head_dim], alike in "
                              "shape, type and strides")
         if k.stride(3) != 1:
             raise ValueError("the head dimension must be contiguous")
-        e4m3 = k.dtype == torch.float8_e4m3fn
-        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
-            raise ValueError("k_scale and v_scale belong to float8_e4m3fn caches, and only there")
+        e4m3, u4 = k.dtype == torch.float8_e4m3fn, k.dtype == torch.uint8
+        scaled = e4m3 or u4
+        if scaled != (k_scale is not None) or scaled != (v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to float8_e4m3fn and uint8 caches, and only there")
         if e4m3:
             for s in (k_scale, v_scale):
                 if s.dtype != torch.uint8 or tuple(s.shape) != tuple(k.shape[:3]):
                     raise ValueError("scales: uint8 [num_pages, kv_heads, page_size]")
+        if u4:
+            for s in (k_scale, v_scale):
+                if s.dtype != torch.bfloat16 or tuple(s.shape) != (*k.shape[:3], 2):
+                    raise ValueError("steps and zeros: bfloat16 [num_pages, kv_heads, page_size, 2]")
         if not (k.is_cuda and v.device == k.device):
             raise ValueError("k and v must be CUDA tensors of one device (the library has no CPU path)")
         _check_cuda(k_scale, v_scale, device=k.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.num_pages, self.kv_heads, self.page_size, _ = k.shape
+        held = 2 if u4 else 1  # elements of a pool's entry
+        self.head_dim = held * k.shape[3]
         self.dtype, self.device = k.dtype, k.device
         self._struct = _CacheStruct(
-            k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
-            v_scale.data_ptr() if e4m3 else None, k.shape[0], k.stride(0), k.stride(1),
-            k.stride(2), k.shape[1], k.shape[2], k.shape[3], codes[k.dtype])
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if scaled else None,
+            v_scale.data_ptr() if scaled else None, k.shape[0], held * k.stride(0),
+            held * k.stride(1), held * k.stride(2), k.shape[1], k.shape[2], self.head_dim,
+            codes[k.dtype])
         self._ref = ctypes.addressof(self._struct)
         self._attention_ws = {}  # workspace bytes by query heads
 
 
 def alloc_kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, *, dtype,
                    device="cuda") -> KVCache:
-    """A head-major cache of zeros."""
+    """A head-major cache of zeros.  dtype torch.uint8: 4-bit codes."""
     torch = _torch()
+    if dtype == torch.uint8:
+        if head_dim % 2:
+            raise ValueError("4-bit codes: an even head_dim")
+        shape = (num_pages, kv_heads, page_size, head_dim // 2)
+        return KVCache(*(torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)),
+                       *(torch.zeros((*shape[:3], 2), dtype=torch.bfloat16, device=device)
+                         for _ in range(2)))
     shape = (num_pages, kv_heads, page_size, head_dim)
     k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
     if dtype != torch.float8_e4m3fn:
@@ -589,17 +617,62 @@ def spec_kv_append(cache: KVCache, new_k, new_v, block_table, q_start, kv_len, *
     return o
 
 
+def spec_kv_append_rope(cache: KVCache, new_k, new_v, block_table, q_start, kv_len, cos_sin, *,
+                        q=None, interleaved: bool = False, want_flags: bool = False, out=None,
+                        stream=None):
+    """spec_kv_append of a chunk whose keys, and queries q [total, heads, head_dim] (as new_k
+    in type, any token and head strides; None: no queries), are rotated by their positions on
+    the way.  cos_sin [positions, rot_dim] float32: for each position rot_dim / 2 cosines,
+    then as many sines; the pairs of a head's first rot_dim elements are (i, i + rot_dim / 2),
+    or (2i, 2i + 1) if interleaved.  Returns a dict: q [total, heads, head_dim], the rotated
+    queries (if q is given; out={"q": q} rotates a contiguous q in place), flags [B] uint8 (if
+    want_flags)."""
+    torch = _torch()
+    L = _lib or load()
+    _check_rows(new_k, cache.kv_heads, cache, "new_k")
+    if new_v.shape != new_k.shape or new_v.dtype != new_k.dtype or \
+            new_v.stride() != new_k.stride() or new_v.device != cache.device:
+        raise ValueError("new_v must match new_k in shape, type, strides and device")
+    B = _check_index(block_table, q_start, kv_len, cache.device)
+    _check_cuda(cos_sin, device=cache.device)
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+        raise ValueError("cos_sin: [positions, rot_dim] float32")
+    dev, total = new_k.device, new_k.shape[0]
+    o = dict(out or {})
+    heads, q_strides = 0, (0, 0)
+    if q is not None:
+        _check_rows(q, 0, cache, "q")
+        if q.shape[0] != total or q.dtype != new_k.dtype:
+            raise ValueError("q must match new_k in rows and type")
+        heads, q_strides = q.shape[1], (q.stride(0), q.stride(1))
+        _output(o, "q", (total, heads, cache.head_dim), q.dtype, dev, stream)
+        if o["q"] is None:
+            raise ValueError("out q: the rotated queries have to go somewhere")
+    _output(o, "flags", (B,), torch.uint8, dev, stream, want_flags)
+    batch = _BatchStruct(block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), total, B,
+                         block_table.shape[1])
+    rope = _RopeStruct(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)))
+    rc = _queue(L.spec_kv_append_rope, dev, cache._ref, ctypes.addressof(batch),
+                ctypes.addressof(rope), _address(new_k), _address(new_v), _row_code(new_k),
+                new_k.stride(0), new_k.stride(1), _address(q), heads, *q_strides,
+                _address(o["q"]) if heads else None, _address(o.get("flags")),
+                _stream_of(stream, dev))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_kv_append_rope")
+    return o
+
+
 def spec_kv_read(cache: KVCache, block_table, first, out_start, total: int, *, dtype=None,
                  want_flags: bool = False, out=None, stream=None):
     """Tokens first[b] .. of every sequence out of the pages, out_start[b+1] -
     out_start[b] of them, packed.  dtype: the cache's own (the default), or either
-    16-bit type (default bfloat16) for a float8_e4m3fn cache.  Returns a dict:
+    16-bit type (default bfloat16) for a float8_e4m3fn or uint8 cache.  Returns a dict:
     k, v [total, kv_heads, head_dim], flags [B] uint8 (if want_flags)."""
     torch = _torch()
     L = _lib or load()
     B = _check_index(block_table, out_start, first, cache.device)
     if dtype is None:
-        dtype = torch.bfloat16 if cache.dtype == torch.float8_e4m3fn else cache.dtype
+        dtype = torch.bfloat16 if cache.k_scale is not None else cache.dtype
     dev = cache.device
     o = dict(out or {})
     for name in ("k", "v"):

@@ -39,6 +39,11 @@ size_t lmhead_draft_workspace_bytes(int B, int64_t V);
 cudaError_t launch_kv_append(const sv_kv_cache& c, const sv_kv_batch& b, const void* new_k,
                              const void* new_v, int dtype, int64_t token_stride,
                              int64_t head_stride, uint8_t* out_flags, cudaStream_t stream);
+cudaError_t launch_kv_append_rope(const sv_kv_cache& c, const sv_kv_batch& b, const sv_rope& rope,
+                                  const void* new_k, const void* new_v, int dtype,
+                                  int64_t token_stride, int64_t head_stride, const void* q,
+                                  int heads, int64_t q_token_stride, int64_t q_head_stride,
+                                  void* out_q, uint8_t* out_flags, cudaStream_t stream);
 cudaError_t launch_kv_read(const sv_kv_cache& c, const int32_t* block_table, const int32_t* first,
                            const int32_t* out_start, int B, int max_pages, int64_t total,
                            void* out_k, void* out_v, int dtype, uint8_t* out_flags,
@@ -89,14 +94,18 @@ constexpr int64_t kMaxTokens = kMaxRows - 1024;
 // A cache whose shape, type and strides the kernels can walk.
 int check_cache(const sv_kv_cache* c) {
   if (!c) return SV_ERR_ARG;
-  if (c->dtype != SV_BF16 && c->dtype != SV_F16 && c->dtype != SV_E4M3) return SV_ERR_DTYPE;
+  if (c->dtype != SV_BF16 && c->dtype != SV_F16 && c->dtype != SV_E4M3 && c->dtype != SV_U4)
+    return SV_ERR_DTYPE;
   if (c->num_pages < 0 || c->num_pages >= kMaxRows || c->kv_heads < 1 || c->page_size < 1 ||
       c->head_dim < 1 || c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0)
     return SV_ERR_ARG;
-  if (c->head_dim % 16 || c->head_dim > kMaxHeadDim) return SV_ERR_UNSUPPORTED;
+  if (c->head_dim % (c->dtype == SV_U4 ? 32 : 16) || c->head_dim > kMaxHeadDim)
+    return SV_ERR_UNSUPPORTED;
   if (c->num_pages == 0) return SV_OK;  // every page index is then out of range
-  if (!c->k || !c->v || (c->dtype == SV_E4M3 && (!c->k_scale || !c->v_scale))) return SV_ERR_ARG;
-  const int64_t vec = c->dtype == SV_E4M3 ? 16 : 8;
+  const bool scaled = c->dtype == SV_E4M3 || c->dtype == SV_U4;
+  if (!c->k || !c->v || (scaled && (!c->k_scale || !c->v_scale))) return SV_ERR_ARG;
+  if (c->dtype == SV_U4 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))) return SV_ERR_ALIGN;
+  const int64_t vec = c->dtype == SV_U4 ? 32 : c->dtype == SV_E4M3 ? 16 : 8;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % vec || c->head_stride % vec ||
       c->token_stride % vec)
     return SV_ERR_ALIGN;
@@ -117,7 +126,7 @@ int check_batch(const int32_t* table, const int32_t* start, const int32_t* len, 
 // The packed rows' type beside the cache's.
 int check_row_type(const sv_kv_cache* c, int dtype) {
   if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
-  if (c->dtype != SV_E4M3 && c->dtype != dtype) return SV_ERR_DTYPE;
+  if (c->dtype != SV_E4M3 && c->dtype != SV_U4 && c->dtype != dtype) return SV_ERR_DTYPE;
   return SV_OK;
 }
 
@@ -293,6 +302,37 @@ int spec_kv_append(const sv_kv_cache* cache, const sv_kv_batch* batch, const voi
              : SV_ERR_CUDA;
 }
 
+int spec_kv_append_rope(const sv_kv_cache* cache, const sv_kv_batch* batch,
+                        const sv_rope* rope, const void* new_k, const void* new_v, int dtype,
+                        int64_t token_stride, int64_t head_stride, const void* q, int heads,
+                        int64_t q_token_stride, int64_t q_head_stride, void* out_q,
+                        uint8_t* out_flags, void* cuda_stream) {
+  int st = check_cache(cache);
+  if (st == SV_OK && (!batch || !rope)) st = SV_ERR_ARG;
+  if (st == SV_OK) st = check_row_type(cache, dtype);
+  if (st == SV_OK) st = check_strides(token_stride, head_stride);
+  if (st == SV_OK) st = check_strides(q_token_stride, q_head_stride);
+  if (st == SV_OK)
+    st = check_batch(batch->block_table, batch->q_start, batch->kv_len, batch->B, batch->max_pages,
+                     batch->total, cache->page_size);
+  if (st != SV_OK) return st;
+  if (heads < 0 || rope->positions < 0 || rope->positions >= kMaxRows || rope->rot_dim < 1 ||
+      rope->rot_dim > cache->head_dim || rope->interleaved < 0 || rope->interleaved > 1)
+    return SV_ERR_ARG;
+  if (rope->rot_dim % 16 || batch->total * heads > kMaxTokens) return SV_ERR_UNSUPPORTED;
+  if (batch->B == 0) return SV_OK;
+  if (rope->positions > 0 && !rope->cos_sin) return SV_ERR_ARG;
+  if (batch->total > 0 && (!new_k || !new_v || (heads && (!q || !out_q)))) return SV_ERR_ARG;
+  if (!aligned(new_k, 16) || !aligned(new_v, 16) || !aligned(rope->cos_sin, 16) ||
+      (heads && (!aligned(q, 16) || !aligned(out_q, 16))))
+    return SV_ERR_ALIGN;
+  return sv::launch_kv_append_rope(*cache, *batch, *rope, new_k, new_v, dtype, token_stride,
+                                   head_stride, q, heads, q_token_stride, q_head_stride, out_q,
+                                   out_flags, (cudaStream_t)cuda_stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
 int spec_kv_read(const sv_kv_cache* cache, const int32_t* block_table, const int32_t* first,
                  const int32_t* out_start, int B, int max_pages, int64_t total, void* out_k,
                  void* out_v, int dtype, uint8_t* out_flags, void* cuda_stream) {
@@ -314,7 +354,7 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads) {
   if (check_cache(cache) != SV_OK || heads < 1 || heads % cache->kv_heads ||
       heads / cache->kv_heads > kMaxGroup)
     return 0;
-  return sv::attention_workspace_bytes(sv::cache_view(*cache), cache->dtype == SV_E4M3);
+  return sv::attention_workspace_bytes(sv::cache_view(*cache), cache->dtype, heads / cache->kv_heads);
 }
 
 int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, const void* q,
@@ -356,7 +396,7 @@ int spec_chunk_attention(const sv_kv_cache* cache, const sv_kv_batch* batch, con
   a.lse = out_lse;
   a.flags = out_flags;
   a.ws = (char*)workspace;
-  return sv::launch_attention(a, dtype, cache->dtype == SV_E4M3, (cudaStream_t)cuda_stream) ==
+  return sv::launch_attention(a, dtype, cache->dtype, (cudaStream_t)cuda_stream) ==
                  cudaSuccess
              ? SV_OK
              : SV_ERR_CUDA;

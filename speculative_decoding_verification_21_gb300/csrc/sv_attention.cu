@@ -99,12 +99,14 @@ __global__ void __launch_bounds__(256) k_attend_flags(AttendArgs a) {
 
 }  // namespace
 
-size_t attention_workspace_bytes(const CacheView& c, bool e4m3) {
-  return tiles_take(c, e4m3) ? attention_tiles_workspace(c.head_dim) : 0;
+size_t attention_workspace_bytes(const CacheView& c, int cache_dtype, int group) {
+  if (cache_dtype == SV_U4) return 0;
+  return tiles_take(c, cache_dtype == SV_E4M3) ? attention_tiles_workspace(c.head_dim) : 0;
 }
 
-cudaError_t launch_attention(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream) {
-  if (tiles_take(a.c, e4m3) && a.scale_log2 >= 0.0f) {
+cudaError_t launch_attention(const AttendArgs& a, int dtype, int cache_dtype, cudaStream_t stream) {
+  const bool e4m3 = cache_dtype == SV_E4M3, u4 = cache_dtype == SV_U4;
+  if (!u4 && tiles_take(a.c, e4m3) && a.scale_log2 >= 0.0f) {
     bool taken = false;
     const cudaError_t e = launch_attention_tiles(a, dtype, e4m3, stream, &taken);
     if (e != cudaSuccess || taken) return e;
@@ -114,6 +116,7 @@ cudaError_t launch_attention(const AttendArgs& a, int dtype, bool e4m3, cudaStre
     if (e != cudaSuccess) return e;
   }
   if (a.b.total == 0) return cudaSuccess;
+  if (u4) return launch_attention_rows_u4(a, dtype, stream);
   auto* k = dtype == SV_BF16 ? (e4m3 ? k_attend_rows<SV_BF16, true> : k_attend_rows<SV_BF16, false>)
                              : (e4m3 ? k_attend_rows<SV_F16, true> : k_attend_rows<SV_F16, false>);
   return launch_pdl(k, dim3((unsigned)((int64_t)a.b.total * a.heads)), dim3(kRowWarps * 32), 0,

@@ -49,9 +49,11 @@ __device__ __forceinline__ uint8_t sequence_flags(const AttendArgs& a, int b) {
   return (uint8_t)((q.bad ? SV_FLAG_BAD_LENGTH : 0) | (bad ? SV_FLAG_BAD_PAGE : 0));
 }
 
-size_t attention_workspace_bytes(const CacheView& c, bool e4m3);
+// cache_dtype: the sv_dtype of the cache; group: query heads to a key head.
+size_t attention_workspace_bytes(const CacheView& c, int cache_dtype, int group);
 size_t attention_tiles_workspace(int head_dim);
-cudaError_t launch_attention(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream);
+cudaError_t launch_attention(const AttendArgs& a, int dtype, int cache_dtype, cudaStream_t stream);
+cudaError_t launch_attention_rows_u4(const AttendArgs& a, int dtype, cudaStream_t stream);
 
 // Test only (sv_test_attention_stall).
 void set_attention_stall(int cta, long long clocks);

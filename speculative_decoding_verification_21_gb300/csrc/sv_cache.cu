@@ -5,12 +5,10 @@
 // k and of v) are contiguous on the packed side, and head_dim-long runs on the
 // pool's.  One warp takes one token or four, so that the search for its sequence and
 // its page is done once for all of its rows; a lane moves 16 elements of a row (two
-// 16-byte vectors of 16-bit floats, one of codes), and a row's lanes form an
+// 16-byte vectors of 16-bit floats, 16 bytes of e4m3 codes, 8 of 4-bit codes), and a row's lanes form an
 // aligned group of 1, 2, 4, 8 or 16 so that its largest value is a few shuffles.
 //
-// e4m3: with amax = f 2^e, 1 <= f < 2, the largest code 448 = 1.75 2^8 holds
-// amax / 2^k for k = e - 8 if f <= 1.75 and k = e - 7 else; x 2^-k is exact in
-// fp32 (k >= -120 keeps 2^-k finite), so each code is rounded once.
+// (encode_e4m3, encode_u4: the rows' codes.)
 //
 // Measured on GB300: 84 thousand tokens of 8 heads of 128 into e4m3 94 us, 5.5 TB/s
 // (0.81 of a copy's rate; what is missing is the arithmetic between loads and stores);
@@ -29,7 +27,6 @@ namespace sv {
 namespace {
 
 constexpr int kMoveWarps = 8;
-constexpr int kMinScaleExp = -120;
 
 struct MoveArgs {
   CacheView c;
@@ -88,48 +85,6 @@ __device__ void write_flags(const MoveArgs& a, int b) {
     a.flags[b] = (uint8_t)((q.bad ? SV_FLAG_BAD_LENGTH : 0) | (any ? SV_FLAG_BAD_PAGE : 0));
 }
 
-// 16 values as codes: the row's largest finite |x| over its group of lanes, the
-// exponent, the codes.
-template <int DT>
-__device__ __forceinline__ uint4 encode16(const uint4& x0, const uint4& x1, int group_shift, int& k) {
-  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-  const float inf = __int_as_float(0x7f800000);
-  float f[16], m = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 p = F16<DT>::up(w[j]);
-    f[2 * j] = p.x;
-    f[2 * j + 1] = p.y;
-    m = fmaxf(m, fmaxf(fabsf(p.x), fabsf(p.y)));  // (a NaN is passed over)
-  }
-  if (__any_sync(0xffffffffu, m == inf)) {
-    // the largest finite one instead; infinities become the NaN code (the conversion
-    // would make them the largest)
-    m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (fabsf(f[j]) == inf) f[j] = __int_as_float(0x7fffffff);
-      m = fmaxf(m, fabsf(f[j]));
-    }
-  }
-  for (int o = 1; o < (1 << group_shift); o <<= 1)
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const uint32_t bits = __float_as_uint(m);
-  k = (int)(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
-  k = k < kMinScaleExp ? kMinScaleExp : k;
-  const float inv = __uint_as_float((uint32_t)(127 - k) << 23);
-  uint32_t o4[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * j] * inv, f[4 * j + 1] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * j + 2] * inv, f[4 * j + 3] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    o4[j] = lo | (hi << 16);
-  }
-  return make_uint4(o4[0], o4[1], o4[2], o4[3]);
-}
-
 // 16 codes times 2^(byte - 127) as 16-bit values.
 template <int DT>
 __device__ __forceinline__ void decode16(const uint4& x, uint32_t byte, uint4& x0, uint4& x1) {
@@ -142,6 +97,20 @@ __device__ __forceinline__ void decode16(const uint4& x, uint32_t byte, uint4& x
     o8[2 * j] = F16<DT>::down(lo.x * s, lo.y * s);
     o8[2 * j + 1] = F16<DT>::down(hi.x * s, hi.y * s);
   }
+  x0 = make_uint4(o8[0], o8[1], o8[2], o8[3]);
+  x1 = make_uint4(o8[4], o8[5], o8[6], o8[7]);
+}
+
+// 16 4-bit codes as 16-bit values z + s c (s c is exact in fp32).
+template <int DT>
+__device__ __forceinline__ void decode_u4(const uint4& x, uint32_t sz, uint4& x0, uint4& x1) {
+  const float s = step_of(sz), z = zero_of(sz);
+  const uint32_t w[2] = {x.x, x.y};
+  uint32_t o8[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    o8[j] = F16<DT>::down(fmaf(s, code_of(w[j >> 2], 2 * j & 7), z),
+                          fmaf(s, code_of(w[j >> 2], (2 * j & 7) + 1), z));
   x0 = make_uint4(o8[0], o8[1], o8[2], o8[3]);
   x1 = make_uint4(o8[4], o8[5], o8[6], o8[7]);
 }
@@ -176,11 +145,11 @@ __device__ __forceinline__ Place place_of(const MoveArgs& a, int b, int t, int64
 // 84 thousand tokens of 8 heads of 128 into e4m3: 94 us (5.5 TB/s), with four steps 98,
 // with one 116; 175 thousand out of e4m3: 171 us (6.3 TB/s), with 48 warps 176, with four
 // steps 204.
-constexpr int batch_of(bool e4m3, bool append) { return e4m3 && append ? 2 : 1; }
+constexpr int batch_of(int fmt, bool append) { return fmt != kHalf && append ? 2 : 1; }
 
-template <int DT, bool E4M3, bool APPEND>
-__global__ void __launch_bounds__(kMoveWarps * 32, batch_of(E4M3, APPEND) > 1 ? 4 : APPEND ? 6 : 8) k_move(const __grid_constant__ MoveArgs a,
-                                                          int group_shift, int per) {
+template <int DT, int FMT, bool APPEND>
+__global__ void __launch_bounds__(kMoveWarps * 32, batch_of(FMT, APPEND) > 1 ? 4 : APPEND ? 6 : 8)
+    k_move(const __grid_constant__ MoveArgs a, int group_shift, int per) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -213,7 +182,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, batch_of(E4M3, APPEND) > 1 ? 
   const int at_once = 32 >> group_shift;
   const int steps = (rows + at_once - 1) / at_once;
   // the loads of a batch of steps, then the rest of them
-  constexpr int kBatch = batch_of(E4M3, APPEND);
+  constexpr int kBatch = batch_of(FMT, APPEND);
   const int all = n * steps;
   int j = 0, step = 0;
   for (int e0 = 0; e0 < all; e0 += kBatch) {
@@ -248,9 +217,14 @@ __global__ void __launch_bounds__(kMoveWarps * 32, batch_of(E4M3, APPEND) > 1 ? 
       } else {
         out[i] = (is_v[i] ? a.out_v : a.out_k) + ((t * c.kv_heads + h) * c.head_dim) * 2;
         if (live[i] && page >= 0) {
-          if (E4M3) {
+          if (FMT == kE4m3) {
             x0[i] = ld_stream16(pool + 16 * sub);
             x1[i].x = __ldg((is_v[i] ? c.vs : c.ks) + at[i]);
+          } else if (FMT == kU4) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(pool) + sub);
+            x0[i].x = w.x;
+            x0[i].y = w.y;
+            x1[i].x = __ldg(reinterpret_cast<const uint32_t*>(is_v[i] ? c.vs : c.ks) + at[i]);
           } else {
             x0[i] = ld_stream16(pool + 32 * sub);
             x1[i] = ld_stream16(pool + 32 * sub + 16);
@@ -261,16 +235,30 @@ __global__ void __launch_bounds__(kMoveWarps * 32, batch_of(E4M3, APPEND) > 1 ? 
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       uint4* const dst = reinterpret_cast<uint4*>(out[i]);
-      if (APPEND && E4M3) {
-        int k;
-        const uint4 o = encode16<DT>(x0[i], x1[i], group_shift, k);
-        if (live[i]) {
-          dst[sub] = o;
-          if (sub == 0) (is_v[i] ? c.vs : c.ks)[at[i]] = (uint8_t)(k + 127);
+      if (APPEND && FMT != kHalf) {
+        float f[16];
+        widen16<DT>(x0[i], x1[i], f);
+        if (FMT == kE4m3) {
+          int k;
+          const uint4 o = encode_e4m3(f, amax16(f), group_shift, k);
+          if (live[i]) {
+            dst[sub] = o;
+            if (sub == 0) (is_v[i] ? c.vs : c.ks)[at[i]] = (uint8_t)(k + 127);
+          }
+        } else {
+          float lo, hi;
+          uint32_t sz;
+          range16(f, on, lo, hi);
+          const uint2 o = encode_u4(f, lo, hi, group_shift, sz);
+          if (live[i]) {
+            reinterpret_cast<uint2*>(out[i])[sub] = o;
+            if (sub == 0) reinterpret_cast<uint32_t*>(is_v[i] ? c.vs : c.ks)[at[i]] = sz;
+          }
         }
         continue;
       }
-      if (E4M3) decode16<DT>(x0[i], x1[i].x, x0[i], x1[i]);
+      if (FMT == kE4m3) decode16<DT>(x0[i], x1[i].x, x0[i], x1[i]);
+      if (FMT == kU4) decode_u4<DT>(x0[i], x1[i].x, x0[i], x1[i]);
       if (live[i]) {
         dst[2 * sub] = x0[i];
         dst[2 * sub + 1] = x1[i];
@@ -280,7 +268,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, batch_of(E4M3, APPEND) > 1 ? 
 }
 
 template <bool APPEND>
-cudaError_t launch_move(MoveArgs a, int dtype, bool e4m3, cudaStream_t stream) {
+cudaError_t launch_move(MoveArgs a, int dtype, Format fmt, cudaStream_t stream) {
   int shift = 0;
   while ((16 << shift) < a.c.head_dim) ++shift;
   // four tokens a warp where that still gives every SM 16 warps
@@ -288,8 +276,10 @@ cudaError_t launch_move(MoveArgs a, int dtype, bool e4m3, cudaStream_t stream) {
   a.move_blocks = (int)(((int64_t)a.total + kMoveWarps * per - 1) / (kMoveWarps * per));
   const int flag_blocks = a.flags ? (a.B + kMoveWarps - 1) / kMoveWarps : 0;
   if (a.move_blocks + flag_blocks == 0) return cudaSuccess;
-  auto* k = e4m3 ? (dtype == SV_BF16 ? k_move<SV_BF16, true, APPEND> : k_move<SV_F16, true, APPEND>)
-                 : k_move<SV_BF16, false, APPEND>;  // a plain copy of 16-bit values
+  const bool bf = dtype == SV_BF16;
+  auto* k = fmt == kE4m3 ? (bf ? k_move<SV_BF16, kE4m3, APPEND> : k_move<SV_F16, kE4m3, APPEND>)
+            : fmt == kU4 ? (bf ? k_move<SV_BF16, kU4, APPEND> : k_move<SV_F16, kU4, APPEND>)
+                         : k_move<SV_BF16, kHalf, APPEND>;  // a plain copy of 16-bit values
   return launch_pdl(k, dim3(a.move_blocks + flag_blocks), dim3(kMoveWarps * 32), 0, stream, a, shift, per);
 }
 
@@ -311,7 +301,7 @@ cudaError_t launch_kv_append(const sv_kv_cache& c, const sv_kv_batch& b, const v
   a.total = (int)b.total;
   a.B = b.B;
   a.max_pages = b.max_pages;
-  return launch_move<true>(a, dtype, c.dtype == SV_E4M3, stream);
+  return launch_move<true>(a, dtype, format_of(c.dtype), stream);
 }
 
 cudaError_t launch_kv_read(const sv_kv_cache& c, const int32_t* block_table, const int32_t* first,
@@ -329,7 +319,7 @@ cudaError_t launch_kv_read(const sv_kv_cache& c, const int32_t* block_table, con
   a.total = (int)total;
   a.B = B;
   a.max_pages = max_pages;
-  return launch_move<false>(a, dtype, c.dtype == SV_E4M3, stream);
+  return launch_move<false>(a, dtype, format_of(c.dtype), stream);
 }
 
 }  // namespace sv
