@@ -100,12 +100,17 @@ __global__ void __launch_bounds__(256) k_attend_flags(AttendArgs a) {
 }  // namespace
 
 size_t attention_workspace_bytes(const CacheView& c, int cache_dtype, int group) {
-  if (cache_dtype == SV_U4) return 0;
+  if (cache_dtype == SV_U4) return u4_tiles_take(c, group) ? attention_u4_workspace(c.head_dim) : 0;
   return tiles_take(c, cache_dtype == SV_E4M3) ? attention_tiles_workspace(c.head_dim) : 0;
 }
 
 cudaError_t launch_attention(const AttendArgs& a, int dtype, int cache_dtype, cudaStream_t stream) {
   const bool e4m3 = cache_dtype == SV_E4M3, u4 = cache_dtype == SV_U4;
+  if (u4 && u4_tiles_take(a.c, a.heads / a.c.kv_heads) && a.b.total > 0) {
+    bool taken = false;
+    const cudaError_t e = launch_attention_u4_tiles(a, dtype, stream, &taken);
+    if (e != cudaSuccess || taken) return e;
+  }
   if (!u4 && tiles_take(a.c, e4m3) && a.scale_log2 >= 0.0f) {
     bool taken = false;
     const cudaError_t e = launch_attention_tiles(a, dtype, e4m3, stream, &taken);

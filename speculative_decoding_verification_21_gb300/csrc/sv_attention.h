@@ -55,8 +55,21 @@ size_t attention_tiles_workspace(int head_dim);
 cudaError_t launch_attention(const AttendArgs& a, int dtype, int cache_dtype, cudaStream_t stream);
 cudaError_t launch_attention_rows_u4(const AttendArgs& a, int dtype, cudaStream_t stream);
 
+// Whether the tile kernel of 4-bit caches takes one: head_dim up to 128, pages of a power of
+// two of tokens, at least 16, at most 80 query heads to a key head, steps and zeros on
+// 16-byte boundaries.
+bool u4_tiles_take(const CacheView& c, int group);
+size_t attention_u4_workspace(int head_dim);
+// *taken = false: the cache cannot be described by a tensor map; nothing was queued.
+cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream_t stream, bool* taken);
+
 // Test only (sv_test_attention_stall).
 void set_attention_stall(int cta, long long clocks);
+struct AttentionTest {
+  int stall_cta;         // -1: none
+  long long wait_clocks; // limit of a wait
+};
+AttentionTest attention_test();
 
 // *taken = false: the cache cannot be described by a tensor map; nothing was queued.
 cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cudaStream_t stream,

@@ -10,11 +10,8 @@
 // key tile is read once for all of them.  An item is up to two such tiles of one
 // (sequence, key head); its keys are cut into tiles of 128 counted from token 0.
 //
-// Balance: all key tiles of all items form one line, an item's start worth kItemUnits
-// tiles more, cut into equal shares, one per CTA (one CTA per SM).  An item cut by a share's end leaves partial (m, l, O)
-// in the workspace, at most two per CTA, which k_attend_join adds up; an item
-// inside a share is written at once.  Lengths live on the device, so every CTA
-// finds its own place in the line at its start.
+// Balance: equal shares of one line of key tiles, one per CTA, and a join of the items
+// that a share's end cuts (sv_attention_line.cuh).
 //
 // Two softmax warpgroups keep the tensor cores busy: while one works on its S,
 // the other's products run.  An item of two row tiles gives one to each; an item
@@ -61,6 +58,7 @@
 
 #include "specverify.h"
 #include "sv_attention.h"
+#include "sv_attention_line.cuh"
 #include "sv_attention_row.cuh"
 #include "sv_cache.cuh"
 #include "sv_device.cuh"
@@ -71,9 +69,8 @@
 namespace sv {
 namespace {
 
-constexpr int kTile = 128;          // query rows and keys per tile
+// (kTile: query rows of a tile too)
 constexpr int kSpan = 16384;        // 128 rows of one 128-byte swizzle span
-constexpr int kMaxCtas = 160;       // shares (GB300: 152 SMs)
 constexpr int kMaxRows = 2 * kTile;
 constexpr int kMaxStages = 12, kMaxRaw = 8;
 constexpr long long kWaitClocks = 1ll << 32;  // about two seconds
@@ -90,11 +87,6 @@ constexpr int kQBytes = 2 * kSpan;                // one query tile
 // round of 64 sequences of bf16, 6 tiles in flight instead of 5: 203 us instead of 212).
 constexpr int kCodes = 64 * 1024, kRing16 = 160 * 1024, kRing8 = 96 * 1024;
 constexpr int kScaleBytes = kMaxRaw * kTile;
-// What an item costs beside its key tiles (its queries, the end of its pipeline, its
-// outputs), in key tiles.  (Shares of key tiles alone: a round of 64 sequences 203 us,
-// with 1, 2, 3, 4 a start 201, 198, 197, 197; the prompt chunk 449 and 443, 439, 439, 440.)
-constexpr int kItemUnits = 3;
-constexpr int kJoinThreads = 256;
 // The running maximum may lag by this many powers of two before O is rescaled: P
 // stays within 2^8, exact enough in 16-bit floats and far from their range.
 constexpr float kLag = 8.0f;
@@ -109,12 +101,11 @@ constexpr int kHelpRegs8 = 64, kSoftRegs8 = 128, kWideRegs8 = 80;
 static_assert(128 * kHelpRegs16 + 256 * kSoftRegs16 <= kThreads16 * kRegs16, "registers");
 static_assert(128 * kHelpRegs8 + 256 * kSoftRegs8 + 64 * kWideWarps * kWideRegs8 <= kThreads8 * kRegs8, "registers");
 
-// Slots of a ring, and ceil(2^32 / slots): slot and turn of tile k without a division.
-struct Ring {
-  uint32_t n, inv;
-};
-
 struct TileArgs {
+  // What an item costs beside its key tiles (its queries, the end of its pipeline, its
+  // outputs), in key tiles.  (Shares of key tiles alone: a round of 64 sequences 203 us,
+  // with 1, 2, 3, 4 a start 201, 198, 197, 197; the prompt chunk 449 and 443, 439, 439, 440.)
+  static constexpr int kItemUnits = 3, kRowTiles = 2, kSlotRows = kMaxRows;
   AttendArgs a;
   int group, tpt;      // query heads per key head; tokens per row tile
   int nhalf;           // swizzle spans per row: 1 (head_dim <= 64) or 2
@@ -130,14 +121,6 @@ struct TileArgs {
   float2* ml;          // [2 * kMaxCtas][kMaxRows]
   struct Rec* rec;     // [kMaxCtas]
   int* err;            // [kMaxCtas]: kLate, kMend; above 8 bits a wait that gave up
-};
-
-constexpr int kLate = 1, kMend = 2;
-
-// What a CTA leaves for the join: the item that it began and did not end.
-struct Rec {
-  int more;            // further CTAs with a part of it (0: nothing to join)
-  int row0, ntok, h;   // first packed row, tokens, key head
 };
 
 // Control words of a CTA.
@@ -156,223 +139,6 @@ struct Ctl {
   };
 };
 
-// ---------------------------------------------------------------------------
-// The line of work.
-// ---------------------------------------------------------------------------
-struct Span {
-  int lo, hi;        // keys [lo, hi) that some row of the item sees
-  int first, count;  // key tiles; count >= 1 (a masked one if nothing is seen)
-};
-
-__device__ __forceinline__ Span item_span(const Seq& q, int per_item, int qt, int window) {
-  const int i0 = qt * per_item, i1 = min(q.n, i0 + per_item);
-  Span s;
-  const int seen = q.pos0 + i0 + 1;  // keys up to the first row's own; negative in front of token 0
-  s.hi = max(0, q.pos0 + i1);
-  s.lo = window && seen > window ? seen - window : 0;
-  if (s.hi <= s.lo) {
-    s.lo = s.hi = s.first = 0;
-    s.count = 1;
-  } else {
-    s.first = s.lo / kTile;
-    s.count = (s.hi + kTile - 1) / kTile - s.first;
-  }
-  return s;
-}
-
-__device__ __forceinline__ long long warp_sum64(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ long long warp_scan64(long long v) {  // inclusive
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long w = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += w;
-  }
-  return v;
-}
-
-// Units of one head of the lane's sequence (n = 0: none).  A sequence of many
-// items is summed by the whole warp.
-__device__ __forceinline__ long long head_units(const Seq& q, int per_item, int window) {
-  const int lane = threadIdx.x & 31;
-  const int nqt = (q.n + per_item - 1) / per_item;
-  long long u = 0;
-  if (nqt <= 4)
-    for (int t = 0; t < nqt; ++t) u += kItemUnits + item_span(q, per_item, t, window).count;
-  unsigned big = __ballot_sync(0xffffffffu, nqt > 4);
-  while (big) {
-    const int src = __ffs(big) - 1;
-    big &= big - 1;
-    Seq s{};
-    s.n = __shfl_sync(0xffffffffu, q.n, src);
-    s.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
-    long long v = 0;
-    const int m = (s.n + per_item - 1) / per_item;
-    for (int t = lane; t < m; t += 32) v += kItemUnits + item_span(s, per_item, t, window).count;
-    v = warp_sum64(v);
-    if (lane == src) u = v;
-  }
-  return u;
-}
-
-// a / b and a % b of non-negative numbers, in 32 bits where they fit (a 64-bit division
-// is a long subroutine).
-__device__ __forceinline__ long long divide(long long a, long long b, long long& rest) {
-  if (((a | b) >> 32) == 0) {
-    const uint32_t q = (uint32_t)a / (uint32_t)b;
-    rest = (uint32_t)a - q * (uint32_t)b;
-    return q;
-  }
-  const long long q = a / b;
-  rest = a - q * b;
-  return q;
-}
-
-// The start of this CTA's share (all threads; ends with a barrier).  Each warp looks
-// at its stretch of the sequences, 32 at a time.
-__device__ void find_share(const TileArgs& t, Ctl& ctl) {
-  const BatchView& bv = t.a.b;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (int)(blockDim.x >> 5);
-  const int per_item = 2 * t.tpt, H = t.a.c.kv_heads, ps = t.a.c.page_size;
-  const int chunk = (bv.B + nw - 1) / nw;
-  const int b0 = min(bv.B, warp * chunk), b1 = min(bv.B, b0 + chunk);
-  Seq q{};
-  long long per_head = 0, sum = 0;
-  auto look = [&](int base) {
-    q = Seq{};
-    if (base + lane < b1) q = load_seq(bv, base + lane, ps);
-    per_head = head_units(q, per_item, t.a.window);
-  };
-  for (int base = b0; base < b1; base += 32) {
-    look(base);
-    sum += warp_sum64(per_head * H);
-    if (q.n > t.tpt) ctl.two = 1;
-  }
-  if (lane == 0) ctl.warp_units[warp] = sum;
-  if (threadIdx.x == 0) {
-    ctl.left = 0;
-    ctl.b = bv.B;
-    ctl.h = ctl.qt = ctl.off = 0;
-  }
-  __syncthreads();
-  // the units of the warps before this one, and of all
-  const long long mine = lane < nw ? ctl.warp_units[lane] : 0;
-  const long long total = warp_sum64(mine);
-  long long before = __shfl_sync(0xffffffffu, warp_scan64(mine) - mine, warp);
-  long long rest;
-  const long long share = max(1ll, divide(total + gridDim.x - 1, (long long)gridDim.x, rest));
-  const long long start = share * blockIdx.x;
-  if (start >= before && start < before + sum) {  // this warp's sequences hold the start
-    for (int base = b0; base < b1; base += 32) {
-      if (b1 - b0 > 32) look(base);  // (else they are still here)
-      const long long scan = warp_scan64(per_head * H);
-      const unsigned hit = __ballot_sync(0xffffffffu, start < before + scan);
-      if (!hit) {
-        before += __shfl_sync(0xffffffffu, scan, 31);
-        continue;
-      }
-      const int src = __ffs(hit) - 1;
-      Seq s{};
-      s.n = __shfl_sync(0xffffffffu, q.n, src);
-      s.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
-      const long long ph = __shfl_sync(0xffffffffu, per_head, src);
-      long long r = start - before - __shfl_sync(0xffffffffu, scan - per_head * H, src);
-      const int h = (int)divide(r, ph, r);
-      const int m = (s.n + per_item - 1) / per_item;
-      for (int q0 = 0; q0 < m; q0 += 32) {
-        const long long c =
-            q0 + lane < m ? kItemUnits + item_span(s, per_item, q0 + lane, t.a.window).count : 0;
-        const long long sc = warp_scan64(c);
-        const unsigned in = __ballot_sync(0xffffffffu, r < sc);
-        if (!in) {
-          r -= __shfl_sync(0xffffffffu, sc, 31);
-          continue;
-        }
-        const int l = __ffs(in) - 1;
-        const long long off = r - __shfl_sync(0xffffffffu, sc - c, l);
-        if (lane == 0) {
-          ctl.b = base + src;
-          ctl.h = h;
-          ctl.qt = q0 + l;
-          ctl.off = (int)off;
-          ctl.left = min(share, total - start);
-        }
-        break;
-      }
-      break;
-    }
-  }
-  if (threadIdx.x == 0) ctl.share = share;
-  __syncthreads();
-}
-
-// One CTA's part of one item.
-struct Seg {
-  int b, h;
-  int row0, ntok;    // first packed row, tokens
-  int pos;           // position of the first token
-  int lo, hi;
-  int t0, n;         // key tiles t0 .. t0+n-1
-  bool two;          // two row tiles
-  int slot;          // -1: the whole item; else the partial slot of the CTA (0, 1)
-  int more;          // slot 1: further CTAs with a part of it
-};
-
-struct Walk {
-  int b, h, qt, off, nqt;
-  long long left;
-  Seq q;
-  bool loaded;
-
-  __device__ __forceinline__ Walk(const Ctl& c)
-      : b(c.b), h(c.h), qt(c.qt), off(c.off), nqt(0), left(c.left), loaded(false) {}
-
-  __device__ __forceinline__ bool next(const TileArgs& t, const Ctl& ctl, Seg& s) {
-    if (left <= 0) return false;
-    const int per_item = 2 * t.tpt;
-    while (!loaded) {
-      if (b >= t.a.b.B) return false;
-      q = load_seq(t.a.b, b, t.a.c.page_size);
-      nqt = (q.n + per_item - 1) / per_item;
-      if (nqt) loaded = true;
-      else ++b;
-    }
-    const Span sp = item_span(q, per_item, qt, t.a.window);
-    // units off .. off + take of the item: its start, then a unit a tile
-    const int avail = sp.count + kItemUnits - off;
-    const int take = (int)min((long long)avail, left);
-    const int t0 = max(0, off - kItemUnits), t1 = off + take - kItemUnits;
-    left -= take;
-    if (t1 <= t0) return false;  // the share ends in front of the item's first tile
-    s.b = b;
-    s.h = h;
-    s.row0 = q.tok0 + qt * per_item;
-    s.ntok = min(per_item, q.n - qt * per_item);
-    s.pos = q.pos0 + qt * per_item;
-    s.lo = sp.lo;
-    s.hi = sp.hi;
-    s.t0 = sp.first + t0;
-    s.n = t1 - t0;
-    s.two = s.ntok > t.tpt;
-    s.slot = s.n == sp.count ? -1 : (t0 ? 0 : 1);
-    s.more = s.slot == 1 ? (int)((avail - take + ctl.share - 1) / ctl.share) : 0;
-    off = 0;
-    if (++qt == nqt) {
-      qt = 0;
-      if (++h == t.a.c.kv_heads) {
-        h = 0;
-        ++b;
-        loaded = false;
-      }
-    }
-    return true;
-  }
-};
-
 // Ring order of an item part's tiles: K0 K1 V0 K2 V1 ... V(n-1), as the products
 // need them when the next S is computed one product ahead.
 __device__ __forceinline__ int k_index(int i) { return i ? 2 * i - 1 : 0; }
@@ -382,19 +148,6 @@ __device__ __forceinline__ void tile_of(int idx, int n, bool& is_v, int& tile) {
   tile = is_v ? (idx == 2 * n - 1 ? n - 1 : idx / 2 - 1) : (idx + 1) / 2;
 }
 
-// Slot and phase of the k-th tile of a ring (k < 2^32 / 12).
-struct Slot {
-  uint32_t i, ph;
-  __device__ __forceinline__ Slot(uint32_t k, const Ring& r) {
-    const uint32_t turn = __umulhi(k, r.inv);
-    i = k - turn * r.n;
-    ph = turn & 1u;
-  }
-};
-
-// A value that is the same in all lanes, in a form that the compiler knows to be.
-__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(0xffffffffu, x); }
-
 // Keys of a tile that some row sees, in steps of 16 (a product's depth).
 __device__ __forceinline__ void key_steps(int lo, int hi, int tile, int& s0, int& s1) {
   const int key0 = tile * kTile;
@@ -402,37 +155,9 @@ __device__ __forceinline__ void key_steps(int lo, int hi, int tile, int& s0, int
   s1 = max(s0, (min(kTile, hi - key0) + 15) / 16);
 }
 
-// ---------------------------------------------------------------------------
-// Waits.
-// ---------------------------------------------------------------------------
 // Which wait gave up, in the CTA's err word, for whoever looks at the workspace after a timeout.
 enum WaitId { kWaitSlot = 1, kWaitQ, kWaitK, kWaitV, kWaitP, kWaitQFree, kWaitS, kWaitO, kWaitX, kWaitRaw,
               kWaitWide };
-
-// A whole warp.  All lanes test and go on together: one that went ahead could let
-// the barrier move a phase further before another tests it.
-struct Guard {
-  volatile int* flag;  // the CTA's abort flag
-  long long clocks;    // limit of a wait
-};
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Guard& guard, int id) {
-  for (int i = 0; i < 64; ++i)
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const long long t0 = clock64();
-  for (;;) {
-    for (int i = 0; i < 16; ++i)
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const bool late = clock64() - t0 >= guard.clocks;
-    if (__any_sync(0xffffffffu, late)) *guard.flag = id;
-    if (__any_sync(0xffffffffu, late || *guard.flag != 0)) return false;
-  }
-}
-// What must have ended before the CTA may go, whether or not the call is aborted.
-__device__ __forceinline__ void wait_end(uint64_t* bar, uint32_t parity, const Guard& guard) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity) && clock64() - t0 < guard.clocks) {
-  }
-}
 
 // ---------------------------------------------------------------------------
 // Softmax of one S tile row (this thread's), 128 scores in tensor memory.
@@ -542,19 +267,6 @@ __device__ __forceinline__ float sum16(const float* x) {
   for (int j = 0; j < 4; ++j)
     s[j] = fadd2(pack2(x[4 * j], x[4 * j + 1]), pack2(x[4 * j + 2], x[4 * j + 3]));
   return sum_of(s);
-}
-
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.0f ? -kInf : ((m == -kInf ? 0.0f : m) + log2f(l)) * kLn2;
-}
-
-template <int REGS>
-__device__ __forceinline__ void take_regs() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS>
-__device__ __forceinline__ void give_regs() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
 template <int DT, bool E4M3>
@@ -1107,55 +819,6 @@ k_attend_tiles(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
   if (threadIdx.x == 0) t.err[wid] = (ctl.abort ? kLate | ctl.abort << 8 : 0) | ctl.mend;
 }
 
-// ---------------------------------------------------------------------------
-// The join: items cut by a share's end, and the flags.
-// ---------------------------------------------------------------------------
-// One row from its parts (at most one per CTA).  The (m, l) of all parts are read at
-// once, a part per lane; the warp then adds up every `stride`-th part's O from `first`
-// on, 32 lanes by four columns.  Returns this lane's columns; M, L: of all parts.
-__device__ __forceinline__ float4 join_parts(const TileArgs& t, int c, int parts, int row, int first,
-                                             int stride, float& M, float& L) {
-  constexpr int kSets = (kMaxCtas + 31) / 32;
-  const int lane = threadIdx.x & 31, D = t.a.c.head_dim;
-  auto place = [&](int p) { return (int64_t)(p ? 2 * (c + p) : 2 * c + 1) * kMaxRows + row; };
-  float2 ml[kSets];
-  M = -kInf;
-#pragma unroll
-  for (int k = 0; k < kSets; ++k) {
-    ml[k] = make_float2(-kInf, 0.0f);
-    if (32 * k + lane < parts) ml[k] = __ldcg(t.ml + place(32 * k + lane));
-    M = fmaxf(M, ml[k].x);
-  }
-  M = warp_max(M);
-  if (M == -kInf) M = 0.0f;
-  L = 0.0f;
-  float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll
-  for (int k = 0; k < kSets; ++k) {
-    if (32 * k >= parts) break;
-    // (a part that sees nothing has l = 0, and its O was never written)
-    const float f = ml[k].y == 0.0f ? 0.0f : ex2(ml[k].x - M);
-    float l = ml[k].y == 0.0f ? 0.0f : f * ml[k].y;
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-    L += l;
-    const unsigned seen = __ballot_sync(0xffffffffu, ml[k].y != 0.0f);
-    const int last = min(32, parts - 32 * k);
-#pragma unroll 8
-    for (int q = first; q < last; q += stride) {
-      const float g = __shfl_sync(0xffffffffu, f, q);
-      if (((seen >> q) & 1u) && lane * 4 < D) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(t.part + place(32 * k + q) * D) + lane);
-        o.x += g * x.x;
-        o.y += g * x.y;
-        o.z += g * x.z;
-        o.w += g * x.w;
-      }
-    }
-  }
-  return o;
-}
-
 // The products of a tile weigh every value of it, and 0 times an infinity is NaN: a value
 // that is not finite reaches rows that do not see it.  So what is not finite in a row's
 // outputs is found again, one warp to the row, from the keys that it sees alone.  (Not
@@ -1212,127 +875,17 @@ __device__ __forceinline__ void mend_row(const AttendArgs& a, int t, int hq, flo
   *at = make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-template <int DT, bool E4M3>
-__global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ TileArgs t,
-                                                              int ctas, int join_blocks) {
-  constexpr int kWarps = kJoinThreads / 32;
-  __shared__ Rec rec[kMaxCtas];
-  __shared__ int rows_to[kMaxCtas];  // rows of records 0..c
-  __shared__ int warp_rows[kWarps];
-  __shared__ int most;
-  __shared__ float4 so[kWarps][32];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const AttendArgs& a = t.a;
-  if ((int)blockIdx.x >= join_blocks) {
-    const int b = ((int)blockIdx.x - join_blocks) * kWarps + warp;
-    if (b >= a.b.B) return;
-    bool late = false;
-    for (int c = lane; c < ctas; c += 32) late |= (__ldcg(t.err + c) & kLate) != 0;
-    late = __any_sync(0xffffffffu, late);
-    const uint8_t f = sequence_flags(a, b);
-    if (lane == 0) a.flags[b] = f | (late ? SV_FLAG_TIMEOUT : 0);
-    return;
+template <bool E4M3>
+struct JoinArgs : TileArgs {
+  template <int DT>
+  static __device__ __forceinline__ void mend(const AttendArgs& a, int t, int hq, float* sq) {
+    mend_row<DT, E4M3>(a, t, hq, sq);
   }
-  // records, and the rows before each (kMaxCtas <= kJoinThreads)
-  static_assert(kMaxCtas <= kJoinThreads, "one record per thread");
-  if (threadIdx.x == 0) most = 0;
-  __syncthreads();
-  int n = 0, err = 0;
-  if ((int)threadIdx.x < ctas) {
-    const Rec r = t.rec[threadIdx.x];
-    err = __ldcg(t.err + threadIdx.x);
-    rec[threadIdx.x] = r;
-    n = r.more ? r.ntok * t.group : 0;
-    if (r.more) atomicMax(&most, r.more);
-  }
-  int scan = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += v;
-  }
-  if (lane == 31) warp_rows[warp] = scan;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) scan += warp_rows[w];
-  if (threadIdx.x < kMaxCtas) rows_to[threadIdx.x] = scan;
-  __syncthreads();
-  const int total = rows_to[kMaxCtas - 1];
-  // few rows of many parts: a whole block to a row; else a warp to a row
-  const bool wide = most >= 8 && total <= 2 * join_blocks;
-  const int step = wide ? join_blocks : join_blocks * kWarps;
-  const int begin = wide ? (int)blockIdx.x : (int)blockIdx.x * kWarps + warp;
-  auto locate = [&](int j, int& c, int& tok, int& hd) {
-    c = 0;
-    for (int half = 128; half; half >>= 1)
-      if (c + half <= ctas && rows_to[c + half - 1] <= j) c += half;
-    const int k = j - (c ? rows_to[c - 1] : 0);
-    tok = k / t.group;
-    hd = k - tok * t.group;
-  };
-  bool odd = false;
-  for (int j = begin; j < total; j += step) {
-    int c, tok, hd;
-    locate(j, c, tok, hd);
-    const Rec r = rec[c];
-    const int row = tok / t.tpt * kTile + tok % t.tpt * t.group + hd;
-    const int parts = r.more + 1;
-    float M, L;
-    float4 o = join_parts(t, c, parts, row, wide ? warp : 0, wide ? kWarps : 1, M, L);
-    if (wide) {
-      __syncthreads();
-      so[warp][lane] = o;
-      __syncthreads();
-      if (warp) continue;
-      for (int w = 1; w < kWarps; ++w) {
-        const float4 x = so[w][lane];
-        o.x += x.x;
-        o.y += x.y;
-        o.z += x.z;
-        o.w += x.w;
-      }
-    }
-    const int64_t orow = (int64_t)(r.row0 + tok) * a.heads + r.h * t.group + hd;
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    const int D = a.c.head_dim;
-    if (lane * 4 < D) {
-      odd |= L == L && !(fabsf(o.x * inv + o.y * inv + o.z * inv + o.w * inv) < kInf);
-      const uint2 w = make_uint2(F16<DT>::down(o.x * inv, o.y * inv),
-                                 F16<DT>::down(o.z * inv, o.w * inv));
-      reinterpret_cast<uint2*>(a.out + orow * D * 2)[lane] = w;
-    }
-    if (lane == 0 && a.lse) a.lse[orow] = lse_of(M, L);
-  }
-  if (!__syncthreads_or(odd || (err & kMend))) return;
-  // rare: the rows joined here, and those that the tile kernel wrote itself
-  float* sq = reinterpret_cast<float*>(so[warp]);
-  if (!wide || !warp)
-    for (int j = begin; j < total; j += step) {
-      int c, tok, hd;
-      locate(j, c, tok, hd);
-      mend_row<DT, E4M3>(a, rec[c].row0 + tok, rec[c].h * t.group + hd, sq);
-    }
-  if (!__syncthreads_or(err & kMend)) return;
-  const int64_t rows = (int64_t)a.b.total * a.heads;
-  for (int64_t j = (int64_t)blockIdx.x * kWarps + warp; j < rows; j += (int64_t)join_blocks * kWarps) {
-    const int tok = (int)(j / a.heads), hq = (int)(j - (int64_t)tok * a.heads);
-    bool cut = false;
-    for (int c = lane; c < ctas; c += 32)
-      cut |= rec[c].more && rec[c].h == hq / t.group && tok >= rec[c].row0 &&
-             tok - rec[c].row0 < rec[c].ntok;
-    if (!__any_sync(0xffffffffu, cut)) mend_row<DT, E4M3>(a, tok, hq, sq);
-  }
-}
+};
 
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 std::mutex g_mu;
 EncodeTiled g_encode = nullptr;
 int g_sms[64] = {};
@@ -1344,12 +897,8 @@ cudaError_t device_ready(int* sms) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q);
-    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-    g_encode = reinterpret_cast<EncodeTiled>(fn);
+    e = tensor_encoder(&g_encode);
+    if (e != cudaSuccess) return e;
   }
   if (!g_sms[dev]) {
     const struct {
@@ -1410,11 +959,6 @@ bool encode_queries(CUtensorMap* map, const AttendArgs& a, int dim, int group, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-Ring make_ring(int n, int most) {
-  const uint32_t k = (uint32_t)(n < most ? n : most);
-  return Ring{k, (uint32_t)((0x100000000ull + k - 1) / k)};
-}
-
 constexpr size_t kRecBytes = 4096, kMlBytes = sizeof(float2) * 2 * kMaxCtas * kMaxRows;
 static_assert(kMaxCtas * (sizeof(Rec) + sizeof(int)) <= kRecBytes, "records");
 
@@ -1424,6 +968,8 @@ void set_attention_stall(int cta, long long clocks) {
   g_stall_cta = cta;
   g_wait_clocks = clocks > 0 ? clocks : kWaitClocks;
 }
+
+AttentionTest attention_test() { return AttentionTest{g_stall_cta, g_wait_clocks}; }
 
 size_t attention_tiles_workspace(int head_dim) {
   return kRecBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * (size_t)head_dim;
@@ -1491,10 +1037,13 @@ cudaError_t launch_attention_tiles(const AttendArgs& a, int dtype, bool e4m3, cu
   const int most = (e4m3 ? 2 : 6) * ctas;
   const int join_blocks = (int)(rows < most ? rows : most);
   const int flag_blocks = a.flags ? (a.b.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
-  auto* j = dtype == SV_BF16 ? (e4m3 ? k_attend_join<SV_BF16, true> : k_attend_join<SV_BF16, false>)
-                             : (e4m3 ? k_attend_join<SV_F16, true> : k_attend_join<SV_F16, false>);
-  return launch_pdl(j, dim3(join_blocks + flag_blocks), dim3(kJoinThreads), 0, stream, t, ctas,
-                    join_blocks);
+  auto join = [&](auto args) {
+    auto* j = dtype == SV_BF16 ? k_attend_join<decltype(args), SV_BF16, true>
+                               : k_attend_join<decltype(args), SV_F16, true>;
+    return launch_pdl(j, dim3(join_blocks + flag_blocks), dim3(kJoinThreads), 0, stream, args, ctas,
+                      join_blocks);
+  };
+  return e4m3 ? join(JoinArgs<true>{t}) : join(JoinArgs<false>{t});
 }
 
 }  // namespace sv
