@@ -18,9 +18,9 @@
 //
 // Work: items of one row tile, cut into equal shares of key tiles (sv_attention_line.cuh).
 //
-// Roles of the 20 warps: 0 fetches pages (tensor copies; steps and zeros by bulk copies), 1
-// issues the products, 2 and 3 convert queries, 4-7 and 8-11 spread K's and V's codes, 12-19
-// are two softmax groups of half the columns each.  A softmax thread has one key and N/2
+// Roles of the 16 or 20 warps: 0 fetches pages (tensor copies; steps and zeros by bulk
+// copies), 1 issues the products, 2 and 3 convert queries, then four or eight spread K's and
+// V's codes, and eight are two softmax groups of half the columns each.  A softmax thread has one key and N/2
 // rows.  The running maxima are columns: they are looked at again only when some score
 // passes one by kLag (a vote of the group's threads), so a tile needs no reduction across
 // lanes, and the sums stay per thread to the item's end.
@@ -50,16 +50,22 @@ constexpr int kMaxN = 80;              // 3 N columns beside 256 of operands in 
 constexpr int kMaxStages = 12;
 constexpr int kSpan = 16384;           // 128 rows of a 128-byte swizzle span
 constexpr size_t kSmemBytes = 227 * 1024;
-constexpr int kThreads = 640;
-// Registers of a thread at launch, and then by role (the roles' sum must not pass what the
-// launch gave, or the takers would wait forever).
-constexpr int kRegs = 96, kHelpRegs = 64, kSoftRegs = 144;
-static_assert(384 * kHelpRegs + 256 * kSoftRegs <= kThreads * kRegs, "registers");
-// A maximum may lag by this many powers of two, and a weight p s is at most 2^(kLag + kUp)
-// = 2^15 in fp16, s relative to the largest step seen: weights keep all their bits down to
-// 2^-27 of that, and some to 2^-37.
-constexpr float kLag = 2.0f;
-constexpr float kUp = 8192.0f;
+// By N: groups of four warps that spread codes, threads, and the registers of a thread at
+// launch and then by role (the roles' sum must not pass what the launch gave, or the takers
+// would wait forever).
+template <int N>
+struct Shape {
+  static constexpr int kSpread = N <= 32 ? 2 : 1;
+  static constexpr int kWarps = 4 + 4 * kSpread + 8, kThreads = 32 * kWarps;
+  static constexpr int kRegs = kSpread == 2 ? 96 : 128;
+  static constexpr int kHelpRegs = 64, kSoftRegs = kSpread == 2 ? 144 : 192;
+  static_assert((kThreads - 256) * kHelpRegs + 256 * kSoftRegs <= kThreads * kRegs, "registers");
+};
+// A maximum may lag by this many powers of two, and a weight p s is at most 2^kLag kUp = 2^15
+// in fp16, s relative to the largest step seen: weights keep all their bits down to 2^-23
+// of that, and some to 2^-33.
+constexpr float kLag = 6.0f;
+constexpr float kUp = 512.0f;
 // Queries times 2^kQShift (and 2^-4 of that where the code sits four bits higher): rows with
 // a largest value within [2^-4, 2^9) fit fp16 so, to the last bit of all that matters (what
 // is below 2^-19 is rounded to 2^-27).  Other rows get a factor of their own.
@@ -91,7 +97,7 @@ struct Ctl {
   int two;             // (find_share's; not used)
   int b, h, qt, off;   // start of the CTA's share (off in units)
   long long left, share;
-  long long warp_units[kThreads / 32];
+  long long warp_units[Shape<16>::kWarps];
   float qsum[2][kMaxN], qfac[2][kMaxN];  // of each query row: sum, factor back to kQShift
   int odd[2][2];                         // a row (of a converting warp) has a factor of its own
   // by softmax group:
@@ -141,11 +147,6 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float warp_max_of(float v) {  // NaNs are passed over
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
 // The 128 threads of a softmax group.
 __device__ __forceinline__ void group_sync(int id) {
   asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
@@ -179,24 +180,25 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t* r) {
 enum WaitId { kWaitSlot = 1, kWaitQ, kWaitK, kWaitV, kWaitP, kWaitQFree, kWaitS, kWaitO, kWaitCodes,
               kWaitFree };
 
-// Sums over a warp's lanes of C values (a multiple of 8) each: lane l ends with those of
-// C / 8 columns from first_column(l) on.
-template <int C>
-__device__ __forceinline__ void sum_columns(float (&v)[C]) {
+// Sums (or largest, NaNs passed over) over a warp's lanes of C values (a multiple of 8)
+// each: lane l ends with those of C / 8 columns from first_column(l) on, in v[0..].
+template <int C, bool MAX>
+__device__ __forceinline__ void over_lanes(float (&v)[C]) {
   const int lane = threadIdx.x & 31;
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
 #pragma unroll
   for (int o = 16, n = C / 2; o >= 4; o >>= 1, n >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const float keep = up ? v[n + i] : v[i], send = up ? v[i] : v[n + i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
 #pragma unroll
   for (int o = 2; o; o >>= 1)
 #pragma unroll
-    for (int i = 0; i < C / 8; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int i = 0; i < C / 8; ++i) v[i] = join(v[i], __shfl_xor_sync(0xffffffffu, v[i], o));
 }
 template <int C>
 __device__ __forceinline__ int first_column(int lane) {
@@ -209,11 +211,12 @@ __device__ __forceinline__ void set_m(float4* qm, int n, float neg_m) {
 }
 
 template <int DT, int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<N>::kThreads, 1)
     k_attend_u4(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                 const __grid_constant__ U4Args t) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int C = N / 2;                            // rows of a softmax group
+  constexpr int kSpread = Shape<N>::kSpread, kSoft = 4 + 4 * kSpread;  // first softmax warp
   constexpr int kPBytes = N > 64 ? 2 * kSpan : kSpan;
   constexpr uint32_t kColV = 128, kColS = 256, kColO = 256 + 2 * N;  // tensor memory
   const AttendArgs& a = t.a;
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl.abort = (smem_u32(smem) & 1023u) ? 1 : 0;  // the swizzles need this alignment
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(ctl.full + i, 1);
-      mbar_init(ctl.empty + i, 16);
+      mbar_init(ctl.empty + i, 4 * kSpread + 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(ctl.qfull + i, 2);
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk walk(ctl);
   Seg s;
   bool ok = *guard.flag == 0;
-  if (warp < 12) give_regs<kHelpRegs>();
+  if (warp < kSoft) give_regs<Shape<N>::kHelpRegs>();
 
   if (warp == 0) {
     // ---------------- fetch key and value pages ----------------
@@ -436,22 +439,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ctl.qfull + qb);
     }
-  } else if (warp < 12) {
+  } else if (warp < kSoft) {
     // ---------------- spread codes ----------------
-    const bool is_v = warp >= 8;
+    // One group of four warps for K and one for V, or one for both.
     const int quad = warp & 3, row = 32 * quad + lane;
+    const bool does_k = kSpread == 1 || warp < 8, does_v = kSpread == 1 || warp >= 8;
     const uint32_t lanes = tbase + ((uint32_t)(32 * quad) << 16);
     uint32_t j = 0;
     while (ok && walk.next(t, ctl, s)) {
       for (int i = 0; i < s.n; ++i, ++j) {
         const Slot at(j, t.ring);
         const uint32_t b = j & 1u, ph = (j >> 1) & 1u;
-        ok = wait_warp(ctl.full + at.i, at.ph, guard, kWaitCodes) &&
-             wait_warp((is_v ? ctl.pfree : ctl.kfree) + b, ph ^ 1u, guard, kWaitFree);
-        if (!ok) break;
-        tc_fence_after();
         const uint8_t* const codes = ring + (size_t)at.i * t.stage_bytes;
-        if (!is_v) {
+        ok = wait_warp(ctl.full + at.i, at.ph, guard, kWaitCodes);
+        if (!ok) break;
+        if (does_k) {
+          ok = wait_warp(ctl.kfree + b, ph ^ 1u, guard, kWaitFree);
+          if (!ok) break;
+          tc_fence_after();
           // a key to a lane: pairs (i, i + 4) of each eight dimensions
 #pragma unroll 2
           for (int ch = 0; ch < D / 32; ++ch) {
@@ -463,45 +468,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             spread(x.w, r + 12);
             tmem_st16(lanes + b * 64 + 16 * ch, r);
           }
-        } else if (32 * quad < D) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ctl.kfull + b);
+        }
+        if (does_v) {
+          ok = wait_warp(ctl.pfree + b, ph ^ 1u, guard, kWaitFree);
+          if (!ok) break;
+          tc_fence_after();
           // a dimension to a lane, pairs of tokens: lane 8i + c of the warp's 32 takes
           // dimension 4c + i of its 32
-          const uint32_t base = smem_u32(codes + code_bytes);
+          if (32 * quad < D) {
+            const uint32_t base = smem_u32(codes + code_bytes);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t lo[16], hi[16];
+            for (int half = 0; half < 2; ++half) {
+              uint32_t lo[16], hi[16];
 #pragma unroll
-            for (int m4 = 0; m4 < 2; ++m4) {
-              const int token = 64 * half + 32 * m4 + lane;
-              uint32_t x[4];
-              ld_transposed4(base + token * (D / 2) + 16 * code_chunk(D, token, quad), x);
+              for (int m4 = 0; m4 < 2; ++m4) {
+                const int token = 64 * half + 32 * m4 + lane;
+                uint32_t x[4];
+                ld_transposed4(base + token * (D / 2) + 16 * code_chunk(D, token, quad), x);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t r[4];
-                spread(x[e], r);
-                lo[8 * m4 + 2 * e] = r[0];
-                lo[8 * m4 + 2 * e + 1] = r[1];
-                hi[8 * m4 + 2 * e] = r[2];
-                hi[8 * m4 + 2 * e + 1] = r[3];
+                for (int e = 0; e < 4; ++e) {
+                  uint32_t r[4];
+                  spread(x[e], r);
+                  lo[8 * m4 + 2 * e] = r[0];
+                  lo[8 * m4 + 2 * e + 1] = r[1];
+                  hi[8 * m4 + 2 * e] = r[2];
+                  hi[8 * m4 + 2 * e + 1] = r[3];
+                }
               }
+              tmem_st_rows8(lanes + kColV + b * 64 + 32 * half, lo);
+              tmem_st_rows8(lanes + (16u << 16) + kColV + b * 64 + 32 * half, hi);
             }
-            tmem_st_rows8(lanes + kColV + b * 64 + 32 * half, lo);
-            tmem_st_rows8(lanes + (16u << 16) + kColV + b * 64 + 32 * half, hi);
+            tmem_wait_st();
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ctl.vfull + b);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive((is_v ? ctl.vfull : ctl.kfull) + b);
-          mbar_arrive(ctl.empty + at.i);
-        }
+        if (lane == 0) mbar_arrive(ctl.empty + at.i);
       }
     }
   } else {
     // ---------------- softmax and output ----------------
-    take_regs<kSoftRegs>();
-    const int wg = (warp - 12) >> 2, quad = warp & 3, row = 32 * quad + lane, id = 1 + wg;
+    take_regs<Shape<N>::kSoftRegs>();
+    const int wg = (warp - kSoft) >> 2, quad = warp & 3, row = 32 * quad + lane, id = 1 + wg;
     const int tid = row;                          // of the group's 128
     const uint32_t lanes = tbase + ((uint32_t)(32 * quad) << 16);
     const uint32_t o_tm = lanes + kColO + wg * C;
@@ -527,8 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Slot at(g, t.ring);
         const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
         const uint32_t s_tm = lanes + kColS + b * N + wg * C;
+        // S is there, so the tile's steps and zeros are too, and O's product of two tiles ago
+        // is done (it was issued before this S): P's place is free
+        if (ok) ok = wait_warp(ctl.sfull + b, ph, guard, kWaitS);
+        tc_fence_after();
         // the key's step and zero, and the rows that see it: [first, first + span) of the group's
-        if (ok) ok = wait_warp(ctl.full + at.i, at.ph, guard, kWaitCodes);
         const uint32_t* const words =
             reinterpret_cast<const uint32_t*>(ring + (size_t)at.i * t.stage_bytes + 2 * code_bytes);
         uint32_t ksz = words[row], vsz = words[kTile + row];
@@ -551,8 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool masked = edge && __any_sync(0xffffffffu, span < C);
         const float A = step_of(ksz) * c18, B = zero_of(ksz) * t.c;
         const float step = step_of(vsz), zero = zero_of(vsz);
-        if (ok) ok = wait_warp(ctl.sfull + b, ph, guard, kWaitS);
-        tc_fence_after();
         uint32_t r[C];
         auto load = [&]() {
 #pragma unroll
@@ -591,24 +605,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           // some maximum rises, or the largest step
           load();
           const uint64_t A2 = pack2(A, A), B2 = pack2(B, B);
-          float mine[(C + 31) / 32];
+          float v[C];
 #pragma unroll
           for (int n = 0; n < C; n += 2) {
             const float4 k = qm[n >> 1];
-            float x, y;
             unpack2(ffma2(pack2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), A2,
-                          fmul2(pack2(k.x, k.y), B2)), x, y);
-            if ((unsigned)(n - first) >= (unsigned)span) x = -kInf;
-            if ((unsigned)(n + 1 - first) >= (unsigned)span) y = -kInf;
-            x = warp_max_of(x);
-            y = warp_max_of(y);
-            if (lane == (n & 31)) mine[n >> 5] = x;
-            if (lane == (n & 31) + 1) mine[n >> 5] = y;
+                          fmul2(pack2(k.x, k.y), B2)), v[n], v[n + 1]);
+            if ((unsigned)(n - first) >= (unsigned)span) v[n] = -kInf;
+            if ((unsigned)(n + 1 - first) >= (unsigned)span) v[n + 1] = -kInf;
           }
+          over_lanes<C, true>(v);
+          if ((lane & 3) == 0)
 #pragma unroll
-          for (int u = 0; u < C; u += 32)
-            if (u + lane < C) ctl.wmax[wg][quad][u + lane] = mine[u >> 5];
-          const float ws = warp_max_of(step < kInf ? step : 0.0f);
+            for (int n = 0; n < C / 8; ++n) ctl.wmax[wg][quad][first_column<C>(lane) + n] = v[n];
+          const float ws = warp_max(step < kInf ? step : 0.0f);
           if (lane == 0) ctl.wstep[wg][quad] = ws;
           group_sync(id);
           if (tid < C) {
@@ -640,11 +650,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int u = 0; u < C; u += 8) {
               uint32_t o[8];
+              float f[8];
+              bool still = true;
+#pragma unroll
+              for (int n = 0; n < 8; ++n) {
+                f[n] = ctl.fac[wg][u + n] * fe;
+                still = still && f[n] == 1.0f;
+              }
+              if (still) continue;  // (the same for all threads)
               tmem_ld8_async(o_tm + u, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int n = 0; n < 8; ++n)
-                o[n] = __float_as_uint(__uint_as_float(o[n]) * (ctl.fac[wg][u + n] * fe));
+              for (int n = 0; n < 8; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n]);
               tmem_st8(o_tm + u, o);
             }
             tmem_wait_st();
@@ -656,10 +673,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           load();
           exponents();
         }
-        // weights; P's place was freed two tiles ago
-        if (ok) ok = wait_warp(ctl.pfree + b, ph ^ 1u, guard, kWaitFree);
-        const float up = step * inv_e * kUp;
-        const uint64_t up2 = pack2(up, up), zero2 = pack2(zero, zero);
+        // weights.  A value row that is not finite weighs nothing here (0 times it would not
+        // be 0 where it is not seen); the rows that do see it get their NaN below
+        const bool bad = !(step < kInf && fabsf(zero) < kInf);
+        const float up = bad ? 0.0f : step * inv_e * kUp, zero_in = bad ? 0.0f : zero;
+        const uint64_t up2 = pack2(up, up), zero2 = pack2(zero_in, zero_in);
         uint8_t* const prow = pbuf + b * kPBytes + row * 128;
 #pragma unroll
         for (int u = 0; u < C; u += 8) {
@@ -669,25 +687,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = u + e;
             const uint64_t p = pack2(ex2(__uint_as_float(r[n])), ex2(__uint_as_float(r[n + 1])));
             l2[n / 2] = fadd2(l2[n / 2], p);
+            z2[n / 2] = ffma2(p, zero2, z2[n / 2]);
             float x, y;
-            if (!masked) {
-              z2[n / 2] = ffma2(p, zero2, z2[n / 2]);
-              unpack2(fmul2(p, up2), x, y);
-            } else {
-              // (0 times a step or zero that is NaN is not 0)
-              const bool v0 = (unsigned)(n - first) < (unsigned)span;
-              const bool v1 = (unsigned)(n + 1 - first) < (unsigned)span;
-              unpack2(fmul2(p, zero2), x, y);
-              z2[n / 2] = fadd2(z2[n / 2], pack2(v0 ? x : 0.0f, v1 ? y : 0.0f));
-              unpack2(fmul2(p, up2), x, y);
-              x = v0 ? x : 0.0f;
-              y = v1 ? y : 0.0f;
-            }
+            unpack2(fmul2(p, up2), x, y);
             w[e / 2] = F16<SV_F16>::down(x, y);
           }
           const int ch = (n0 + u) >> 3;
           *reinterpret_cast<uint4*>(prow + (ch >> 3) * kSpan + (((ch & 7) ^ (row & 7)) << 4)) =
               make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (__any_sync(0xffffffffu, bad)) {
+          const float nan = bad ? __int_as_float(0x7fffffff) : 0.0f;
+#pragma unroll
+          for (int n = 0; n < C; n += 2)
+            z2[n / 2] = fadd2(z2[n / 2], pack2((unsigned)(n - first) < (unsigned)span ? nan : 0.0f,
+                                               (unsigned)(n + 1 - first) < (unsigned)span ? nan : 0.0f));
         }
         fence_proxy_async();
         tc_fence_before();
@@ -702,14 +716,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[C];
 #pragma unroll
         for (int n = 0; n < C; n += 2) unpack2(l2[n / 2], v[n], v[n + 1]);
-        sum_columns<C>(v);
+        over_lanes<C, false>(v);
         const int col = first_column<C>(lane);
         if ((lane & 3) == 0)
 #pragma unroll
           for (int n = 0; n < C / 8; ++n) ctl.lz[wg][quad][col + n].x = v[n];
 #pragma unroll
         for (int n = 0; n < C; n += 2) unpack2(z2[n / 2], v[n], v[n + 1]);
-        sum_columns<C>(v);
+        over_lanes<C, false>(v);
         if ((lane & 3) == 0)
 #pragma unroll
           for (int n = 0; n < C / 8; ++n) ctl.lz[wg][quad][col + n].y = v[n];
@@ -795,6 +809,8 @@ EncodeTiled g_encode = nullptr;
 int g_sms[64] = {};
 
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const U4Args);
+int threads_of(int n) { return n <= 32 ? Shape<16>::kThreads : Shape<80>::kThreads; }
+int regs_of(int n) { return n <= 32 ? Shape<16>::kRegs : Shape<80>::kRegs; }
 template <int DT>
 Kernel kernel_of(int n) {
   switch (n) {
@@ -822,7 +838,7 @@ cudaError_t device_ready(int* sms) {
         cudaFuncAttributes attr{};
         e = cudaFuncGetAttributes(&attr, (const void*)k);
         if (e != cudaSuccess) return e;
-        if (attr.numRegs < kRegs) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
+        if (attr.numRegs < regs_of(n)) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
         e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return e;
       }
@@ -899,8 +915,8 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   *taken = encode_codes(&mk, c, c.k, t.box) && encode_codes(&mv, c, c.v, t.box);
   if (!*taken) return cudaSuccess;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  e = launch_pdl(dtype == SV_BF16 ? kernel_of<SV_BF16>(N) : kernel_of<SV_F16>(N), dim3(ctas), dim3(kThreads),
-                 kSmemBytes, stream, mk, mv, t);
+  e = launch_pdl(dtype == SV_BF16 ? kernel_of<SV_BF16>(N) : kernel_of<SV_F16>(N), dim3(ctas),
+                 dim3(threads_of(N)), kSmemBytes, stream, mk, mv, t);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.b.total * a.heads;
   const int join_blocks = (int)(rows < 6 * ctas ? rows : 6 * ctas);

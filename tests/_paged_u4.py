@@ -108,9 +108,10 @@ class CaseU4(Case):
                     ~seen[:, None, None], 0.0).amax(-1) * abs(scale)
                 mass = torch.einsum("nhgl,lhd->nhgd", p,
                                     self.c["v"][b].double() * vs[..., :1] + vs[..., 1:].abs())
-                # a weight p s is a 16-bit float relative to the largest step: what is below half
-                # of 2^-37 of that is lost
-                lost = L * 15 * vs[..., 0].amax(0)[None, :, None, None] * 2.0 ** -38
+                # a weight p s enters the product as an fp16 number of 2^9 p s / E, E the largest
+                # step rounded up to a power of two: half a step of the smallest, 2^-25, is
+                # 2^-34 E, at most 2^-33 of the largest step, times a code of up to 15
+                lost = L * 15 * vs[..., 0].amax(0)[None, :, None, None] * 2.0 ** -33
             else:
                 big, mass, lost = torch.zeros_like(lse), torch.zeros_like(o), 0.0
             delta = ((self.D + 8) * big + 8) * 2.0 ** -23
