@@ -300,6 +300,18 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
     if (__any_sync(0xffffffffu, late || *guard.flag != 0)) return false;
   }
 }
+// The same in a shorter form, for a kernel of many roles (a try holds the warp for some 8000
+// clocks before it gives up, so the loop goes round rarely).
+__device__ __forceinline__ bool wait_held(uint64_t* bar, uint32_t parity, const Guard& guard, int id) {
+  if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), true)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const bool late = clock64() - t0 >= guard.clocks;
+    if (__any_sync(0xffffffffu, late)) *guard.flag = id;
+    if (__any_sync(0xffffffffu, late || *guard.flag != 0)) return false;
+  }
+}
 // What must have ended before the CTA may go, whether or not the call is aborted.
 __device__ __forceinline__ void wait_end(uint64_t* bar, uint32_t parity, const Guard& guard) {
   const long long t0 = clock64();

@@ -18,16 +18,14 @@
 //
 // Work: items of one row tile, cut into equal shares of key tiles (sv_attention_line.cuh).
 //
-// Roles of the 16 or 20 warps: 0 fetches pages (tensor copies; steps and zeros by bulk
-// copies), 1 issues the products, 2 and 3 convert queries, then four or eight spread K's and
-// V's codes, and eight are two softmax groups of half the columns each.  A softmax thread has one key and N/2
+// Roles of the 20 warps: 0 finds the items and fetches their pages, 1 and 3 issue the
+// products S and O, 2 converts queries, 4-7 and 8-11 spread K's and V's codes, 12-19 are two
+// softmax groups.  A softmax thread has one key and N/2
 // rows.  The running maxima are columns: they are looked at again only when some score
 // passes one by kLag (a vote of the group's threads), so a tile needs no reduction across
 // lanes, and the sums stay per thread to the item's end.
 //
-// Every wait is bounded; one that gives up ends the CTA's roles and flags the call.  The
-// softmax warps, which meet at barriers of their own, then go through their tiles without
-// waiting for anything.
+// Every wait is bounded; one that gives up ends the CTA's roles and flags the call.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -47,19 +45,16 @@ namespace sv {
 namespace {
 
 constexpr int kMaxN = 80;              // 3 N columns beside 256 of operands in tensor memory
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 6;  // of two key tiles
 constexpr int kSpan = 16384;           // 128 rows of a 128-byte swizzle span
 constexpr size_t kSmemBytes = 227 * 1024;
-// By N: groups of four warps that spread codes, threads, and the registers of a thread at
-// launch and then by role (the roles' sum must not pass what the launch gave, or the takers
-// would wait forever).
+// Registers of a thread at launch, and then by role (the roles' sum must not pass what the
+// launch gave, or the takers would wait forever).
+constexpr int kThreads = 640, kSoft = 12;  // first softmax warp
 template <int N>
-struct Shape {
-  static constexpr int kSpread = N <= 32 ? 2 : 1;
-  static constexpr int kWarps = 4 + 4 * kSpread + 8, kThreads = 32 * kWarps;
-  static constexpr int kRegs = kSpread == 2 ? 96 : 128;
-  static constexpr int kHelpRegs = 64, kSoftRegs = kSpread == 2 ? 144 : 192;
-  static_assert((kThreads - 256) * kHelpRegs + 256 * kSoftRegs <= kThreads * kRegs, "registers");
+struct Regs {
+  static constexpr int kLaunch = 96, kHelp = N <= 64 ? 64 : 48, kSoft = N <= 64 ? 144 : 168;
+  static_assert((kThreads - 256) * kHelp + 256 * kSoft <= kThreads * kLaunch, "registers");
 };
 // A maximum may lag by this many powers of two, and a weight p s is at most 2^kLag kUp = 2^15
 // in fp16, s relative to the largest step seen: weights keep all their bits down to 2^-23
@@ -75,6 +70,7 @@ struct U4Args {
   static constexpr int kItemUnits = 3, kRowTiles = 1, kSlotRows = kMaxN;
   AttendArgs a;
   int group, tpt;      // query heads per key head; tokens per row tile
+  uint32_t group_inv;  // ceil(2^16 / group): row n of an item is of token n group_inv >> 16
   int box;             // tokens per copy: min(page_size, 128)
   int spans;           // of 64 dimensions, of a query row: 1 or 2
   Ring ring;
@@ -90,23 +86,29 @@ struct U4Args {
 
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t qfull[2], qempty[2], kfull[2], kfree[2], vfull[2], sfull[2], pfull[2], pfree[2];
-  uint64_t ofull, oempty, fin;
+  uint64_t qfull[2], qempty[2], kfull[2], kfree[2], sfull[2], sfree[2], pvfull[2], pvfree[2];
+  uint64_t ofull, oempty, fin[2], segfull[4], segempty[4];
   uint32_t tmem;
   int abort;
   int two;             // (find_share's; not used)
   int b, h, qt, off;   // start of the CTA's share (off in units)
   long long left, share;
-  long long warp_units[Shape<16>::kWarps];
-  float qsum[2][kMaxN], qfac[2][kMaxN];  // of each query row: sum, factor back to kQShift
-  int odd[2][2];                         // a row (of a converting warp) has a factor of its own
-  // by softmax group:
-  float4 qm[2][kMaxN / 4];               // of two rows: sums, -m
-  float m[2][kMaxN / 2];
+  long long warp_units[kThreads / 32];
+  float qfac[2][kMaxN];                  // of each query row: factor back to kQShift
+  int odd[2];                            // some row has a factor of its own
+  Seg seg[4];                            // the items, as warp 0 finds them (n = 0: no more)
+  Walk walk;                             // where it is (no registers between items)
+  float2 kv[4][kTile];                   // by tile: a key's factor of the product; V's step and zero
+  // by softmax group (of kMaxN / 2 rows, or of all where the groups take tiles in turn):
+  float m[2][kMaxN / 2];                 // maxima (-inf: nothing seen yet)
+  float2 mv[2][2][kMaxN / 2];            // by S buffer: the m in its product; that of before less m
   float fac[2][kMaxN / 2];               // of a rise: old over new weights
   float wmax[2][4][kMaxN / 2], wstep[2][4];
+  int rose[2];                           // some maximum rose; some row has seen nothing yet
+  int unset[2];
   float2 lz[2][4][kMaxN / 2];            // sums of a warp's keys
-  float2 fin_lz[2][kMaxN / 2];           // factor of O, what is added
+  float4 ends[2][kMaxN / 2];              // a group's m, l, Z, E
+  float4 out[kMaxN];                     // of a row: factors of the two O, what is added
 };
 
 // ---------------------------------------------------------------------------
@@ -125,14 +127,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 // 16 lanes: registers 2j and 2j+1 of thread t go to lanes t/4 and t/4 + 8, column 4j + t%4.
-__device__ __forceinline__ void tmem_st_rows8(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(taddr)
-      : "memory");
+__device__ __forceinline__ void tmem_st_rows4(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
 }
 // Four 8 x 8 matrices of 16-bit entries, transposed: thread t gets entries t/4 of rows
 // 2(t%4) and 2(t%4)+1 of each; lane l gives the address of row l%8 of matrix l/8.
@@ -147,19 +145,39 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// The 128 threads of a softmax group.
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaNs are passed over
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// The 128 threads of a softmax group (or the 256 of both).
 __device__ __forceinline__ void group_sync(int id) {
   asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
+template <int THREADS = 128>
 __device__ __forceinline__ bool group_any(int id, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(x ? 1u : 0u), "r"(id)
+      : "r"(x ? 1u : 0u), "r"(id), "n"(THREADS)
       : "memory");
   return r != 0;
+}
+// 16 bytes into shared memory (zeros if not `real`), and this thread's arrival at a barrier
+// once all its copies before it have landed.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"(__cvta_generic_to_global(src)), "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_when_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
@@ -177,21 +195,49 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t* r) {
   r[3] = v & 0x00F000F0u;
 }
 
-enum WaitId { kWaitSlot = 1, kWaitQ, kWaitK, kWaitV, kWaitP, kWaitQFree, kWaitS, kWaitO, kWaitCodes,
+// A key's row of codes into tensor memory (this thread's lane).
+__device__ __forceinline__ void spread_row(const uint8_t* from, int D, int row, bool drop, uint32_t to) {
+  const int swizzled = code_chunk(D, row, 0);
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint4 x = *reinterpret_cast<const uint4*>(from + 16 * (c ^ swizzled));
+    if (drop) x = make_uint4(0, 0, 0, 0);
+    uint32_t r[16];
+    spread(x.x, r);
+    spread(x.y, r + 4);
+    spread(x.z, r + 8);
+    spread(x.w, r + 12);
+    tmem_st16(to + 16 * c, r);
+  }
+}
+
+// (code for what is rare goes out of the way: the warps' eight pieces of code share instruction
+// caches that do not hold them all)
+__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, false); }
+
+enum WaitId { kWaitItem = 12, kWaitSlot = 1, kWaitQ, kWaitK, kWaitV, kWaitP, kWaitQFree, kWaitS, kWaitO, kWaitCodes,
               kWaitFree };
 
 // Sums (or largest, NaNs passed over) over a warp's lanes of C values (a multiple of 8)
 // each: lane l ends with those of C / 8 columns from first_column(l) on, in v[0..].
-template <int C, bool MAX>
-__device__ __forceinline__ void over_lanes(float (&v)[C]) {
+template <int C, bool MAX, class T>
+__device__ __forceinline__ void over_lanes(T (&v)[C]) {
+  static_assert(sizeof(T) == 4, "floats, or their bits");
   const int lane = threadIdx.x & 31;
-  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+  auto join = [](T a, T b) -> T {
+    float x, y;
+    memcpy(&x, &a, 4);
+    memcpy(&y, &b, 4);
+    x = MAX ? fmaxf(x, y) : x + y;
+    memcpy(&a, &x, 4);
+    return a;
+  };
 #pragma unroll
   for (int o = 16, n = C / 2; o >= 4; o >>= 1, n >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-      const float keep = up ? v[n + i] : v[i], send = up ? v[i] : v[n + i];
+      const T keep = up ? v[n + i] : v[i], send = up ? v[i] : v[n + i];
       v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
@@ -205,26 +251,66 @@ __device__ __forceinline__ int first_column(int lane) {
   return (lane & 16 ? C / 2 : 0) + (lane & 8 ? C / 4 : 0) + (lane & 4 ? C / 8 : 0);
 }
 
-// Of row n of two (Q: sums, M: -m): n = 2i, 2i+1.
-__device__ __forceinline__ void set_m(float4* qm, int n, float neg_m) {
-  reinterpret_cast<float*>(qm + (n >> 1))[2 + (n & 1)] = neg_m;
+// ---------------------------------------------------------------------------
+// The affine part of a score as one more product, of 16 in bf16: with a key's step s and zero
+// z, and a row's sum Q of queries and maximum m,
+//   t = s c (q.code + (z / s) Q - m / (s c)),
+// both 1 / s and z / s times a number of the row.  Each of the four numbers is a sum of three
+// bf16 (24 bits), and the six largest products of their parts are taken, in this order:
+//   1 / s: 1 1 2 1 2 3 0 0, m: 1 2 1 3 2 1 0 0; z / s and Q alike in the other eight.
+// ---------------------------------------------------------------------------
+struct Parts {
+  uint32_t p1, p2, p3;  // bf16 bits
+};
+__device__ __forceinline__ Parts parts_of(float x) {
+  Parts p;
+  p.p1 = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+  const float r = x - __uint_as_float(p.p1 << 16);
+  p.p2 = __bfloat16_as_ushort(__float2bfloat16_rn(r));
+  p.p3 = __bfloat16_as_ushort(__float2bfloat16_rn(r - __uint_as_float(p.p2 << 16)));
+  return p;
+}
+__device__ __forceinline__ uint4 key_side(const Parts& p) {
+  return make_uint4(p.p1 | p.p1 << 16, p.p2 | p.p1 << 16, p.p2 | p.p3 << 16, 0);
+}
+__device__ __forceinline__ uint4 row_side(const Parts& p) {
+  return make_uint4(p.p1 | p.p2 << 16, p.p1 | p.p3 << 16, p.p2 | p.p1 << 16, 0);
+}
+// The step that a key's products are in.  Where the codes cannot matter (a constant row has
+// the smallest step there is, or none), a step from the zero instead, and the codes are dropped:
+// z / s stays in range.
+__device__ __forceinline__ float working_step(float s, float z, bool& drop) {
+  drop = fabsf(s) < fmaxf(fabsf(z) * 0x1p-40f, 0x1p-120f);
+  return drop ? fmaxf(fabsf(z) * 0x1p-30f, 0x1p-120f) : s;
+}
+// Where row n has its eight entries for m (half 0) or Q (half 1): rows of 32 bytes, swizzled.
+__device__ __forceinline__ uint4* row_entries(uint8_t* tile, int n, int half) {
+  return reinterpret_cast<uint4*>(tile + n * 32 + ((half ^ ((n >> 2) & 1)) << 4));
+}
+__device__ __forceinline__ uint64_t umma_desc_32(uint32_t smem_addr) {  // 32-byte swizzle
+  return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | (uint64_t)1 << 16 | (uint64_t)(256 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)6 << 61;
 }
 
 template <int DT, int N>
-__global__ void __launch_bounds__(Shape<N>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     k_attend_u4(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                 const __grid_constant__ U4Args t) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int C = N / 2;                            // rows of a softmax group
-  constexpr int kSpread = Shape<N>::kSpread, kSoft = 4 + 4 * kSpread;  // first softmax warp
+  // Few rows: the two softmax groups take tiles in turn, all rows each, with sums, maxima and O
+  // of their own that the item's end adds up; a tile's fixed costs then fall on half the
+  // warps.  More rows would not fit a thread's registers: the groups take half the rows each.
+  constexpr bool kTurns = N <= 32;
+  constexpr int C = kTurns ? N : N / 2;               // rows of a softmax group
   constexpr int kPBytes = N > 64 ? 2 * kSpan : kSpan;
-  constexpr uint32_t kColV = 128, kColS = 256, kColO = 256 + 2 * N;  // tensor memory
+  constexpr uint32_t kColK = 72, kColV = 144, kColS = 272, kColO = 272 + 2 * N;  // tensor memory
   const AttendArgs& a = t.a;
   const int D = a.c.head_dim;
   const int q_bytes = t.spans * N * 128, code_bytes = kTile * D / 2;
   uint8_t* const pbuf = smem;
   uint8_t* const qbuf = pbuf + 2 * kPBytes;
-  uint8_t* const ring = qbuf + 2 * q_bytes;
+  uint8_t* const affine = qbuf + 2 * q_bytes;  // [query tile][S buffer][N] rows of 32 bytes
+  uint8_t* const ring = affine + 4 * N * 32;
   Ctl& ctl = *reinterpret_cast<Ctl*>(ring + (size_t)t.ring.n * t.stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wid = (int)blockIdx.x;
@@ -235,22 +321,26 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1)
     ctl.two = 0;
     ctl.abort = (smem_u32(smem) & 1023u) ? 1 : 0;  // the swizzles need this alignment
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(ctl.full + i, 1);
-      mbar_init(ctl.empty + i, 4 * kSpread + 8);
+      mbar_init(ctl.full + i, 33);
+      mbar_init(ctl.empty + i, 8);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(ctl.qfull + i, 2);
+      mbar_init(ctl.qfull + i, 1);
       mbar_init(ctl.qempty + i, 1 + 8);
       mbar_init(ctl.kfull + i, 4);
       mbar_init(ctl.kfree + i, 1);
-      mbar_init(ctl.vfull + i, 4);
       mbar_init(ctl.sfull + i, 1);
-      mbar_init(ctl.pfull + i, 8);
-      mbar_init(ctl.pfree + i, 1);
+      mbar_init(ctl.sfree + i, kTurns ? 4 : 8);
+      mbar_init(ctl.pvfull + i, 4 + (kTurns ? 4 : 8));
+      mbar_init(ctl.pvfree + i, 1);
+      mbar_init(ctl.fin + i, 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(ctl.segfull + i, 1);
+      mbar_init(ctl.segempty + i, 19);
     }
     mbar_init(&ctl.ofull, 1);
     mbar_init(&ctl.oempty, 8);
-    mbar_init(&ctl.fin, 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -263,372 +353,475 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1)
   const uint32_t tbase = ctl.tmem;
   pdl_wait();
   find_share(t, ctl);
-  Walk walk(ctl);
-  Seg s;
   bool ok = *guard.flag == 0;
-  if (warp < kSoft) give_regs<Shape<N>::kHelpRegs>();
+  // The CTA's items, one after another: warp 0 writes them down, everybody else takes them.
+  uint32_t items = 0;
+  auto take = [&](Seg& s) {
+    const uint32_t i = items & 3u;
+    if (!wait_held(ctl.segfull + i, (items >> 2) & 1u, guard, kWaitItem)) return false;
+    s = ctl.seg[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(ctl.segempty + i);
+    ++items;
+    return s.n > 0;
+  };
+  Seg s;
+  if (warp < kSoft) give_regs<Regs<N>::kHelp>();
 
   if (warp == 0) {
-    // ---------------- fetch key and value pages ----------------
-    // Lanes 0-7 and 16-23 hold a tile's copies of K and of V; page numbers are read a tile
-    // ahead.
+    // ---------------- items, and their key and value pages ----------------
+    // A copy takes the issuing warp about 53 clocks, so a stage has two tiles, and all its
+    // copies are lanes of one instruction: lane 16 t + 8 v + p has part p of K (v = 0) or V of
+    // tile t.  Steps and zeros come 16 bytes a lane (of a page outside the pool codes, steps
+    // and zeros arrive as zeros).  The page numbers of 32 copies are read together, a batch of
+    // tiles ahead.
     const uint64_t pol = l2_policy_evict_first();
-    const int which = lane >> 4, part = lane & 15;
-    const int copies = kTile / t.box;
+    const int tile = lane >> 4, is_v = (lane >> 3) & 1, part = lane & 7;
+    const int copies = kTile / t.box, batch = 32 / copies;
+    const int word_part = 4 * lane / t.box;  // the copy beside this lane's steps and zeros
+    const uint32_t half_bytes = (uint32_t)(t.box * (D / 2));
     uint32_t k = 0;
-    while (ok && walk.next(t, ctl, s)) {
+    if (lane == 0) ctl.walk = Walk(ctl);
+    __syncwarp();
+    auto write_down = [&]() {  // (an item ahead of the tiles: its queries take a while)
+      Walk w = ctl.walk;
+      Seg x;
+      if (!w.next(t, ctl, x)) x.n = 0;
+      const uint32_t i = items & 3u;
+      ok = wait_held(ctl.segempty + i, ((items >> 2) & 1u) ^ 1u, guard, kWaitItem);
+      if (lane == 0) {
+        ctl.walk = w;
+        ctl.seg[i] = x;
+        mbar_arrive(ctl.segfull + i);
+      }
+      __syncwarp();
+      ++items;
+    };
+    write_down();
+    while (ok && ctl.seg[(items - 1) & 3u].n > 0) {
+      write_down();
+      const Seg& s = ctl.seg[(items - 2) & 3u];  // (stays while this warp has not come round to it)
+      const int n = s.n, t0 = s.t0, lo = s.lo, hi = s.hi, h = s.h;
       const int32_t* table = a.b.table + (int64_t)s.b * a.b.max_pages;
-      auto look = [&](int i, int& from, int& upto) {
-        const int key0 = (s.t0 + i) * kTile;
-        from = max(0, s.lo - key0) / t.box;
-        upto = min(copies, (max(0, s.hi - key0) + t.box - 1) / t.box);
-        return part >= from && part < upto ? __ldg(table + ((key0 + part * t.box) >> a.c.page_shift)) : -1;
+      const int64_t head = (int64_t)h * a.c.page_size;
+      auto seen = [&](int key) { return key + t.box > lo && key < hi; };
+      auto look = [&](int i0) {  // pages of the tiles from i0 on
+        const int i = i0 + lane / copies, key = (t0 + i) * kTile + lane % copies * t.box;
+        return i < n && seen(key) ? __ldg(table + (key >> a.c.page_shift)) : -1;
       };
-      int from, upto;
-      int page = look(0, from, upto);
-      for (int i = 0; ok && i < s.n; ++i) {
+      int next = look(0), pages = 0, at_tile = batch;
+      for (int i = 0; ok && i < n; i += 2, ++k) {
+        if (at_tile == batch) {
+          at_tile = 0;
+          pages = next;
+          if (i + batch < n) next = look(i + batch);
+        }
         const Slot at(k, t.ring);
-        ok = wait_warp(ctl.empty + at.i, at.ph ^ 1u, guard, kWaitSlot);
-        if (!ok) break;
+        const int first = at_tile * copies, key0 = (t0 + i) * kTile;
+        at_tile += 2;
+        const int key = key0 + tile * kTile + part * t.box;
+        const int page = __shfl_sync(0xffffffffu, pages, (first + tile * copies + part) & 31);
+        const bool mine = part < copies && i + tile < n && seen(key);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * half_bytes;
         uint8_t* const stage = ring + (size_t)at.i * t.stage_bytes;
-        const int live = max(0, upto - from);
-        const bool mine = part >= from && part < upto;
-        const bool sound = page >= 0 && page < a.c.num_pages;  // (then `mine` too)
-        const int in_page = ((s.t0 + i) * kTile + part * t.box) & (a.c.page_size - 1);
-        uint8_t* const words = stage + 2 * code_bytes + (which * kTile + part * t.box) * 4;
-        // a page outside the pool arrives as zeros; so do its steps and zeros
-        if (mine && !sound)
-          for (int e = 0; e < 4 * t.box; e += 16)
-            *reinterpret_cast<uint4*>(words + e) = make_uint4(0, 0, 0, 0);
-        const uint32_t bytes = (uint32_t)(2 * live * t.box * (D / 2)) +
-                               __popc(__ballot_sync(0xffffffffu, sound)) * 4 * t.box;
-        __syncwarp();
+        ok = wait_held(ctl.empty + at.i, at.ph ^ 1u, guard, kWaitSlot);
+        if (rare(!ok)) break;
         if (lane == 0) mbar_arrive_expect_tx(ctl.full + at.i, bytes);
         __syncwarp();
-        if (mine) {
-          tma_load_4d_hint(stage + which * code_bytes + part * t.box * (D / 2), which ? &mv : &mk, 0,
-                           in_page, s.h, page, ctl.full + at.i, pol);
-          if (sound)
-            bulk_load(words,
-                      (which ? a.c.vs : a.c.ks) +
-                          (((int64_t)page * a.c.kv_heads + s.h) * a.c.page_size + in_page) * 4,
-                      (uint32_t)(4 * t.box), ctl.full + at.i);
+        if (mine)
+          tma_load_4d_hint(stage + (2 * tile + is_v) * code_bytes + part * half_bytes, is_v ? &mv : &mk, 0,
+                           key & (a.c.page_size - 1), h, page, ctl.full + at.i, pol);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int word_page = __shfl_sync(0xffffffffu, pages, (first + e * copies + word_part) & 31);
+          const int word_key = key0 + e * kTile + 4 * lane;
+          if (i + e < n && seen(word_key - (4 * lane & (t.box - 1)))) {
+            const bool sound = word_page >= 0 && word_page < a.c.num_pages;
+            const int64_t from =
+                sound ? ((int64_t)word_page * a.c.kv_heads * a.c.page_size + head + (word_key & (a.c.page_size - 1))) * 4
+                      : 0;
+            uint8_t* const words = stage + 4 * code_bytes + e * 1024 + 16 * lane;
+            copy16(words, a.c.ks + from, sound);
+            copy16(words + 4 * kTile, a.c.vs + from, sound);
+          }
         }
-        __syncwarp();
-        ++k;
-        if (i + 1 < s.n) page = look(i + 1, from, upto);
+        arrive_when_copied(ctl.full + at.i);
       }
     }
     // every copy has landed before the CTA may exit
+    __syncwarp();
     for (uint32_t i = k > t.ring.n ? k - t.ring.n : 0; i < k; ++i) {
       const Slot at(i, t.ring);
       if (lane == 0) wait_end(ctl.full + at.i, at.ph, guard);
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- issue the products ----------------
+    // ---------------- issue the products S ----------------
     const uint32_t leader = elect_leader();
     const uint32_t idesc_s = umma_idesc_16(false, kTile, N, false);
-    const uint32_t idesc_o = umma_idesc_16(false, kTile, N, true);
+    const uint32_t idesc_a = umma_idesc_16(true, kTile, N, false);
     const uint32_t tb = (uint32_t)uniform((int)tbase);
     const int ksteps = D / 16;
     const uint64_t qdesc = umma_smem_desc(smem_u32(qbuf), 16, 1024);
-    const uint64_t pdesc = umma_smem_desc(smem_u32(pbuf), kSpan, 1024);
-    uint32_t g = 0, qn = 0;  // tiles and items before
-    while (ok && walk.next(t, ctl, s)) {
+    const uint64_t adesc = umma_desc_32(smem_u32(affine));
+    uint32_t j = 0, qn = 0;  // tiles and items before
+    for (; ok && take(s); ++qn) {
       const int n = uniform(s.n);
       const uint32_t qb = qn & 1u;
-      auto scores = [&](uint32_t j, bool last) {
-        const uint32_t b = j & 1u;
-        if (!wait_warp(ctl.kfull + b, (j >> 1) & 1u, guard, kWaitK)) return false;
+      const uint64_t qd = qdesc + qb * ((uint32_t)q_bytes >> 4);
+      ok = wait_held(ctl.qfull + qb, (qn >> 1) & 1u, guard, kWaitQ);
+      for (int i = 0; ok && i < n; ++i, ++j) {
+        const uint32_t b = j & 1u, ph = (j >> 1) & 1u;
+        ok = wait_held(ctl.sfree + b, ph ^ 1u, guard, kWaitS) && wait_held(ctl.kfull + b, ph, guard, kWaitK);
+        if (rare(!ok)) break;
         tc_fence_after();
-        const uint32_t acc = tb + kColS + b * N, ka = tb + b * 64;
-        const uint64_t qd = qdesc + qb * ((uint32_t)q_bytes >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t o = (uint64_t)((kk >> 2) * (N * 128 >> 4) + (kk & 3) * 2);
-          if (kk < ksteps) umma_ts_if(leader, acc, ka + kk * 8, qd + o, idesc_s, kk != 0);
-        }
-        umma_commit_if(leader, ctl.kfree + b);
+        const uint32_t acc = tb + kColS + b * N, ka = tb + b * kColK;
+        umma_ts_if(leader, acc, ka + 64, adesc + (2 * qb + b) * (uint32_t)(N * 32 >> 4), idesc_a, false);
+#pragma unroll 1
+        for (int kk = 0; kk < ksteps; ++kk)
+          umma_ts_if(leader, acc, ka + kk * 8, qd + (uint64_t)((kk >> 2) * (N * 128 >> 4) + (kk & 3) * 2), idesc_s, true);
         // (a test may withhold a CTA's first scores: the softmax's wait then runs out)
         umma_commit_if(t.stall == wid && j == 0 ? 0u : leader, ctl.sfull + b);
-        if (last) umma_commit_if(leader, ctl.qempty + qb);
-        return true;
-      };
-      ok = wait_warp(ctl.qfull + qb, (qn >> 1) & 1u, guard, kWaitQ) && scores(g, n == 1);
-      for (int i = 0; ok && i < n; ++i) {
-        const uint32_t j = g + (uint32_t)i, b = j & 1u;
-        if (i + 1 < n) ok = scores(j + 1, i + 2 == n);
-        ok = ok && wait_warp(ctl.vfull + b, (j >> 1) & 1u, guard, kWaitV) &&
-             (i > 0 || wait_warp(&ctl.oempty, (qn & 1u) ^ 1u, guard, kWaitO)) &&
-             wait_warp(ctl.pfull + b, (j >> 1) & 1u, guard, kWaitP);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t va = tb + kColV + b * 64;
-        const uint64_t pd = pdesc + b * (kPBytes >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ts_if(leader, tb + kColO, va + kk * 8, pd + (uint64_t)(kk * 128), idesc_o, kk || i);
-        umma_commit_if(leader, ctl.pfree + b);
-        if (i == n - 1) umma_commit_if(leader, &ctl.ofull);
+        umma_commit_if(leader, ctl.kfree + b);
+        if (i == n - 1) umma_commit_if(leader, ctl.qempty + qb);
       }
-      g += (uint32_t)n;
-      ++qn;
     }
     // all products complete before tensor memory is released
-    umma_commit_if(leader, &ctl.fin);
-    wait_end(&ctl.fin, 0, guard);
-  } else if (warp < 4) {
+    umma_commit_if(leader, ctl.fin);
+    wait_end(ctl.fin, 0, guard);
+  } else if (warp == 3) {
+    // ---------------- issue the products O ----------------
+    const uint32_t leader = elect_leader();
+    const uint32_t idesc_o = umma_idesc_16(false, kTile, N, true);
+    const uint32_t tb = (uint32_t)uniform((int)tbase);
+    const uint64_t pdesc = umma_smem_desc(smem_u32(pbuf), kSpan, 1024);
+    uint32_t j = 0, qn = 0;
+    for (; ok && take(s); ++qn) {
+      const int n = uniform(s.n);
+      ok = wait_held(&ctl.oempty, (qn & 1u) ^ 1u, guard, kWaitO);
+      for (int i = 0; ok && i < n; ++i, ++j) {
+        const uint32_t b = j & 1u;
+        ok = wait_held(ctl.pvfull + b, (j >> 1) & 1u, guard, kWaitP);
+        if (rare(!ok)) break;
+        tc_fence_after();
+        const uint32_t va = tb + kColV + b * 64, acc = tb + kColO + (kTurns ? b * N : 0);
+        const uint64_t pd = pdesc + b * (kPBytes >> 4);
+        const bool more = i > (kTurns ? 1 : 0);
+#pragma unroll 1
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ts_if(leader, acc, va + kk * 8, pd + (uint64_t)(kk * 128), idesc_o, kk || more);
+        umma_commit_if(leader, ctl.pvfree + b);
+      }
+      if (ok) umma_commit_if(leader, &ctl.ofull);
+    }
+    umma_commit_if(leader, ctl.fin + 1);
+    wait_end(ctl.fin + 1, 0, guard);
+  } else if (warp == 2) {
     // ---------------- convert queries ----------------
     // Half a warp to a row, eight elements a lane, in the order of the codes' pairs:
     // 0 4 1 5 2 6 3 7.
-    const int sub = lane & 15, side = 2 * (warp - 2) + (lane >> 4);
+    const int sub = lane & 15, side = lane >> 4;
     uint32_t qn = 0;
-    if (warp == 2 && lane == 0) t.rec[wid].more = 0;
-    for (; ok && walk.next(t, ctl, s); ++qn) {
-      if (warp == 2 && lane == 0 && s.slot == 1) t.rec[wid] = Rec{s.more, s.row0, s.ntok, s.h};
+    if (lane == 0) t.rec[wid].more = 0;
+    for (; ok && take(s); ++qn) {
+      if (lane == 0 && s.slot == 1) t.rec[wid] = Rec{s.more, s.row0, s.ntok, s.h};
       const uint32_t qb = qn & 1u;
-      ok = wait_warp(ctl.qempty + qb, ((qn >> 1) & 1u) ^ 1u, guard, kWaitQFree);
+      ok = wait_held(ctl.qempty + qb, ((qn >> 1) & 1u) ^ 1u, guard, kWaitQFree);
       if (!ok) break;
       bool odd = false;
       const int rows = s.ntok * t.group;
-#pragma unroll 2
-      for (int n = side; n < N; n += 4) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (n < rows && sub * 8 < D) {
-          const int tok = n / t.group, hd = n - tok * t.group;
-          x = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + tok) * a.q_token +
-                                                   (int64_t)(s.h * t.group + hd) * a.q_head) + sub);
-        }
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        float f[8], top = 0.0f, sum = 0.0f;
+      constexpr int kAtOnce = 4;  // rows whose loads stand together
+#pragma unroll 1
+      for (int base = side; base < N; base += 2 * kAtOnce) {
+        uint4 x[kAtOnce];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 p = F16<DT>::up(w[e]);
-          f[2 * e] = p.x;
-          f[2 * e + 1] = p.y;
-          top = fmaxf(top, fmaxf(fabsf(p.x), fabsf(p.y)));
-          sum += p.x + p.y;
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int n = base + 2 * j;
+          x[j] = make_uint4(0, 0, 0, 0);
+          if (n < rows && sub * 8 < D) {
+            const int tok = (int)(n * t.group_inv >> 16), hd = n - tok * t.group;
+            x[j] = __ldg(reinterpret_cast<const uint4*>(a.q + (int64_t)(s.row0 + tok) * a.q_token +
+                                                        (int64_t)(s.h * t.group + hd) * a.q_head) + sub);
+          }
         }
 #pragma unroll
-        for (int o = 8; o; o >>= 1) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        }
-        int shift = kQShift;
-        if (!(top >= 0.0625f && top < 512.0f) && top > 0.0f && top < kInf) {
-          // the largest value into [2^14, 2^15)
-          shift = min(126, 14 + 127 - (int)(__float_as_uint(top) >> 23));
-          odd = true;
-        }
-        const float f0 = pow2f(shift), f1 = f0 * 0.0625f;
-        if (sub * 8 < D) {
-          uint8_t* const to = qbuf + qb * q_bytes + (sub >> 3) * (N * 128) + n * 128 + (((sub & 7) ^ (n & 7)) << 4);
-          *reinterpret_cast<uint4*>(to) =
-              make_uint4(F16<SV_F16>::down(f[0] * f0, f[4] * f0), F16<SV_F16>::down(f[1] * f1, f[5] * f1),
-                         F16<SV_F16>::down(f[2] * f0, f[6] * f0), F16<SV_F16>::down(f[3] * f1, f[7] * f1));
-        }
-        if (sub == 0) {
-          ctl.qsum[qb][n] = sum;
-          ctl.qfac[qb][n] = pow2f(kQShift - shift);
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int n = base + 2 * j;
+          const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+          float f[8], top = 0.0f, sum = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 p = F16<DT>::up(w[e]);
+            f[2 * e] = p.x;
+            f[2 * e + 1] = p.y;
+            top = fmaxf(top, fmaxf(fabsf(p.x), fabsf(p.y)));
+            sum += p.x + p.y;
+          }
+#pragma unroll
+          for (int o = 8; o; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          }
+          int shift = kQShift;
+          if (!(top >= 0.0625f && top < 512.0f) && top > 0.0f && top < kInf) {
+            // the largest value into [2^14, 2^15)
+            shift = min(126, 14 + 127 - (int)(__float_as_uint(top) >> 23));
+            odd = true;
+          }
+          const float f0 = pow2f(shift), f1 = f0 * 0.0625f;
+          if (sub * 8 < D && n < N) {
+            uint8_t* const to =
+                qbuf + qb * q_bytes + (sub >> 3) * (N * 128) + n * 128 + (((sub & 7) ^ (n & 7)) << 4);
+            *reinterpret_cast<uint4*>(to) =
+                make_uint4(F16<SV_F16>::down(f[0] * f0, f[4] * f0), F16<SV_F16>::down(f[1] * f1, f[5] * f1),
+                           F16<SV_F16>::down(f[2] * f0, f[6] * f0), F16<SV_F16>::down(f[3] * f1, f[7] * f1));
+          }
+          if (sub == 0 && n < N) {
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            const uint4 q = row_side(parts_of(sum * pow2f(shift - kQShift) * pow2f(kQShift - 24)));
+            ctl.qfac[qb][n] = pow2f(kQShift - shift);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              uint8_t* const tile = affine + (2 * qb + b) * (N * 32);
+              *row_entries(tile, n, 0) = none;
+              *row_entries(tile, n, 1) = q;
+            }
+          }
         }
       }
       const bool any = __any_sync(0xffffffffu, odd);
-      if (lane == 0) ctl.odd[qb][warp - 2] = any;
+      if (lane == 0) ctl.odd[qb] = any;
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(ctl.qfull + qb);
     }
   } else if (warp < kSoft) {
     // ---------------- spread codes ----------------
-    // One group of four warps for K and one for V, or one for both.
+    // Warps 4-7 those of K, 8-11 those of V.
     const int quad = warp & 3, row = 32 * quad + lane;
-    const bool does_k = kSpread == 1 || warp < 8, does_v = kSpread == 1 || warp >= 8;
+    const bool is_k = warp < 8;
+    const float c18 = t.c * pow2f(24 - kQShift);  // undoes the codes' and the queries' powers
     const uint32_t lanes = tbase + ((uint32_t)(32 * quad) << 16);
-    uint32_t j = 0;
-    while (ok && walk.next(t, ctl, s)) {
+    uint32_t j = 0, k = 0;  // tiles and stages before
+    while (ok && take(s)) {
       for (int i = 0; i < s.n; ++i, ++j) {
-        const Slot at(j, t.ring);
+        const Slot at(k, t.ring);
         const uint32_t b = j & 1u, ph = (j >> 1) & 1u;
-        const uint8_t* const codes = ring + (size_t)at.i * t.stage_bytes;
-        ok = wait_warp(ctl.full + at.i, at.ph, guard, kWaitCodes);
-        if (!ok) break;
-        if (does_k) {
-          ok = wait_warp(ctl.kfree + b, ph ^ 1u, guard, kWaitFree);
-          if (!ok) break;
+        const uint8_t* const stage = ring + (size_t)at.i * t.stage_bytes;
+        const uint8_t* const codes = stage + (2 * (i & 1) + (is_k ? 0 : 1)) * code_bytes;
+        if (!(i & 1)) ok = wait_held(ctl.full + at.i, at.ph, guard, kWaitCodes);
+        if (rare(!ok)) break;
+        if (is_k) {
+          // a key to a lane: pairs (i, i + 4) of each eight dimensions, and its 1 / s and z / s
+          const uint32_t* const words =
+              reinterpret_cast<const uint32_t*>(stage + 4 * code_bytes + (i & 1) * 1024);
+          const uint32_t sz = words[row];
+          bool drop;
+          const float step = working_step(step_of(sz), zero_of(sz), drop), inv = __frcp_rn(step);
+          const uint4 m4 = key_side(parts_of(inv)), q4 = key_side(parts_of(zero_of(sz) * inv));
+          ok = wait_held(ctl.kfree + b, ph ^ 1u, guard, kWaitFree);
+          if (rare(!ok)) break;
           tc_fence_after();
-          // a key to a lane: pairs (i, i + 4) of each eight dimensions
-#pragma unroll 2
-          for (int ch = 0; ch < D / 32; ++ch) {
-            const uint4 x = *reinterpret_cast<const uint4*>(codes + row * (D / 2) + 16 * code_chunk(D, row, ch));
-            uint32_t r[16];
-            spread(x.x, r);
-            spread(x.y, r + 4);
-            spread(x.z, r + 8);
-            spread(x.w, r + 12);
-            tmem_st16(lanes + b * 64 + 16 * ch, r);
-          }
+          ctl.kv[j & 3u][row] = make_float2(step * c18, __uint_as_float(words[kTile + row]));
+          const uint32_t e[8] = {m4.x, m4.y, m4.z, m4.w, q4.x, q4.y, q4.z, q4.w};
+          tmem_st8(lanes + b * kColK + 64, e);
+          const uint8_t* const from = codes + row * (D / 2);
+          const uint32_t to = lanes + b * kColK;
+          spread_row(from, D, row, drop, to);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(ctl.kfull + b);
-        }
-        if (does_v) {
-          ok = wait_warp(ctl.pfree + b, ph ^ 1u, guard, kWaitFree);
-          if (!ok) break;
-          tc_fence_after();
+        } else {
           // a dimension to a lane, pairs of tokens: lane 8i + c of the warp's 32 takes
           // dimension 4c + i of its 32
+          ok = wait_held(ctl.pvfree + b, ph ^ 1u, guard, kWaitFree);
+          if (rare(!ok)) break;
+          tc_fence_after();
           if (32 * quad < D) {
-            const uint32_t base = smem_u32(codes + code_bytes);
+            const uint32_t base = smem_u32(codes) + lane * (D / 2) + 16 * code_chunk(D, lane, quad);
+            const uint32_t to = lanes + kColV + b * 64;
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) {
+              uint32_t x[4], lo[8], hi[8];
+              ld_transposed4(base + m * 16 * D, x);  // (of tokens 32 m + lane)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t lo[16], hi[16];
-#pragma unroll
-              for (int m4 = 0; m4 < 2; ++m4) {
-                const int token = 64 * half + 32 * m4 + lane;
-                uint32_t x[4];
-                ld_transposed4(base + token * (D / 2) + 16 * code_chunk(D, token, quad), x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  uint32_t r[4];
-                  spread(x[e], r);
-                  lo[8 * m4 + 2 * e] = r[0];
-                  lo[8 * m4 + 2 * e + 1] = r[1];
-                  hi[8 * m4 + 2 * e] = r[2];
-                  hi[8 * m4 + 2 * e + 1] = r[3];
-                }
+              for (int e = 0; e < 4; ++e) {
+                uint32_t r[4];
+                spread(x[e], r);
+                lo[2 * e] = r[0];
+                lo[2 * e + 1] = r[1];
+                hi[2 * e] = r[2];
+                hi[2 * e + 1] = r[3];
               }
-              tmem_st_rows8(lanes + kColV + b * 64 + 32 * half, lo);
-              tmem_st_rows8(lanes + (16u << 16) + kColV + b * 64 + 32 * half, hi);
+              tmem_st_rows4(to + 16 * m, lo);
+              tmem_st_rows4(to + (16u << 16) + 16 * m, hi);
             }
             tmem_wait_st();
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(ctl.vfull + b);
+          if (lane == 0) mbar_arrive(ctl.pvfull + b);
         }
-        if (lane == 0) mbar_arrive(ctl.empty + at.i);
+        if ((i & 1) || i == s.n - 1) {
+          if (lane == 0) mbar_arrive(ctl.empty + at.i);
+          ++k;
+        }
       }
     }
   } else {
     // ---------------- softmax and output ----------------
-    take_regs<Shape<N>::kSoftRegs>();
+    take_regs<Regs<N>::kSoft>();
     const int wg = (warp - kSoft) >> 2, quad = warp & 3, row = 32 * quad + lane, id = 1 + wg;
     const int tid = row;                          // of the group's 128
     const uint32_t lanes = tbase + ((uint32_t)(32 * quad) << 16);
-    const uint32_t o_tm = lanes + kColO + wg * C;
-    const int n0 = wg * C;                        // the group's first row
-    float4* const qm = ctl.qm[wg];
-    const float c18 = t.c * pow2f(24 - kQShift);  // undoes the codes' and the queries' powers
+    const int n0 = kTurns ? 0 : wg * C;           // the group's first row
+    const uint32_t o_tm = lanes + kColO + (kTurns ? wg * N : n0);
+    // maxima go into the products (unless the scale is next to nothing: then all tiles take
+    // the slow way)
+    const bool applies = fabsf(t.c) >= 0x1p-100f;
+    const float inv_c = applies ? 1.0f / t.c : 0.0f;
+    // (one of the warps whose wait gave up goes on as far as the next vote, where its group
+    // leaves the item, and both groups leave together: they meet at barriers without a limit)
     uint32_t g = 0, qn = 0;
-    for (; walk.next(t, ctl, s); ++qn) {
+    for (;; ++qn) {
+      const Seg& seg = ctl.seg[items & 3u];  // (given back at the item's end)
+      ok = ok && wait_held(ctl.segfull + (items & 3u), (items >> 2) & 1u, guard, kWaitItem);
+      if (group_any<256>(3, !ok || seg.n == 0)) break;
+      const int tiles = seg.n, tile0 = seg.t0, pos = seg.pos;
+      const int rows = seg.ntok * t.group;  // live ones of the item
+      // tiles [whole0, whole1) hold keys that all tokens see
+      const int whole1 = (pos + 1) / kTile - tile0;
+      const int whole0 = a.window ? max(0, pos + seg.ntok - 1 - a.window) / kTile + 1 - tile0 : 0;
       const uint32_t qb = qn & 1u;
-      if (ok) ok = wait_warp(ctl.qfull + qb, (qn >> 1) & 1u, guard, kWaitQ);
+      ok = wait_held(ctl.qfull + qb, (qn >> 1) & 1u, guard, kWaitQ);
       if (tid < C) {
-        reinterpret_cast<float*>(qm + (tid >> 1))[tid & 1] = ctl.qsum[qb][n0 + tid];
-        set_m(qm, tid, kInf);
         ctl.m[wg][tid] = -kInf;
+        ctl.mv[wg][0][tid] = ctl.mv[wg][1][tid] = make_float2(0.0f, 0.0f);
       }
-      const bool odd = ctl.odd[qb][0] | ctl.odd[qb][1];
+      bool unset = true;                    // some row has seen nothing yet
+      bool stale[2] = {true, true};         // a buffer's products lack the present maxima
+      const bool odd = ctl.odd[qb];
       group_sync(id);
       uint64_t l2[C / 2], z2[C / 2];
 #pragma unroll
       for (int i = 0; i < C / 2; ++i) l2[i] = z2[i] = 0;
-      float E = 0.0f, inv_e = 0.0f;  // largest step so far, up to a power of two; its inverse
-      for (int i = 0; i < s.n; ++i, ++g) {
-        const Slot at(g, t.ring);
-        const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
-        const uint32_t s_tm = lanes + kColS + b * N + wg * C;
-        // S is there, so the tile's steps and zeros are too, and O's product of two tiles ago
-        // is done (it was issued before this S): P's place is free
-        if (ok) ok = wait_warp(ctl.sfull + b, ph, guard, kWaitS);
+      float E = 0.0f, e_up = 0.0f;  // largest step so far, up to a power of two; kUp over it
+      bool late = false;
+      // (in turns a group's tiles are those of one S buffer, whose products always have the
+      // present maxima in them: they change before the buffer's next one is issued)
+      for (int i = kTurns ? (wg ^ (int)(g & 1u)) : 0; i < tiles; i += kTurns ? 2 : 1) {
+        const uint32_t j = g + (uint32_t)i, b = kTurns ? (uint32_t)wg : j & 1u, ph = (j >> 1) & 1u;
+        const uint32_t s_tm = lanes + kColS + b * N + n0;
+        ok = wait_held(ctl.sfull + b, ph, guard, kWaitS);  // (then the tile's factors are there too)
         tc_fence_after();
-        // the key's step and zero, and the rows that see it: [first, first + span) of the group's
-        const uint32_t* const words =
-            reinterpret_cast<const uint32_t*>(ring + (size_t)at.i * t.stage_bytes + 2 * code_bytes);
-        uint32_t ksz = words[row], vsz = words[kTile + row];
-        const int key = (s.t0 + i) * kTile + row;
+        const float2 kv = ctl.kv[j & 3u][row];
+        float step = step_of(__float_as_uint(kv.y)), zero = zero_of(__float_as_uint(kv.y));
+        // the rows that see the key: [first, first + span) of the group's
         int first = 0, span = C;
-        const bool edge = (s.t0 + i + 1) * kTile > s.pos + 1 ||
-                          (a.window && (s.t0 + i) * kTile <= s.pos + s.ntok - 1 - a.window);
-        if (edge) {
+        const bool edge = i >= whole1 || i < whole0;
+        if (rare(edge)) {
           // token i sees it if key - pos <= i < key - pos + window
-          const int d = key - s.pos;
+          const int key = (tile0 + i) * kTile + row, d = key - pos;
           const int t0 = max(0, min(d, t.tpt));
           const int t1 = a.window && d <= t.tpt - a.window ? max(0, d + a.window) : t.tpt;
-          const int r0 = max(0, t0 * t.group - n0);
-          const int r1 = t1 == t.tpt ? C : min(C, t1 * t.group - n0);
-          first = r0;
-          span = max(0, r1 - r0);
-          if (key < s.lo || key >= s.hi) span = 0;
-          if (!span) ksz = vsz = 0;
+          first = max(0, t0 * t.group - n0);
+          span = max(0, (t1 == t.tpt ? C : min(C, t1 * t.group - n0)) - first);
+          if (key < seg.lo || key >= seg.hi) span = 0;
+          if (!span) step = zero = 0.0f;
         }
         const bool masked = edge && __any_sync(0xffffffffu, span < C);
-        const float A = step_of(ksz) * c18, B = zero_of(ksz) * t.c;
-        const float step = step_of(vsz), zero = zero_of(vsz);
+        const uint64_t A2 = pack2(kv.x, kv.x);
         uint32_t r[C];
         auto load = [&]() {
+          if constexpr (C % 32 == 0) {
+            tmem_ld32_async(s_tm, r);
+          } else if constexpr (C % 16 == 0) {
+            tmem_ld16_async(s_tm, r);
+          } else {
 #pragma unroll
-          for (int u = 0; u < C; u += 8) tmem_ld8_async(s_tm + u, r + u);
+            for (int u = 0; u < C; u += 8) tmem_ld8_async(s_tm + u, r + u);
+          }
           tmem_wait_ld();
-          if (odd) {
+          if (rare(odd)) {
 #pragma unroll
             for (int n = 0; n < C; ++n)
               r[n] = __float_as_uint(__uint_as_float(r[n]) * ctl.qfac[qb][n0 + n]);
           }
         };
-        // t of all rows
-        auto exponents = [&]() {
-          const uint64_t A2 = pack2(A, A), B2 = pack2(B, B);
-#pragma unroll
-          for (int n = 0; n < C; n += 2) {
-            const float4 k = qm[n >> 1];
-            float x, y;
-            unpack2(ffma2(pack2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), A2,
-                          ffma2(pack2(k.x, k.y), B2, pack2(k.z, k.w))), x, y);
-            r[n] = __float_as_uint(x);
-            r[n + 1] = __float_as_uint(y);
-          }
-          if (masked) {
+        auto hide = [&]() {
+          if (rare(masked)) {
 #pragma unroll
             for (int n = 0; n < C; ++n)
               if ((unsigned)(n - first) >= (unsigned)span) r[n] = 0xff800000u;
           }
         };
         load();
-        exponents();
-        float top = -kInf;
-#pragma unroll
-        for (int n = 0; n < C; ++n) top = fmaxf(top, __uint_as_float(r[n]));
-        if (group_any(id, top > kLag || step > E)) {
-          // some maximum rises, or the largest step
-          load();
-          const uint64_t A2 = pack2(A, A), B2 = pack2(B, B);
-          float v[C];
+        bool slow = unset || (!kTurns && (b ? stale[1] : stale[0]));  // (the same for the group)
+        if (!slow) {
 #pragma unroll
           for (int n = 0; n < C; n += 2) {
-            const float4 k = qm[n >> 1];
-            unpack2(ffma2(pack2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), A2,
-                          fmul2(pack2(k.x, k.y), B2)), v[n], v[n + 1]);
-            if ((unsigned)(n - first) >= (unsigned)span) v[n] = -kInf;
-            if ((unsigned)(n + 1 - first) >= (unsigned)span) v[n + 1] = -kInf;
+            float x, y;
+            unpack2(fmul2(pack2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), A2), x, y);
+            r[n] = __float_as_uint(x);
+            r[n + 1] = __float_as_uint(y);
           }
-          over_lanes<C, true>(v);
+          hide();
+          float top = __uint_as_float(r[0]), top2 = __uint_as_float(r[1]);
+#pragma unroll
+          for (int n = 2; n < C; n += 4) {
+            top = max3(top, __uint_as_float(r[n]), __uint_as_float(r[n + 1]));
+            if (n + 2 < C) top2 = max3(top2, __uint_as_float(r[n + 2]), __uint_as_float(r[n + 3]));
+          }
+          // (a step or zero that is not finite takes the slow way too)
+          slow = group_any(id, fmaxf(top, top2) > kLag || !(fmaf(zero, 0.0f, step) <= E) || !ok);
+          if (rare(slow)) load();
+        }
+        if (rare(slow)) {
+          // a maximum rises, or the largest step, or the product was issued with older maxima
+          if (group_any(id, !ok)) {
+            late = true;
+            break;
+          }
+          // scores, maxima taken off from column `off` of mv
+          auto scores = [&](int off) {
+#pragma unroll
+            for (int n = 0; n < C; n += 2) {
+              const float* k = reinterpret_cast<const float*>(ctl.mv[wg][b] + n) + off;
+              float x, y;
+              unpack2(ffma2(pack2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), A2, pack2(k[0], k[2])), x, y);
+              r[n] = __float_as_uint(x);
+              r[n + 1] = __float_as_uint(y);
+            }
+            hide();
+          };
+          scores(0);
+          over_lanes<C, true>(r);
           if ((lane & 3) == 0)
 #pragma unroll
-            for (int n = 0; n < C / 8; ++n) ctl.wmax[wg][quad][first_column<C>(lane) + n] = v[n];
-          const float ws = warp_max(step < kInf ? step : 0.0f);
+            for (int n = 0; n < C / 8; ++n)
+              ctl.wmax[wg][quad][first_column<C>(lane) + n] = __uint_as_float(r[n]);
+          const bool bad = !(fmaf(zero, 0.0f, step) < kInf);
+          const float ws = warp_max(bad ? 0.0f : step);
           if (lane == 0) ctl.wstep[wg][quad] = ws;
+          if (tid == 0) ctl.rose[wg] = ctl.unset[wg] = 0;
           group_sync(id);
           if (tid < C) {
-            const float was = ctl.m[wg][tid];
-            float now = was;
+            float most = -kInf;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) now = fmaxf(now, ctl.wmax[wg][w][tid]);
+            for (int w = 0; w < 4; ++w) most = fmaxf(most, ctl.wmax[wg][w][tid]);
+            const float was = ctl.m[wg][tid], now = most > was + kLag ? most : was;
             ctl.m[wg][tid] = now;
             ctl.fac[wg][tid] = now > was ? ex2(was - now) : 1.0f;
-            set_m(qm, tid, -now);
+            if (now > was) ctl.rose[wg] = 1;
+            const bool none = now == -kInf;
+            if (none && n0 + tid < rows) ctl.unset[wg] = 1;
+            // the buffer's next product (two tiles on) has the present maximum in it
+            const float m = none ? 0.0f : now, in = applies && fabsf(m) < kInf ? m : 0.0f;
+            // (and this one: with the maximum that it was issued with, less the present one)
+            ctl.mv[wg][b][tid] = make_float2(in, ctl.mv[wg][b][tid].x - m);
+            *row_entries(affine + (2 * qb + b) * (N * 32), n0 + tid, 0) =
+                row_side(parts_of(-in * inv_c * (pow2f(kQShift - 24) / ctl.qfac[qb][n0 + tid])));
           }
           float most = 0.0f;
 #pragma unroll
@@ -637,15 +830,21 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1)
           const float e_now = fmaxf(E, __uint_as_float(up));
           const float fe = E < e_now ? E * (1.0f / e_now) : 1.0f;
           group_sync(id);
-          if (i) {
+          const bool rose = ctl.rose[wg] != 0;
+          unset = ctl.unset[wg] != 0 || (kTurns && !applies);
+          stale[0] = b ? stale[0] || rose || !applies : !applies;
+          stale[1] = b ? !applies : stale[1] || rose || !applies;
+          const bool opened = kTurns ? i > 1 : i > 0;  // O holds something of the item
+          if (opened && (rose || fe != 1.0f)) {
 #pragma unroll
             for (int n = 0; n < C; n += 2) {
               const float2 f = *reinterpret_cast<const float2*>(ctl.fac[wg] + n);
               l2[n / 2] = fmul2(l2[n / 2], pack2(f.x, f.y));
               z2[n / 2] = fmul2(z2[n / 2], pack2(f.x, f.y));
             }
-            // O: the product of the tile before is done
-            if (ok) ok = wait_warp(ctl.pfree + (b ^ 1u), ((g - 1) >> 1) & 1u, guard, kWaitFree);
+            // O: its last product is done (in turns that of two tiles ago)
+            ok = kTurns ? wait_held(ctl.pvfree + b, ph ^ 1u, guard, kWaitFree)
+                        : wait_held(ctl.pvfree + (b ^ 1u), ((j - 1) >> 1) & 1u, guard, kWaitFree);
             tc_fence_after();
 #pragma unroll 1
             for (int u = 0; u < C; u += 8) {
@@ -668,17 +867,32 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1)
           }
           if (E < e_now) {
             E = e_now;
-            inv_e = 1.0f / e_now;
+            e_up = kUp / e_now;
+          }
+          if (__any_sync(0xffffffffu, bad)) {
+            // a value row that is not finite weighs nothing (0 times it would not be 0 where
+            // it is not seen); the rows that do see it get their NaN here
+            const float nan = bad ? __int_as_float(0x7fffffff) : 0.0f;
+#pragma unroll
+            for (int n = 0; n < C; n += 2)
+              z2[n / 2] = fadd2(z2[n / 2], pack2((unsigned)(n - first) < (unsigned)span ? nan : 0.0f,
+                                                 (unsigned)(n + 1 - first) < (unsigned)span ? nan : 0.0f));
+            if (bad) step = zero = 0.0f;
           }
           load();
-          exponents();
+          scores(1);
+          group_sync(id);  // (mv and the maxima's votes are written again by the next slow tile)
         }
-        // weights.  A value row that is not finite weighs nothing here (0 times it would not
-        // be 0 where it is not seen); the rows that do see it get their NaN below
-        const bool bad = !(step < kInf && fabsf(zero) < kInf);
-        const float up = bad ? 0.0f : step * inv_e * kUp, zero_in = bad ? 0.0f : zero;
-        const uint64_t up2 = pack2(up, up), zero2 = pack2(zero_in, zero_in);
-        uint8_t* const prow = pbuf + b * kPBytes + row * 128;
+        // S has been read, and the next product in its place has the present maxima to take
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ctl.sfree + b);
+        // weights, into P's place of two tiles ago
+        ok = wait_held(ctl.pvfree + b, ph ^ 1u, guard, kWaitFree);
+        const float up = step * e_up;
+        const uint64_t up2 = pack2(up, up), zero2 = pack2(zero, zero);
+        const uint32_t prow = smem_u32(pbuf + b * kPBytes + row * 128) | ((row & 7) << 4);
 #pragma unroll
         for (int u = 0; u < C; u += 8) {
           uint32_t w[4];
@@ -693,44 +907,28 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1)
             w[e / 2] = F16<SV_F16>::down(x, y);
           }
           const int ch = (n0 + u) >> 3;
-          *reinterpret_cast<uint4*>(prow + (ch >> 3) * kSpan + (((ch & 7) ^ (row & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if (__any_sync(0xffffffffu, bad)) {
-          const float nan = bad ? __int_as_float(0x7fffffff) : 0.0f;
-#pragma unroll
-          for (int n = 0; n < C; n += 2)
-            z2[n / 2] = fadd2(z2[n / 2], pack2((unsigned)(n - first) < (unsigned)span ? nan : 0.0f,
-                                               (unsigned)(n + 1 - first) < (unsigned)span ? nan : 0.0f));
+          st_shared16((prow ^ ((ch & 7) << 4)) + (ch >> 3) * kSpan, w);
         }
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(ctl.pfull + b);
-          mbar_arrive(ctl.empty + at.i);
-        }
+        if (lane == 0) mbar_arrive(ctl.pvfull + b);
       }
+      g += (uint32_t)tiles;
       // ---- the item's end: sums over the keys, then O ----
-      {
+      auto sum_up = [&](uint64_t (&x2)[C / 2], int which) {
         float v[C];
 #pragma unroll
-        for (int n = 0; n < C; n += 2) unpack2(l2[n / 2], v[n], v[n + 1]);
-        over_lanes<C, false>(v);
-        const int col = first_column<C>(lane);
-        if ((lane & 3) == 0)
-#pragma unroll
-          for (int n = 0; n < C / 8; ++n) ctl.lz[wg][quad][col + n].x = v[n];
-#pragma unroll
-        for (int n = 0; n < C; n += 2) unpack2(z2[n / 2], v[n], v[n + 1]);
+        for (int n = 0; n < C; n += 2) unpack2(x2[n / 2], v[n], v[n + 1]);
         over_lanes<C, false>(v);
         if ((lane & 3) == 0)
 #pragma unroll
-          for (int n = 0; n < C / 8; ++n) ctl.lz[wg][quad][col + n].y = v[n];
-      }
+          for (int n = 0; n < C / 8; ++n)
+            reinterpret_cast<float*>(ctl.lz[wg][quad] + first_column<C>(lane) + n)[which] = v[n];
+      };
+      sum_up(l2, 0);
+      sum_up(z2, 1);
       group_sync(id);
-      const int rows = s.ntok * t.group;  // live ones of the item
-      const int64_t prow = (int64_t)(2 * wid + (s.slot > 0 ? 1 : 0)) * kMaxN + n0;
       if (tid < C) {
         float L = 0.0f, Z = 0.0f;
 #pragma unroll
@@ -739,49 +937,70 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1)
           L += x.x;
           Z += x.y;
         }
-        const float m = ctl.m[wg][tid];
-        if (s.slot >= 0) {
-          ctl.fin_lz[wg][tid] = make_float2(1.0f, Z);
-          if (n0 + tid < rows) t.ml[prow + tid] = make_float2(m, L);
-        } else {
-          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-          ctl.fin_lz[wg][tid] = make_float2(inv, L == 0.0f ? 0.0f : Z * inv);
-          if (a.lse && n0 + tid < rows) {
-            const int tok = (n0 + tid) / t.group, hd = n0 + tid - tok * t.group;
-            a.lse[(int64_t)(s.row0 + tok) * a.heads + s.h * t.group + hd] = lse_of(m, L);
+        ctl.ends[wg][tid] = make_float4(ctl.m[wg][tid], L, Z, E);
+      }
+      if (group_any<256>(3, late)) break;
+      // half the rows' outputs each
+      constexpr int kOut = N / 2;
+      const int r0 = wg * kOut;
+      const int64_t prow = (int64_t)(2 * wid + (seg.slot > 0 ? 1 : 0)) * kMaxN;
+      if (tid < kOut) {
+        const int n = r0 + tid;
+        const float4 x = ctl.ends[kTurns ? 0 : wg][kTurns ? n : tid];
+        float m = x.x, L = x.y, Z = x.z, f0 = x.w, f1 = 0.0f;
+        if (kTurns) {
+          const float4 y = ctl.ends[1][n];
+          m = fmaxf(x.x, y.x);
+          // (a group that saw nothing: l is 0, and its O was never written)
+          const float a0 = x.y == 0.0f ? 0.0f : ex2(x.x - m), a1 = y.y == 0.0f ? 0.0f : ex2(y.x - m);
+          L = (x.y == 0.0f ? 0.0f : a0 * x.y) + (y.y == 0.0f ? 0.0f : a1 * y.y);
+          Z = (x.y == 0.0f ? 0.0f : a0 * x.z) + (y.y == 0.0f ? 0.0f : a1 * y.z);
+          f0 = a0 * x.w;
+          f1 = a1 * y.w;
+        }
+        const float inv = seg.slot >= 0 ? 1.0f : L == 0.0f ? 0.0f : 1.0f / L;
+        ctl.out[n] = make_float4(f0 * inv, f1 * inv, L == 0.0f ? 0.0f : Z * inv, 0.0f);
+        if (n < rows) {
+          if (seg.slot >= 0) {
+            t.ml[prow + n] = make_float2(m, L);
+          } else if (a.lse) {
+            const int tok = (int)(n * t.group_inv >> 16), hd = n - tok * t.group;
+            a.lse[(int64_t)(seg.row0 + tok) * a.heads + seg.h * t.group + hd] = lse_of(m, L);
           }
         }
       }
       group_sync(id);
-      if (ok) ok = wait_warp(&ctl.ofull, qn & 1u, guard, kWaitO);
+      ok = wait_held(&ctl.ofull, qn & 1u, guard, kWaitO);
       tc_fence_after();
       // lane 8i + c of the warp's 32 has dimension 4c + i, with codes 2^-24 or 2^-20 high
       const int dim = 32 * quad + 4 * (lane & 7) + (lane >> 3);
       const float back = (lane & 8 ? pow2f(20) : pow2f(24)) / kUp;
-      int tok = n0 / t.group, hd = n0 - tok * t.group;
+      int hd = r0 - (int)(r0 * t.group_inv >> 16) * t.group;
+      int64_t at = ((int64_t)(seg.row0 + (int)(r0 * t.group_inv >> 16)) * a.heads + seg.h * t.group + hd) * D + dim;
 #pragma unroll 1
-      for (int u = 0; u < C; u += 8) {
-        uint32_t o[8];
+      for (int u = 0; u < kOut; u += 8) {
+        uint32_t o[8], q[8];
         __syncwarp();
-        tmem_ld8_async(o_tm + u, o);
+        tmem_ld8_async(lanes + kColO + r0 + u, o);
+        if (kTurns) tmem_ld8_async(lanes + kColO + N + r0 + u, q);
         tmem_wait_ld();
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          if (n0 + u + n < rows && dim < D) {
-            const float2 f = ctl.fin_lz[wg][u + n];
-            // (rows that saw nothing: O was never weighed, f is 0)
-            const float x = E == 0.0f ? 0.0f : __uint_as_float(o[n]) * back * E;
-            const float y = fmaf(x, f.x, f.y);
-            if (s.slot < 0) {
-              const int64_t orow = (int64_t)(s.row0 + tok) * a.heads + s.h * t.group + hd;
-              reinterpret_cast<uint16_t*>(a.out)[orow * D + dim] = (uint16_t)F16<DT>::down(y, 0.0f);
-            } else {
-              t.part[(prow + u + n) * D + dim] = y;
-            }
+          if (r0 + u + n < rows && dim < D) {
+            const float4 f = ctl.out[r0 + u + n];
+            // (an O without weights is not read: it may hold anything)
+            float y = f.z;
+            if (f.x != 0.0f) y = fmaf(__uint_as_float(o[n]) * back, f.x, y);
+            if (kTurns && f.y != 0.0f) y = fmaf(__uint_as_float(q[n]) * back, f.y, y);
+            if (seg.slot < 0)
+              reinterpret_cast<uint16_t*>(a.out)[at] = (uint16_t)F16<DT>::down(y, 0.0f);
+            else
+              t.part[(prow + r0 + u + n) * D + dim] = y;
           }
+          at += D;
           if (++hd == t.group) {
             hd = 0;
-            ++tok;
+            at += (int64_t)(a.heads - t.group) * D;
           }
         }
       }
@@ -790,7 +1009,9 @@ __global__ void __launch_bounds__(Shape<N>::kThreads, 1)
       if (lane == 0) {
         mbar_arrive(&ctl.oempty);
         mbar_arrive(ctl.qempty + qb);
+        mbar_arrive(ctl.segempty + (items & 3u));
       }
+      ++items;
     }
   }
   __syncwarp();
@@ -809,8 +1030,7 @@ EncodeTiled g_encode = nullptr;
 int g_sms[64] = {};
 
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const U4Args);
-int threads_of(int n) { return n <= 32 ? Shape<16>::kThreads : Shape<80>::kThreads; }
-int regs_of(int n) { return n <= 32 ? Shape<16>::kRegs : Shape<80>::kRegs; }
+
 template <int DT>
 Kernel kernel_of(int n) {
   switch (n) {
@@ -838,7 +1058,7 @@ cudaError_t device_ready(int* sms) {
         cudaFuncAttributes attr{};
         e = cudaFuncGetAttributes(&attr, (const void*)k);
         if (e != cudaSuccess) return e;
-        if (attr.numRegs < regs_of(n)) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
+        if (attr.numRegs < Regs<16>::kLaunch) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
         e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return e;
       }
@@ -864,8 +1084,14 @@ bool encode_codes(CUtensorMap* map, const CacheView& c, const void* base, int bo
   const CUtensorMapSwizzle swizzle = c.head_dim == 128  ? CU_TENSOR_MAP_SWIZZLE_64B
                                      : c.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                         : CU_TENSOR_MAP_SWIZZLE_NONE;
+  // Rows of one head that lie apart (token-major pages): what L2 fetches beside them is other
+  // heads', and gone again before those are read (rows of 64 bytes, 512 apart: 10.5 bytes a
+  // clock and SM with 256-byte fetches, 22.7 with 64).
+  const CUtensorMapL2promotion promotion = c.token_bytes == c.head_dim / 2
+                                               ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                               : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, bx, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -899,10 +1125,11 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   t.tpt = (int)(chunk < 1 ? 1 : (chunk + items - 1) / items);
   const int N = (t.tpt * t.group + 15) / 16 * 16;
   t.tpt = N / t.group;
+  t.group_inv = (uint32_t)((65536 + t.group - 1) / t.group);
   t.box = c.page_size < kTile ? c.page_size : kTile;
   t.spans = c.head_dim > 64 ? 2 : 1;
-  t.stage_bytes = kTile * c.head_dim + 1024;
-  const int fixed = 2 * (N > 64 ? 2 : 1) * kSpan + 2 * t.spans * N * 128 + (int)sizeof(Ctl);
+  t.stage_bytes = 2 * (kTile * c.head_dim + 1024);
+  const int fixed = 2 * (N > 64 ? 2 : 1) * kSpan + 2 * t.spans * N * 128 + 4 * N * 32 + (int)sizeof(Ctl);
   t.ring = make_ring(((int)kSmemBytes - fixed) / t.stage_bytes, kMaxStages);
   t.stall = attention_test().stall_cta;
   t.wait_clocks = attention_test().wait_clocks;
@@ -915,8 +1142,8 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   *taken = encode_codes(&mk, c, c.k, t.box) && encode_codes(&mv, c, c.v, t.box);
   if (!*taken) return cudaSuccess;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  e = launch_pdl(dtype == SV_BF16 ? kernel_of<SV_BF16>(N) : kernel_of<SV_F16>(N), dim3(ctas),
-                 dim3(threads_of(N)), kSmemBytes, stream, mk, mv, t);
+  e = launch_pdl(dtype == SV_BF16 ? kernel_of<SV_BF16>(N) : kernel_of<SV_F16>(N), dim3(ctas), dim3(kThreads),
+                 kSmemBytes, stream, mk, mv, t);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.b.total * a.heads;
   const int join_blocks = (int)(rows < 6 * ctas ? rows : 6 * ctas);
