@@ -35,6 +35,7 @@
 #include "specverify.h"
 #include "sv_attention.h"
 #include "sv_attention_line.cuh"
+#include "sv_attention_u4.cuh"
 #include "sv_cache.cuh"
 #include "sv_device.cuh"
 #include "sv_launch.h"
@@ -44,8 +45,6 @@
 namespace sv {
 namespace {
 
-constexpr int kMaxN = 80;              // 3 N columns beside 256 of operands in tensor memory
-constexpr int kMaxStages = 6;  // of two key tiles
 constexpr int kSpan = 16384;           // 128 rows of a 128-byte swizzle span
 constexpr size_t kSmemBytes = 227 * 1024;
 // Registers of a thread at launch, and then by role (the roles' sum must not pass what the
@@ -56,34 +55,6 @@ struct Regs {
   static constexpr int kLaunch = 96, kHelp = N <= 64 ? 64 : 48, kSoft = N <= 64 ? 144 : 168;
   static_assert((kThreads - 256) * kHelp + 256 * kSoft <= kThreads * kLaunch, "registers");
 };
-// A maximum may lag by this many powers of two, and a weight p s is at most 2^kLag kUp = 2^15
-// in fp16, s relative to the largest step seen: weights keep all their bits down to 2^-23
-// of that, and some to 2^-33.
-constexpr float kLag = 6.0f;
-constexpr float kUp = 512.0f;
-// Queries times 2^kQShift (and 2^-4 of that where the code sits four bits higher): rows with
-// a largest value within [2^-4, 2^9) fit fp16 so, to the last bit of all that matters (what
-// is below 2^-19 is rounded to 2^-27).  Other rows get a factor of their own.
-constexpr int kQShift = 6;
-
-struct U4Args {
-  static constexpr int kItemUnits = 3, kRowTiles = 1, kSlotRows = kMaxN;
-  AttendArgs a;
-  int group, tpt;      // query heads per key head; tokens per row tile
-  uint32_t group_inv;  // ceil(2^16 / group): row n of an item is of token n group_inv >> 16
-  int box;             // tokens per copy: min(page_size, 128)
-  int spans;           // of 64 dimensions, of a query row: 1 or 2
-  Ring ring;
-  int stage_bytes;
-  int stall;           // test only: the CTA whose first scores are withheld (-1: none)
-  long long wait_clocks;
-  float c;             // scale log2 e
-  float* part;         // [2 * kMaxCtas][kMaxN][head_dim]
-  float2* ml;          // [2 * kMaxCtas][kMaxN]
-  Rec* rec;            // [kMaxCtas]
-  int* err;            // [kMaxCtas]
-};
-
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t qfull[2], qempty[2], kfull[2], kfree[2], sfull[2], sfree[2], pvfull[2], pvfree[2];
@@ -132,24 +103,6 @@ __device__ __forceinline__ void tmem_st_rows4(uint32_t taddr, const uint32_t* r)
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
                : "memory");
 }
-// Four 8 x 8 matrices of 16-bit entries, transposed: thread t gets entries t/4 of rows
-// 2(t%4) and 2(t%4)+1 of each; lane l gives the address of row l%8 of matrix l/8.
-__device__ __forceinline__ void ld_transposed4(uint32_t addr, uint32_t* r) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {  // NaNs are passed over
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // The 128 threads of a softmax group (or the 256 of both).
 __device__ __forceinline__ void group_sync(int id) {
   asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
@@ -165,34 +118,9 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
       : "memory");
   return r != 0;
 }
-// 16 bytes into shared memory (zeros if not `real`), and this thread's arrival at a barrier
-// once all its copies before it have landed.
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
-               "l"(__cvta_generic_to_global(src)), "r"(real ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void arrive_when_copied(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                : "memory");
-}
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-
-// The 16-byte chunk of a code row that holds its i-th, as the copies lay it out (a 64- or
-// 32-byte swizzle where rows of 16 bytes' steps would meet in the banks).
-__device__ __forceinline__ int code_chunk(int D, int row, int i) {
-  return D == 128 ? i ^ ((row >> 1) & 3) : D == 64 ? i ^ ((row >> 2) & 1) : i;
-}
-// Eight codes as four pairs (i, i + 4), i = 0..3.
-__device__ __forceinline__ void spread(uint32_t w, uint32_t* r) {
-  const uint32_t v = w >> 8;
-  r[0] = w & 0x000F000Fu;
-  r[1] = w & 0x00F000F0u;
-  r[2] = v & 0x000F000Fu;
-  r[3] = v & 0x00F000F0u;
 }
 
 // A key's row of codes into tensor memory (this thread's lane).
@@ -211,12 +139,6 @@ __device__ __forceinline__ void spread_row(const uint8_t* from, int D, int row, 
   }
 }
 
-// (code for what is rare goes out of the way: the warps' eight pieces of code share instruction
-// caches that do not hold them all)
-__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, false); }
-
-enum WaitId { kWaitItem = 12, kWaitSlot = 1, kWaitQ, kWaitK, kWaitV, kWaitP, kWaitQFree, kWaitS, kWaitO, kWaitCodes,
-              kWaitFree };
 
 // Sums (or largest, NaNs passed over) over a warp's lanes of C values (a multiple of 8)
 // each: lane l ends with those of C / 8 columns from first_column(l) on, in v[0..].
@@ -370,91 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------- items, and their key and value pages ----------------
-    // A copy takes the issuing warp about 53 clocks, so a stage has two tiles, and all its
-    // copies are lanes of one instruction: lane 16 t + 8 v + p has part p of K (v = 0) or V of
-    // tile t.  Steps and zeros come 16 bytes a lane (of a page outside the pool codes, steps
-    // and zeros arrive as zeros).  The page numbers of 32 copies are read together, a batch of
-    // tiles ahead.
-    const uint64_t pol = l2_policy_evict_first();
-    const int tile = lane >> 4, is_v = (lane >> 3) & 1, part = lane & 7;
-    const int copies = kTile / t.box, batch = 32 / copies;
-    const int word_part = 4 * lane / t.box;  // the copy beside this lane's steps and zeros
-    const uint32_t half_bytes = (uint32_t)(t.box * (D / 2));
-    uint32_t k = 0;
-    if (lane == 0) ctl.walk = Walk(ctl);
-    __syncwarp();
-    auto write_down = [&]() {  // (an item ahead of the tiles: its queries take a while)
-      Walk w = ctl.walk;
-      Seg x;
-      if (!w.next(t, ctl, x)) x.n = 0;
-      const uint32_t i = items & 3u;
-      ok = wait_held(ctl.segempty + i, ((items >> 2) & 1u) ^ 1u, guard, kWaitItem);
-      if (lane == 0) {
-        ctl.walk = w;
-        ctl.seg[i] = x;
-        mbar_arrive(ctl.segfull + i);
-      }
-      __syncwarp();
-      ++items;
-    };
-    write_down();
-    while (ok && ctl.seg[(items - 1) & 3u].n > 0) {
-      write_down();
-      const Seg& s = ctl.seg[(items - 2) & 3u];  // (stays while this warp has not come round to it)
-      const int n = s.n, t0 = s.t0, lo = s.lo, hi = s.hi, h = s.h;
-      const int32_t* table = a.b.table + (int64_t)s.b * a.b.max_pages;
-      const int64_t head = (int64_t)h * a.c.page_size;
-      auto seen = [&](int key) { return key + t.box > lo && key < hi; };
-      auto look = [&](int i0) {  // pages of the tiles from i0 on
-        const int i = i0 + lane / copies, key = (t0 + i) * kTile + lane % copies * t.box;
-        return i < n && seen(key) ? __ldg(table + (key >> a.c.page_shift)) : -1;
-      };
-      int next = look(0), pages = 0, at_tile = batch;
-      for (int i = 0; ok && i < n; i += 2, ++k) {
-        if (at_tile == batch) {
-          at_tile = 0;
-          pages = next;
-          if (i + batch < n) next = look(i + batch);
-        }
-        const Slot at(k, t.ring);
-        const int first = at_tile * copies, key0 = (t0 + i) * kTile;
-        at_tile += 2;
-        const int key = key0 + tile * kTile + part * t.box;
-        const int page = __shfl_sync(0xffffffffu, pages, (first + tile * copies + part) & 31);
-        const bool mine = part < copies && i + tile < n && seen(key);
-        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * half_bytes;
-        uint8_t* const stage = ring + (size_t)at.i * t.stage_bytes;
-        ok = wait_held(ctl.empty + at.i, at.ph ^ 1u, guard, kWaitSlot);
-        if (rare(!ok)) break;
-        if (lane == 0) mbar_arrive_expect_tx(ctl.full + at.i, bytes);
-        __syncwarp();
-        if (mine)
-          tma_load_4d_hint(stage + (2 * tile + is_v) * code_bytes + part * half_bytes, is_v ? &mv : &mk, 0,
-                           key & (a.c.page_size - 1), h, page, ctl.full + at.i, pol);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int word_page = __shfl_sync(0xffffffffu, pages, (first + e * copies + word_part) & 31);
-          const int word_key = key0 + e * kTile + 4 * lane;
-          if (i + e < n && seen(word_key - (4 * lane & (t.box - 1)))) {
-            const bool sound = word_page >= 0 && word_page < a.c.num_pages;
-            const int64_t from =
-                sound ? ((int64_t)word_page * a.c.kv_heads * a.c.page_size + head + (word_key & (a.c.page_size - 1))) * 4
-                      : 0;
-            uint8_t* const words = stage + 4 * code_bytes + e * 1024 + 16 * lane;
-            copy16(words, a.c.ks + from, sound);
-            copy16(words + 4 * kTile, a.c.vs + from, sound);
-          }
-        }
-        arrive_when_copied(ctl.full + at.i);
-      }
-    }
-    // every copy has landed before the CTA may exit
-    __syncwarp();
-    for (uint32_t i = k > t.ring.n ? k - t.ring.n : 0; i < k; ++i) {
-      const Slot at(i, t.ring);
-      if (lane == 0) wait_end(ctl.full + at.i, at.ph, guard);
-    }
-    __syncwarp();
+    copy_tiles(mk, mv, t, ctl, ring, guard, ok);
   } else if (warp == 1) {
     // ---------------- issue the products S ----------------
     const uint32_t leader = elect_leader();
@@ -1034,7 +872,6 @@ using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const U4Args);
 template <int DT>
 Kernel kernel_of(int n) {
   switch (n) {
-    case 16: return k_attend_u4<DT, 16>;
     case 32: return k_attend_u4<DT, 32>;
     case 48: return k_attend_u4<DT, 48>;
     case 64: return k_attend_u4<DT, 64>;
@@ -1053,12 +890,12 @@ cudaError_t device_ready(int* sms) {
     if (e != cudaSuccess) return e;
   }
   if (!g_sms[dev]) {
-    for (int n = 16; n <= kMaxN; n += 16)
+    for (int n = 32; n <= kMaxN; n += 16)
       for (Kernel k : {kernel_of<SV_BF16>(n), kernel_of<SV_F16>(n)}) {
         cudaFuncAttributes attr{};
         e = cudaFuncGetAttributes(&attr, (const void*)k);
         if (e != cudaSuccess) return e;
-        if (attr.numRegs < Regs<16>::kLaunch) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
+        if (attr.numRegs < Regs<32>::kLaunch) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
         e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return e;
       }
@@ -1123,28 +960,34 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   const int64_t chunk = a.b.B ? ((int64_t)a.b.total + a.b.B - 1) / a.b.B : 1;
   const int64_t items = chunk > most ? (chunk + most - 1) / most : 1;
   t.tpt = (int)(chunk < 1 ? 1 : (chunk + items - 1) / items);
-  const int N = (t.tpt * t.group + 15) / 16 * 16;
-  t.tpt = N / t.group;
   t.group_inv = (uint32_t)((65536 + t.group - 1) / t.group);
-  t.box = c.page_size < kTile ? c.page_size : kTile;
-  t.spans = c.head_dim > 64 ? 2 : 1;
-  t.stage_bytes = 2 * (kTile * c.head_dim + 1024);
-  const int fixed = 2 * (N > 64 ? 2 : 1) * kSpan + 2 * t.spans * N * 128 + 4 * N * 32 + (int)sizeof(Ctl);
-  t.ring = make_ring(((int)kSmemBytes - fixed) / t.stage_bytes, kMaxStages);
-  t.stall = attention_test().stall_cta;
-  t.wait_clocks = attention_test().wait_clocks;
   t.c = a.scale_log2;
   t.rec = reinterpret_cast<Rec*>(a.ws);
   t.err = reinterpret_cast<int*>(a.ws + kMaxCtas * sizeof(Rec));
   t.ml = reinterpret_cast<float2*>(a.ws + kRecBytes);
   t.part = reinterpret_cast<float*>(a.ws + kRecBytes + kMlBytes);
+  t.box = c.page_size < kTile ? c.page_size : kTile;
+  t.stage_bytes = 2 * (kTile * c.head_dim + 1024);
+  t.stall = attention_test().stall_cta;
+  t.wait_clocks = attention_test().wait_clocks;
   alignas(64) CUtensorMap mk{}, mv{};
   *taken = encode_codes(&mk, c, c.k, t.box) && encode_codes(&mv, c, c.v, t.box);
   if (!*taken) return cudaSuccess;
+  if (u4_few_take(c.head_dim, t.tpt * t.group))
+    return launch_attention_u4_few(t, mk, mv, t.tpt * t.group, dtype, stream);
+  const int N = (t.tpt * t.group + 15) / 16 * 16;
+  t.tpt = N / t.group;
+  t.spans = c.head_dim > 64 ? 2 : 1;
+  const int fixed = 2 * (N > 64 ? 2 : 1) * kSpan + 2 * t.spans * N * 128 + 4 * N * 32 + (int)sizeof(Ctl);
+  t.ring = make_ring(((int)kSmemBytes - fixed) / t.stage_bytes, kMaxStages);
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   e = launch_pdl(dtype == SV_BF16 ? kernel_of<SV_BF16>(N) : kernel_of<SV_F16>(N), dim3(ctas), dim3(kThreads),
                  kSmemBytes, stream, mk, mv, t);
-  if (e != cudaSuccess) return e;
+  return e == cudaSuccess ? launch_u4_join(t, dtype, ctas, stream) : e;
+}
+
+cudaError_t launch_u4_join(const U4Args& t, int dtype, int ctas, cudaStream_t stream) {
+  const AttendArgs& a = t.a;
   const int64_t rows = (int64_t)a.b.total * a.heads;
   const int join_blocks = (int)(rows < 6 * ctas ? rows : 6 * ctas);
   const int flag_blocks = a.flags ? (a.b.B + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
