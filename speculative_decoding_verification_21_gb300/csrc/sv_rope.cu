@@ -192,38 +192,50 @@ __global__ void __launch_bounds__(kRopeWarps * 32, 3)
         cs[4 * i + 3] = x.w;
       }
     }
-    // queries
-    for (int step = from; step < min(upto, q_steps); ++step) {
-      const int h = step * at_once + row;
-      if (h >= a.heads || !on) continue;
-      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-      if (angle >= 0) {
-        const char* src = a.q + t * a.q_token + (int64_t)h * a.q_head;
-        x0 = ld_row16(src + 2 * e0);
-        x1 = ld_row16(src + 2 * e1);
-        if (turned) {
+    // A step's rows are loaded while those of the step before are turned and stored.
+    const int last = page < 0 ? min(upto, q_steps) : upto;
+    uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
+    auto fetch = [&](int step) {
+      if (step < q_steps) {
+        const int h = step * at_once + row;
+        if (h < a.heads && on && angle >= 0) {
+          const char* src = a.q + t * a.q_token + (int64_t)h * a.q_head;
+          n0 = ld_row16(src + 2 * e0);
+          n1 = ld_row16(src + 2 * e1);
+        }
+      } else {
+        const int r = (step - q_steps) * at_once + row;
+        n0 = n1 = make_uint4(0, 0, 0, 0);
+        if (r < 2 * c.kv_heads && on) {
+          const int h = r >= c.kv_heads ? r - c.kv_heads : r;
+          const char* src = (r >= c.kv_heads ? a.in_v : a.in_k) + t * a.in_token + (int64_t)h * a.in_head;
+          n0 = ld_stream16(src + 2 * e0);
+          n1 = ld_stream16(src + 2 * e1);
+        }
+      }
+    };
+    if (from < last) fetch(from);
+    for (int step = from; step < last; ++step) {
+      uint4 x0 = n0, x1 = n1;
+      if (step + 1 < last) fetch(step + 1);
+      if (step < q_steps) {  // queries
+        const int h = step * at_once + row;
+        if (h >= a.heads || !on) continue;
+        if (turned && angle >= 0) {
           float f[16];
           widen16<DT>(x0, x1, f);
           turn<NEXT>(f, cs);
           narrow16<DT>(f, x0, x1);
         }
+        char* dst = a.out_q + (t * a.heads + h) * c.head_dim * 2;
+        *reinterpret_cast<uint4*>(dst + 2 * e0) = x0;
+        *reinterpret_cast<uint4*>(dst + 2 * e1) = x1;
+        continue;
       }
-      char* dst = a.out_q + (t * a.heads + h) * c.head_dim * 2;
-      *reinterpret_cast<uint4*>(dst + 2 * e0) = x0;
-      *reinterpret_cast<uint4*>(dst + 2 * e1) = x1;
-    }
-    if (page < 0) continue;
-    // keys, then values
-    for (int step = max(from, q_steps); step < upto; ++step) {
+      // keys, then values
       const int r = (step - q_steps) * at_once + row;
       const bool live = r < 2 * c.kv_heads && on, is_v = r >= c.kv_heads;
       const int h = is_v ? r - c.kv_heads : r;
-      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-      if (live) {
-        const char* src = (is_v ? a.in_v : a.in_k) + t * a.in_token + (int64_t)h * a.in_head;
-        x0 = ld_stream16(src + 2 * e0);
-        x1 = ld_stream16(src + 2 * e1);
-      }
       char* dst = (is_v ? c.v : c.k) + (int64_t)page * c.page_bytes + (int64_t)h * c.head_bytes +
                   (int64_t)slot * c.token_bytes;
       const int64_t at = ((int64_t)page * c.kv_heads + h) * c.page_size + slot;
