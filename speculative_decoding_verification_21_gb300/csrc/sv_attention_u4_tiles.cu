@@ -813,8 +813,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // lane 8i + c of the warp's 32 has dimension 4c + i, with codes 2^-24 or 2^-20 high
       const int dim = 32 * quad + 4 * (lane & 7) + (lane >> 3);
       const float back = (lane & 8 ? pow2f(20) : pow2f(24)) / kUp;
-      int hd = r0 - (int)(r0 * t.group_inv >> 16) * t.group;
-      int64_t at = ((int64_t)(seg.row0 + (int)(r0 * t.group_inv >> 16)) * a.heads + seg.h * t.group + hd) * D + dim;
+      // Outputs go by way of shared memory (P's place: the item's last product is done, and both
+      // groups meet before the next one's first), so that the stores are 16 bytes of a row: two
+      // bytes at a time an item's 80 rows took 6000 clocks.
+      const int pitch = 2 * D + 16;
+      uint8_t* const staged = pbuf + wg * (kOut * (2 * 128 + 16));
+      const bool whole = seg.slot < 0;
+      float* const part = t.part + (prow + r0) * D + dim;
 #pragma unroll 1
       for (int u = 0; u < kOut; u += 8) {
         uint32_t o[8], q[8];
@@ -822,24 +827,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld8_async(lanes + kColO + r0 + u, o);
         if (kTurns) tmem_ld8_async(lanes + kColO + N + r0 + u, q);
         tmem_wait_ld();
+        if (32 * quad >= D) continue;
+        float y[8];
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-          if (r0 + u + n < rows && dim < D) {
-            const float4 f = ctl.out[r0 + u + n];
-            // (an O without weights is not read: it may hold anything)
-            float y = f.z;
-            if (f.x != 0.0f) y = fmaf(__uint_as_float(o[n]) * back, f.x, y);
-            if (kTurns && f.y != 0.0f) y = fmaf(__uint_as_float(q[n]) * back, f.y, y);
-            if (seg.slot < 0)
-              reinterpret_cast<uint16_t*>(a.out)[at] = (uint16_t)F16<DT>::down(y, 0.0f);
-            else
-              t.part[(prow + r0 + u + n) * D + dim] = y;
-          }
-          at += D;
-          if (++hd == t.group) {
-            hd = 0;
-            at += (int64_t)(a.heads - t.group) * D;
-          }
+          const float4 f = ctl.out[r0 + u + n];
+          // (an O without weights is not read: it may hold anything)
+          y[n] = f.z;
+          if (f.x != 0.0f) y[n] = fmaf(__uint_as_float(o[n]) * back, f.x, y[n]);
+          if (kTurns && f.y != 0.0f) y[n] = fmaf(__uint_as_float(q[n]) * back, f.y, y[n]);
+        }
+        if (whole) {
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+            *reinterpret_cast<uint16_t*>(staged + (u + n) * pitch + 2 * dim) =
+                (uint16_t)F16<DT>::down(y[n], 0.0f);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+            if (r0 + u + n < rows) part[(u + n) * D] = y[n];
+        }
+      }
+      if (whole) {
+        group_sync(id);
+        for (int n = r0 + (tid >> 4); n < min(r0 + kOut, rows); n += 8) {
+          const int ch = tid & 15, tok = (int)(n * t.group_inv >> 16), hd = n - tok * t.group;
+          if (8 * ch < D)
+            reinterpret_cast<uint4*>(a.out + ((int64_t)(seg.row0 + tok) * a.heads + seg.h * t.group + hd) * D * 2)[ch] =
+                *reinterpret_cast<const uint4*>(staged + (n - r0) * pitch + 16 * ch);
         }
       }
       tc_fence_before();
