@@ -33,7 +33,11 @@ constexpr float kUp = 512.0f;
 constexpr int kQShift = 6;
 
 struct U4Args {
-  static constexpr int kItemUnits = 3, kRowTiles = 1, kSlotRows = kMaxN;
+  // An item's start and end count as so many tiles (its queries, the first maxima, sums and
+  // outputs, and a join if it is cut).  3, 8, 12, 18: a window of 1000 keys 534, 442, 418, 408
+  // us, long rounds 400, 391, 394, 397.
+  static constexpr int kItemUnits = 12;
+  static constexpr int kRowTiles = 1, kSlotRows = kMaxN;
   AttendArgs a;
   int group, tpt;      // query heads per key head; tokens per row tile
   uint32_t group_inv;  // ceil(2^16 / group): row n of an item is of token n group_inv >> 16
@@ -105,8 +109,8 @@ __device__ __forceinline__ void arrive_when_copied(uint64_t* bar) {
 }
 // One warp's work: the CTA's items, written down one after another (an item ahead of its tiles:
 // queries take a while), and their key and value pages, two tiles to a stage of the ring.
-template <class Ctl>
-__device__ __forceinline__ void copy_tiles(const CUtensorMap& mk, const CUtensorMap& mv, const U4Args& t, Ctl& ctl,
+template <class Args, class Ctl>
+__device__ __forceinline__ void copy_tiles(const CUtensorMap& mk, const CUtensorMap& mv, const Args& t, Ctl& ctl,
                                            uint8_t* ring, const Guard& guard, bool ok) {
   const AttendArgs& a = t.a;
   const int lane = threadIdx.x & 31, D = a.c.head_dim, code_bytes = kTile * D / 2;
@@ -203,7 +207,7 @@ cudaError_t launch_u4_join(const U4Args& t, int dtype, int ctas, cudaStream_t st
 // The kernel of few rows (sv_attention_u4_few.cu): whether it takes items of `rows` rows; the
 // call, with all of t set but what belongs to the tiles' copies.
 bool u4_few_take(int head_dim, int rows);
-cudaError_t launch_attention_u4_few(U4Args t, const CUtensorMap& mk, const CUtensorMap& mv, int rows, int dtype,
+cudaError_t launch_attention_u4_few(const U4Args& call, const CUtensorMap& mk, const CUtensorMap& mv, int rows, int dtype,
                                     cudaStream_t stream);
 
 }  // namespace sv

@@ -45,6 +45,11 @@ constexpr int kFewN = 64;                  // rows of an item, at most
 constexpr int kBlock = 16;                 // keys of a tile that are a warp's
 constexpr size_t kFewSmem = 227 * 1024;
 
+struct FewArgs : U4Args {
+  // (3, 5, 8, 11: rounds of 64 sequences 139, 131, 132, 136 us)
+  static constexpr int kItemUnits = 6;
+};
+
 struct FewCtl {
   uint64_t full[kMaxStages], empty[kMaxStages], segfull[4], segempty[4], qfull[2], qempty[2];
   int abort;
@@ -115,7 +120,7 @@ __device__ __forceinline__ void ld_words(uint32_t addr, uint32_t (&w)[W]) {
 template <int W, int NT>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_attend_u4_few(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                    const __grid_constant__ U4Args t, int bf16) {
+                    const __grid_constant__ FewArgs t, int bf16) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int D = 32 * W, N = 8 * NT;
   const AttendArgs& a = t.a;
@@ -647,7 +652,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-using FewKernel = void (*)(const CUtensorMap, const CUtensorMap, const U4Args, int);
+using FewKernel = void (*)(const CUtensorMap, const CUtensorMap, const FewArgs, int);
 struct Few {
   FewKernel kernel;
   int dim, rows, fixed;  // head_dim; rows of an item; bytes of shared memory beside the ring
@@ -698,11 +703,12 @@ const Few* few_for(int dim, int rows) {
 
 bool u4_few_take(int head_dim, int rows) { return few_for(head_dim, rows) != nullptr; }
 
-cudaError_t launch_attention_u4_few(U4Args t, const CUtensorMap& mk, const CUtensorMap& mv, int rows, int dtype,
+cudaError_t launch_attention_u4_few(const U4Args& call, const CUtensorMap& mk, const CUtensorMap& mv, int rows, int dtype,
                                     cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = few_ready(&sms);
   if (e != cudaSuccess) return e;
+  FewArgs t{call};
   const Few& f = *few_for(t.a.c.head_dim, rows);
   t.tpt = f.rows / t.group;
   t.ring = make_ring(((int)kFewSmem - f.fixed) / t.stage_bytes, kMaxStages);
