@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(ctl.segempty + (items & 3u));
-          mbar_arrive(ctl.qfull + b);
+          // (a test may withhold a CTA's first queries: the waits for them then run out)
+          if (t.stall != wid || items) mbar_arrive(ctl.qfull + b);
         }
       }
     }

@@ -1,0 +1,114 @@
+"""Attention over 4-bit codes by the number of an item's rows: both sides of every count at which
+another kernel or another variant of one takes over, what few rows do with masks, rows that are
+not finite and scores that rise, and waits that run out (one CTA's queries or first scores are
+withheld; it gives up after a short limit, the call returns with every sequence flagged, and the
+next call gives what a call that never stalled gives)."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import speculative_decoding_verification_21_gb300 as sv
+from tests._paged_u4 import BF, FP, CaseU4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sv.load()
+
+
+@pytest.mark.parametrize("window", [0, 150])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+@pytest.mark.parametrize("n", [7, 8, 9, 16, 17, 24, 25, 32, 33, 48, 49, 64, 65])
+def test_rows_around_the_variants_bounds(n, dim, window):
+    CaseU4([(n, 700), (n, n + 130)], group=1, dim=dim, dtype=FP if n & 1 else BF).check(window=window)
+
+
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+@pytest.mark.parametrize("L", [1, 16, 17, 127, 128, 129, 256, 257, 385, 2000])
+def test_single_tokens(dim, L):
+    """From one block of a tile to several stages, one tile or two in the last."""
+    CaseU4([(1, L), (1, 3)], group=5, dim=dim, page=32, layout="nhd").check()
+
+
+def test_batches_of_uneven_chunks():
+    """Items of the average chunk's rows: longer chunks are several, shorter ones leave rows empty."""
+    CaseU4([(1, 300), (0, 20), (13, 500), (1, 1), (2, 2), (7, 130)], group=3, dim=128).check()
+    CaseU4([(1, 300), (0, 20), (13, 500), (1, 1), (2, 2), (7, 130)], group=3, dim=96).check(window=10)
+
+
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+def test_scores_that_rise_and_fall(dim):
+    """Keys in order of their scores, upwards for one head and downwards for the other: maxima and
+    sums are rescaled at nearly every tile, or never."""
+    c = CaseU4([(2, 1500)], group=2, dim=dim)
+    c.q[:] = 6.0 * c.q[:1, :1]
+    score = torch.einsum("d,lhd->hl", c.q[0, 0].double(), c.k64[0])
+    order = torch.stack([score[0].argsort(), score[1].argsort(descending=True)])
+    for h in range(2):
+        c.k64[0][:, h] = c.k64[0][order[h], h]
+        c.c["k"][0][:, h] = c.c["k"][0][order[h], h]
+        c.sz["k"][0][:, h] = c.sz["k"][0][order[h], h]
+        j = torch.arange(1500, device="cuda")
+        p = torch.tensor(c.owned[0], device="cuda")[j // c.ps]
+        codes = c.c["k"][0][:, h]
+        c.cache.k[p, h, j % c.ps] = codes[:, 0::2] | (codes[:, 1::2] << 4)
+        c.cache.k_scale[p, h, j % c.ps] = c.sz["k"][0][:, h]
+    c.check()
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+def test_rows_that_are_not_finite_reach_few_readers_alone(which, dim):
+    c = CaseU4([(6, 200), (3, 300)], group=2, dim=dim)
+    want = c.attend()
+    page, slot = c.owned[0][197 // c.ps], 197 % c.ps
+    (c.cache.k_scale if which == "k" else c.cache.v_scale)[page, 1, slot] = math.nan
+    o = c.attend()
+    reads = torch.zeros((c.total, 4), dtype=torch.bool, device="cuda")
+    reads[3:6, 2:] = True  # positions 197 .. 199 of head 1
+    assert bool(torch.isnan(o["out"][reads]).all())
+    assert torch.equal(o["out"][~reads], want["out"][~reads])
+    assert torch.equal(o["lse"][~reads], want["lse"][~reads])
+    if which == "v":
+        assert torch.equal(o["lse"], want["lse"])
+    else:
+        assert bool(torch.isnan(o["lse"][reads]).all())
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** 30])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+def test_few_queries_of_any_size(dim, size):
+    c = CaseU4([(3, 300), (2, 150)], group=2, dim=dim)
+    c.q.mul_(size)
+    c.q[1, 0, ::2] *= 2.0 ** -20
+    c.check(scale=0.1 / size)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_a_wait_that_runs_out_is_flagged_and_the_context_survives(n):
+    """A CTA's share is some tiles of an item here, CTA 3's too.  (one token: the queries are
+    withheld; 40 tokens by four heads: the first scores)"""
+    c = CaseU4([(n, 40000)], dim=128)
+    ws = torch.zeros(sv.attention_workspace_bytes(c.cache, 8), dtype=torch.uint8, device="cuda")
+    err = ws[160 * 16:160 * 20].view(torch.int32)  # (behind 160 records of 16 bytes)
+    want = c.attend(want_flags=True, workspace=ws)
+    assert not bool(want["flags"].any()) and not bool(err.any())
+    sv.test_attention_stall(3, 1 << 22)
+    try:
+        stalled = c.attend(want_flags=True, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        sv.test_attention_stall(-1, 0)
+    assert bool((stalled["flags"] & sv.FLAG_TIMEOUT).all())
+    e = err.tolist()
+    assert e[3] & 1 and e[3] >> 8 and not any(e[:3] + e[4:])
+    for _ in range(3):
+        again = c.attend(want_flags=True, workspace=ws)
+        assert torch.equal(again["out"], want["out"]) and torch.equal(again["lse"], want["lse"])
+        assert not bool(again["flags"].any())
