@@ -13,15 +13,14 @@
 // The codes are operand A and go through tensor memory, a key (of K) or a dimension (of V)
 // to a lane:  S^T [128 keys x N rows] = K Q^T,  O^T [dims x N rows] += V^T P^T.  Shared memory
 // then carries the codes once (4 bits), Q, and P; and the products cost by the query rows
-// that there are, not by 128.  N is 16 to 80, the rows of an item: tokens of a chunk times
-// the query heads that share a key head.
+// that there are, not by 128.  N is 32 to 80, the rows of an item: tokens of a chunk times
+// the query heads that share a key head (fewer rows: sv_attention_u4_few.cu).
 //
 // Work: items of one row tile, cut into equal shares of key tiles (sv_attention_line.cuh).
 //
 // Roles of the 20 warps: 0 finds the items and fetches their pages, 1 and 3 issue the
 // products S and O, 2 converts queries, 4-7 and 8-11 spread K's and V's codes, 12-19 are two
-// softmax groups.  A softmax thread has one key and N/2
-// rows.  The running maxima are columns: they are looked at again only when some score
+// softmax groups.  A softmax thread has one key and N/2 rows.  The running maxima are columns: they are looked at again only when some score
 // passes one by kLag (a vote of the group's threads), so a tile needs no reduction across
 // lanes, and the sums stay per thread to the item's end.
 //
