@@ -204,10 +204,11 @@ __device__ __forceinline__ void copy_tiles(const CUtensorMap& mk, const CUtensor
 
 // Adds up the shares of items that were cut (and raises the flags of a call that gave up).
 cudaError_t launch_u4_join(const U4Args& t, int dtype, int ctas, cudaStream_t stream);
-// The kernel of few rows (sv_attention_u4_few.cu): whether it takes items of `rows` rows; the
-// call, with all of t set but what belongs to the tiles' copies.
-bool u4_few_take(int head_dim, int rows);
-cudaError_t launch_attention_u4_few(const U4Args& call, const CUtensorMap& mk, const CUtensorMap& mv, int rows, int dtype,
-                                    cudaStream_t stream);
+// The kernel of few rows (sv_attention_u4_few.cu).  exact: weights good to 2^-22, not 2^-11.  The
+// rows of the items that it would make of `rows` (fewer, where it does not take as many); the
+// call, with all of U4Args set but what belongs to the kernel.
+int u4_few_rows(int head_dim, int rows, bool exact);
+cudaError_t launch_attention_u4_few(const U4Args& call, const CUtensorMap& mk, const CUtensorMap& mv,
+                                    int rows, bool exact, int dtype, cudaStream_t stream);
 
 }  // namespace sv

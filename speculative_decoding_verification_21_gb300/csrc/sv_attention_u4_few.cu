@@ -29,6 +29,7 @@
 #include <cfloat>
 #include <cstdint>
 #include <mutex>
+#include <vector>
 
 #include "specverify.h"
 #include "sv_attention.h"
@@ -129,7 +130,10 @@ __device__ __forceinline__ void ld_words(uint32_t addr, uint32_t (&w)[W]) {
 }
 
 // W: words of a lane (head_dim = 32 W).  NT: eight-row tiles of an item.
-template <int W, int NT>
+// EXACT: a weight is rounded to fp16, as an fp16 output is.  Among many keys that averages out,
+// among a few it would nearly double the output's error (22 keys: 3.6e-4 of the values against
+// 2.1e-4), so there what the rounding takes off goes through a second product.
+template <int W, int NT, bool EXACT>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_attend_u4_few(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                     const __grid_constant__ FewArgs t, int bf16) {
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (__all_sync(0xffffffffu, unset == 0)) lag = kLag;
           }
           // ---- weights, as the second operand of V^T P^T ----
-          uint2 p[2][NT];
+          uint2 p[2][NT], rest[EXACT ? 2 : 1][EXACT ? NT : 1];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const uint64_t u0 = pack2(step[2 * u] * e_up, step[2 * u] * e_up),
@@ -485,37 +489,51 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               const uint64_t p0 = pack2(ex2(c[0]), ex2(c[1])), p1 = pack2(ex2(c[2]), ex2(c[3]));
               l2[nt] = fadd2(l2[nt], fadd2(p0, p1));
               z2[nt] = ffma2(p0, v0, ffma2(p1, v1, z2[nt]));
-              float w0, w1;
-              unpack2(fmul2(p0, u0), w0, w1);
-              p[u][nt].x = transposed(F16<SV_F16>::down(w0, w1));
-              unpack2(fmul2(p1, u1), w0, w1);
-              p[u][nt].y = transposed(F16<SV_F16>::down(w0, w1));
+              float w[4];
+              unpack2(fmul2(p0, u0), w[0], w[1]);
+              unpack2(fmul2(p1, u1), w[2], w[3]);
+              const uint32_t h0 = F16<SV_F16>::down(w[0], w[1]), h1 = F16<SV_F16>::down(w[2], w[3]);
+              p[u][nt] = make_uint2(transposed(h0), transposed(h1));
+              if constexpr (EXACT) {
+                const float2 r0 = F16<SV_F16>::up(h0), r1 = F16<SV_F16>::up(h1);
+                rest[u][nt] = make_uint2(transposed(F16<SV_F16>::down(w[0] - r0.x, w[1] - r0.y)),
+                                         transposed(F16<SV_F16>::down(w[2] - r1.x, w[3] - r1.y)));
+              }
             }
           }
           opened = true;
           // ---- O: 32 dimensions to a chunk, dimension 4 c + i of them to class i of column c ----
           const int vr = 8 * ((lane >> 3) & 1) + (lane & 7);
           const uint32_t vrow = block + kCode + vr * 16 * W;
+#pragma unroll 1
+          for (int turn = 0; turn < (EXACT ? 2 : 1); ++turn) {
 #pragma unroll
-          for (int q = 0; q < W; q += 2) {
+            for (int q = 0; q < W; q += 2) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t r[4];
-              if (q + 1 < W)
-                ld_transposed4(vrow + 2 * kCode * u + 16 * code_chunk(D, vr, q + (lane >> 4)), r);
-              else
-                ld_transposed2(vrow + 2 * kCode * u + 16 * code_chunk(D, vr, q), r);
+              for (int u = 0; u < 2; ++u) {
+                uint32_t r[4];
+                if (q + 1 < W)
+                  ld_transposed4(vrow + 2 * kCode * u + 16 * code_chunk(D, vr, q + (lane >> 4)), r);
+                else
+                  ld_transposed2(vrow + 2 * kCode * u + 16 * code_chunk(D, vr, q), r);
 #pragma unroll
-              for (int e = 0; e < 2 && q + e < W; ++e) {
-                uint32_t y0[4], y1[4];
-                spread(r[2 * e], y0);
-                spread(r[2 * e + 1], y1);
+                for (int e = 0; e < 2 && q + e < W; ++e) {
+                  uint32_t y0[4], y1[4];
+                  spread(r[2 * e], y0);
+                  spread(r[2 * e + 1], y1);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                  for (int h = 0; h < 2; ++h)
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt)
-                    mma16(o[2 * (q + e) + h][nt], y0[2 * h], y0[2 * h + 1], y1[2 * h], y1[2 * h + 1], p[u][nt]);
+                    for (int nt = 0; nt < NT; ++nt)
+                      mma16(o[2 * (q + e) + h][nt], y0[2 * h], y0[2 * h + 1], y1[2 * h], y1[2 * h + 1], p[u][nt]);
+                }
               }
+            }
+            if constexpr (EXACT) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) p[u][nt] = rest[u][nt];
             }
           }
         }
@@ -670,9 +688,9 @@ struct Few {
   FewKernel kernel;
   int dim, rows, fixed;  // head_dim; rows of an item; bytes of shared memory beside the ring
 };
-template <int W, int NT>
+template <int W, int NT, bool EXACT = false>
 constexpr Few few() {
-  return Few{k_attend_u4_few<W, NT>, 32 * W, 8 * NT,
+  return Few{k_attend_u4_few<W, NT, EXACT>, 32 * W, 8 * NT,
              4 * W * NT * 64 * 16 + 2 * NT * W * 32 * 16 + (int)sizeof(FewCtl)};
 }
 // By width, the items' rows that there are: as many as the warps' registers hold.  Rounds of 64
@@ -682,8 +700,19 @@ constexpr Few few() {
 const Few kFew[] = {few<4, 1>(), few<4, 2>(), few<4, 3>(), few<3, 1>(), few<3, 2>(), few<3, 3>(), few<3, 4>(),
                     few<2, 1>(), few<2, 2>(), few<2, 4>(), few<2, 6>(), few<1, 1>(), few<1, 2>(), few<1, 4>()};
 
+// The same of the exact variant, which takes more tokens as more items.
+const Few kFewExact[] = {few<4, 1, true>(), few<4, 3, true>(), few<3, 1, true>(), few<3, 4, true>(),
+                         few<2, 1, true>(), few<2, 4, true>(), few<1, 1, true>(), few<1, 4, true>()};
+
 std::mutex g_few_mu;
 int g_few_sms[64] = {};
+
+std::vector<FewKernel> few_kernels() {
+  std::vector<FewKernel> all;
+  for (const Few& f : kFew) all.push_back(f.kernel);
+  for (const Few& f : kFewExact) all.push_back(f.kernel);
+  return all;
+}
 
 cudaError_t few_ready(int* sms) {
   int dev = 0;
@@ -692,12 +721,12 @@ cudaError_t few_ready(int* sms) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_few_mu);
   if (!g_few_sms[dev]) {
-    for (const Few& f : kFew) {
+    for (FewKernel k : few_kernels()) {
       cudaFuncAttributes attr{};
-      e = cudaFuncGetAttributes(&attr, (const void*)f.kernel);
+      e = cudaFuncGetAttributes(&attr, (const void*)k);
       if (e != cudaSuccess) return e;
       if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
-      e = cudaFuncSetAttribute((const void*)f.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+      e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
       if (e != cudaSuccess) return e;
     }
     int n = 0;
@@ -709,23 +738,27 @@ cudaError_t few_ready(int* sms) {
   return cudaSuccess;
 }
 
-const Few* few_for(int dim, int rows) {
-  for (const Few& f : kFew)
-    if (f.dim == dim && f.rows >= rows) return &f;
-  return nullptr;
+// The smallest that takes `rows` rows, or else the largest there is.
+const Few* few_for(int dim, int rows, bool exact) {
+  const Few* best = nullptr;
+  const Few* const all = exact ? kFewExact : kFew;
+  const int n = (int)(exact ? sizeof(kFewExact) : sizeof(kFew)) / (int)sizeof(Few);
+  for (int i = 0; i < n; ++i)
+    if (all[i].dim == dim && !(best && best->rows >= rows)) best = all + i;
+  return best;
 }
 
 }  // namespace
 
-bool u4_few_take(int head_dim, int rows) { return few_for(head_dim, rows) != nullptr; }
+int u4_few_rows(int head_dim, int rows, bool exact) { return few_for(head_dim, rows, exact)->rows; }
 
 cudaError_t launch_attention_u4_few(const U4Args& call, const CUtensorMap& mk, const CUtensorMap& mv,
-                                    int rows, int dtype, cudaStream_t stream) {
+                                    int rows, bool exact, int dtype, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = few_ready(&sms);
   if (e != cudaSuccess) return e;
   FewArgs t{call};
-  const Few& f = *few_for(t.a.c.head_dim, rows);
+  const Few& f = *few_for(t.a.c.head_dim, rows, exact);
   t.tpt = f.rows / t.group;
   t.ring = make_ring(((int)kFewSmem - f.fixed) / t.stage_bytes, kMaxStages);
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;

@@ -987,8 +987,19 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   alignas(64) CUtensorMap mk{}, mv{};
   *taken = encode_codes(&mk, c, c.k, t.box) && encode_codes(&mv, c, c.v, t.box);
   if (!*taken) return cudaSuccess;
-  if (u4_few_take(c.head_dim, t.tpt * t.group))
-    return launch_attention_u4_few(t, mk, mv, t.tpt * t.group, dtype, stream);
+  const int rows = t.tpt * t.group;
+  if (dtype == SV_F16) {
+    // Up to 512 keys an fp16 output shows its weights' rounding, and the kernel of few rows, which
+    // can do without it, takes any number of them.  (us there and here: ten prompts of up to 450
+    // tokens, 128 wide, 225 and 197, of up to 200 85 and 83; 40 tokens behind up to 360, 96 wide, 20
+    // times, 58 and 68.)
+    const int64_t held = (int64_t)a.b.max_pages * c.page_size;
+    const int64_t keys = a.window && a.window < held - t.tpt ? a.window + t.tpt : held;
+    if (keys <= 512 && t.group <= u4_few_rows(c.head_dim, rows, true))
+      return launch_attention_u4_few(t, mk, mv, rows, true, dtype, stream);
+  }
+  if (rows <= u4_few_rows(c.head_dim, rows, false))
+    return launch_attention_u4_few(t, mk, mv, rows, false, dtype, stream);
   const int N = (t.tpt * t.group + 15) / 16 * 16;
   t.tpt = N / t.group;
   t.spans = c.head_dim > 64 ? 2 : 1;

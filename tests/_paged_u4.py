@@ -52,6 +52,8 @@ class CaseU4(Case):
     """tests._paged.Case over a cache of 4-bit codes.  What a call must not read holds NaN steps and
     zeros (a code by itself is never NaN)."""
 
+    weight = 2.0 ** -11  # what a weight may be off by, relative: an fp16 number's half step
+
     def __init__(self, lens, *, kv_heads=2, dim=64, page=16, layout="hnd", dtype=BF, shift=1.0,
                  device="cuda", **kw):
         super().__init__(lens, kv_heads=kv_heads, dim=dim, page=page, layout=layout, dtype=dtype,
@@ -117,7 +119,7 @@ class CaseU4(Case):
             delta = ((self.D + 8) * big + 8) * 2.0 ** -23
             # sums of L terms in fp32 in any order, and of 128 at a time on the tensor cores
             delta = delta + L * 2.0 ** -23
-            tol = half * o.abs() + (2.0 ** -11 + 2 * delta[..., None]) * mass * (1 + half) + lost + tiny
+            tol = half * o.abs() + (self.weight + 2 * delta[..., None]) * mass * (1 + half) + lost + tiny
             outs.append(o.reshape(n, -1, self.D))
             lses.append(lse.reshape(n, -1))
             tols.append(tol.reshape(n, -1, self.D))

@@ -90,6 +90,17 @@ def test_few_queries_of_any_size(dim, size):
     c.check(scale=0.1 / size)
 
 
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+@pytest.mark.parametrize("n,L,window", [(1, 3, 0), (1, 22, 0), (6, 23, 0), (24, 40, 0), (90, 100, 0),
+                                        (2, 224, 0), (200, 400, 0), (1, 2000, 200), (150, 1000, 16)])
+def test_few_keys_and_fp16_outputs(n, L, window, dim):
+    """Tables of up to 512 keys, or windows: a weight is the sum of two fp16 numbers there, the second the first
+    one's rounding error rounded, at most 2^-11 of 2^-11 off."""
+    c = CaseU4([(n, L), (1, 9)], group=4, dim=dim, page=32, dtype=FP)
+    c.weight = 2.0 ** -22
+    c.check(window=window)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_a_wait_that_runs_out_is_flagged_and_the_context_survives(n):
     """A CTA's share is some tiles of an item here, CTA 3's too.  (one token: the queries are
