@@ -5,14 +5,14 @@
 // k and of v) are contiguous on the packed side, and head_dim-long runs on the
 // pool's.  One warp takes one token or four, so that the search for its sequence and
 // its page is done once for all of its rows; a lane moves 16 elements of a row (two
-// 16-byte vectors of 16-bit floats, 16 bytes of e4m3 codes, 8 of 4-bit codes), and a row's lanes form an
-// aligned group of 1, 2, 4, 8 or 16 so that its largest value is a few shuffles.
-//
-// (encode_e4m3, encode_u4: the rows' codes.)
+// 16-byte vectors of 16-bit floats, 16 bytes of e4m3 codes, 8 of 4-bit codes), and a
+// row's lanes form an aligned group of 1, 2, 4, 8 or 16 so that its largest value (and
+// smallest, for 4 bits) is a few shuffles.
 //
 // Measured on GB300: 84 thousand tokens of 8 heads of 128 into e4m3 94 us, 5.5 TB/s
 // (0.81 of a copy's rate; what is missing is the arithmetic between loads and stores);
-// 174 thousand out of e4m3 171 us, 6.3 TB/s (0.93); 320 tokens 4 us.
+// 174 thousand out of e4m3 171 us, 6.3 TB/s (0.93), as many out of 4 bits 153 us, 5.9 TB/s
+// (0.89); 320 tokens 4 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>

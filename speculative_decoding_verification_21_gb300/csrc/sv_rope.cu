@@ -6,10 +6,17 @@
 //   so that equal inputs give equal codes whatever computes them.
 //
 // Bound by HBM: rows in, rows and codes out.  A warp takes one token (or a part of its
-// rows, where there are few tokens; or four tokens, where there are many).  A lane has 16
+// rows, where there are few tokens; or two tokens, where there are many).  A lane has 16
 // elements of a row as two pieces of 8, chosen so that both halves of a pair are its own:
 // [8p, 8p + 8) and [rot/2 + 8p, ...) of pairs (i, i + rot/2), neighbours else.  Its eight
 // cosines and sines are then the same for every row of the token: 64 bytes read once.
+//
+// Measured: 94 thousand tokens of 32 + 8 + 8 heads of 128 into 4 bits, and their reading back,
+// 2.4 GB, 457 us, 5.3 TB/s (0.80 of a copy's rate); what is missing is the arithmetic between
+// loads and stores, more than half of the issue slots.  Steps on the way: a step's rows loaded
+// while those before are turned 514 -> 488 us; 32 warps an SM instead of 24 (64 registers) 470,
+// 40 warps 544 (what is spilled then); two tokens a warp instead of four 457, one 461.  320
+// tokens into e4m3 6 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -137,7 +144,7 @@ __device__ __forceinline__ void narrow16(const float (&f)[16], uint4& x0, uint4&
 
 // NEXT: pairs (2i, 2i + 1).
 template <int DT, int FMT, bool NEXT>
-__global__ void __launch_bounds__(kRopeWarps * 32, 3)
+__global__ void __launch_bounds__(kRopeWarps * 32, 4)
     k_append_rope(const __grid_constant__ RopeArgs a) {
   pdl_launch_dependents();
   pdl_wait();
@@ -311,10 +318,10 @@ cudaError_t launch_kv_append_rope(const sv_kv_cache& c, const sv_kv_batch& b, co
   while ((16 << a.group_shift) < c.head_dim) ++a.group_shift;
   const int at_once = 32 >> a.group_shift;
   const int steps = (heads + at_once - 1) / at_once + (2 * c.kv_heads + at_once - 1) / at_once;
-  // four tokens a warp where that still gives every SM 16 warps; fewer tokens than that
+  // two tokens a warp where that still gives every SM 16 warps; fewer tokens than that
   // are cut into parts for as many warps
   constexpr int64_t kWarps = 152 * 16;
-  a.per = b.total >= kWarps * 4 ? 4 : 1;
+  a.per = b.total >= kWarps * 2 ? 2 : 1;
   a.parts = 1;
   a.part_steps = steps;
   if (b.total > 0 && b.total < kWarps) {
