@@ -164,10 +164,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       mbar_init(ctl.qempty + i, kFewWarps);
     }
     fence_mbar_init();
-    t.rec[wid].more = 0;
   }
   __syncthreads();
   pdl_wait();
+  if (threadIdx.x == 0) t.rec[wid].more = 0;  // (the call before may have been reading it till here)
   find_share(t, ctl);
   bool ok = *guard.flag == 0;
 

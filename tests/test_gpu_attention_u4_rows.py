@@ -90,6 +90,15 @@ def test_few_queries_of_any_size(dim, size):
     c.check(scale=0.1 / size)
 
 
+@pytest.mark.parametrize("n", [1, 40])
+def test_calls_one_behind_another_share_a_workspace(n):
+    """A call's kernels start while the last one's end: its records of what was cut are read till then."""
+    c = CaseU4([(n, 30000), (1, 500)], dim=128)
+    want = c.attend()
+    got = [c.attend() for _ in range(60)]
+    assert all(torch.equal(o["out"], want["out"]) and torch.equal(o["lse"], want["lse"]) for o in got)
+
+
 @pytest.mark.parametrize("dim", [32, 64, 96, 128])
 @pytest.mark.parametrize("n,L,window", [(1, 3, 0), (1, 22, 0), (6, 23, 0), (24, 40, 0), (90, 100, 0),
                                         (2, 224, 0), (200, 400, 0), (1, 2000, 200), (150, 1000, 16)])
