@@ -96,6 +96,13 @@ __device__ __forceinline__ void spread(uint32_t w, uint32_t* r) {
   r[3] = v & 0x00F000F0u;
 }
 
+// The E of a largest step: the next power of two, 2^-100 at least (kUp over it is finite, and what
+// weighs by so small a step is nothing); 0 where there is none.
+__device__ __forceinline__ float step_bound(float most) {
+  const float up = __uint_as_float((__float_as_uint(most) + 0x7fffffu) & 0x7f800000u);
+  return up > 0.0f ? fmaxf(up, 0x1p-100f) : 0.0f;
+}
+
 // (code for what is rare goes out of the way: the warps' eight pieces of code share instruction
 // caches that do not hold them all)
 __device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, false); }

@@ -430,8 +430,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
             }
             ws = warp_max(ws);
-            const uint32_t up = (__float_as_uint(ws) + 0x7fffffu) & 0x7f800000u;  // to a power of two
-            const float e_now = fmaxf(E, __uint_as_float(up));
+            const float e_now = fmaxf(E, step_bound(ws));
             const float fe = E < e_now ? E * (1.0f / e_now) : 1.0f;
             if (E < e_now) {
               E = e_now;

@@ -663,8 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float most = 0.0f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) most = fmaxf(most, ctl.wstep[wg][w]);
-          const uint32_t up = (__float_as_uint(most) + 0x7fffffu) & 0x7f800000u;  // to a power of two
-          const float e_now = fmaxf(E, __uint_as_float(up));
+          const float e_now = fmaxf(E, step_bound(most));
           const float fe = E < e_now ? E * (1.0f / e_now) : 1.0f;
           group_sync(id);
           const bool rose = ctl.rose[wg] != 0;

@@ -62,6 +62,25 @@ def test_scores_that_rise_and_fall(dim):
     c.check()
 
 
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+@pytest.mark.parametrize("step", [0.0, 2.0 ** -120, 2.0 ** -101])
+@pytest.mark.parametrize("n,dim", [(1, 64), (2, 128), (40, 64), (40, 128)])
+def test_rows_of_the_smallest_steps_alone(n, dim, step, which):
+    """Every row constant, as zeros that were appended are: a step of 2^-120 (or of a pool as it is
+    made, 0) is the largest there is."""
+    c = CaseU4([(n, 500)], dim=dim, dtype=FP)
+    for name, store, pool, sz in (("k", c.k64, c.cache.k, c.cache.k_scale),
+                                  ("v", c.v64, c.cache.v, c.cache.v_scale)):
+        if which not in (name, "both"):
+            continue
+        pool.zero_()
+        sz[..., 0] = step
+        c.sz[name][0][..., 0] = step
+        c.c[name][0].zero_()
+        store[0][:] = c.sz[name][0][..., 1:].double()
+    c.check()
+
+
 @pytest.mark.parametrize("which", ["k", "v"])
 @pytest.mark.parametrize("dim", [32, 64, 96, 128])
 def test_rows_that_are_not_finite_reach_few_readers_alone(which, dim):
