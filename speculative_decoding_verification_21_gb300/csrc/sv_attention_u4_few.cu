@@ -14,7 +14,8 @@
 // some 2300 clocks of hand-overs between roles, whatever its rows.  Here one of 24 rows takes 1370,
 // one of 8 rows 1050 (sequences of 16000 keys on average), where HBM would allow 756: up to 24 rows
 // of 128 dimensions are faster here, 32 are not (O no longer fits the registers).  Narrower heads
-// leave room for more; the bounds are kFew's.
+// leave room for more; the bounds are kFew's.  (Where keys are few it takes many rows too, as more
+// items: the rule stands where the calls are told apart.)
 //
 // What bounds it: latency.  Two warps share a scheduler, O's registers allow no more; of a
 // stage's 3000 clocks (two tiles, 24 rows) the products take 1570, the exponentials 400, waits 360.

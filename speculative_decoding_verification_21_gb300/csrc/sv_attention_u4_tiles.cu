@@ -987,18 +987,21 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   *taken = encode_codes(&mk, c, c.k, t.box) && encode_codes(&mv, c, c.v, t.box);
   if (!*taken) return cudaSuccess;
   const int rows = t.tpt * t.group;
-  if (dtype == SV_F16) {
-    // Up to 512 keys an fp16 output shows its weights' rounding, and the kernel of few rows, which
-    // can do without it, takes any number of them.  (us there and here: ten prompts of up to 450
-    // tokens, 128 wide, 225 and 197, of up to 200 85 and 83; 40 tokens behind up to 360, 96 wide, 20
-    // times, 58 and 68.)
-    const int64_t held = (int64_t)a.b.max_pages * c.page_size;
-    const int64_t keys = a.window && a.window < held - t.tpt ? a.window + t.tpt : held;
-    if (keys <= 512 && t.group <= u4_few_rows(c.head_dim, rows, true))
-      return launch_attention_u4_few(t, mk, mv, rows, true, dtype, stream);
-  }
-  if (rows <= u4_few_rows(c.head_dim, rows, false))
-    return launch_attention_u4_few(t, mk, mv, rows, false, dtype, stream);
+  // Keys of an item, at most.
+  const int64_t held = (int64_t)a.b.max_pages * c.page_size;
+  const int64_t keys = a.window && a.window < held - t.tpt ? a.window + t.tpt : held;
+  // Up to 512 keys an fp16 output shows its weights' rounding, and the kernel of few rows, which
+  // can do without it, takes any number of them.  (us there and here: ten prompts of up to 450
+  // tokens, 128 wide, 225 and 197, of up to 200 85 and 83; 40 tokens behind up to 360, 96 wide, 20
+  // times, 58 and 68.)
+  const bool exact = dtype == SV_F16 && keys <= 512;
+  // Its items have fewer rows, but their starts and ends cost it less: with narrow heads and few
+  // keys it is ahead for many rows too.  (us there and here: a window of 1000 keys 64 wide 350 and
+  // 406, 96 wide 381 and 417, 128 wide 543 and 413; ten prompts of up to 900 tokens 64 wide 214
+  // and 259, 128 wide 314 and 294; long chunks on 8192 keys 64 wide 1290 and 1000.)
+  const int fit = u4_few_rows(c.head_dim, rows, exact);
+  if (rows <= fit || (t.group <= fit && (exact || (c.head_dim <= 96 && keys <= 10 * kTile))))
+    return launch_attention_u4_few(t, mk, mv, rows, exact, dtype, stream);
   const int N = (t.tpt * t.group + 15) / 16 * 16;
   t.tpt = N / t.group;
   t.spans = c.head_dim > 64 ? 2 : 1;

@@ -29,6 +29,45 @@ def test_rows_around_the_variants_bounds(n, dim, window):
     CaseU4([(n, 700), (n, n + 130)], group=1, dim=dim, dtype=FP if n & 1 else BF).check(window=window)
 
 
+def widened(c, keys):
+    """The same with a table of `keys` keys at least: which kernel takes a call goes by that too."""
+    more = -(-keys // c.ps) - c.table.shape[1]
+    if more > 0:
+        c.table = torch.nn.functional.pad(c.table, (0, more), value=2 ** 30)
+    return c
+
+
+@pytest.mark.parametrize("window", [0, 150, 1500])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128])
+@pytest.mark.parametrize("n", [7, 16, 25, 33, 49, 65, 81, 200])
+def test_rows_in_wide_tables(n, dim, window):
+    """Many rows of narrow heads, of few keys in tables of many."""
+    widened(CaseU4([(n, 1700 if window > 150 else 700), (n, n + 130)], group=1, dim=dim,
+                   dtype=FP if n & 1 else BF), 4000).check(window=window)
+
+
+@pytest.mark.parametrize("dim", [32, 64, 96])
+@pytest.mark.parametrize("group,n", [(3, 40), (5, 20), (8, 12), (16, 7), (40, 2), (80, 1)])
+def test_groups_in_wide_tables(group, n, dim):
+    widened(CaseU4([(n, 300), (1, 129), (2 * n, 400)], group=group, dim=dim, kv_heads=1), 2000).check()
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("dim", [64, 96])
+def test_rows_that_are_not_finite_in_wide_tables(which, dim):
+    c = widened(CaseU4([(40, 200), (6, 300)], dim=dim), 2000)
+    want = c.attend()
+    for pos in (170, 199):
+        page, slot = c.owned[0][pos // c.ps], pos % c.ps
+        (c.cache.k_scale if which == "k" else c.cache.v_scale)[page, 1, slot] = math.nan
+    o = c.attend()
+    reads = torch.zeros((c.total, 2 * c.G), dtype=torch.bool, device="cuda")
+    reads[10:40, c.G:] = True
+    assert bool(torch.isnan(o["out"][reads]).all())
+    assert torch.equal(o["out"][~reads], want["out"][~reads])
+    assert torch.equal(o["lse"][~reads], want["lse"][~reads])
+
+
 @pytest.mark.parametrize("dim", [32, 64, 96, 128])
 @pytest.mark.parametrize("L", [1, 16, 17, 127, 128, 129, 256, 257, 385, 2000])
 def test_single_tokens(dim, L):
