@@ -22,7 +22,7 @@
 //
 // Tried: a ring of asynchronous copies for each warp (no page warp: 567 instructions for 16 keys
 // and 24 rows, now 350; 228 us); sixteen warps, half the rows each, at 104 registers (they spill:
-// 260 us); one tile at a time.
+// 260 us).
 //
 // Work: items of one row tile, cut into equal shares of key tiles (sv_attention_line.cuh).
 #include <cuda_runtime.h>
