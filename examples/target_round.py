@@ -4,7 +4,8 @@ A one-layer attention model with random weights is the target; the same model wi
 attention is the draft (the next token from the last one alone).  Prompts of different lengths enter the paged
 cache as one chunk; every round then
 
-  1. writes the chunk's keys and values into the cache (spec_kv_append),
+  1. writes the chunk's keys and values into the cache (spec_kv_append; with rotary positions
+     spec_kv_append_rope, which turns the keys and the queries on the way),
   2. attends over the cache (spec_chunk_attention),
   3. verifies the drafts against the target's probabilities with given uniforms
      (spec_verify_probs), and
@@ -12,7 +13,7 @@ cache as one chunk; every round then
 
 At the end the cached prefixes are read back (spec_kv_read), as for a move to another pool.
 
-    python examples/target_round.py [--rounds 8] [--e4m3]
+    python examples/target_round.py [--rounds 8] [--e4m3 | --u4] [--rotary]
 """
 from __future__ import annotations
 
@@ -27,9 +28,10 @@ import speculative_decoding_verification_21_gb300 as sv  # noqa: E402
 
 
 class ToyTarget:
-    """Embedding, one grouped-head attention layer over a paged cache, output head."""
+    """Embedding, one grouped-head attention layer over a paged cache, output head.  rotary: for how
+    many positions (0: the attention knows none)."""
 
-    def __init__(self, vocab=512, heads=8, kv_heads=2, head_dim=64, seed=0, device="cuda"):
+    def __init__(self, vocab=512, heads=8, kv_heads=2, head_dim=64, seed=0, device="cuda", rotary=0):
         g = torch.Generator(device=device)
         g.manual_seed(seed)
         width = heads * head_dim
@@ -40,6 +42,11 @@ class ToyTarget:
             torch.bfloat16)
         self.w_out = (randn(width, width) * width ** -0.5).to(torch.bfloat16)
         self.head = (randn(width, vocab) * 0.3).to(torch.bfloat16)
+        self.cos_sin = None
+        if rotary:
+            i = torch.arange(head_dim // 2, device=device).double()
+            turn = torch.arange(rotary, device=device)[:, None] * 10000.0 ** (-2 * i / head_dim)
+            self.cos_sin = torch.cat([turn.cos(), turn.sin()], 1).float()
 
     def draft_logits(self, tokens):
         """The draft model: logits of the next token from the last token's embedding."""
@@ -51,7 +58,10 @@ class ToyTarget:
         x = self.embed[tokens]
         qkv = (x @ self.w_qkv).view(len(tokens), -1, self.head_dim)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
-        sv.spec_kv_append(cache, k, v, table, q_start, kv_len)
+        if self.cos_sin is None:
+            sv.spec_kv_append(cache, k, v, table, q_start, kv_len)
+        else:
+            q = sv.spec_kv_append_rope(cache, k, v, table, q_start, kv_len, self.cos_sin, q=q)["q"]
         a = sv.spec_chunk_attention(q, cache, table, q_start, kv_len, want_lse=False)["out"]
         y = x + a.reshape(len(tokens), -1) @ self.w_out
         return y.float() @ self.head.float()
@@ -61,13 +71,13 @@ class Rounds:
     """A batch of sequences and their cache."""
 
     def __init__(self, model: ToyTarget, prompts, *, gamma=4, room=512, page_size=16, e4m3=False,
-                 seed=1):
+                 seed=1, u4=False):
         self.model, self.gamma, self.tokens = model, gamma, [list(p) for p in prompts]
         dev = model.embed.device
         B, pages = len(prompts), -(-room // page_size)
         self.room = pages * page_size
         self.check_room(-1)
-        dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+        dtype = torch.uint8 if u4 else torch.float8_e4m3fn if e4m3 else torch.bfloat16
         self.cache = sv.alloc_kv_cache(B * pages, model.kv_heads, page_size, model.head_dim,
                                        dtype=dtype, device=dev)
         self.gen = torch.Generator(device=dev)
@@ -128,10 +138,13 @@ class Rounds:
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--rounds", type=int, default=8)
-    ap.add_argument("--e4m3", action="store_true", help="hold the cache in 8 bits")
+    held = ap.add_mutually_exclusive_group()
+    held.add_argument("--e4m3", action="store_true", help="hold the cache in 8 bits")
+    held.add_argument("--u4", action="store_true", help="hold the cache in 4 bits")
+    ap.add_argument("--rotary", action="store_true", help="rotary positions")
     a = ap.parse_args()
     prompts = [list(range(3 + 5 * b, 3 + 5 * b + n)) for b, n in enumerate((40, 7, 130, 1))]
-    r = Rounds(ToyTarget(), prompts, e4m3=a.e4m3)
+    r = Rounds(ToyTarget(rotary=512 if a.rotary else 0), prompts, e4m3=a.e4m3, u4=a.u4)
     for _ in range(a.rounds):
         r.round()
     k, _, start = r.cached()

@@ -50,7 +50,7 @@ namespace {
 constexpr int kFewWarps = 8, kFewThreads = 32 * (kFewWarps + 4);
 constexpr int kLaunchRegs = 168, kCopyRegs = 64, kWorkRegs = 216;
 static_assert(32 * kFewWarps * kWorkRegs + 128 * kCopyRegs <= kFewThreads * kLaunchRegs, "registers");
-constexpr int kFewN = 64;                  // rows of an item, at most
+constexpr int kFewN = 48;                  // rows of an item, at most
 constexpr int kBlock = 16;                 // keys of a tile that are a warp's
 constexpr size_t kFewSmem = 227 * 1024;
 
