@@ -477,8 +477,8 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  * rounded to `dtype` for the product with v, and an SV_E4M3 cache is dequantised
  * to `dtype` (exact in SV_BF16; in SV_F16 to nearest, so that what lies beyond 65504
  * becomes an infinity and what lies below 2^-25 a zero).  An SV_U4 cache is not
- * dequantised: q.k_j = z_j sum(q) + s_j (q.c_j) in fp32, out = sum_j (p_j s_j) c_j +
- * sum_j p_j z_j with p_j s_j in fp16, relative to the largest step that the sequence's
+ * dequantised: q.k_j = z_j sum(q) + s_j (q.c_j) in fp32, out = sum_j (p_j s_j) (c_j - 8) +
+ * sum_j p_j (z_j + 8 s_j) with p_j s_j in fp16, relative to the largest step that the sequence's
  * key head has shown so far (weights below 2^-33 of that step are lost; with an SV_F16
  * output and at most 512 keys in the table or the window, p_j s_j is the sum of two).
  *   out       [total][heads][head_dim] of `dtype`, contiguous, 16-byte aligned

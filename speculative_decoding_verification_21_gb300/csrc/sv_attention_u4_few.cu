@@ -2,7 +2,7 @@
 // query rows: single tokens and short rounds.
 //
 //   k_j = z_j + s_j c_j:  t_jn = scale log2e (z_j sum(q_n) + s_j (q_n.c_j)) - m_n,
-//   p = 2^t,  l_n += p,  Z_n += p z_j,  O_n += (p s_j) c_j;  out_n = (O_n + Z_n) / l_n
+//   p = 2^t,  l_n += p,  Z_n += p (z_j + 8 s_j),  O_n += (p s_j) (c_j - 8);  out_n = (O_n + Z_n) / l_n
 //
 // Eight warps multiply.  Each has 16 of a tile's 128 keys and works by itself, on two tiles at
 // once: products of 16 keys by 8 rows (S^T = K Q^T) and of 16 dimensions by 8 rows (O^T += V^T
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               A2[e] = pack2(A, A);
               B2[e] = pack2(B, B);
               step[2 * u + e] = step_of(words[u][2 + e]);
-              zero[2 * u + e] = zero_of(words[u][2 + e]);
+              zero[2 * u + e] = centre_of(words[u][2 + e]);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -519,8 +519,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 2 && q + e < W; ++e) {
                   uint32_t y0[4], y1[4];
-                  spread(r[2 * e], y0);
-                  spread(r[2 * e + 1], y1);
+                  spread_centred(r[2 * e], y0);
+                  spread_centred(r[2 * e + 1], y1);
 #pragma unroll
                   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (e.y != 0.0f) {  // (a warp that saw nothing has l = 0)
               L += f * e.y;
               Z += f * e.z;
-              if (w == warp) co[k] = f * e.w / kUp;
+              if (w == warp) co[k] = f * e.w * (pow2f(kDown) / kUp);
             }
           }
           const float inv = s.slot >= 0 ? 1.0f : L == 0.0f ? 0.0f : 1.0f / L;
@@ -618,15 +618,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               const float* x = o[mt][nt];
               float4 y = make_float4(0, 0, 0, 0);
               if (turn) y = mine[(mt * NT + nt) * 32];
-              // (an O of no weight is not finite only where nothing may be read from it); rows
-              // g and g + 8 of a tile are of codes 2^24 and 2^20 times too small
+              // (an O of no weight is not finite only where nothing may be read from it)
               if (f.x != 0.0f) {
-                y.x += x[0] * pow2f(24) * f.x;
-                y.z += x[2] * pow2f(20) * f.x;
+                y.x += x[0] * f.x;
+                y.z += x[2] * f.x;
               }
               if (f.y != 0.0f) {
-                y.y += x[1] * pow2f(24) * f.y;
-                y.w += x[3] * pow2f(20) * f.y;
+                y.y += x[1] * f.y;
+                y.w += x[3] * f.y;
               }
               mine[(mt * NT + nt) * 32] = y;
             }

@@ -2,13 +2,9 @@
 // cores: tiles of 128 keys against up to 80 query rows, transposed.
 //
 //   k_j = z_j + s_j c_j:  t_jn = scale log2e (z_j sum(q_n) + s_j (q_n.c_j)) - m_n,
-//   p = 2^t,  l_n += p,  Z_n += p z_j,  O_n += (p s_j) c_j;  out_n = (O_n + Z_n) / l_n
+//   p = 2^t,  l_n += p,  Z_n += p (z_j + 8 s_j),  O_n += (p s_j) (c_j - 8);  out_n = (O_n + Z_n) / l_n
 //
-// A code c in 0..15 is a 16-bit float by itself: the subnormal c 2^-24, or c 2^-20 four bits
-// further up.  So a word of eight codes becomes four pairs of tensor-core operands by four
-// masks and a shift, nothing is dequantised, and the powers of two go into the queries
-// and the outputs.  The products are exact; steps and zeros act in fp32 on the scores (a row
-// of k) and on the weights (a row of v).
+// Codes as operands: sv_attention_u4.cuh.
 //
 // The codes are operand A and go through tensor memory, a key (of K) or a dimension (of V)
 // to a lane:  S^T [128 keys x N rows] = K Q^T,  O^T [dims x N rows] += V^T P^T.  Shared memory
@@ -493,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 uint32_t r[4];
-                spread(x[e], r);
+                spread_centred(x[e], r);
                 lo[2 * e] = r[0];
                 lo[2 * e + 1] = r[1];
                 hi[2 * e] = r[2];
@@ -561,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_held(ctl.sfull + b, ph, guard, kWaitS);  // (then the tile's factors are there too)
         tc_fence_after();
         const float2 kv = ctl.kv[j & 3u][row];
-        float step = step_of(__float_as_uint(kv.y)), zero = zero_of(__float_as_uint(kv.y));
+        float step = step_of(__float_as_uint(kv.y)), zero = centre_of(__float_as_uint(kv.y));
         // the rows that see the key: [first, first + span) of the group's
         int first = 0, span = C;
         const bool edge = i >= whole1 || i < whole0;
@@ -803,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f1 = a1 * y.w;
         }
         const float inv = seg.slot >= 0 ? 1.0f : L == 0.0f ? 0.0f : 1.0f / L;
-        ctl.out[n] = make_float4(f0 * inv, f1 * inv, L == 0.0f ? 0.0f : Z * inv, 0.0f);
+        ctl.out[n] = make_float4(f0 * inv * (pow2f(kDown) / kUp), f1 * inv * (pow2f(kDown) / kUp), L == 0.0f ? 0.0f : Z * inv, 0.0f);
         if (n < rows) {
           if (seg.slot >= 0) {
             t.ml[prow + n] = make_float2(m, L);
@@ -816,9 +812,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       group_sync(id);
       ok = wait_held(&ctl.ofull, qn & 1u, guard, kWaitO);
       tc_fence_after();
-      // lane 8i + c of the warp's 32 has dimension 4c + i, with codes 2^-24 or 2^-20 high
+      // lane 8i + c of the warp's 32 has dimension 4c + i
       const int dim = 32 * quad + 4 * (lane & 7) + (lane >> 3);
-      const float back = (lane & 8 ? pow2f(20) : pow2f(24)) / kUp;
       // Outputs go by way of shared memory (P's place: the item's last product is done, and both
       // groups meet before the next one's first), so that the stores are 16 bytes of a row: two
       // bytes at a time an item's 80 rows took 6000 clocks.
@@ -840,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float4 f = ctl.out[r0 + u + n];
           // (an O without weights is not read: it may hold anything)
           y[n] = f.z;
-          if (f.x != 0.0f) y[n] = fmaf(__uint_as_float(o[n]) * back, f.x, y[n]);
-          if (kTurns && f.y != 0.0f) y[n] = fmaf(__uint_as_float(q[n]) * back, f.y, y[n]);
+          if (f.x != 0.0f) y[n] = fmaf(__uint_as_float(o[n]), f.x, y[n]);
+          if (kTurns && f.y != 0.0f) y[n] = fmaf(__uint_as_float(q[n]), f.y, y[n]);
         }
         if (whole) {
 #pragma unroll
