@@ -479,8 +479,8 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  * becomes an infinity and what lies below 2^-25 a zero).  An SV_U4 cache is not
  * dequantised: q.k_j = z_j sum(q) + s_j (q.c_j) in fp32, out = sum_j (p_j s_j) (c_j - 8) +
  * sum_j p_j (z_j + 8 s_j) with p_j s_j in fp16, relative to the largest step that the sequence's
- * key head has shown so far (weights below 2^-33 of that step are lost; with an SV_F16
- * output and at most 512 keys in the table or the window, p_j s_j is the sum of two).
+ * key head has shown so far (weights below 2^-33 of that step are lost; for an SV_F16
+ * output of a query that sees at most 512 keys, p_j s_j is the sum of two).
  *   out       [total][heads][head_dim] of `dtype`, contiguous, 16-byte aligned
  *   out_lse   [total][heads] float or NULL: log sum_j exp(scale q.k_j)
  *   out_flags [B] uint8 or NULL: SV_FLAG_BAD_PAGE, SV_FLAG_BAD_LENGTH, and

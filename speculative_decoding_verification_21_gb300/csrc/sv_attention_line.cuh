@@ -1,15 +1,16 @@
 // sv_attention_line.cuh -- what the tile kernels of spec_chunk_attention share: the line of
 // work and its shares, bounded waits, rings of tiles, the join of cut items.
 //
-// Balance: all key tiles of all items form one line, an item's start worth
-// Args::kItemUnits tiles more, cut into equal shares, one per CTA (one CTA per SM).  An
+// Balance: all key tiles of all items form one line, an item's start worth some
+// tiles more (start_units), cut into equal shares, one per CTA (one CTA per SM).  An
 // item cut by a share's end leaves partial (m, l, O) in the workspace, at most two per
 // CTA, which k_attend_join adds up; an item inside a share is written at once.  Lengths
 // live on the device, so every CTA finds its own place in the line at its start.
 //
 // Args, a kernel's arguments, has: a (AttendArgs), group, tpt (tokens of a row tile), ml,
-// part, rec, err (workspace), kRowTiles (row tiles of an item), kItemUnits, kSlotRows (rows
-// of a partial slot).
+// part, rec, err (workspace), kRowTiles (row tiles of an item), kSlotRows (rows of a partial
+// slot), kItemUnits and slow_units(pos, count): what an item costs beside its `count` tiles, any
+// item and one whose first token is at position pos, in tiles.
 #pragma once
 
 #include <cuda.h>
@@ -83,15 +84,26 @@ __device__ __forceinline__ long long warp_scan64(long long v) {  // inclusive
   return v;
 }
 
+// Units of an item's start, and of all of it.
+template <class Args>
+__device__ __forceinline__ int start_units(const Args& t, const Seq& q, int per_item, int qt, int count) {
+  return Args::kItemUnits + t.slow_units(q.pos0 + qt * per_item, count);
+}
+template <class Args>
+__device__ __forceinline__ int item_units(const Args& t, const Seq& q, int per_item, int qt) {
+  const int count = item_span(q, per_item, qt, t.a.window).count;
+  return start_units(t, q, per_item, qt, count) + count;
+}
+
 // Units of one head of the lane's sequence (n = 0: none).  A sequence of many
 // items is summed by the whole warp.
-template <int UNITS>
-__device__ __forceinline__ long long head_units(const Seq& q, int per_item, int window) {
+template <class Args>
+__device__ __forceinline__ long long head_units(const Args& args, const Seq& q, int per_item) {
   const int lane = threadIdx.x & 31;
   const int nqt = (q.n + per_item - 1) / per_item;
   long long u = 0;
   if (nqt <= 4)
-    for (int t = 0; t < nqt; ++t) u += UNITS + item_span(q, per_item, t, window).count;
+    for (int t = 0; t < nqt; ++t) u += item_units(args, q, per_item, t);
   unsigned big = __ballot_sync(0xffffffffu, nqt > 4);
   while (big) {
     const int src = __ffs(big) - 1;
@@ -101,7 +113,7 @@ __device__ __forceinline__ long long head_units(const Seq& q, int per_item, int 
     s.pos0 = __shfl_sync(0xffffffffu, q.pos0, src);
     long long v = 0;
     const int m = (s.n + per_item - 1) / per_item;
-    for (int t = lane; t < m; t += 32) v += UNITS + item_span(s, per_item, t, window).count;
+    for (int t = lane; t < m; t += 32) v += item_units(args, s, per_item, t);
     v = warp_sum64(v);
     if (lane == src) u = v;
   }
@@ -135,7 +147,7 @@ __device__ void find_share(const Args& t, Ctl& ctl) {
   auto look = [&](int base) {
     q = Seq{};
     if (base + lane < b1) q = load_seq(bv, base + lane, ps);
-    per_head = head_units<Args::kItemUnits>(q, per_item, t.a.window);
+    per_head = head_units(t, q, per_item);
   };
   for (int base = b0; base < b1; base += 32) {
     look(base);
@@ -174,8 +186,7 @@ __device__ void find_share(const Args& t, Ctl& ctl) {
       const int h = (int)divide(r, ph, r);
       const int m = (s.n + per_item - 1) / per_item;
       for (int q0 = 0; q0 < m; q0 += 32) {
-        const long long c =
-            q0 + lane < m ? Args::kItemUnits + item_span(s, per_item, q0 + lane, t.a.window).count : 0;
+        const long long c = q0 + lane < m ? item_units(t, s, per_item, q0 + lane) : 0;
         const long long sc = warp_scan64(c);
         const unsigned in = __ballot_sync(0xffffffffu, r < sc);
         if (!in) {
@@ -224,7 +235,6 @@ struct Walk {
 
   template <class Args, class Ctl>
   __device__ __forceinline__ bool next(const Args& t, const Ctl& ctl, Seg& s) {
-    constexpr int kItemUnits = Args::kItemUnits;
     if (left <= 0) return false;
     const int per_item = t.tpt * Args::kRowTiles;
     while (!loaded) {
@@ -236,9 +246,9 @@ struct Walk {
     }
     const Span sp = item_span(q, per_item, qt, t.a.window);
     // units off .. off + take of the item: its start, then a unit a tile
-    const int avail = sp.count + kItemUnits - off;
+    const int start = start_units(t, q, per_item, qt, sp.count), avail = sp.count + start - off;
     const int take = (int)min((long long)avail, left);
-    const int t0 = max(0, off - kItemUnits), t1 = off + take - kItemUnits;
+    const int t0 = max(0, off - start), t1 = off + take - start;
     left -= take;
     if (t1 <= t0) return false;  // the share ends in front of the item's first tile
     s.b = b;

@@ -106,6 +106,7 @@ struct TileArgs {
   // outputs), in key tiles.  (Shares of key tiles alone: a round of 64 sequences 203 us,
   // with 1, 2, 3, 4 a start 201, 198, 197, 197; the prompt chunk 449 and 443, 439, 439, 440.)
   static constexpr int kItemUnits = 3, kRowTiles = 2, kSlotRows = kMaxRows;
+  static __device__ __forceinline__ int slow_units(int, int) { return 0; }
   AttendArgs a;
   int group, tpt;      // query heads per key head; tokens per row tile
   int nhalf;           // swizzle spans per row: 1 (head_dim <= 64) or 2

@@ -30,7 +30,7 @@
 #include <cfloat>
 #include <cstdint>
 #include <mutex>
-#include <vector>
+#include <type_traits>
 
 #include "specverify.h"
 #include "sv_attention.h"
@@ -131,9 +131,7 @@ __device__ __forceinline__ void ld_words(uint32_t addr, uint32_t (&w)[W]) {
 }
 
 // W: words of a lane (head_dim = 32 W).  NT: eight-row tiles of an item.
-// EXACT: a weight is rounded to fp16, as an fp16 output is.  Among many keys that averages out,
-// among a few it would nearly double the output's error (22 keys: 3.6e-4 of the values against
-// 2.1e-4), so there what the rounding takes off goes through a second product.
+// EXACT: outputs are fp16, items of few keys have exact weights (kExactKeys).
 template <int W, int NT, bool EXACT>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_attend_u4_few(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -280,269 +278,285 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const int whole1 = (s.pos + 1) / kTile - s.t0;
       const int whole0 = a.window ? max(0, s.pos + s.ntok - 1 - a.window) / kTile + 1 - s.t0 : 0;
 
+      // Two loops, for the registers: a window of 1000 keys, in fp16 and 96 wide, takes 388 us without
+      // the exact one, 408 with it, 445 with a branch in one loop for both, and 410 with two bodies of
+      // all that an item takes.
+      auto all_tiles = [&](auto exact) {
+        constexpr int U = exact ? 1 : 2;  // tiles at once (what is exact takes registers)
 #pragma unroll 1
-      for (int i = 0; i < tiles; i += 2) {
-        ok = wait_held(ctl.full + slot, phase, guard, kWaitSlot);
-        if (rare(!ok)) break;
-        if (i < seen1 && i + 1 >= seen0) {
-          // Two blocks at once, u of tile i + u (of one that is not there, or not seen, all is
-          // hidden).
-          constexpr int kCode = kTile * D / 2;
-          const uint32_t stage = smem_u32(ring) + slot * t.stage_bytes, block = stage + kBlock * 16 * W * warp;
-          uint32_t words[2][4];  // of K, K + 8, V, V + 8
+        for (int i = 0; i < tiles; i += 2) {
+          ok = wait_held(ctl.full + slot, phase, guard, kWaitSlot);
+          if (rare(!ok)) break;
+#pragma unroll 1
+          for (int v = 0; v < 2; v += U) {
+            // Block u is tile i + v + u's (of one that is not there, or not seen, all is hidden).
+            const int i0 = i + v;
+            if (i0 >= seen1 || i0 + U <= seen0) continue;
+            constexpr int kCode = kTile * D / 2;
+            const uint32_t stage = smem_u32(ring) + slot * t.stage_bytes,
+                           block = stage + 2 * kCode * v + kBlock * 16 * W * warp;
+            uint32_t words[U][4];  // of K, K + 8, V, V + 8
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              asm volatile("ld.shared.u32 %0, [%1];"
-                           : "=r"(words[u][e])
-                           : "r"(stage + 4 * kCode + 1024 * u + 4 * kBlock * warp + 4 * kTile * (e >> 1) +
-                                 4 * (g + 8 * (e & 1)))
-                           : "memory");
-          // ---- S: keys g and g + 8 ----
-          float x[2][NT][4];
-          {
-            uint32_t k0[2][W], k1[2][W];
-            // (a lane's words of a row lie in one 16-byte chunk, or W is 1 or 3 and nothing is swizzled)
-            const uint32_t in = W == 4   ? 16 * code_chunk(D, g, q4)
-                                : W == 2 ? 16 * code_chunk(D, g, q4 >> 1) + 8 * (q4 & 1)
-                                         : 4 * W * q4;
-            const uint32_t in8 = W == 4   ? 16 * code_chunk(D, g + 8, q4)
-                                 : W == 2 ? 16 * code_chunk(D, g + 8, q4 >> 1) + 8 * (q4 & 1)
-                                          : 4 * W * q4;
+              for (int e = 0; e < 4; ++e)
+                asm volatile("ld.shared.u32 %0, [%1];"
+                             : "=r"(words[u][e])
+                             : "r"(stage + 4 * kCode + 1024 * (v + u) + 4 * kBlock * warp + 4 * kTile * (e >> 1) +
+                                   4 * (g + 8 * (e & 1)))
+                             : "memory");
+            // ---- S: keys g and g + 8 ----
+            float x[U][NT][4];
+            {
+              uint32_t k0[U][W], k1[U][W];
+              // (a lane's words of a row lie in one 16-byte chunk, or W is 1 or 3 and nothing is swizzled)
+              const uint32_t in = W == 4   ? 16 * code_chunk(D, g, q4)
+                                  : W == 2 ? 16 * code_chunk(D, g, q4 >> 1) + 8 * (q4 & 1)
+                                           : 4 * W * q4;
+              const uint32_t in8 = W == 4   ? 16 * code_chunk(D, g + 8, q4)
+                                   : W == 2 ? 16 * code_chunk(D, g + 8, q4 >> 1) + 8 * (q4 & 1)
+                                            : 4 * W * q4;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              ld_words<W>(block + 2 * kCode * u + g * 16 * W + in, k0[u]);
-              ld_words<W>(block + 2 * kCode * u + (g + 8) * 16 * W + in8, k1[u]);
+              for (int u = 0; u < U; ++u) {
+                ld_words<W>(block + 2 * kCode * u + g * 16 * W + in, k0[u]);
+                ld_words<W>(block + 2 * kCode * u + (g + 8) * 16 * W + in8, k1[u]);
+              }
+#pragma unroll
+              for (int w = 0; w < W; ++w) {
+                uint32_t a0[U][4], a1[U][4];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                  spread(k0[u][w], a0[u]);
+                  spread(k1[u][w], a1[u]);
+                }
+                uint4 q[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) q[nt] = qb[(nt * W + w) * 32];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int u = 0; u < U; ++u)
+                    if (w == 0)
+                      mma16_zero(x[u][nt], a0[u][0], a1[u][0], a0[u][1], a1[u][1], make_uint2(q[nt].x, q[nt].y));
+                    else
+                      mma16(x[u][nt], a0[u][0], a1[u][0], a0[u][1], a1[u][1], make_uint2(q[nt].x, q[nt].y));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int u = 0; u < U; ++u)
+                    mma16(x[u][nt], a0[u][2], a1[u][2], a0[u][3], a1[u][3], make_uint2(q[nt].z, q[nt].w));
+              }
+            }
+            if (rare(odd)) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float2 f = *reinterpret_cast<const float2*>(ctl.qfac[items & 1u] + 8 * nt + 2 * q4);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                  x[u][nt][0] *= f.x;
+                  x[u][nt][1] *= f.y;
+                  x[u][nt][2] *= f.x;
+                  x[u][nt][3] *= f.y;
+                }
+              }
+            }
+            // ---- exponents: key 2 u + e is g + 8 e of block u ----
+            float step[2 * U], zero[2 * U];
+            float top = -kInf;
+            bool sound = true;  // no step is larger than E, and no value row is not finite
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              uint64_t A2[2], B2[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float A = step_of(words[u][e]) * c18, B = zero_of(words[u][e]) * t.c;
+                A2[e] = pack2(A, A);
+                B2[e] = pack2(B, B);
+                step[2 * u + e] = step_of(words[u][2 + e]);
+                zero[2 * u + e] = centre_of(words[u][2 + e]);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float2 sum = *reinterpret_cast<const float2*>(qsum + 8 * nt);
+                const uint64_t Q = pack2(sum.x, sum.y);
+                float* const c = x[u][nt];
+                unpack2(ffma2(pack2(c[0], c[1]), A2[0], ffma2(Q, B2[0], M2[nt])), c[0], c[1]);
+                unpack2(ffma2(pack2(c[2], c[3]), A2[1], ffma2(Q, B2[1], M2[nt])), c[2], c[3]);
+              }
+            }
+            if (rare(i0 + U > whole1 || i0 < whole0 || i0 + U > tiles)) {
+              // the rows that see a key: [first, first + span)
+#pragma unroll
+              for (int k = 0; k < 2 * U; ++k) {
+                // token j sees a key if key - pos <= j < key - pos + window
+                const int key = first_key + (i0 + (k >> 1)) * kTile + g + 8 * (k & 1), d = key - s.pos;
+                const int t0 = max(0, min(d, t.tpt));
+                const int t1 = a.window && d <= t.tpt - a.window ? max(0, d + a.window) : t.tpt;
+                const int first = t0 * t.group;
+                int span = max(0, (t1 == t.tpt ? N : t1 * t.group) - first);
+                if (key < s.lo || key >= s.hi || i0 + (k >> 1) >= tiles) span = 0;
+                if (!span) step[k] = zero[k] = 0.0f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r)
+                    if ((unsigned)(8 * nt + 2 * q4 + r - first) >= (unsigned)span)
+                      x[k >> 1][nt][2 * (k & 1) + r] = -kInf;
+              }
             }
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-              uint32_t a0[2][4], a1[2][4];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                spread(k0[u][w], a0[u]);
-                spread(k1[u][w], a1[u]);
-              }
-              uint4 q[NT];
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) q[nt] = qb[(nt * W + w) * 32];
+            for (int u = 0; u < U; ++u)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
+                top = max3(max3(top, x[u][nt][0], x[u][nt][1]), x[u][nt][2], x[u][nt][3]);
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                  if (w == 0)
-                    mma16_zero(x[u][nt], a0[u][0], a1[u][0], a0[u][1], a1[u][1], make_uint2(q[nt].x, q[nt].y));
+            for (int k = 0; k < 2 * U; ++k) sound &= fmaf(zero[k], 0.0f, step[k]) <= E;
+            if (rare(__any_sync(0xffffffffu, top > lag || !sound))) {
+              // a maximum rises, or the largest step; or a value row is not finite: it weighs nothing
+              // (0 times it would not be 0 where it is not seen), the rows that see it get their NaN
+              // here
+              float ws = 0.0f;
+              bool bad = false;
+#pragma unroll
+              for (int k = 0; k < 2 * U; ++k) {
+                const bool finite = fmaf(zero[k], 0.0f, step[k]) < kInf;
+                bad |= !finite;
+                ws = fmaxf(ws, finite ? step[k] : 0.0f);
+              }
+              if (rare(__any_sync(0xffffffffu, bad))) {
+                const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+                for (int k = 0; k < 2 * U; ++k)
+                  if (!(fmaf(zero[k], 0.0f, step[k]) < kInf)) {
+                    step[k] = zero[k] = 0.0f;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                      const float* c = x[k >> 1][nt] + 2 * (k & 1);
+                      z2[nt] = fadd2(z2[nt], pack2(c[0] == -kInf ? 0.0f : nan, c[1] == -kInf ? 0.0f : nan));
+                    }
+                  }
+              }
+              ws = warp_max(ws);
+              const float e_now = fmaxf(E, step_bound(ws));
+              const float fe = E < e_now ? E * (1.0f / e_now) : 1.0f;
+              if (E < e_now) {
+                E = e_now;
+                e_up = kUp / e_now;
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float m[2], f[2];  // (-m)
+                unpack2(M2[nt], m[0], m[1]);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  float most = fmaxf(x[0][nt][r], x[0][nt][2 + r]);
+                  if constexpr (U == 2) most = max3(most, x[U - 1][nt][r], x[U - 1][nt][2 + r]);
+#pragma unroll
+                  for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                  const bool first = (unset >> (2 * nt + r)) & 1u;
+                  f[r] = 1.0f;
+                  if (first ? most > -kInf : most > kLag) {
+                    unset &= ~(1u << (2 * nt + r));
+                    f[r] = first ? 0.0f : ex2(-most);
+                    m[r] -= most;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                      x[u][nt][r] -= most;
+                      x[u][nt][2 + r] -= most;
+                    }
+                  }
+                }
+                M2[nt] = pack2(m[0], m[1]);
+                // (a row that is seen first has no sums yet but such a NaN)
+                const uint64_t f2 = pack2(f[0], f[1]);
+                l2[nt] = fmul2(l2[nt], f2);
+                z2[nt] = fmul2(z2[nt], f2);
+                if (opened) {
+#pragma unroll
+                  for (int mt = 0; mt < 2 * W; ++mt) {
+                    o[mt][nt][0] *= f[0] * fe;
+                    o[mt][nt][1] *= f[1] * fe;
+                    o[mt][nt][2] *= f[0] * fe;
+                    o[mt][nt][3] *= f[1] * fe;
+                  }
+                }
+              }
+              if (__all_sync(0xffffffffu, unset == 0)) lag = kLag;
+            }
+            // ---- weights, as the second operand of V^T P^T ----
+            uint2 p[U][NT], rest[U][exact ? NT : 1];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const uint64_t u0 = pack2(step[2 * u] * e_up, step[2 * u] * e_up),
+                             u1 = pack2(step[2 * u + 1] * e_up, step[2 * u + 1] * e_up);
+              const uint64_t v0 = pack2(zero[2 * u], zero[2 * u]), v1 = pack2(zero[2 * u + 1], zero[2 * u + 1]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float* c = x[u][nt];
+                const uint64_t p0 = pack2(ex2(c[0]), ex2(c[1])), p1 = pack2(ex2(c[2]), ex2(c[3]));
+                l2[nt] = fadd2(l2[nt], fadd2(p0, p1));
+                z2[nt] = ffma2(p0, v0, ffma2(p1, v1, z2[nt]));
+                float w[4];
+                unpack2(fmul2(p0, u0), w[0], w[1]);
+                unpack2(fmul2(p1, u1), w[2], w[3]);
+                const uint32_t h0 = F16<SV_F16>::down(w[0], w[1]), h1 = F16<SV_F16>::down(w[2], w[3]);
+                p[u][nt] = make_uint2(transposed(h0), transposed(h1));
+                if constexpr (exact) {
+                  const float2 r0 = F16<SV_F16>::up(h0), r1 = F16<SV_F16>::up(h1);
+                  rest[u][nt] = make_uint2(transposed(F16<SV_F16>::down(w[0] - r0.x, w[1] - r0.y)),
+                                           transposed(F16<SV_F16>::down(w[2] - r1.x, w[3] - r1.y)));
+                }
+              }
+            }
+            opened = true;
+            // ---- O: 32 dimensions to a chunk, dimension 4 c + i of them to class i of column c ----
+            const int vr = 8 * ((lane >> 3) & 1) + (lane & 7);
+            const uint32_t vrow = block + kCode + vr * 16 * W;
+#pragma unroll 1
+            for (int turn = 0; turn < (exact ? 2 : 1); ++turn) {
+#pragma unroll
+              for (int q = 0; q < W; q += 2) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                  uint32_t r[4];
+                  if (q + 1 < W)
+                    ld_transposed4(vrow + 2 * kCode * u + 16 * code_chunk(D, vr, q + (lane >> 4)), r);
                   else
-                    mma16(x[u][nt], a0[u][0], a1[u][0], a0[u][1], a1[u][1], make_uint2(q[nt].x, q[nt].y));
+                    ld_transposed2(vrow + 2 * kCode * u + 16 * code_chunk(D, vr, q), r);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+                  for (int e = 0; e < 2 && q + e < W; ++e) {
+                    uint32_t y0[4], y1[4];
+                    spread_centred(r[2 * e], y0);
+                    spread_centred(r[2 * e + 1], y1);
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-                  mma16(x[u][nt], a0[u][2], a1[u][2], a0[u][3], a1[u][3], make_uint2(q[nt].z, q[nt].w));
-            }
-          }
-          if (rare(odd)) {
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float2 f = *reinterpret_cast<const float2*>(ctl.qfac[items & 1u] + 8 * nt + 2 * q4);
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                x[u][nt][0] *= f.x;
-                x[u][nt][1] *= f.y;
-                x[u][nt][2] *= f.x;
-                x[u][nt][3] *= f.y;
-              }
-            }
-          }
-          // ---- exponents: key 2 u + e is g + 8 e of block u ----
-          float step[4], zero[4];
-          float top = -kInf;
-          bool sound = true;  // no step is larger than E, and no value row is not finite
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint64_t A2[2], B2[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float A = step_of(words[u][e]) * c18, B = zero_of(words[u][e]) * t.c;
-              A2[e] = pack2(A, A);
-              B2[e] = pack2(B, B);
-              step[2 * u + e] = step_of(words[u][2 + e]);
-              zero[2 * u + e] = centre_of(words[u][2 + e]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float2 sum = *reinterpret_cast<const float2*>(qsum + 8 * nt);
-              const uint64_t Q = pack2(sum.x, sum.y);
-              float* const c = x[u][nt];
-              unpack2(ffma2(pack2(c[0], c[1]), A2[0], ffma2(Q, B2[0], M2[nt])), c[0], c[1]);
-              unpack2(ffma2(pack2(c[2], c[3]), A2[1], ffma2(Q, B2[1], M2[nt])), c[2], c[3]);
-            }
-          }
-          if (rare(i + 1 >= whole1 || i < whole0 || i + 1 >= tiles)) {
-            // the rows that see a key: [first, first + span)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              // token j sees a key if key - pos <= j < key - pos + window
-              const int key = first_key + (i + (k >> 1)) * kTile + g + 8 * (k & 1), d = key - s.pos;
-              const int t0 = max(0, min(d, t.tpt));
-              const int t1 = a.window && d <= t.tpt - a.window ? max(0, d + a.window) : t.tpt;
-              const int first = t0 * t.group;
-              int span = max(0, (t1 == t.tpt ? N : t1 * t.group) - first);
-              if (key < s.lo || key >= s.hi || i + (k >> 1) >= tiles) span = 0;
-              if (!span) step[k] = zero[k] = 0.0f;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-                  if ((unsigned)(8 * nt + 2 * q4 + r - first) >= (unsigned)span)
-                    x[k >> 1][nt][2 * (k & 1) + r] = -kInf;
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              top = max3(max3(top, x[u][nt][0], x[u][nt][1]), x[u][nt][2], x[u][nt][3]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sound &= fmaf(zero[k], 0.0f, step[k]) <= E;
-          if (rare(__any_sync(0xffffffffu, top > lag || !sound))) {
-            // a maximum rises, or the largest step; or a value row is not finite: it weighs nothing
-            // (0 times it would not be 0 where it is not seen), the rows that see it get their NaN
-            // here
-            float ws = 0.0f;
-            bool bad = false;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const bool finite = fmaf(zero[k], 0.0f, step[k]) < kInf;
-              bad |= !finite;
-              ws = fmaxf(ws, finite ? step[k] : 0.0f);
-            }
-            if (rare(__any_sync(0xffffffffu, bad))) {
-              const float nan = __int_as_float(0x7fffffff);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (!(fmaf(zero[k], 0.0f, step[k]) < kInf)) {
-                  step[k] = zero[k] = 0.0f;
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    const float* c = x[k >> 1][nt] + 2 * (k & 1);
-                    z2[nt] = fadd2(z2[nt], pack2(c[0] == -kInf ? 0.0f : nan, c[1] == -kInf ? 0.0f : nan));
-                  }
-                }
-            }
-            ws = warp_max(ws);
-            const float e_now = fmaxf(E, step_bound(ws));
-            const float fe = E < e_now ? E * (1.0f / e_now) : 1.0f;
-            if (E < e_now) {
-              E = e_now;
-              e_up = kUp / e_now;
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float m[2], f[2];  // (-m)
-              unpack2(M2[nt], m[0], m[1]);
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                float most = max3(fmaxf(x[0][nt][r], x[0][nt][2 + r]), x[1][nt][r], x[1][nt][2 + r]);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-                const bool first = (unset >> (2 * nt + r)) & 1u;
-                f[r] = 1.0f;
-                if (first ? most > -kInf : most > kLag) {
-                  unset &= ~(1u << (2 * nt + r));
-                  f[r] = first ? 0.0f : ex2(-most);
-                  m[r] -= most;
-#pragma unroll
-                  for (int u = 0; u < 2; ++u) {
-                    x[u][nt][r] -= most;
-                    x[u][nt][2 + r] -= most;
+                      for (int nt = 0; nt < NT; ++nt)
+                        mma16(o[2 * (q + e) + h][nt], y0[2 * h], y0[2 * h + 1], y1[2 * h], y1[2 * h + 1], p[u][nt]);
                   }
                 }
               }
-              M2[nt] = pack2(m[0], m[1]);
-              // (a row that is seen first has no sums yet but such a NaN)
-              const uint64_t f2 = pack2(f[0], f[1]);
-              l2[nt] = fmul2(l2[nt], f2);
-              z2[nt] = fmul2(z2[nt], f2);
-              if (opened) {
+              if constexpr (exact) {
 #pragma unroll
-                for (int mt = 0; mt < 2 * W; ++mt) {
-                  o[mt][nt][0] *= f[0] * fe;
-                  o[mt][nt][1] *= f[1] * fe;
-                  o[mt][nt][2] *= f[0] * fe;
-                  o[mt][nt][3] *= f[1] * fe;
-                }
-              }
-            }
-            if (__all_sync(0xffffffffu, unset == 0)) lag = kLag;
-          }
-          // ---- weights, as the second operand of V^T P^T ----
-          uint2 p[2][NT], rest[EXACT ? 2 : 1][EXACT ? NT : 1];
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint64_t u0 = pack2(step[2 * u] * e_up, step[2 * u] * e_up),
-                           u1 = pack2(step[2 * u + 1] * e_up, step[2 * u + 1] * e_up);
-            const uint64_t v0 = pack2(zero[2 * u], zero[2 * u]), v1 = pack2(zero[2 * u + 1], zero[2 * u + 1]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float* c = x[u][nt];
-              const uint64_t p0 = pack2(ex2(c[0]), ex2(c[1])), p1 = pack2(ex2(c[2]), ex2(c[3]));
-              l2[nt] = fadd2(l2[nt], fadd2(p0, p1));
-              z2[nt] = ffma2(p0, v0, ffma2(p1, v1, z2[nt]));
-              float w[4];
-              unpack2(fmul2(p0, u0), w[0], w[1]);
-              unpack2(fmul2(p1, u1), w[2], w[3]);
-              const uint32_t h0 = F16<SV_F16>::down(w[0], w[1]), h1 = F16<SV_F16>::down(w[2], w[3]);
-              p[u][nt] = make_uint2(transposed(h0), transposed(h1));
-              if constexpr (EXACT) {
-                const float2 r0 = F16<SV_F16>::up(h0), r1 = F16<SV_F16>::up(h1);
-                rest[u][nt] = make_uint2(transposed(F16<SV_F16>::down(w[0] - r0.x, w[1] - r0.y)),
-                                         transposed(F16<SV_F16>::down(w[2] - r1.x, w[3] - r1.y)));
+                  for (int nt = 0; nt < NT; ++nt) p[u][nt] = rest[u][nt];
               }
             }
           }
-          opened = true;
-          // ---- O: 32 dimensions to a chunk, dimension 4 c + i of them to class i of column c ----
-          const int vr = 8 * ((lane >> 3) & 1) + (lane & 7);
-          const uint32_t vrow = block + kCode + vr * 16 * W;
-#pragma unroll 1
-          for (int turn = 0; turn < (EXACT ? 2 : 1); ++turn) {
-#pragma unroll
-            for (int q = 0; q < W; q += 2) {
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                uint32_t r[4];
-                if (q + 1 < W)
-                  ld_transposed4(vrow + 2 * kCode * u + 16 * code_chunk(D, vr, q + (lane >> 4)), r);
-                else
-                  ld_transposed2(vrow + 2 * kCode * u + 16 * code_chunk(D, vr, q), r);
-#pragma unroll
-                for (int e = 0; e < 2 && q + e < W; ++e) {
-                  uint32_t y0[4], y1[4];
-                  spread_centred(r[2 * e], y0);
-                  spread_centred(r[2 * e + 1], y1);
-#pragma unroll
-                  for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                      mma16(o[2 * (q + e) + h][nt], y0[2 * h], y0[2 * h + 1], y1[2 * h], y1[2 * h + 1], p[u][nt]);
-                }
-              }
-            }
-            if constexpr (EXACT) {
-#pragma unroll
-              for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) p[u][nt] = rest[u][nt];
-            }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ctl.empty + slot);
+          if (++slot == t.ring.n) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ctl.empty + slot);
-        if (++slot == t.ring.n) {
-          slot = 0;
-          phase ^= 1u;
-        }
+      };
+      if constexpr (EXACT) {
+        if (rare(t.exact(s.pos))) all_tiles(std::true_type{});
+        else all_tiles(std::false_type{});
+      } else {
+        all_tiles(std::false_type{});
       }
       // ---- the item's end: the warps' results into one ----
 #pragma unroll
@@ -684,12 +698,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // ---------------------------------------------------------------------------
 using FewKernel = void (*)(const CUtensorMap, const CUtensorMap, const FewArgs, int);
 struct Few {
-  FewKernel kernel;
+  FewKernel bf16, fp16;
   int dim, rows, fixed;  // head_dim; rows of an item; bytes of shared memory beside the ring
 };
-template <int W, int NT, bool EXACT = false>
+template <int W, int NT>
 constexpr Few few() {
-  return Few{k_attend_u4_few<W, NT, EXACT>, 32 * W, 8 * NT,
+  return Few{k_attend_u4_few<W, NT, false>, k_attend_u4_few<W, NT, true>, 32 * W, 8 * NT,
              4 * W * NT * 64 * 16 + 2 * NT * W * 32 * 16 + (int)sizeof(FewCtl)};
 }
 // By width, the items' rows that there are: as many as the warps' registers hold.  Rounds of 64
@@ -699,19 +713,8 @@ constexpr Few few() {
 const Few kFew[] = {few<4, 1>(), few<4, 2>(), few<4, 3>(), few<3, 1>(), few<3, 2>(), few<3, 3>(), few<3, 4>(),
                     few<2, 1>(), few<2, 2>(), few<2, 4>(), few<2, 6>(), few<1, 1>(), few<1, 2>(), few<1, 4>()};
 
-// The same of the exact variant, which takes more tokens as more items.
-const Few kFewExact[] = {few<4, 1, true>(), few<4, 3, true>(), few<3, 1, true>(), few<3, 4, true>(),
-                         few<2, 1, true>(), few<2, 4, true>(), few<1, 1, true>(), few<1, 4, true>()};
-
 std::mutex g_few_mu;
 int g_few_sms[64] = {};
-
-std::vector<FewKernel> few_kernels() {
-  std::vector<FewKernel> all;
-  for (const Few& f : kFew) all.push_back(f.kernel);
-  for (const Few& f : kFewExact) all.push_back(f.kernel);
-  return all;
-}
 
 cudaError_t few_ready(int* sms) {
   int dev = 0;
@@ -720,14 +723,15 @@ cudaError_t few_ready(int* sms) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_few_mu);
   if (!g_few_sms[dev]) {
-    for (FewKernel k : few_kernels()) {
-      cudaFuncAttributes attr{};
-      e = cudaFuncGetAttributes(&attr, (const void*)k);
-      if (e != cudaSuccess) return e;
-      if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
-      e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
-      if (e != cudaSuccess) return e;
-    }
+    for (const Few& f : kFew)
+      for (FewKernel k : {f.bf16, f.fp16}) {
+        cudaFuncAttributes attr{};
+        e = cudaFuncGetAttributes(&attr, (const void*)k);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
+        e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+        if (e != cudaSuccess) return e;
+      }
     int n = 0;
     e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -738,30 +742,29 @@ cudaError_t few_ready(int* sms) {
 }
 
 // The smallest that takes `rows` rows, or else the largest there is.
-const Few* few_for(int dim, int rows, bool exact) {
+const Few* few_for(int dim, int rows) {
   const Few* best = nullptr;
-  const Few* const all = exact ? kFewExact : kFew;
-  const int n = (int)(exact ? sizeof(kFewExact) : sizeof(kFew)) / (int)sizeof(Few);
-  for (int i = 0; i < n; ++i)
-    if (all[i].dim == dim && !(best && best->rows >= rows)) best = all + i;
+  for (const Few& f : kFew)
+    if (f.dim == dim && !(best && best->rows >= rows)) best = &f;
   return best;
 }
 
 }  // namespace
 
-int u4_few_rows(int head_dim, int rows, bool exact) { return few_for(head_dim, rows, exact)->rows; }
+int u4_few_rows(int head_dim, int rows) { return few_for(head_dim, rows)->rows; }
 
 cudaError_t launch_attention_u4_few(const U4Args& call, const CUtensorMap& mk, const CUtensorMap& mv,
-                                    int rows, bool exact, int dtype, cudaStream_t stream) {
+                                    int rows, int dtype, cudaStream_t stream) {
   int sms = 0;
   cudaError_t e = few_ready(&sms);
   if (e != cudaSuccess) return e;
   FewArgs t{call};
-  const Few& f = *few_for(t.a.c.head_dim, rows, exact);
+  const Few& f = *few_for(t.a.c.head_dim, rows);
   t.tpt = f.rows / t.group;
   t.ring = make_ring(((int)kFewSmem - f.fixed) / t.stage_bytes, kMaxStages);
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  e = launch_pdl(f.kernel, dim3(ctas), dim3(kFewThreads), kFewSmem, stream, mk, mv, t, dtype == SV_BF16 ? 1 : 0);
+  const bool bf16 = dtype == SV_BF16;
+  e = launch_pdl(bf16 ? f.bf16 : f.fp16, dim3(ctas), dim3(kFewThreads), kFewSmem, stream, mk, mv, t, bf16 ? 1 : 0);
   return e == cudaSuccess ? launch_u4_join(t, dtype, ctas, stream) : e;
 }
 

@@ -32,8 +32,10 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "specverify.h"
 #include "sv_attention.h"
@@ -217,6 +219,9 @@ __device__ __forceinline__ uint64_t umma_desc_32(uint32_t smem_addr) {  // 32-by
          (uint64_t)1 << 46 | (uint64_t)6 << 61;
 }
 
+// Places of P, a key tile's weights each.
+constexpr int p_places(bool fp16, int n) { return fp16 && n <= 32 ? 4 : 2; }
+
 template <int DT, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attend_u4(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -228,12 +233,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kTurns = N <= 32;
   constexpr int C = kTurns ? N : N / 2;               // rows of a softmax group
   constexpr int kPBytes = N > 64 ? 2 * kSpan : kSpan;
+  // What the rounding takes off an exact item's weights has the place of the tile before, whose
+  // product is then waited for (in turns, where that is the other group's, one of its own).
+  constexpr bool kExact = DT == SV_F16;
+  constexpr int kRest = kTurns ? 2 : 1;  // from P's place b: b + 2, or b ^ 1
   constexpr uint32_t kColK = 72, kColV = 144, kColS = 272, kColO = 272 + 2 * N;  // tensor memory
   const AttendArgs& a = t.a;
   const int D = a.c.head_dim;
   const int q_bytes = t.spans * N * 128, code_bytes = kTile * D / 2;
   uint8_t* const pbuf = smem;
-  uint8_t* const qbuf = pbuf + 2 * kPBytes;
+  uint8_t* const qbuf = pbuf + p_places(DT == SV_F16, N) * kPBytes;
   uint8_t* const affine = qbuf + 2 * q_bytes;  // [query tile][S buffer][N] rows of 32 bytes
   uint8_t* const ring = affine + 4 * N * 32;
   Ctl& ctl = *reinterpret_cast<Ctl*>(ring + (size_t)t.ring.n * t.stage_bytes);
@@ -339,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t j = 0, qn = 0;
     for (; ok && take(s); ++qn) {
       const int n = uniform(s.n);
+      const bool exact = kExact && t.exact(uniform(s.pos));
       ok = wait_held(&ctl.oempty, (qn & 1u) ^ 1u, guard, kWaitO);
       for (int i = 0; ok && i < n; ++i, ++j) {
         const uint32_t b = j & 1u;
@@ -351,6 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int kk = 0; kk < 8; ++kk)
           umma_ts_if(leader, acc, va + kk * 8, pd + (uint64_t)(kk * 128), idesc_o, kk || more);
+        if (kExact && exact) {
+          const uint64_t rd = pdesc + (kTurns ? b + kRest : b ^ kRest) * (kPBytes >> 4);
+#pragma unroll 1
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts_if(leader, acc, va + kk * 8, rd + (uint64_t)(kk * 128), idesc_o, true);
+        }
         umma_commit_if(leader, ctl.pvfree + b);
       }
       if (ok) umma_commit_if(leader, &ctl.ofull);
@@ -551,208 +567,230 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool late = false;
       // (in turns a group's tiles are those of one S buffer, whose products always have the
       // present maxima in them: they change before the buffer's next one is issued)
-      for (int i = kTurns ? (wg ^ (int)(g & 1u)) : 0; i < tiles; i += kTurns ? 2 : 1) {
-        const uint32_t j = g + (uint32_t)i, b = kTurns ? (uint32_t)wg : j & 1u, ph = (j >> 1) & 1u;
-        const uint32_t s_tm = lanes + kColS + b * N + n0;
-        ok = wait_held(ctl.sfull + b, ph, guard, kWaitS);  // (then the tile's factors are there too)
-        tc_fence_after();
-        const float2 kv = ctl.kv[j & 3u][row];
-        float step = step_of(__float_as_uint(kv.y)), zero = centre_of(__float_as_uint(kv.y));
-        // the rows that see the key: [first, first + span) of the group's
-        int first = 0, span = C;
-        const bool edge = i >= whole1 || i < whole0;
-        if (rare(edge)) {
-          // token i sees it if key - pos <= i < key - pos + window
-          const int key = (tile0 + i) * kTile + row, d = key - pos;
-          const int t0 = max(0, min(d, t.tpt));
-          const int t1 = a.window && d <= t.tpt - a.window ? max(0, d + a.window) : t.tpt;
-          first = max(0, t0 * t.group - n0);
-          span = max(0, (t1 == t.tpt ? C : min(C, t1 * t.group - n0)) - first);
-          if (key < seg.lo || key >= seg.hi) span = 0;
-          if (!span) step = zero = 0.0f;
-        }
-        const bool masked = edge && __any_sync(0xffffffffu, span < C);
-        const uint64_t A2 = pack2(kv.x, kv.x);
-        uint32_t r[C];
-        auto load = [&]() {
-          if constexpr (C % 32 == 0) {
-            tmem_ld32_async(s_tm, r);
-          } else if constexpr (C % 16 == 0) {
-            tmem_ld16_async(s_tm, r);
-          } else {
+      // Two loops: a prompt chunk in fp16, which has no exact item, takes 1085 us without the exact
+      // loop, 1126 with it, and 1233 with a branch in one loop for both.
+      auto all_tiles = [&](auto exact) {
+        for (int i = kTurns ? (wg ^ (int)(g & 1u)) : 0; i < tiles; i += kTurns ? 2 : 1) {
+          const uint32_t j = g + (uint32_t)i, b = kTurns ? (uint32_t)wg : j & 1u, ph = (j >> 1) & 1u;
+          const uint32_t s_tm = lanes + kColS + b * N + n0;
+          ok = wait_held(ctl.sfull + b, ph, guard, kWaitS);  // (then the tile's factors are there too)
+          tc_fence_after();
+          const float2 kv = ctl.kv[j & 3u][row];
+          float step = step_of(__float_as_uint(kv.y)), zero = centre_of(__float_as_uint(kv.y));
+          // the rows that see the key: [first, first + span) of the group's
+          int first = 0, span = C;
+          const bool edge = i >= whole1 || i < whole0;
+          if (rare(edge)) {
+            // token i sees it if key - pos <= i < key - pos + window
+            const int key = (tile0 + i) * kTile + row, d = key - pos;
+            const int t0 = max(0, min(d, t.tpt));
+            const int t1 = a.window && d <= t.tpt - a.window ? max(0, d + a.window) : t.tpt;
+            first = max(0, t0 * t.group - n0);
+            span = max(0, (t1 == t.tpt ? C : min(C, t1 * t.group - n0)) - first);
+            if (key < seg.lo || key >= seg.hi) span = 0;
+            if (!span) step = zero = 0.0f;
+          }
+          const bool masked = edge && __any_sync(0xffffffffu, span < C);
+          const uint64_t A2 = pack2(kv.x, kv.x);
+          uint32_t r[C];
+          auto load = [&]() {
+            if constexpr (C % 32 == 0) {
+              tmem_ld32_async(s_tm, r);
+            } else if constexpr (C % 16 == 0) {
+              tmem_ld16_async(s_tm, r);
+            } else {
 #pragma unroll
-            for (int u = 0; u < C; u += 8) tmem_ld8_async(s_tm + u, r + u);
-          }
-          tmem_wait_ld();
-          if (rare(odd)) {
+              for (int u = 0; u < C; u += 8) tmem_ld8_async(s_tm + u, r + u);
+            }
+            tmem_wait_ld();
+            if (rare(odd)) {
 #pragma unroll
-            for (int n = 0; n < C; ++n)
-              r[n] = __float_as_uint(__uint_as_float(r[n]) * ctl.qfac[qb][n0 + n]);
-          }
-        };
-        auto hide = [&]() {
-          if (rare(masked)) {
+              for (int n = 0; n < C; ++n)
+                r[n] = __float_as_uint(__uint_as_float(r[n]) * ctl.qfac[qb][n0 + n]);
+            }
+          };
+          auto hide = [&]() {
+            if (rare(masked)) {
 #pragma unroll
-            for (int n = 0; n < C; ++n)
-              if ((unsigned)(n - first) >= (unsigned)span) r[n] = 0xff800000u;
-          }
-        };
-        load();
-        bool slow = unset || (!kTurns && (b ? stale[1] : stale[0]));  // (the same for the group)
-        if (!slow) {
-#pragma unroll
-          for (int n = 0; n < C; n += 2) {
-            float x, y;
-            unpack2(fmul2(pack2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), A2), x, y);
-            r[n] = __float_as_uint(x);
-            r[n + 1] = __float_as_uint(y);
-          }
-          hide();
-          float top = __uint_as_float(r[0]), top2 = __uint_as_float(r[1]);
-#pragma unroll
-          for (int n = 2; n < C; n += 4) {
-            top = max3(top, __uint_as_float(r[n]), __uint_as_float(r[n + 1]));
-            if (n + 2 < C) top2 = max3(top2, __uint_as_float(r[n + 2]), __uint_as_float(r[n + 3]));
-          }
-          // (a step or zero that is not finite takes the slow way too)
-          slow = group_any(id, fmaxf(top, top2) > kLag || !(fmaf(zero, 0.0f, step) <= E) || !ok);
-          if (rare(slow)) load();
-        }
-        if (rare(slow)) {
-          // a maximum rises, or the largest step, or the product was issued with older maxima
-          if (group_any(id, !ok)) {
-            late = true;
-            break;
-          }
-          // scores, maxima taken off from column `off` of mv
-          auto scores = [&](int off) {
+              for (int n = 0; n < C; ++n)
+                if ((unsigned)(n - first) >= (unsigned)span) r[n] = 0xff800000u;
+            }
+          };
+          load();
+          bool slow = unset || (!kTurns && (b ? stale[1] : stale[0]));  // (the same for the group)
+          if (!slow) {
 #pragma unroll
             for (int n = 0; n < C; n += 2) {
-              const float* k = reinterpret_cast<const float*>(ctl.mv[wg][b] + n) + off;
               float x, y;
-              unpack2(ffma2(pack2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), A2, pack2(k[0], k[2])), x, y);
+              unpack2(fmul2(pack2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), A2), x, y);
               r[n] = __float_as_uint(x);
               r[n + 1] = __float_as_uint(y);
             }
             hide();
-          };
-          scores(0);
-          over_lanes<C, true>(r);
-          if ((lane & 3) == 0)
+            float top = __uint_as_float(r[0]), top2 = __uint_as_float(r[1]);
 #pragma unroll
-            for (int n = 0; n < C / 8; ++n)
-              ctl.wmax[wg][quad][first_column<C>(lane) + n] = __uint_as_float(r[n]);
-          const bool bad = !(fmaf(zero, 0.0f, step) < kInf);
-          const float ws = warp_max(bad ? 0.0f : step);
-          if (lane == 0) ctl.wstep[wg][quad] = ws;
-          if (tid == 0) ctl.rose[wg] = ctl.unset[wg] = 0;
-          group_sync(id);
-          if (tid < C) {
-            float most = -kInf;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) most = fmaxf(most, ctl.wmax[wg][w][tid]);
-            const float was = ctl.m[wg][tid], now = most > was + kLag ? most : was;
-            ctl.m[wg][tid] = now;
-            ctl.fac[wg][tid] = now > was ? ex2(was - now) : 1.0f;
-            if (now > was) ctl.rose[wg] = 1;
-            const bool none = now == -kInf;
-            if (none && n0 + tid < rows) ctl.unset[wg] = 1;
-            // the buffer's next product (two tiles on) has the present maximum in it
-            const float m = none ? 0.0f : now, in = applies && fabsf(m) < kInf ? m : 0.0f;
-            // (and this one: with the maximum that it was issued with, less the present one)
-            ctl.mv[wg][b][tid] = make_float2(in, ctl.mv[wg][b][tid].x - m);
-            *row_entries(affine + (2 * qb + b) * (N * 32), n0 + tid, 0) =
-                row_side(parts_of(-in * inv_c * (pow2f(kQShift - 24) / ctl.qfac[qb][n0 + tid])));
-          }
-          float most = 0.0f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) most = fmaxf(most, ctl.wstep[wg][w]);
-          const float e_now = fmaxf(E, step_bound(most));
-          const float fe = E < e_now ? E * (1.0f / e_now) : 1.0f;
-          group_sync(id);
-          const bool rose = ctl.rose[wg] != 0;
-          unset = ctl.unset[wg] != 0 || (kTurns && !applies);
-          stale[0] = b ? stale[0] || rose || !applies : !applies;
-          stale[1] = b ? !applies : stale[1] || rose || !applies;
-          const bool opened = kTurns ? i > 1 : i > 0;  // O holds something of the item
-          if (opened && (rose || fe != 1.0f)) {
-#pragma unroll
-            for (int n = 0; n < C; n += 2) {
-              const float2 f = *reinterpret_cast<const float2*>(ctl.fac[wg] + n);
-              l2[n / 2] = fmul2(l2[n / 2], pack2(f.x, f.y));
-              z2[n / 2] = fmul2(z2[n / 2], pack2(f.x, f.y));
+            for (int n = 2; n < C; n += 4) {
+              top = max3(top, __uint_as_float(r[n]), __uint_as_float(r[n + 1]));
+              if (n + 2 < C) top2 = max3(top2, __uint_as_float(r[n + 2]), __uint_as_float(r[n + 3]));
             }
-            // O: its last product is done (in turns that of two tiles ago)
-            ok = kTurns ? wait_held(ctl.pvfree + b, ph ^ 1u, guard, kWaitFree)
-                        : wait_held(ctl.pvfree + (b ^ 1u), ((j - 1) >> 1) & 1u, guard, kWaitFree);
-            tc_fence_after();
-#pragma unroll 1
-            for (int u = 0; u < C; u += 8) {
-              uint32_t o[8];
-              float f[8];
-              bool still = true;
+            // (a step or zero that is not finite takes the slow way too)
+            slow = group_any(id, fmaxf(top, top2) > kLag || !(fmaf(zero, 0.0f, step) <= E) || !ok);
+            if (rare(slow)) load();
+          }
+          if (rare(slow)) {
+            // a maximum rises, or the largest step, or the product was issued with older maxima
+            if (group_any(id, !ok)) {
+              late = true;
+              break;
+            }
+            // scores, maxima taken off from column `off` of mv
+            auto scores = [&](int off) {
 #pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                f[n] = ctl.fac[wg][u + n] * fe;
-                still = still && f[n] == 1.0f;
+              for (int n = 0; n < C; n += 2) {
+                const float* k = reinterpret_cast<const float*>(ctl.mv[wg][b] + n) + off;
+                float x, y;
+                unpack2(ffma2(pack2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), A2, pack2(k[0], k[2])), x, y);
+                r[n] = __float_as_uint(x);
+                r[n + 1] = __float_as_uint(y);
               }
-              if (still) continue;  // (the same for all threads)
-              tmem_ld8_async(o_tm + u, o);
-              tmem_wait_ld();
+              hide();
+            };
+            scores(0);
+            over_lanes<C, true>(r);
+            if ((lane & 3) == 0)
 #pragma unroll
-              for (int n = 0; n < 8; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n]);
-              tmem_st8(o_tm + u, o);
+              for (int n = 0; n < C / 8; ++n)
+                ctl.wmax[wg][quad][first_column<C>(lane) + n] = __uint_as_float(r[n]);
+            const bool bad = !(fmaf(zero, 0.0f, step) < kInf);
+            const float ws = warp_max(bad ? 0.0f : step);
+            if (lane == 0) ctl.wstep[wg][quad] = ws;
+            if (tid == 0) ctl.rose[wg] = ctl.unset[wg] = 0;
+            group_sync(id);
+            if (tid < C) {
+              float most = -kInf;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) most = fmaxf(most, ctl.wmax[wg][w][tid]);
+              const float was = ctl.m[wg][tid], now = most > was + kLag ? most : was;
+              ctl.m[wg][tid] = now;
+              ctl.fac[wg][tid] = now > was ? ex2(was - now) : 1.0f;
+              if (now > was) ctl.rose[wg] = 1;
+              const bool none = now == -kInf;
+              if (none && n0 + tid < rows) ctl.unset[wg] = 1;
+              // the buffer's next product (two tiles on) has the present maximum in it
+              const float m = none ? 0.0f : now, in = applies && fabsf(m) < kInf ? m : 0.0f;
+              // (and this one: with the maximum that it was issued with, less the present one)
+              ctl.mv[wg][b][tid] = make_float2(in, ctl.mv[wg][b][tid].x - m);
+              *row_entries(affine + (2 * qb + b) * (N * 32), n0 + tid, 0) =
+                  row_side(parts_of(-in * inv_c * (pow2f(kQShift - 24) / ctl.qfac[qb][n0 + tid])));
             }
-            tmem_wait_st();
-          }
-          if (E < e_now) {
-            E = e_now;
-            e_up = kUp / e_now;
-          }
-          if (__any_sync(0xffffffffu, bad)) {
-            // a value row that is not finite weighs nothing (0 times it would not be 0 where
-            // it is not seen); the rows that do see it get their NaN here
-            const float nan = bad ? __int_as_float(0x7fffffff) : 0.0f;
+            float most = 0.0f;
 #pragma unroll
-            for (int n = 0; n < C; n += 2)
-              z2[n / 2] = fadd2(z2[n / 2], pack2((unsigned)(n - first) < (unsigned)span ? nan : 0.0f,
-                                                 (unsigned)(n + 1 - first) < (unsigned)span ? nan : 0.0f));
-            if (bad) step = zero = 0.0f;
+            for (int w = 0; w < 4; ++w) most = fmaxf(most, ctl.wstep[wg][w]);
+            const float e_now = fmaxf(E, step_bound(most));
+            const float fe = E < e_now ? E * (1.0f / e_now) : 1.0f;
+            group_sync(id);
+            const bool rose = ctl.rose[wg] != 0;
+            unset = ctl.unset[wg] != 0 || (kTurns && !applies);
+            stale[0] = b ? stale[0] || rose || !applies : !applies;
+            stale[1] = b ? !applies : stale[1] || rose || !applies;
+            const bool opened = kTurns ? i > 1 : i > 0;  // O holds something of the item
+            if (opened && (rose || fe != 1.0f)) {
+#pragma unroll
+              for (int n = 0; n < C; n += 2) {
+                const float2 f = *reinterpret_cast<const float2*>(ctl.fac[wg] + n);
+                l2[n / 2] = fmul2(l2[n / 2], pack2(f.x, f.y));
+                z2[n / 2] = fmul2(z2[n / 2], pack2(f.x, f.y));
+              }
+              // O: its last product is done (in turns that of two tiles ago)
+              ok = kTurns ? wait_held(ctl.pvfree + b, ph ^ 1u, guard, kWaitFree)
+                          : wait_held(ctl.pvfree + (b ^ 1u), ((j - 1) >> 1) & 1u, guard, kWaitFree);
+              tc_fence_after();
+#pragma unroll 1
+              for (int u = 0; u < C; u += 8) {
+                uint32_t o[8];
+                float f[8];
+                bool still = true;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                  f[n] = ctl.fac[wg][u + n] * fe;
+                  still = still && f[n] == 1.0f;
+                }
+                if (still) continue;  // (the same for all threads)
+                tmem_ld8_async(o_tm + u, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int n = 0; n < 8; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n]);
+                tmem_st8(o_tm + u, o);
+              }
+              tmem_wait_st();
+            }
+            if (E < e_now) {
+              E = e_now;
+              e_up = kUp / e_now;
+            }
+            if (__any_sync(0xffffffffu, bad)) {
+              // a value row that is not finite weighs nothing (0 times it would not be 0 where
+              // it is not seen); the rows that do see it get their NaN here
+              const float nan = bad ? __int_as_float(0x7fffffff) : 0.0f;
+#pragma unroll
+              for (int n = 0; n < C; n += 2)
+                z2[n / 2] = fadd2(z2[n / 2], pack2((unsigned)(n - first) < (unsigned)span ? nan : 0.0f,
+                                                   (unsigned)(n + 1 - first) < (unsigned)span ? nan : 0.0f));
+              if (bad) step = zero = 0.0f;
+            }
+            load();
+            scores(1);
+            group_sync(id);  // (mv and the maxima's votes are written again by the next slow tile)
           }
-          load();
-          scores(1);
-          group_sync(id);  // (mv and the maxima's votes are written again by the next slow tile)
+          // S has been read, and the next product in its place has the present maxima to take
+          fence_proxy_async();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ctl.sfree + b);
+          // weights, into P's place of two tiles ago
+          ok = wait_held(ctl.pvfree + b, ph ^ 1u, guard, kWaitFree);
+          if (exact && !kTurns)
+            ok = wait_held(ctl.pvfree + (b ^ 1u), ((j - 1) >> 1) & 1u, guard, kWaitFree) && ok;
+          const float up = step * e_up;
+          const uint64_t up2 = pack2(up, up), zero2 = pack2(zero, zero);
+          const uint32_t prow = smem_u32(pbuf + b * kPBytes + row * 128) | ((row & 7) << 4);
+          // rest: where what the rounding takes off goes, from P's place
+          auto weights = [&](auto rest_too, uint32_t rest) {
+#pragma unroll
+            for (int u = 0; u < C; u += 8) {
+              uint32_t w[4], v[4];
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) {
+                const int n = u + e;
+                const uint64_t p = pack2(ex2(__uint_as_float(r[n])), ex2(__uint_as_float(r[n + 1])));
+                l2[n / 2] = fadd2(l2[n / 2], p);
+                z2[n / 2] = ffma2(p, zero2, z2[n / 2]);
+                float x, y;
+                unpack2(fmul2(p, up2), x, y);
+                w[e / 2] = F16<SV_F16>::down(x, y);
+                if constexpr (rest_too) {
+                  const float2 had = F16<SV_F16>::up(w[e / 2]);
+                  v[e / 2] = F16<SV_F16>::down(x - had.x, y - had.y);
+                }
+              }
+              const int ch = (n0 + u) >> 3;
+              const uint32_t to = (prow ^ ((ch & 7) << 4)) + (ch >> 3) * kSpan;
+              st_shared16(to, w);
+              if constexpr (rest_too) st_shared16(to + rest, v);
+            }
+          };
+          weights(exact, ((kTurns ? b + kRest : b ^ kRest) - b) * kPBytes);
+          fence_proxy_async();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ctl.pvfull + b);
         }
-        // S has been read, and the next product in its place has the present maxima to take
-        fence_proxy_async();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ctl.sfree + b);
-        // weights, into P's place of two tiles ago
-        ok = wait_held(ctl.pvfree + b, ph ^ 1u, guard, kWaitFree);
-        const float up = step * e_up;
-        const uint64_t up2 = pack2(up, up), zero2 = pack2(zero, zero);
-        const uint32_t prow = smem_u32(pbuf + b * kPBytes + row * 128) | ((row & 7) << 4);
-#pragma unroll
-        for (int u = 0; u < C; u += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int n = u + e;
-            const uint64_t p = pack2(ex2(__uint_as_float(r[n])), ex2(__uint_as_float(r[n + 1])));
-            l2[n / 2] = fadd2(l2[n / 2], p);
-            z2[n / 2] = ffma2(p, zero2, z2[n / 2]);
-            float x, y;
-            unpack2(fmul2(p, up2), x, y);
-            w[e / 2] = F16<SV_F16>::down(x, y);
-          }
-          const int ch = (n0 + u) >> 3;
-          st_shared16((prow ^ ((ch & 7) << 4)) + (ch >> 3) * kSpan, w);
-        }
-        fence_proxy_async();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ctl.pvfull + b);
+      };
+      if constexpr (kExact) {
+        if (rare(t.exact(pos))) all_tiles(std::true_type{});
+        else all_tiles(std::false_type{});
+      } else {
+        all_tiles(std::false_type{});
       }
       g += (uint32_t)tiles;
       // ---- the item's end: sums over the keys, then O ----
@@ -978,6 +1016,7 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   t.tpt = (int)(chunk < 1 ? 1 : (chunk + items - 1) / items);
   t.group_inv = (uint32_t)((65536 + t.group - 1) / t.group);
   t.c = a.scale_log2;
+  t.exact_keys = dtype == SV_F16 ? kExactKeys : INT_MIN;
   t.rec = reinterpret_cast<Rec*>(a.ws);
   t.err = reinterpret_cast<int*>(a.ws + kMaxCtas * sizeof(Rec));
   t.ml = reinterpret_cast<float2*>(a.ws + kRecBytes);
@@ -993,22 +1032,18 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   // Keys of an item, at most.
   const int64_t held = (int64_t)a.b.max_pages * c.page_size;
   const int64_t keys = a.window && a.window < held - t.tpt ? a.window + t.tpt : held;
-  // Up to 512 keys an fp16 output shows its weights' rounding, and the kernel of few rows, which
-  // can do without it, takes any number of them.  (us there and here: ten prompts of up to 450
-  // tokens, 128 wide, 225 and 197, of up to 200 85 and 83; 40 tokens behind up to 360, 96 wide, 20
-  // times, 58 and 68.)
-  const bool exact = dtype == SV_F16 && keys <= 512;
   // Its items have fewer rows, but their starts and ends cost it less: with narrow heads and few
   // keys it is ahead for many rows too.  (us there and here: a window of 1000 keys 64 wide 350 and
   // 406, 96 wide 381 and 417, 128 wide 543 and 413; ten prompts of up to 900 tokens 64 wide 214
   // and 259, 128 wide 314 and 294; long chunks on 8192 keys 64 wide 1290 and 1000.)
-  const int fit = u4_few_rows(c.head_dim, rows, exact);
-  if (rows <= fit || (t.group <= fit && (exact || (c.head_dim <= 96 && keys <= 10 * kTile))))
-    return launch_attention_u4_few(t, mk, mv, rows, exact, dtype, stream);
+  const int fit = u4_few_rows(c.head_dim, rows);
+  if (rows <= fit || (t.group <= fit && c.head_dim <= 96 && keys <= 10 * kTile))
+    return launch_attention_u4_few(t, mk, mv, rows, dtype, stream);
   const int N = (t.tpt * t.group + 15) / 16 * 16;
   t.tpt = N / t.group;
   t.spans = c.head_dim > 64 ? 2 : 1;
-  const int fixed = 2 * (N > 64 ? 2 : 1) * kSpan + 2 * t.spans * N * 128 + 4 * N * 32 + (int)sizeof(Ctl);
+  const int fixed = p_places(dtype == SV_F16, N) * (N > 64 ? 2 : 1) * kSpan + 2 * t.spans * N * 128 +
+                    4 * N * 32 + (int)sizeof(Ctl);
   t.ring = make_ring(((int)kSmemBytes - fixed) / t.stage_bytes, kMaxStages);
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   e = launch_pdl(dtype == SV_BF16 ? kernel_of<SV_BF16>(N) : kernel_of<SV_F16>(N), dim3(ctas), dim3(kThreads),
