@@ -347,6 +347,7 @@ int spec_lmhead_verify_drafted(const void* h_target, const void* W_target, int H
  * the fp32 number nearest to 1/7.5.  The zero follows rows that are not centred (keys
  * mostly are not), which a step alone would pay for with a bit.  A row that holds NaN or
  * an infinity gets z = s = NaN and reads as NaN throughout: there is no code for one.
+ * A pool that was filled elsewhere may hold steps of zero and below.
  * What reaches the end of its type can read as an infinity there, because z and s are
  * rounded: fp16 values from 65280 on, bf16 ones of a row that spans 1.99 of the largest.
  * ------------------------------------------------------------------------- */
@@ -478,7 +479,7 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  * to `dtype` (exact in SV_BF16; in SV_F16 to nearest, so that what lies beyond 65504
  * becomes an infinity and what lies below 2^-25 a zero).  An SV_U4 cache is not
  * dequantised: q.k_j = z_j sum(q) + s_j (q.c_j) in fp32, out = sum_j (p_j s_j) (c_j - 8) +
- * sum_j p_j (z_j + 8 s_j) with p_j s_j in fp16, relative to the largest step that the sequence's
+ * sum_j p_j (z_j + 8 s_j) with p_j s_j in fp16, relative to the largest |step| that the sequence's
  * key head has shown so far (weights below 2^-33 of that step are lost; for an SV_F16
  * output of a query that sees at most 512 keys, p_j s_j is the sum of two).
  *   out       [total][heads][head_dim] of `dtype`, contiguous, 16-byte aligned

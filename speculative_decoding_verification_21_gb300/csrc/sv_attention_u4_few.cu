@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               for (int nt = 0; nt < NT; ++nt)
                 top = max3(max3(top, x[u][nt][0], x[u][nt][1]), x[u][nt][2], x[u][nt][3]);
 #pragma unroll
-            for (int k = 0; k < 2 * U; ++k) sound &= fmaf(zero[k], 0.0f, step[k]) <= E;
+            for (int k = 0; k < 2 * U; ++k) sound &= fabsf(fmaf(zero[k], 0.0f, step[k])) <= E;
             if (rare(__any_sync(0xffffffffu, top > lag || !sound))) {
               // a maximum rises, or the largest step; or a value row is not finite: it weighs nothing
               // (0 times it would not be 0 where it is not seen), the rows that see it get their NaN
@@ -419,15 +419,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               bool bad = false;
 #pragma unroll
               for (int k = 0; k < 2 * U; ++k) {
-                const bool finite = fmaf(zero[k], 0.0f, step[k]) < kInf;
+                const bool finite = fabsf(fmaf(zero[k], 0.0f, step[k])) < kInf;
                 bad |= !finite;
-                ws = fmaxf(ws, finite ? step[k] : 0.0f);
+                ws = fmaxf(ws, finite ? fabsf(step[k]) : 0.0f);
               }
               if (rare(__any_sync(0xffffffffu, bad))) {
                 const float nan = __int_as_float(0x7fffffff);
 #pragma unroll
                 for (int k = 0; k < 2 * U; ++k)
-                  if (!(fmaf(zero[k], 0.0f, step[k]) < kInf)) {
+                  if (!(fabsf(fmaf(zero[k], 0.0f, step[k])) < kInf)) {
                     step[k] = zero[k] = 0.0f;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {

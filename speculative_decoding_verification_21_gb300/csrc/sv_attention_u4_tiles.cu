@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (n + 2 < C) top2 = max3(top2, __uint_as_float(r[n + 2]), __uint_as_float(r[n + 3]));
             }
             // (a step or zero that is not finite takes the slow way too)
-            slow = group_any(id, fmaxf(top, top2) > kLag || !(fmaf(zero, 0.0f, step) <= E) || !ok);
+            slow = group_any(id, fmaxf(top, top2) > kLag || !(fabsf(fmaf(zero, 0.0f, step)) <= E) || !ok);
             if (rare(slow)) load();
           }
           if (rare(slow)) {
@@ -661,8 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int n = 0; n < C / 8; ++n)
                 ctl.wmax[wg][quad][first_column<C>(lane) + n] = __uint_as_float(r[n]);
-            const bool bad = !(fmaf(zero, 0.0f, step) < kInf);
-            const float ws = warp_max(bad ? 0.0f : step);
+            const bool bad = !(fabsf(fmaf(zero, 0.0f, step)) < kInf);
+            const float ws = warp_max(bad ? 0.0f : fabsf(step));
             if (lane == 0) ctl.wstep[wg][quad] = ws;
             if (tid == 0) ctl.rose[wg] = ctl.unset[wg] = 0;
             group_sync(id);

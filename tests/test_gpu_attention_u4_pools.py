@@ -1,0 +1,47 @@
+"""Attention over 4-bit pools of unusual contents: steps of either sign, as a pool that was filled
+elsewhere may hold."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import speculative_decoding_verification_21_gb300 as sv
+from tests._paged_u4 import BF, FP, CaseU4, values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    sv.load()
+
+
+def hold(c, name, b, sz):
+    """Sequence b's steps and zeros [L, H, 2] into c's pool; bounds go by the steps' size."""
+    scales, store = (c.cache.k_scale, c.k64) if name == "k" else (c.cache.v_scale, c.v64)
+    j = torch.arange(sz.shape[0], device="cuda")
+    page = torch.tensor(c.owned[b] + [0], device="cuda")[j // c.ps]
+    scales[page, :, j % c.ps] = sz
+    store[b] = values(c.c[name][b], sz)
+    c.sz[name][b] = torch.stack([sz[..., 0].abs(), sz[..., 1]], -1)
+
+
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+@pytest.mark.parametrize("signs", ["all", "some"])
+@pytest.mark.parametrize("n,dim,dtype", [(1, 64, BF), (5, 128, FP), (40, 64, FP), (40, 128, BF), (10, 128, FP),
+                                         (3, 160, BF)])
+def test_steps_below_zero(n, dim, dtype, signs, which):
+    c = CaseU4([(n, 700), (n, n + 130)], dim=dim, dtype=dtype)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    for name in ("k", "v"):
+        if which not in (name, "both"):
+            continue
+        for b in range(2):
+            sz = c.sz[name][b].clone()
+            down = torch.rand(sz.shape[:-1], generator=g, device="cuda") < (2.0 if signs == "all" else 0.4)
+            sz[..., 0] = torch.where(down, -sz[..., 0], sz[..., 0])
+            sz[..., 1] = torch.where(down, -sz[..., 1], sz[..., 1])
+            hold(c, name, b, sz)
+    c.check()
