@@ -204,11 +204,13 @@ __device__ __forceinline__ uint4 row_side(const Parts& p) {
   return make_uint4(p.p1 | p.p2 << 16, p.p1 | p.p3 << 16, p.p2 | p.p1 << 16, 0);
 }
 // The step that a key's products are in.  Where the codes cannot matter (a constant row has
-// the smallest step there is, or none), a step from the zero instead, and the codes are dropped:
-// z / s stays in range.
+// the smallest step there is, or none), a step from the zero instead, or 1, and the codes are
+// dropped: z / s and m / (s c) stay in range.  (A maximum is at most 2^4 times the largest |key| in
+// units of Q, so 1 / s of 2^64 leaves keys up to 2^59; a row whose step is below 2^-64 weighs by
+// its zero.)
 __device__ __forceinline__ float working_step(float s, float z, bool& drop) {
-  drop = fabsf(s) < fmaxf(fabsf(z) * 0x1p-40f, 0x1p-120f);
-  return drop ? fmaxf(fabsf(z) * 0x1p-30f, 0x1p-120f) : s;
+  drop = fabsf(s) < fmaxf(fabsf(z) * 0x1p-40f, 0x1p-64f);
+  return drop ? fmaxf(fabsf(z) * 0x1p-30f, 1.0f) : s;
 }
 // Where row n has its eight entries for m (half 0) or Q (half 1): rows of 32 bytes, swizzled.
 __device__ __forceinline__ uint4* row_entries(uint8_t* tile, int n, int half) {

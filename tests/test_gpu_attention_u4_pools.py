@@ -1,5 +1,5 @@
 """Attention over 4-bit pools of unusual contents: steps of either sign, as a pool that was filled
-elsewhere may hold."""
+elsewhere may hold, and zero rows among keys of very large products."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -45,3 +45,20 @@ def test_steps_below_zero(n, dim, dtype, signs, which):
             sz[..., 1] = torch.where(down, -sz[..., 1], sz[..., 1])
             hold(c, name, b, sz)
     c.check()
+
+
+@pytest.mark.parametrize("step", [0.0, 2.0 ** -120])
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 40])
+@pytest.mark.parametrize("n,dim", [(1, 64), (1, 128), (40, 64), (10, 128), (40, 128)])
+def test_zero_rows_among_large_products(n, dim, size, step):
+    """q.k around -2^38 or -2^58 and a scale that brings them back to -8; some later keys are zeros,
+    as bad pages read and appended zeros are held: they outweigh the rest.  (As many sequences as it
+    takes for a CTA to have several tiles of one.)"""
+    c = CaseU4([(n, 700)] * 40 + [(n, n + 430)], dim=dim)
+    c.q = -c.q.abs() * 2.0 ** 8
+    for b in range(41):
+        sz = (c.sz["k"][b].double() * size).to(BF)
+        sz[..., 1].abs_()
+        sz[300::71] = torch.tensor([step, 0.0], device="cuda").to(BF)
+        hold(c, "k", b, sz)
+    c.check(scale=1.28 / dim / size / 2.0 ** 8)
