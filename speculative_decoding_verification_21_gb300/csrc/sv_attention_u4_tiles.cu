@@ -1031,15 +1031,28 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   *taken = encode_codes(&mk, c, c.k, t.box) && encode_codes(&mv, c, c.v, t.box);
   if (!*taken) return cudaSuccess;
   const int rows = t.tpt * t.group;
-  // Keys of an item, at most.
+  // Keys of an item, at most.  (The lengths are on the device: without a window the table's width
+  // counts, not what of it is used.)
   const int64_t held = (int64_t)a.b.max_pages * c.page_size;
   const int64_t keys = a.window && a.window < held - t.tpt ? a.window + t.tpt : held;
-  // Its items have fewer rows, but their starts and ends cost it less: with narrow heads and few
-  // keys it is ahead for many rows too.  (us there and here: a window of 1000 keys 64 wide 350 and
-  // 406, 96 wide 381 and 417, 128 wide 543 and 413; ten prompts of up to 900 tokens 64 wide 214
-  // and 259, 128 wide 314 and 294; long chunks on 8192 keys 64 wide 1290 and 1000.)
-  const int fit = u4_few_rows(c.head_dim, rows);
-  if (rows <= fit || (t.group <= fit && c.head_dim <= 96 && keys <= 10 * kTile))
+  // Up to the rows of its items the kernel of few rows takes a call.  More rows are several items
+  // there, whose starts and ends cost it less than they cost this kernel: with narrow heads, items
+  // nearly full and few keys it is ahead for many rows too.  us there and here, prompts of up to
+  // 2001 tokens in a window, groups of 5 heads:
+  //   window     1000        2000        2600        3300        4500
+  //   32 wide  295  430    458  527    538  564    608  586    698  625
+  //   64 wide  371  430    491  533    541  574    590  592    661  631
+  //   96 wide  402  431    527  524    616  565    694  595    791  633
+  // and tables of 2000, 3300, 4500 keys as wide as the prompts are long: 32 wide 484 603, 1007 1062,
+  // 2002 1898; 96 wide 587 640, 1152 1144, 2279 1935; 64 wide ahead throughout.  By an item's rows,
+  // window of 1000: 96 wide, of 32 rows 27 (235 and 244) and 24 (340 and 318), 17 (659 and 448); 64
+  // wide, of 48 rows 42 (162 and 180), 40 (851 and 807), 34 (435 and 419), 32 (844 and 715); 32 wide, of
+  // 32 rows 24 (242 and 305), 17 (469 and 427).  128 wide: 543 and 413.
+  const int fit = u4_few_rows(c.head_dim, rows), live = fit / t.group * t.group;
+  const bool few_keys = c.head_dim == 32   ? keys <= 25 * kTile && live >= 24
+                        : c.head_dim == 64 ? keys <= 32 * kTile && live >= 41
+                                           : c.head_dim == 96 && keys <= 16 * kTile && live >= 26;
+  if (rows <= fit || few_keys)
     return launch_attention_u4_few(t, mk, mv, rows, dtype, stream);
   const int N = (t.tpt * t.group + 15) / 16 * 16;
   t.tpt = N / t.group;
