@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "sv_attention.h"
 #include "sv_attention_line.cuh"
@@ -28,8 +29,9 @@ constexpr int kMaxN = 80;              // query rows of an item, at most
 constexpr int kMaxStages = 6;          // of two key tiles
 // A weight p s is rounded to fp16, as an fp16 output is.  Among many keys that averages out, among a
 // few it would show (22, 100, 500 keys: errors of 2.29e-4, 2.19e-4, 2.16e-4 of the values, the
-// output's rounding alone 2.07e-4, 2.06e-4, 2.09e-4), so rows of fp16 outputs that see at most so many keys get what the rounding takes off
-// through a second product.  It goes by the item: its first row sees the fewest.
+// output's rounding alone 2.07e-4, 2.06e-4, 2.09e-4), so rows of fp16 outputs that see at most so
+// many keys get what the rounding takes off through a second product.  It goes by the item: its
+// first row sees the fewest.
 constexpr int kExactKeys = 512;
 
 // A maximum may lag by this many powers of two, and a weight p s is at most 2^kLag kUp = 2^15
@@ -48,13 +50,8 @@ struct U4Args {
   // us, long rounds 400, 391, 394, 397.
   static constexpr int kItemUnits = 12;
   static constexpr int kRowTiles = 1, kSlotRows = kMaxN;
-  // Whether an item's weights are good to 2^-22 (the first of its tokens at position pos), and what
-  // that costs its tiles.  (Of 0, 1/4, 1/2 and all of them: a window of 1000 keys over prompts, a
-  // tenth of whose rows see few keys, 445, 420, 410, 413 us.)
-  __device__ __forceinline__ bool exact(int pos) const {
-    return pos < exact_keys || (a.window && a.window <= exact_keys);
-  }
-  __device__ __forceinline__ int slow_units(int pos, int count) const { return exact(pos) ? (count + 1) / 2 : 0; }
+  static __device__ __forceinline__ bool exact(int) { return false; }
+  static __device__ __forceinline__ int slow_units(int, int) { return 0; }
   AttendArgs a;
   int group, tpt;      // query heads per key head; tokens per row tile
   uint32_t group_inv;  // ceil(2^16 / group): row n of an item is of token n group_inv >> 16
@@ -65,12 +62,24 @@ struct U4Args {
   int stall;           // test only: the CTA whose first scores are withheld (-1: none)
   long long wait_clocks;
   float c;             // scale log2 e
-  int exact_keys;      // kExactKeys for fp16 outputs, else the least int
   float* part;         // [2 * kMaxCtas][kMaxN][head_dim]
   float2* ml;          // [2 * kMaxCtas][kMaxN]
   Rec* rec;            // [kMaxCtas]
   int* err;            // [kMaxCtas]
 };
+// The same of a call with fp16 outputs.  (A type of its own: the question costs prompts in bf16, where
+// the answer is no, 18 of 1065 us.)
+struct U4ExactArgs : U4Args {
+  // Whether an item's weights are good to 2^-22 (the first of its tokens at position pos), and what
+  // that costs its tiles.  (Of 0, 1/4, 1/2 and all of them: a window of 1000 keys over prompts, a
+  // tenth of whose rows see few keys, 445, 420, 410, 413 us.)
+  __device__ __forceinline__ bool exact(int pos) const {
+    return pos < kExactKeys || (a.window && a.window <= kExactKeys);
+  }
+  __device__ __forceinline__ int slow_units(int pos, int count) const { return exact(pos) ? (count + 1) / 2 : 0; }
+};
+template <bool FP16>
+using U4ArgsOf = std::conditional_t<FP16, U4ExactArgs, U4Args>;
 
 // ---------------------------------------------------------------------------
 // Primitives.

@@ -54,7 +54,8 @@ constexpr int kFewN = 48;                  // rows of an item, at most
 constexpr int kBlock = 16;                 // keys of a tile that are a warp's
 constexpr size_t kFewSmem = 227 * 1024;
 
-struct FewArgs : U4Args {
+template <bool FP16>
+struct FewArgs : U4ArgsOf<FP16> {
   // (3, 5, 6, 8, 11: rounds of 64 sequences 139, 131, 130, 132, 136 us)
   static constexpr int kItemUnits = 6;
 };
@@ -130,14 +131,15 @@ __device__ __forceinline__ void ld_words(uint32_t addr, uint32_t (&w)[W]) {
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i]) : "r"(addr + 4 * i) : "memory");
 }
 
-// W: words of a lane (head_dim = 32 W).  NT: eight-row tiles of an item.
-// EXACT: outputs are fp16, items of few keys have exact weights (kExactKeys).
+// W: words of a lane (head_dim = 32 W).  NT: eight-row tiles of an item.  EXACT: queries and outputs
+// are fp16, and items of few keys have exact weights (kExactKeys).
 template <int W, int NT, bool EXACT>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_attend_u4_few(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                    const __grid_constant__ FewArgs t, int bf16) {
+                    const __grid_constant__ FewArgs<EXACT> t) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int D = 32 * W, N = 8 * NT;
+  constexpr bool bf16 = !EXACT;
   const AttendArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
   const int wid = (int)blockIdx.x;
@@ -696,9 +698,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-using FewKernel = void (*)(const CUtensorMap, const CUtensorMap, const FewArgs, int);
+template <bool FP16>
+using FewKernel = void (*)(const CUtensorMap, const CUtensorMap, const FewArgs<FP16>);
 struct Few {
-  FewKernel bf16, fp16;
+  FewKernel<false> bf16;
+  FewKernel<true> fp16;
   int dim, rows, fixed;  // head_dim; rows of an item; bytes of shared memory beside the ring
 };
 template <int W, int NT>
@@ -724,12 +728,12 @@ cudaError_t few_ready(int* sms) {
   std::lock_guard<std::mutex> lock(g_few_mu);
   if (!g_few_sms[dev]) {
     for (const Few& f : kFew)
-      for (FewKernel k : {f.bf16, f.fp16}) {
+      for (const void* k : {(const void*)f.bf16, (const void*)f.fp16}) {
         cudaFuncAttributes attr{};
-        e = cudaFuncGetAttributes(&attr, (const void*)k);
+        e = cudaFuncGetAttributes(&attr, k);
         if (e != cudaSuccess) return e;
         if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
-        e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
         if (e != cudaSuccess) return e;
       }
     int n = 0;
@@ -758,13 +762,14 @@ cudaError_t launch_attention_u4_few(const U4Args& call, const CUtensorMap& mk, c
   int sms = 0;
   cudaError_t e = few_ready(&sms);
   if (e != cudaSuccess) return e;
-  FewArgs t{call};
+  U4Args t = call;
   const Few& f = *few_for(t.a.c.head_dim, rows);
   t.tpt = f.rows / t.group;
   t.ring = make_ring(((int)kFewSmem - f.fixed) / t.stage_bytes, kMaxStages);
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  const bool bf16 = dtype == SV_BF16;
-  e = launch_pdl(bf16 ? f.bf16 : f.fp16, dim3(ctas), dim3(kFewThreads), kFewSmem, stream, mk, mv, t, bf16 ? 1 : 0);
+  e = dtype == SV_BF16 ? launch_pdl(f.bf16, dim3(ctas), dim3(kFewThreads), kFewSmem, stream, mk, mv, FewArgs<false>{t})
+                       : launch_pdl(f.fp16, dim3(ctas), dim3(kFewThreads), kFewSmem, stream, mk, mv,
+                                    FewArgs<true>{U4ExactArgs{t}});
   return e == cudaSuccess ? launch_u4_join(t, dtype, ctas, stream) : e;
 }
 

@@ -32,7 +32,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <climits>
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
@@ -227,7 +226,7 @@ constexpr int p_places(bool fp16, int n) { return fp16 && n <= 32 ? 4 : 2; }
 template <int DT, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attend_u4(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                const __grid_constant__ U4Args t) {
+                const __grid_constant__ U4ArgsOf<DT == SV_F16> t) {
   extern __shared__ __align__(1024) uint8_t smem[];
   // Few rows: the two softmax groups take tiles in turn, all rows each, with sums, maxima and O
   // of their own that the item's end adds up; a tile's fixed costs then fall on half the
@@ -756,32 +755,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float up = step * e_up;
           const uint64_t up2 = pack2(up, up), zero2 = pack2(zero, zero);
           const uint32_t prow = smem_u32(pbuf + b * kPBytes + row * 128) | ((row & 7) << 4);
-          // rest: where what the rounding takes off goes, from P's place
-          auto weights = [&](auto rest_too, uint32_t rest) {
+          // where what the rounding takes off goes, from there
+          const uint32_t rest = ((kTurns ? b + kRest : b ^ kRest) - b) * kPBytes;
 #pragma unroll
-            for (int u = 0; u < C; u += 8) {
-              uint32_t w[4], v[4];
+          for (int u = 0; u < C; u += 8) {
+            uint32_t w[4], v[4];
 #pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                const int n = u + e;
-                const uint64_t p = pack2(ex2(__uint_as_float(r[n])), ex2(__uint_as_float(r[n + 1])));
-                l2[n / 2] = fadd2(l2[n / 2], p);
-                z2[n / 2] = ffma2(p, zero2, z2[n / 2]);
-                float x, y;
-                unpack2(fmul2(p, up2), x, y);
-                w[e / 2] = F16<SV_F16>::down(x, y);
-                if constexpr (rest_too) {
-                  const float2 had = F16<SV_F16>::up(w[e / 2]);
-                  v[e / 2] = F16<SV_F16>::down(x - had.x, y - had.y);
-                }
+            for (int e = 0; e < 8; e += 2) {
+              const int n = u + e;
+              const uint64_t p = pack2(ex2(__uint_as_float(r[n])), ex2(__uint_as_float(r[n + 1])));
+              l2[n / 2] = fadd2(l2[n / 2], p);
+              z2[n / 2] = ffma2(p, zero2, z2[n / 2]);
+              float x, y;
+              unpack2(fmul2(p, up2), x, y);
+              w[e / 2] = F16<SV_F16>::down(x, y);
+              if constexpr (exact) {
+                const float2 had = F16<SV_F16>::up(w[e / 2]);
+                v[e / 2] = F16<SV_F16>::down(x - had.x, y - had.y);
               }
-              const int ch = (n0 + u) >> 3;
-              const uint32_t to = (prow ^ ((ch & 7) << 4)) + (ch >> 3) * kSpan;
-              st_shared16(to, w);
-              if constexpr (rest_too) st_shared16(to + rest, v);
             }
-          };
-          weights(exact, ((kTurns ? b + kRest : b ^ kRest) - b) * kPBytes);
+            const int ch = (n0 + u) >> 3;
+            const uint32_t to = (prow ^ ((ch & 7) << 4)) + (ch >> 3) * kSpan;
+            st_shared16(to, w);
+            if constexpr (exact) st_shared16(to + rest, v);
+          }
           fence_proxy_async();
           tc_fence_before();
           __syncwarp();
@@ -923,15 +920,14 @@ std::mutex g_mu;
 EncodeTiled g_encode = nullptr;
 int g_sms[64] = {};
 
-using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const U4Args);
-
-template <int DT>
-Kernel kernel_of(int n) {
+// f of the kernel for items of up to n rows.
+template <int DT, class Fn>
+cudaError_t with_kernel(int n, Fn f) {
   switch (n) {
-    case 32: return k_attend_u4<DT, 32>;
-    case 48: return k_attend_u4<DT, 48>;
-    case 64: return k_attend_u4<DT, 64>;
-    default: return k_attend_u4<DT, 80>;
+    case 32: return f(k_attend_u4<DT, 32>);
+    case 48: return f(k_attend_u4<DT, 48>);
+    case 64: return f(k_attend_u4<DT, 64>);
+    default: return f(k_attend_u4<DT, 80>);
   }
 }
 
@@ -946,15 +942,18 @@ cudaError_t device_ready(int* sms) {
     if (e != cudaSuccess) return e;
   }
   if (!g_sms[dev]) {
-    for (int n = 32; n <= kMaxN; n += 16)
-      for (Kernel k : {kernel_of<SV_BF16>(n), kernel_of<SV_F16>(n)}) {
-        cudaFuncAttributes attr{};
-        e = cudaFuncGetAttributes(&attr, (const void*)k);
-        if (e != cudaSuccess) return e;
-        if (attr.numRegs < Regs<32>::kLaunch) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
-        e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-        if (e != cudaSuccess) return e;
-      }
+    auto ready = [](auto* k) {
+      cudaFuncAttributes attr{};
+      const cudaError_t e = cudaFuncGetAttributes(&attr, (const void*)k);
+      if (e != cudaSuccess) return e;
+      if (attr.numRegs < Regs<32>::kLaunch) return cudaErrorInvalidKernelImage;  // the roles' shares count on them
+      return cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    };
+    for (int n = 32; n <= kMaxN; n += 16) {
+      e = with_kernel<SV_BF16>(n, ready);
+      if (e == cudaSuccess) e = with_kernel<SV_F16>(n, ready);
+      if (e != cudaSuccess) return e;
+    }
     int n = 0;
     e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -1018,7 +1017,6 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
   t.tpt = (int)(chunk < 1 ? 1 : (chunk + items - 1) / items);
   t.group_inv = (uint32_t)((65536 + t.group - 1) / t.group);
   t.c = a.scale_log2;
-  t.exact_keys = dtype == SV_F16 ? kExactKeys : INT_MIN;
   t.rec = reinterpret_cast<Rec*>(a.ws);
   t.err = reinterpret_cast<int*>(a.ws + kMaxCtas * sizeof(Rec));
   t.ml = reinterpret_cast<float2*>(a.ws + kRecBytes);
@@ -1061,8 +1059,11 @@ cudaError_t launch_attention_u4_tiles(const AttendArgs& a, int dtype, cudaStream
                     4 * N * 32 + (int)sizeof(Ctl);
   t.ring = make_ring(((int)kSmemBytes - fixed) / t.stage_bytes, kMaxStages);
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  e = launch_pdl(dtype == SV_BF16 ? kernel_of<SV_BF16>(N) : kernel_of<SV_F16>(N), dim3(ctas), dim3(kThreads),
-                 kSmemBytes, stream, mk, mv, t);
+  auto launch = [&](auto* k, auto args) {
+    return launch_pdl(k, dim3(ctas), dim3(kThreads), kSmemBytes, stream, mk, mv, args);
+  };
+  e = dtype == SV_BF16 ? with_kernel<SV_BF16>(N, [&](auto* k) { return launch(k, t); })
+                       : with_kernel<SV_F16>(N, [&](auto* k) { return launch(k, U4ExactArgs{t}); });
   return e == cudaSuccess ? launch_u4_join(t, dtype, ctas, stream) : e;
 }
 
