@@ -480,8 +480,9 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  * becomes an infinity and what lies below 2^-25 a zero).  An SV_U4 cache is not
  * dequantised: q.k_j = z_j sum(q) + s_j (q.c_j) in fp32, out = sum_j (p_j s_j) (c_j - 8) +
  * sum_j p_j (z_j + 8 s_j) with p_j s_j in fp16, relative to the largest |step| that the sequence's
- * key head has shown so far (weights below 2^-33 of that step are lost; for an SV_F16
- * output of a query that sees at most 512 keys, p_j s_j is the sum of two).
+ * key head has shown its chunk so far, later tokens of the chunk among them (weights keep all
+ * bits down to 2^-23 of that step and are lost below 2^-33; for an SV_F16 output of a query that
+ * sees at most 512 keys, p_j s_j is the sum of two).
  *   out       [total][heads][head_dim] of `dtype`, contiguous, 16-byte aligned
  *   out_lse   [total][heads] float or NULL: log sum_j exp(scale q.k_j)
  *   out_flags [B] uint8 or NULL: SV_FLAG_BAD_PAGE, SV_FLAG_BAD_LENGTH, and
@@ -489,7 +490,8 @@ size_t sv_attention_workspace_bytes(const sv_kv_cache* cache, int heads);
  *             gave up (outputs are then unspecified)
  * A query that sees no key (kv_len shorter than the chunk) gets out = 0 and
  * lse = -inf.  What a query does not see (later tokens of its chunk, slots behind
- * kv_len, tokens in front of its window) never reaches it, and may be NaN or infinite.
+ * kv_len, tokens in front of its window) never reaches it, and may be NaN or infinite (over an
+ * SV_U4 cache it is spared so too, but steps 2^23 times the seen ones cost weights bits, as above).
  * Outputs are the same bits every time.
  *   workspace >= sv_attention_workspace_bytes(cache, heads), 256-byte aligned
  */

@@ -12,7 +12,8 @@
 //
 // Why not the tensor memory that many rows use (sv_attention_u4_tiles.cu): there a tile costs
 // some 2300 clocks of hand-overs between roles, whatever its rows.  Here one of 24 rows takes 1370,
-// one of 8 rows 1050 (sequences of 16000 keys on average), where HBM would allow 756: up to 24 rows
+// one of 8 rows 1050 (sequences of 16000 keys on average; both and what follows with raw codes of v,
+// centring them adds 2%), where HBM would allow 756: up to 24 rows
 // of 128 dimensions are faster here, 32 are not (O no longer fits the registers).  Narrower heads
 // leave room for more; the bounds are kFew's.  (Where keys are few it takes many rows too, as more
 // items: the rule stands where the calls are told apart.)
@@ -711,9 +712,9 @@ constexpr Few few() {
              4 * W * NT * 64 * 16 + 2 * NT * W * 32 * 16 + (int)sizeof(FewCtl)};
 }
 // By width, the items' rows that there are: as many as the warps' registers hold.  Rounds of 64
-// sequences, us here and with the tensor memory: 128 wide 5 rows 101 and 153, 15 rows 108 and
-// 153, 20 rows 132 and 153, 30 rows 264 and 155; 96 wide, 20 rows 132 and 141; 64 wide, 20 rows
-// 111 and 134, 45 rows 168 and 177.
+// sequences, us here and with the tensor memory: 128 wide 5 rows 106 and 157, 15 rows 110 and
+// 157, 20 rows 134 and 157, 30 rows 264 and 155; 96 wide, 20 rows 116 and 146, 30 rows 138 and 147;
+// 64 wide, 20 rows 111 and 140, 45 rows 173 and 178; 32 wide, 20 rows 103 and 135.
 const Few kFew[] = {few<4, 1>(), few<4, 2>(), few<4, 3>(), few<3, 1>(), few<3, 2>(), few<3, 3>(), few<3, 4>(),
                     few<2, 1>(), few<2, 2>(), few<2, 4>(), few<2, 6>(), few<1, 1>(), few<1, 2>(), few<1, 4>()};
 

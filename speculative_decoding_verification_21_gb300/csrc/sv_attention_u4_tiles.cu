@@ -21,12 +21,12 @@
 // threads), so a tile needs no reduction across lanes, and the sums stay per thread to the
 // item's end.  Maxima and zeros enter S through one more product (16 deep, in bf16 parts).
 //
-// Measured: 32 sequences on up to 40000 keys, 9 tokens of 8 heads to a key head, 391 us (2.1 TB/s,
-// 0.55 PFLOP/s); prompts of 4096 tokens 1040 us (0.57 PFLOP/s).  What bounds it: instructions, some
-// 6000 a tile of 128 keys and 80 rows at 2 a clock and SM; loops are short and paths few because
-// the roles' code shares the instruction caches (forty instructions more in the softmax's loop cost
-// 10%).  A tile takes 3100 clocks, its products 680.  Fewer rows an item are slower: prompts in
-// items of 80, 64, 48 rows 1068, 1140, 1419 us.
+// Measured: 32 sequences on up to 40000 keys, 9 tokens of 8 heads to a key head, 396 us (2.0 TB/s,
+// 0.54 PFLOP/s); prompts of 4096 tokens 1050 us (0.57 PFLOP/s), in fp16 1119.  What bounds it:
+// instructions, some 6300 a tile of 128 keys and 80 rows at 2 a clock and SM; loops are short and
+// paths few because the roles' code shares the instruction caches (forty instructions more in the
+// softmax's loop cost 10%).  A tile takes some 3200 clocks, its products 680.  Fewer rows an item
+// are slower: prompts in items of 80, 64, 48 rows 1068, 1140, 1419 us (of raw codes).
 //
 // Every wait is bounded; one that gives up ends the CTA's roles and flags the call.
 #include <cuda.h>
