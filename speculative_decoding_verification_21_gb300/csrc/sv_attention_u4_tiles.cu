@@ -59,6 +59,10 @@ struct Regs {
   static constexpr int kLaunch = 96, kHelp = N <= 64 ? 64 : 48, kSoft = N <= 64 ? 144 : 168;
   static_assert((kThreads - 256) * kHelp + 256 * kSoft <= kThreads * kLaunch, "registers");
 };
+// What small steps of keys are measured against, by an item's queries (small_of).
+struct Small {
+  float codes, step;  // steps below the one do not matter; the other is used in their place
+};
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t qfull[2], qempty[2], kfull[2], kfree[2], sfull[2], sfree[2], pvfull[2], pvfree[2];
@@ -71,6 +75,7 @@ struct Ctl {
   long long warp_units[kThreads / 32];
   float qfac[2][kMaxN];                  // of each query row: factor back to kQShift
   int odd[2];                            // some row has a factor of its own
+  Small small[2];
   Seg seg[4];                            // the items, as warp 0 finds them (n = 0: no more)
   Walk walk;                             // where it is (no registers between items)
   float2 kv[4][kTile];                   // by tile: a key's factor of the product; V's step and zero
@@ -202,14 +207,22 @@ __device__ __forceinline__ uint4 key_side(const Parts& p) {
 __device__ __forceinline__ uint4 row_side(const Parts& p) {
   return make_uint4(p.p1 | p.p2 << 16, p.p1 | p.p3 << 16, p.p2 | p.p1 << 16, 0);
 }
-// The step that a key's products are in.  Where the codes cannot matter (a constant row has
-// the smallest step there is, or none), a step from the zero instead, or 1, and the codes are
-// dropped: z / s and m / (s c) stay in range.  (A maximum is at most 2^4 times the largest |key| in
-// units of Q, so 1 / s of 2^64 leaves keys up to 2^59; a row whose step is below 2^-64 weighs by
-// its zero.)
-__device__ __forceinline__ float working_step(float s, float z, bool& drop) {
-  drop = fabsf(s) < fmaxf(fabsf(z) * 0x1p-40f, 0x1p-64f);
-  return drop ? fmaxf(fabsf(z) * 0x1p-30f, 1.0f) : s;
+// The step that a key's products are in.  Codes that cannot matter are dropped: beside their zero
+// (a constant row has the smallest step there is, or none), or because all of them together move
+// no exponent by 2^-29 (zeros that were appended, bad pages).  Such a row has a step from its zero
+// instead, or one that keeps m / (s c) in range.
+//
+// c: scale log2 e; top: the exponent of the largest of the query rows' factors (-1000: all rows
+// are zeros).  Their elements are below 2^(9 + top), so codes move an exponent by less than
+// 15 2^(16 + top) s c.  A maximum enters the product as m 2^-18 / (s c) over its row's factor, and
+// comes out times that: c s = 2^(-top / 2) keeps both from the ends of the range.
+__device__ __forceinline__ Small small_of(float c, int top) {
+  const int e = (int)((__float_as_uint(c) >> 23) & 255u) - 127;
+  return Small{pow2f(max(-120, min(100, -50 - e - top))), pow2f(max(-120, min(100, -e - top / 2)))};
+}
+__device__ __forceinline__ float working_step(float s, float z, const Small& small, bool& drop) {
+  drop = fabsf(s) < fmaxf(fabsf(z) * 0x1p-40f, small.codes);
+  return drop ? fmaxf(fabsf(z) * 0x1p-30f, small.step) : s;
 }
 // Where row n has its eight entries for m (half 0) or Q (half 1): rows of 32 bytes, swizzled.
 __device__ __forceinline__ uint4* row_entries(uint8_t* tile, int n, int half) {
@@ -387,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait_held(ctl.qempty + qb, ((qn >> 1) & 1u) ^ 1u, guard, kWaitQFree);
       if (!ok) break;
       bool odd = false;
+      int largest = -1000;
       const int rows = s.ntok * t.group;
       constexpr int kAtOnce = 4;  // rows whose loads stand together
 #pragma unroll 1
@@ -426,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             shift = min(126, 14 + 127 - (int)(__float_as_uint(top) >> 23));
             odd = true;
           }
+          if (top > 0.0f && top < kInf) largest = max(largest, kQShift - shift);
           const float f0 = pow2f(shift), f1 = f0 * 0.0625f;
           if (sub * 8 < D && n < N) {
             uint8_t* const to =
@@ -448,7 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const bool any = __any_sync(0xffffffffu, odd);
-      if (lane == 0) ctl.odd[qb] = any;
+      largest = uniform(largest);
+      if (lane == 0) {
+        ctl.odd[qb] = any;
+        ctl.small[qb] = small_of(t.c, largest);
+      }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(ctl.qfull + qb);
@@ -460,9 +479,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool is_k = warp < 8;
     const float c18 = t.c * pow2f(24 - kQShift);  // undoes the codes' and the queries' powers
     const uint32_t lanes = tbase + ((uint32_t)(32 * quad) << 16);
-    uint32_t j = 0, k = 0;  // tiles and stages before
-    while (ok && take(s)) {
-      for (int i = 0; i < s.n; ++i, ++j) {
+    uint32_t j = 0, k = 0, qn = 0;  // tiles, stages and items before
+    for (; ok && take(s); ++qn) {
+      if (is_k) ok = wait_held(ctl.qfull + (qn & 1u), (qn >> 1) & 1u, guard, kWaitQ);
+      for (int i = 0; ok && i < s.n; ++i, ++j) {
         const Slot at(k, t.ring);
         const uint32_t b = j & 1u, ph = (j >> 1) & 1u;
         const uint8_t* const stage = ring + (size_t)at.i * t.stage_bytes;
@@ -475,7 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               reinterpret_cast<const uint32_t*>(stage + 4 * code_bytes + (i & 1) * 1024);
           const uint32_t sz = words[row];
           bool drop;
-          const float step = working_step(step_of(sz), zero_of(sz), drop), inv = __frcp_rn(step);
+          const float step = working_step(step_of(sz), zero_of(sz), ctl.small[qn & 1u], drop);
+          const float inv = __frcp_rn(step);
           const uint4 m4 = key_side(parts_of(inv)), q4 = key_side(parts_of(zero_of(sz) * inv));
           ok = wait_held(ctl.kfree + b, ph ^ 1u, guard, kWaitFree);
           if (rare(!ok)) break;

@@ -62,3 +62,32 @@ def test_zero_rows_among_large_products(n, dim, size, step):
         sz[300::71] = torch.tensor([step, 0.0], device="cuda").to(BF)
         hold(c, "k", b, sz)
     c.check(scale=1.28 / dim / size / 2.0 ** 8)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -64, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("n,dim", [(1, 64), (5, 128), (10, 128), (40, 128)])
+def test_keys_of_any_size(n, dim, size, zeros):
+    """Keys far from 1 and a scale that brings their products back, with zeros among them or not."""
+    c = CaseU4([(n, 700)] * 40 + [(n, n + 430)], dim=dim)
+    for b in range(41):
+        sz = (c.sz["k"][b].double() * size).to(BF)
+        if zeros:
+            sz[300::71] = 0.0
+        hold(c, "k", b, sz)
+    c.check(scale=dim ** -0.5 / size)
+
+
+@pytest.mark.parametrize("q_size,k_size", [(2.0 ** -80, 2.0 ** -20), (2.0 ** -40, 2.0 ** -57), (2.0 ** 50, 2.0 ** 60)])
+@pytest.mark.parametrize("n,dim", [(1, 64), (5, 128), (10, 128), (40, 128)])
+def test_products_of_any_size(n, dim, q_size, k_size):
+    """Queries and keys far from 1, rows of queries of very different sizes, zeros among the keys."""
+    c = CaseU4([(n, 700)] * 40 + [(n, n + 430)], dim=dim)
+    c.q.mul_(q_size)
+    c.q[:, 1].mul_(2.0 ** -20)
+    c.q[::3, 2] = 0
+    for b in range(41):
+        sz = (c.sz["k"][b].double() * k_size).to(BF)
+        sz[300::71] = 0.0
+        hold(c, "k", b, sz)
+    c.check(scale=dim ** -0.5 / k_size / q_size)
