@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
   } else {
     take_regs<kWorkRegs>();
-    const float c18 = t.c * pow2f(24 - kQShift);  // undoes the codes' and the queries' powers
+    constexpr float kUndo = (float)(1 << (24 - kQShift));  // the codes' and the queries' powers
     uint32_t slot = 0, phase = 0;
     for (uint32_t items = 0;; ++items) {
       const Seg& s = ctl.seg[items & 3u];
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               uint64_t A2[2], B2[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float A = step_of(words[u][e]) * c18, B = zero_of(words[u][e]) * t.c;
+                const float A = step_of(words[u][e]) * t.c * kUndo, B = zero_of(words[u][e]) * t.c;
                 A2[e] = pack2(A, A);
                 B2[e] = pack2(B, B);
                 step[2 * u + e] = step_of(words[u][2 + e]);

@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Warps 4-7 those of K, 8-11 those of V.
     const int quad = warp & 3, row = 32 * quad + lane;
     const bool is_k = warp < 8;
-    const float c18 = t.c * pow2f(24 - kQShift);  // undoes the codes' and the queries' powers
+    constexpr float kUndo = (float)(1 << (24 - kQShift));  // the codes' and the queries' powers
     const uint32_t lanes = tbase + ((uint32_t)(32 * quad) << 16);
     uint32_t j = 0, k = 0, qn = 0;  // tiles, stages and items before
     for (; ok && take(s); ++qn) {
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_held(ctl.kfree + b, ph ^ 1u, guard, kWaitFree);
           if (rare(!ok)) break;
           tc_fence_after();
-          ctl.kv[j & 3u][row] = make_float2(step * c18, __uint_as_float(words[kTile + row]));
+          ctl.kv[j & 3u][row] = make_float2(step * t.c * kUndo, __uint_as_float(words[kTile + row]));
           const uint32_t e[8] = {m4.x, m4.y, m4.z, m4.w, q4.x, q4.y, q4.z, q4.w};
           tmem_st8(lanes + b * kColK + 64, e);
           const uint8_t* const from = codes + row * (D / 2);
@@ -556,9 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tbase + ((uint32_t)(32 * quad) << 16);
     const int n0 = kTurns ? 0 : wg * C;           // the group's first row
     const uint32_t o_tm = lanes + kColO + (kTurns ? wg * N : n0);
-    // maxima go into the products (unless the scale is next to nothing: then all tiles take
-    // the slow way)
-    const bool applies = fabsf(t.c) >= 0x1p-100f;
+    // maxima go into the products (unless the scale is next to nothing, or so large that m / c is:
+    // then all tiles take the slow way)
+    const bool applies = fabsf(t.c) >= 0x1p-100f && fabsf(t.c) <= 0x1p100f;
     const float inv_c = applies ? 1.0f / t.c : 0.0f;
     // (one of the warps whose wait gave up goes on as far as the next vote, where its group
     // leaves the item, and both groups leave together: they meet at barriers without a limit)

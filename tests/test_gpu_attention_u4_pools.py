@@ -65,7 +65,7 @@ def test_zero_rows_among_large_products(n, dim, size, step):
 
 
 @pytest.mark.parametrize("zeros", [False, True])
-@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -64, 2.0 ** 60, 2.0 ** 100])
+@pytest.mark.parametrize("size", [2.0 ** -116, 2.0 ** -100, 2.0 ** -64, 2.0 ** 60, 2.0 ** 100])
 @pytest.mark.parametrize("n,dim", [(1, 64), (5, 128), (10, 128), (40, 128)])
 def test_keys_of_any_size(n, dim, size, zeros):
     """Keys far from 1 and a scale that brings their products back, with zeros among them or not."""
@@ -78,7 +78,7 @@ def test_keys_of_any_size(n, dim, size, zeros):
     c.check(scale=dim ** -0.5 / size)
 
 
-@pytest.mark.parametrize("q_size,k_size", [(2.0 ** -80, 2.0 ** -20), (2.0 ** -40, 2.0 ** -57), (2.0 ** 50, 2.0 ** 60)])
+@pytest.mark.parametrize("q_size,k_size", [(2.0 ** -100, 2.0 ** -20), (2.0 ** -60, 2.0 ** -57), (2.0 ** 50, 2.0 ** 60)])
 @pytest.mark.parametrize("n,dim", [(1, 64), (5, 128), (10, 128), (40, 128)])
 def test_products_of_any_size(n, dim, q_size, k_size):
     """Queries and keys far from 1, rows of queries of very different sizes, zeros among the keys."""
