@@ -21,8 +21,8 @@
 // threads), so a tile needs no reduction across lanes, and the sums stay per thread to the
 // item's end.  Maxima and zeros enter S through one more product (16 deep, in bf16 parts).
 //
-// Measured: 32 sequences on up to 40000 keys, 9 tokens of 8 heads to a key head, 396 us (2.0 TB/s,
-// 0.54 PFLOP/s); prompts of 4096 tokens 1050 us (0.57 PFLOP/s), in fp16 1119.  What bounds it:
+// Measured: 32 sequences on up to 40000 keys, 9 tokens of 8 heads to a key head, 400 us (2.0 TB/s,
+// 0.54 PFLOP/s); prompts of 4096 tokens 1060 us (0.56 PFLOP/s), in fp16 1140.  What bounds it:
 // instructions, some 6300 a tile of 128 keys and 80 rows at 2 a clock and SM; loops are short and
 // paths few because the roles' code shares the instruction caches (forty instructions more in the
 // softmax's loop cost 10%).  A tile takes some 3200 clocks, its products 680.  Fewer rows an item
